@@ -264,6 +264,80 @@ cudaError_t launch_prefill_sums(const SumsArgs& a, cudaStream_t s);
 cudaError_t launch_combine(const float* y, const float* gates, int T, int H, int k, int S,
                            const float* residual, float* out, cudaStream_t s);
 
+// ---- decoder-block operators around the experts -----------------------------
+struct NormArgs {
+  const void* x;
+  const void* residual;  // nullable
+  const void* w;
+  void* sum_out;         // nullable, of r_dtype
+  void* y;               // nullable
+  void* q;
+  float* d;
+  int16_t* bsum16;       // nullable
+  int x_dtype, r_dtype, w_dtype, y_dtype, q_fmt;
+  int64_t x_stride, r_stride, sum_stride, y_stride, T;
+  int H;
+  float eps, w_offset;
+  bool wide;             // every row of every array starts on a 16-byte boundary (q: 8), H % 8 == 0
+};
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s);
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;  // nullable
+  int32_t* ids;
+  float* gates;
+  int64_t stride;
+  int dtype, T, E, k, route, n_group, topk_group, group_score, renorm;
+  float scale;
+};
+cudaError_t launch_route_grouped(const RouteArgs& a, cudaStream_t s);
+
+struct KvAppendArgs {
+  moe_kv_desc kv;
+  const void* k;
+  const void* v;
+  int64_t k_stride, k_head_stride, v_stride, v_head_stride;
+  void* k_cache;
+  void* v_cache;
+  const int32_t* table;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int T;
+  int* status;
+  bool wide;          // 16-byte vectors throughout
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s);
+
+struct AttnArgs {
+  moe_kv_desc kv;
+  const void* q;
+  int64_t q_stride, q_head_stride;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* table;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  int Hq, T, window;
+  float scale;
+  void* out;
+  int64_t o_stride, o_head_stride;
+  float* lse;         // nullable
+  char* ws;
+  int* status;
+};
+size_t attn_workspace(int Hq, int Hkv, int D);
+bool attn_tensor_core(const moe_kv_desc& kv);  // the sizes that launch_attn takes
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_general(const AttnArgs& a, cudaStream_t s);
+
+// One sequence's rows and keys, checked: rows q0 .. q0 + n and kv keys.  A
+// sequence whose numbers are out of range has n = 0 (ok = false).
+struct SeqInfo {
+  int q0, n, kv;
+  bool ok;
+};
+
 cudaError_t launch_debug_dots(int fmt, const void* w, int N, int K, const int8_t* q, int T, int32_t* isum,
                               int32_t* bsum, cudaStream_t s);
 

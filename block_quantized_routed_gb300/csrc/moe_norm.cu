@@ -1,0 +1,266 @@
+// Residual addition, root-mean-square norm and an 8-bit output in one pass.
+//
+//   s = x + residual,  z = s * rsqrt(mean(s^2) + eps) * (w + offset)
+//   q = codes of z with one scale per 256 / 128 columns or per row
+//
+// What bounds it: memory.  Every element of x and residual is read once and
+// every output written once; s stays in registers between the sum of squares
+// and the scaling, so there is no second pass over global memory.
+//
+// Layout: one CTA per row.  A thread holds NV vectors of 8 consecutive
+// columns (vector i * blockDim + tid), so a warp's vectors are 256
+// consecutive columns: a q8_K block is one warp-wide maximum, a group of 128
+// columns a half-warp's, and neither needs shared memory.  Rows that are not
+// 16-byte aligned (odd H, odd strides) run the same mapping with element-wise
+// guarded loads (WIDE = false).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "moe_device.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+template <typename T>
+__device__ __forceinline__ float to_f(T v);
+template <>
+__device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <>
+__device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+
+// 8 consecutive elements as fp32; `n` of them exist (WIDE: all 8, 16-byte aligned)
+template <typename T, bool WIDE>
+__device__ __forceinline__ void load8(const T* p, int n, float* v) {
+  if constexpr (WIDE) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      T e[8];
+      *reinterpret_cast<uint4*>(e) = a;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = to_f<T>(e[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f<T>(p[i]) : 0.0f;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ T from_f(float v);
+template <>
+__device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+
+template <typename T, bool WIDE>
+__device__ __forceinline__ void store8(T* p, int n, const float* v) {
+  if constexpr (WIDE) {
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      T e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = from_f<T>(v[i]);
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = from_f<T>(v[i]);
+  }
+}
+
+// the same with the type known at run time (uniform over the grid)
+template <bool WIDE>
+__device__ __forceinline__ void load8_dt(const void* p, int dt, int64_t at, int n, float* v) {
+  if (dt == MOE_DT_F32) load8<float, WIDE>(static_cast<const float*>(p) + at, n, v);
+  else if (dt == MOE_DT_BF16) load8<__nv_bfloat16, WIDE>(static_cast<const __nv_bfloat16*>(p) + at, n, v);
+  else load8<__half, WIDE>(static_cast<const __half*>(p) + at, n, v);
+}
+template <bool WIDE>
+__device__ __forceinline__ void store8_dt(void* p, int dt, int64_t at, int n, const float* v) {
+  if (dt == MOE_DT_F32) store8<float, WIDE>(static_cast<float*>(p) + at, n, v);
+  else if (dt == MOE_DT_BF16) store8<__nv_bfloat16, WIDE>(static_cast<__nv_bfloat16*>(p) + at, n, v);
+  else store8<__half, WIDE>(static_cast<__half*>(p) + at, n, v);
+}
+
+// all threads of the block get the sum / the maximum, in a fixed order
+template <bool MAX>
+__device__ __forceinline__ float block_reduce(float v, float* buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, w) : v + w;
+  }
+  const int nw = blockDim.x >> 5;
+  if (nw == 1) return v;
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int lane = threadIdx.x & 31;
+  v = lane < nw ? buf[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, w) : v + w;
+  }
+  return v;
+}
+
+// the q8_K rounding: half away from zero, clamped; 0 when the scale is 0
+__device__ __forceinline__ int q8k_code(float z, float d) {
+  return d != 0.0f ? (int)fminf(127.0f, fmaxf(-127.0f, roundf(__fdiv_rn(z, d)))) : 0;
+}
+
+template <typename XT, typename RT, int NV, bool WIDE>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
+  __shared__ float buf[2][32];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const XT* x = static_cast<const XT*>(a.x) + row * a.x_stride;
+  const RT* res = static_cast<const RT*>(a.residual) + row * a.r_stride;
+  float s[NV][8];
+  float sq = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8, n = a.H - c;
+    if (n > 0) {
+      load8<XT, WIDE>(x + c, n, s[i]);
+      if (a.residual) {
+        float r[8];
+        load8<RT, WIDE>(res + c, n, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8, n = a.H - c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
+    if (a.sum_out && n > 0) store8<RT, WIDE>(static_cast<RT*>(a.sum_out) + row * a.sum_stride + c, n, s[i]);
+  }
+  sq = block_reduce<false>(sq, buf[0]);
+  const float r = 1.0f / sqrtf(sq / (float)a.H + a.eps);
+  float peak = 0.0f;  // of the row, for the row-scaled outputs
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8, n = a.H - c;
+    float w[8];
+    if (n > 0) {
+      load8_dt<WIDE>(a.w, a.w_dtype, c, n, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * r * (w[j] + a.w_offset);
+      if (a.y) store8_dt<WIDE>(a.y, a.y_dtype, row * a.y_stride + c, n, s[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
+  }
+  if (a.q_fmt == MOE_NORM_Q_NONE) return;
+
+  const bool fp8 = a.q_fmt == MOE_NORM_Q_E4M3_G128 || a.q_fmt == MOE_NORM_Q_E4M3_ROW;
+  const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
+  const float top = fp8 ? 448.0f : 127.0f;
+  float d = 0.0f;
+  if (per_row) {
+    peak = block_reduce<true>(peak, buf[1]);
+    d = __fdiv_rn(peak, top);
+    if (tid == 0) a.d[row] = d;
+  }
+  const int group = a.q_fmt == MOE_NORM_Q_Q8K ? 256 : 128;
+  const int groups = (a.H + group - 1) / group;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8, n = a.H - c;
+    if (!per_row) {
+      float m = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(s[i][j]));
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (group == 256) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      d = __fdiv_rn(m, top);
+      if (n > 0 && c % group == 0) a.d[row * groups + c / group] = d;
+    }
+    uint8_t q[8];
+    int sum = 0;
+    if (fp8) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        // d = 0 only where every z of the group is 0 (or too small for z / 448 to exist)
+        const float2 z = d > 0.0f ? make_float2(__fdiv_rn(s[i][j], d), __fdiv_rn(s[i][j + 1], d)) : make_float2(0.f, 0.f);
+        *reinterpret_cast<__nv_fp8x2_storage_t*>(q + j) = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int code = q8k_code(s[i][j], d);
+        q[j] = (uint8_t)(int8_t)code;
+        sum += code;
+      }
+    }
+    uint8_t* out = static_cast<uint8_t*>(a.q) + row * a.H + c;
+    if constexpr (WIDE) {
+      if (n > 0) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(q);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) out[j] = q[j];
+    }
+    if (a.bsum16) {  // q8_K: two lanes hold the 16 codes
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      if (n > 0 && (tid & 1) == 0) a.bsum16[row * (a.H / 16) + c / 16] = (int16_t)sum;
+    }
+  }
+}
+
+template <typename XT, typename RT, bool WIDE>
+cudaError_t launch_nv(const NormArgs& a, cudaStream_t s) {
+  const int vecs = (a.H + 7) / 8;
+  // Few rows: latency counts, one vector per thread.  Many rows: two to eight
+  // vectors per thread, so that a CTA is small and its loads are in flight together.
+  int nv = 1;
+  if (a.T > 2 * num_sms())
+    while (nv < 4 && vecs > 128 * nv) nv *= 2;
+  while (nv < 8 && vecs > 1024 * nv) nv *= 2;
+  const int threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
+  note_launch();
+  const dim3 grid((unsigned)a.T);
+  switch (nv) {
+    case 1: add_rmsnorm_kernel<XT, RT, 1, WIDE><<<grid, threads, 0, s>>>(a); break;
+    case 2: add_rmsnorm_kernel<XT, RT, 2, WIDE><<<grid, threads, 0, s>>>(a); break;
+    default: add_rmsnorm_kernel<XT, RT, 4, WIDE><<<grid, threads, 0, s>>>(a); break;
+  }
+  return cudaGetLastError();
+}
+
+template <typename XT, typename RT>
+cudaError_t launch_types(const NormArgs& a, cudaStream_t s) {
+  return a.wide ? launch_nv<XT, RT, true>(a, s) : launch_nv<XT, RT, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  if (a.x_dtype == MOE_DT_F32) return launch_types<float, float>(a, s);
+  if (a.x_dtype == MOE_DT_BF16)
+    return a.r_dtype == MOE_DT_F32 ? launch_types<__nv_bfloat16, float>(a, s)
+                                   : launch_types<__nv_bfloat16, __nv_bfloat16>(a, s);
+  return a.r_dtype == MOE_DT_F32 ? launch_types<__half, float>(a, s) : launch_types<__half, __half>(a, s);
+}
+
+}  // namespace moe

@@ -453,6 +453,132 @@ int moe_debug_prefill_sums(int32_t fmt, const void* w, int32_t N, int32_t K, con
                            const int16_t* bsum16, int32_t T, int32_t* S, int32_t* M, void* ws, size_t ws_bytes,
                            void* stream);
 
+/* ======================================================================== *
+ * The decoder-block operators around the experts: residual addition and    *
+ * norm with an 8-bit output, routing of given scores with groups and a     *
+ * balance bias, a paged key/value cache and the attention that reads it.   *
+ * (The Pulsar / Strata pages run them around every MoE layer but do not    *
+ * specify them; formulas and layouts are this library's own.)              *
+ * ======================================================================== */
+typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 } moe_dtype;
+
+/* 8-bit outputs of moe_add_rmsnorm.  z is the normalised fp32 row. */
+typedef enum {
+  MOE_NORM_Q_NONE = 0,
+  MOE_NORM_Q_Q8K = 1,       /* the q8_K rule of moe_q8k_quantize, groups of 256 (+ bsum16); H % 256 == 0 */
+  MOE_NORM_Q_E4M3_G128 = 2, /* e4m3 codes of z / d, d = max|z| / 448 over each 128 columns (last group ragged) */
+  MOE_NORM_Q_E4M3_ROW = 3,  /* the same with one d per row */
+  MOE_NORM_Q_INT8_ROW = 4   /* the q8_K rounding with one d = max|z| / 127 per row */
+} moe_norm_q;
+
+/* Residual addition and root-mean-square norm of T rows of H columns:
+ *   s = x + residual            (fp32; residual may be NULL: s = x)
+ *   z = s * rsqrt(mean(s^2) + eps) * (weight + weight_offset)     (fp32)
+ *   sum_out = s rounded to residual's type (x's without a residual); NULL to skip
+ *   y = z rounded to y_dtype; NULL to skip
+ *   q, d [, bsum16] = the 8-bit output q_fmt of z (not of the rounded y)
+ * The norm is taken of the unrounded s.  Row strides are in elements and may
+ * exceed H; q is [T, H] and d [T, ceil(H / group)] without gaps, bsum16 int16
+ * [T, H/16] (q8_K only, may be NULL).  Types: x and y any moe_dtype, residual
+ * x's type or fp32, weight any.  H in 1..MOE_MAX_DIM, eps >= 0, T >= 0.
+ * sum_out may be x or residual themselves where type and stride agree; no
+ * other overlap.  An all-zero group has d = 0 and codes 0; a row holding NaN
+ * or an infinity has unspecified y and codes, other rows are not affected.
+ * s^2 is summed in fp32: |s| beyond 1e18 overflows it.  Pointers must be
+ * aligned to their element; rows on 16-byte boundaries take the wide loads. */
+int moe_add_rmsnorm(const void* x, int32_t x_dtype, int64_t x_stride, const void* residual, int32_t r_dtype,
+                    int64_t r_stride, const void* weight, int32_t w_dtype, float weight_offset, float eps, int64_t T,
+                    int32_t H, void* sum_out, int64_t sum_stride, void* y, int32_t y_dtype, int64_t y_stride,
+                    int32_t q_fmt, void* q, float* d, int16_t* bsum16, void* stream);
+
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+
+/* Routing of given logits [T, E] (row stride in elements) to k experts:
+ *   p = sigmoid(l) (MOE_ROUTE_SIGMOID) or softmax over all E (MOE_ROUTE_SOFTMAX)
+ *   key = p + bias[e]      (bias fp32 [E] for balance; NULL: key = p)
+ *   With n_group > 1 the experts are n_group runs of E / n_group; a group's
+ *   score is its largest key (MOE_GROUP_MAX) or the sum of its two largest
+ *   (MOE_GROUP_TOP2; the largest alone in groups of one); only experts of the
+ *   topk_group best groups can be selected.
+ *   ids int32 [T, k]: the k largest keys in descending order
+ *   gates float [T, k]: p of the selected (without the bias), divided by their
+ *   sum when renorm is non-zero, times scale.
+ * Equal keys and equal group scores: lower index first.  The selection is that
+ * of keys computed in 64 bits (without a bias: that of the logits): where fp32
+ * cannot tell two keys apart the token is decided again in fp64.  A NaN logit
+ * counts as -inf; -inf has p = 0; a +inf under softmax takes the whole weight
+ * (shared among equals).  A selection whose p sum to 0 has gates 0.
+ * Limits: E <= MOE_MAX_EXPERTS, k <= MOE_MAX_TOPK, n_group divides E and is at
+ * most 32 (else MOE_ERR_UNSUPPORTED), k <= topk_group * (E / n_group). */
+int moe_route_grouped(const void* logits, int32_t dtype, int64_t stride, const float* bias, int32_t T, int32_t E,
+                      int32_t k, int32_t route, int32_t n_group, int32_t topk_group, int32_t group_score,
+                      int32_t renorm, float scale, int32_t* ids, float* gates, void* stream);
+
+/* A paged key/value cache of n_seqs sequences.  Key j of sequence b and head h
+ * is the D elements at
+ *   k_cache + page_table[b * table_stride + j / page_size] * k_page_stride
+ *           + (j % page_size) * k_row_stride + h * k_head_stride   (elements)
+ * and its value likewise with the v_ strides. */
+typedef struct {
+  int32_t n_seqs;    /* sequences of this call, 1..MOE_MAX_SEQS                 */
+  int32_t Hkv;       /* key/value heads                                         */
+  int32_t D;         /* elements per head: a multiple of 8, <= 256              */
+  int32_t dtype;     /* MOE_DT_BF16 or MOE_DT_F16                               */
+  int32_t page_size; /* keys per page, >= 1                                     */
+  int32_t num_pages; /* pages of the cache: valid page numbers are below it     */
+  int32_t max_pages; /* page-table entries per sequence                         */
+  int32_t reserved;  /* 0                                                       */
+  int64_t table_stride;
+  int64_t k_page_stride, k_row_stride, k_head_stride;
+  int64_t v_page_stride, v_row_stride, v_head_stride;
+} moe_kv_desc;
+#define MOE_MAX_SEQS 8192
+
+/* Writes a chunk's new keys and values into the cache.  cu_q int32
+ * [n_seqs + 1]: the tokens of sequence b are rows cu_q[b] .. cu_q[b+1] of
+ * k/v [T, Hkv, D] (token and head strides in elements); kv_len int32
+ * [n_seqs]: keys of each sequence INCLUDING the new ones, so token i of
+ * n = cu_q[b+1] - cu_q[b] goes to position kv_len[b] - n + i.  Rows outside
+ * cu_q are ignored.  Positions that two tokens share (pages listed twice) are
+ * written in no order.  Positions outside 0..max_pages*page_size and page
+ * numbers outside 0..num_pages are skipped and recorded as
+ * MOE_ERR_DEVICE_BOUNDS in the status word, the first 4 bytes of ws (16 bytes,
+ * 16-byte aligned, zero before the first call; see moe_get_status). */
+int moe_kv_append(const moe_kv_desc* kv, const void* k, int64_t k_stride, int64_t k_head_stride, const void* v,
+                  int64_t v_stride, int64_t v_head_stride, void* k_cache, void* v_cache, const int32_t* page_table,
+                  const int32_t* cu_q, const int32_t* kv_len, int32_t T, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe_paged_attention (0 for unsupported sizes): a status
+ * word and counters, zero before the first call, and partial results of
+ * sequences that several CTAs share. */
+size_t moe_paged_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D);
+
+/* Attention of a chunk of new tokens over a paged cache that already holds
+ * their keys and values (moe_kv_append): single tokens, verify windows and
+ * prompt chunks in one call.  Query head g reads key/value head
+ * g / (Hq / Hkv).  Token i of sequence b (n tokens, kv_len[b] keys) stands at
+ * position t = kv_len[b] - n + i and sees the keys j with j <= t, and with
+ * window > 0 only those with j > t - window:
+ *   a_j = scale * (q . k_j),  out = sum_j exp(a_j - m) v_j / sum_j exp(a_j - m)
+ *   lse = log(sum_j exp(a_j))   (natural logarithm; float [T, Hq], NULL to skip)
+ * A token that sees no key (t < 0) has out = 0 and lse = -inf.  Rows of q
+ * outside cu_q are ignored and their out is not written.  q and out
+ * [T, Hq, D] have token and head strides in elements, multiples of 8; all
+ * pointers are 16-byte aligned.  Scores and sums are fp32; the weights are
+ * rounded to the cache's type before the product with the values.  The
+ * values of keys that a token does not see, but another token of its tile
+ * does, have to be finite: they are multiplied by a zero weight.  The cache
+ * beyond kv_len is never used.  Head sizes 64, 128 and 256 with a page size
+ * that is a power of two >= 16 run on the tensor cores; other sizes run on a
+ * general kernel.  Sequences with cu_q out of order or out of range, or
+ * kv_len outside 0..max_pages*page_size, are skipped and recorded as
+ * MOE_ERR_DEVICE_BOUNDS in the status word of ws, as are page numbers outside
+ * 0..num_pages (their keys read as zeros). */
+int moe_paged_attention(const moe_kv_desc* kv, const void* q, int64_t q_stride, int64_t q_head_stride, int32_t Hq,
+                        int32_t T, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                        const int32_t* cu_q, const int32_t* kv_len, float scale, int32_t window, void* out,
+                        int64_t o_stride, int64_t o_head_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
