@@ -1,0 +1,996 @@
+// Attention of a chunk of new tokens over a paged key/value cache, on the
+// tensor cores (tcgen05), for single tokens, verify windows and prompt chunks.
+//
+//   a_j = scale * q . k_j,   out = sum_j 2^(c a_j - m) v_j / sum_j 2^(c a_j - m)
+//
+// in one pass over the keys with a running reference m and sum (c = log2 e).
+//
+// Rows.  The query heads that share a key/value head are rows of the same
+// tile: row R of a sequence is (token R / G, head R % G), so a single token
+// of G heads already fills G rows and every key is read once per key/value
+// head.  A work item is (sequence, key/value head, up to 256 rows) over its
+// visible range of keys, cut into tiles of kN keys.
+//
+// Work split.  All items of a call, laid end to end in tiles, are divided
+// evenly over the CTAs (one per SM): every CTA gets the same number of key
+// tiles whatever the lengths.  An item cut by a CTA boundary leaves partial
+// sums in the workspace; the CTA that arrives last joins them in a fixed
+// order, so results do not depend on timing.  The division is found by each
+// CTA from cu_q and kv_len in a short prologue: no planning launch, no host
+// knowledge of the lengths.
+//
+// Inside a CTA (warp roles): one warp feeds a ring of key and value tiles by
+// TMA through the page table, one issues the MMAs, two gather the query rows,
+// and two groups of four warps run the softmax, each on its own score buffer
+// in tensor memory, thread = row.  Score tile u uses buffer u % 2:
+//   items of more than 128 rows: u = 2 * tile + half, each half a row tile of
+//     its own (both read the same keys);
+//   smaller items: u = tile, the two groups take alternate key tiles with
+//     sums of their own and are joined at the end.
+// The issue order S(0) S(1) | P(u)V, S(u + 2) | keeps one group's softmax
+// beside the other's products.  P replaces its scores in tensor memory as
+// 16-bit numbers (one rounding; sums are taken of the unrounded values) and
+// is the A operand of P V; V is read as it lies in the cache (MN-major).
+//
+// The output accumulator is rescaled only when a row's maximum has grown by
+// more than 2^8 over the reference: weights stay below 2^8, exactly
+// representable in range for fp16 and bf16, and most tiles skip the pass over
+// the accumulator.
+//
+// Every wait is bounded: after about a second a role records
+// MOE_ERR_DEVICE_TIMEOUT, and all roles run to the end without waiting.
+#include <algorithm>
+#include <cmath>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <mutex>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "moe_kv.cuh"
+
+namespace moe {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr long long kWaitCycles = 2000000000ll;  // ~1 s at 2 GHz
+constexpr int kMaxCtas = 160;                    // the workspace holds the partial sums of this many
+constexpr int kCounters = kMaxCtas * 2;
+constexpr size_t kWsHead = 16 + (size_t)kCounters * 4 + 240;  // status, counters; a multiple of 256
+static_assert(kWsHead % 256 == 0, "partials start aligned");
+constexpr float kGrow = 8.0f;                    // log2 of the growth that forces a rescale
+
+template <int D_>
+struct Cfg {
+  static constexpr int D = D_;
+  static constexpr int kN = D == 256 ? 64 : 128;         // keys per tile
+  static constexpr int kGroups = D == 256 ? 1 : 2;       // softmax groups of four warps
+  static constexpr int kRows = 128 * kGroups;            // rows per item
+  static constexpr int kSub = D / 64;                    // 128-byte wide sub-tiles of a row
+  static constexpr int kSlot = kN * D * 2;               // one key or value tile
+  static constexpr int kQ = 128 * D * 2;                 // one row tile of q
+  static constexpr int kStages = (229376 - kGroups * kQ) / kSlot;
+  static constexpr int kThreads = 128 * kGroups + 128;
+  static constexpr int kSmemQ = 0;
+  static constexpr int kSmemRing = kGroups * kQ;
+  static constexpr int kSmemMisc = kSmemRing + kStages * kSlot;
+  static constexpr int kSmem = kSmemMisc + 1024 + 1024;  // barriers and the prologue's results; alignment slack
+  static constexpr uint32_t kColO = 0, kColS = 256;      // tensor memory columns: O per group, two score buffers
+};
+static_assert(Cfg<128>::kSmem <= 232448 && Cfg<64>::kSmem <= 232448 && Cfg<256>::kSmem <= 232448, "shared memory");
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint32_t bar, int n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page,
+                                       uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
+      : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void named_sync(int id, int n) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
+}
+
+// 32 columns of the warp's 32 lanes, one lane (row) per thread
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t f2(float x, float y) {
+  return (uint64_t)__float_as_uint(x) | ((uint64_t)__float_as_uint(y) << 32);
+}
+__device__ __forceinline__ float f2_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float f2_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float ex2(float x) {  // 2^x, within 2 ulp; 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle.  K-major: 8-row groups
+// 1024 bytes apart, K advances by 32 bytes per step of 16 inside the 128.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
+         (uint64_t)2 << 61;
+}
+// MN-major: 64 columns (128 bytes) of one K row per line, 8-row groups 1024
+// bytes apart along K, the next 64 columns `next` bytes further.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t next) {
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// kind::f16, fp32 accumulation, M = 128
+__host__ __device__ constexpr uint32_t idesc(bool bf16, int N, bool b_mn, bool neg_a) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (neg_a ? 1u << 13 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         (uint32_t)(N >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+// ---------------------------------------------------------------- work items
+// One item: a row tile of a (sequence, key/value head) and its range of keys.
+struct Item {
+  int b, h, i;       // sequence, key/value head, row tile
+  SeqInfo s;
+  int tiles_q;       // row tiles of the sequence
+  int r0, rows;      // first row, rows (1 .. kRows)
+  int lo, hi;        // keys that some row sees
+  int t0, tiles;     // first key tile, number of key tiles
+  __device__ __forceinline__ int cost() const { return max(1, tiles); }
+};
+
+template <int kN, int kRows>
+__device__ __forceinline__ void item_range(const AttnArgs& a, int G, Item& it) {
+  const int R = it.s.n * G;
+  it.r0 = it.i * kRows;
+  it.rows = min(kRows, R - it.r0);
+  const int off = it.s.kv - it.s.n;
+  it.hi = max(0, off + (it.r0 + it.rows - 1) / G + 1);
+  it.lo = a.window > 0 ? min(it.hi, max(0, off + it.r0 / G + 1 - a.window)) : 0;
+  it.t0 = it.lo / kN;
+  it.tiles = it.hi > it.lo ? (it.hi + kN - 1) / kN - it.t0 : 0;
+}
+
+// The CTA's run of work: `left` units from unit `off` of the current item on.
+struct Walk {
+  Item it;
+  int off;
+  long long left;
+};
+
+// what the prologue leaves in shared memory for every role
+struct Start {
+  int b, h, i, off;
+  long long first, left, total;
+  int ctas;
+  volatile int abort;
+  uint32_t tmem;
+  int last[2];  // combine: this group arrived last
+};
+
+template <int kN, int kRows>
+__device__ __forceinline__ Walk walk_begin(const AttnArgs& a, int G, const Start& st) {
+  Walk w;
+  w.it.b = st.b;
+  w.it.h = st.h;
+  w.it.i = st.i;
+  w.off = st.off;
+  w.left = st.left;
+  if (w.left > 0) {
+    w.it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, w.it.b);
+    w.it.tiles_q = (w.it.s.n * G + kRows - 1) / kRows;
+    item_range<kN, kRows>(a, G, w.it);
+  }
+  return w;
+}
+// past the current item, if work is left
+template <int kN, int kRows>
+__device__ __forceinline__ void walk_next(const AttnArgs& a, int G, Walk& w, int done) {
+  w.left -= done;
+  if (w.left <= 0) return;
+  w.off = 0;
+  if (++w.it.i == w.it.tiles_q) {
+    w.it.i = 0;
+    if (++w.it.h == a.kv.Hkv) {
+      w.it.h = 0;
+      do {
+        ++w.it.b;
+        w.it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, w.it.b);
+      } while (w.it.s.n == 0 && w.it.b + 1 < a.kv.n_seqs);
+      w.it.tiles_q = (w.it.s.n * G + kRows - 1) / kRows;
+    }
+  }
+  item_range<kN, kRows>(a, G, w.it);
+}
+__device__ __forceinline__ int walk_len(const Walk& w) { return (int)min((long long)(w.it.cost() - w.off), w.left); }
+
+// units before CTA c of n
+__device__ __forceinline__ long long share(long long total, int n, int c) { return total * c / n; }
+// the CTA that holds unit g
+__device__ __forceinline__ int owner(long long total, int n, long long g) { return (int)(((g + 1) * n - 1) / total); }
+
+// The ring's order: pair(o) is the o-th load of a segment of m tiles, a key
+// tile (value = false) or a value tile.  Items of two row tiles consume K0 V0
+// K1 V1 ..; the others run one tile ahead: K0 K1 V0 K2 V1 .. V(m-1).
+__device__ __forceinline__ int ring_op(int o, int m, bool two, bool& value) {
+  if (two) {
+    value = o & 1;
+    return o >> 1;
+  }
+  if (o == 2 * m - 1) {
+    value = true;
+    return m - 1;
+  }
+  if (o < 2) {
+    value = false;
+    return o;
+  }
+  value = !(o & 1);
+  return value ? (o - 2) >> 1 : (o + 1) >> 1;
+}
+
+struct Wait {
+  Start* st;
+  int* status;
+  // false: given up here or by another role
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    if (bar_try(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!bar_try(bar, parity)) {
+      if (st->abort) return false;
+      if (clock64() - t0 > kWaitCycles) {
+        st->abort = 1;
+        set_status(status, MOE_ERR_DEVICE_TIMEOUT);
+        return false;
+      }
+    }
+    return true;
+  }
+};
+
+// every lane of a (converged) warp waits; the warp is converged afterwards.  A
+// wait that was given up is not told: the softmax groups run on, so that all
+// of them reach the same barriers, and the result is void (status word).
+__device__ __forceinline__ void warp_wait(const Wait& w, uint32_t bar, uint32_t parity) {
+  w(bar, parity);
+  __syncwarp();
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using C = Cfg<D>;
+  constexpr int kN = C::kN, kRows = C::kRows, kGroups = C::kGroups, kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const uint32_t base = smem_u32(smem);
+  const uint32_t bars = base + C::kSmemMisc;
+  const auto full = [&](int s) { return bars + 8 * s; };
+  const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
+  const uint32_t q_full = bars + 8 * (2 * kStages), q_empty = q_full + 8, drain = q_full + 16;
+  const auto s_full = [&](int b) { return q_full + 24 + 8 * b; };
+  const auto p_full = [&](int b) { return q_full + 40 + 8 * b; };
+  const auto o_full = [&](int b) { return q_full + 56 + 8 * b; };
+  Start& st = *reinterpret_cast<Start*>(smem + C::kSmemMisc + 512);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarpLoad = 4 * kGroups, kWarpMma = kWarpLoad + 1, kWarpQ = kWarpLoad + 2;
+  const int G = a.Hq / a.kv.Hkv;
+
+  // ---- prologue: the call's work in units, and this CTA's share
+  long long* cost = reinterpret_cast<long long*>(smem + C::kSmemRing);  // per sequence; the ring is not in use yet
+  for (int b = warp; b < a.kv.n_seqs; b += C::kThreads / 32) {
+    Item it;
+    it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, b);
+    if (!it.s.ok && blockIdx.x == 0 && lane == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+    const int nt = (it.s.n * G + kRows - 1) / kRows;
+    long long sum = 0;
+    for (it.i = lane; it.i < nt; it.i += 32) {
+      item_range<kN, kRows>(a, G, it);
+      sum += it.cost();
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+    if (lane == 0) cost[b] = sum * a.kv.Hkv;
+  }
+  if (warp == kWarpMma && lane == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      bar_init(full(s), 1);
+      bar_init(empty(s), 1);
+    }
+    bar_init(q_full, 64);
+    bar_init(q_empty, 2);
+    bar_init(drain, 1);
+    for (int b = 0; b < 2; ++b) {
+      bar_init(s_full(b), 1);
+      bar_init(p_full(b), 4);
+      bar_init(o_full(b), 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    st.abort = 0;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    long long total = 0;
+    for (int b = lane; b < a.kv.n_seqs; b += 32) total += cost[b];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+    const int n = (int)max(1ll, min((long long)gridDim.x, total));
+    const int c = blockIdx.x;
+    const bool work = c < n && total > 0;
+    const long long g0 = work ? share(total, n, c) : 0, g1 = work ? share(total, n, c + 1) : 0;
+    int fb = 0, fh = 0, fi = 0;
+    long long at = 0;  // units before sequence fb
+    if (work) {
+      for (int b0 = 0; b0 < a.kv.n_seqs; b0 += 32) {
+        const int b = b0 + lane;
+        const long long mine = b < a.kv.n_seqs ? cost[b] : 0;
+        long long inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(kAll, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const unsigned hit = __ballot_sync(kAll, at + inc > g0);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          fb = b0 + src;
+          at += __shfl_sync(kAll, inc - mine, src);
+          break;
+        }
+        at += __shfl_sync(kAll, inc, 31);
+      }
+      Item it;
+      it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, fb);
+      const int nt = (it.s.n * G + kRows - 1) / kRows;
+      const long long per = cost[fb] / a.kv.Hkv;
+      long long rem = g0 - at;
+      fh = (int)(rem / per);
+      rem -= fh * per;
+      for (int i0 = 0; i0 < nt; i0 += 32) {
+        it.i = i0 + lane;
+        long long mine = 0;
+        if (it.i < nt) {
+          item_range<kN, kRows>(a, G, it);
+          mine = it.cost();
+        }
+        long long inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(kAll, inc, o);
+          if (lane >= o) inc += v;
+        }
+        const unsigned hit = __ballot_sync(kAll, inc > rem);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          fi = i0 + src;
+          rem -= __shfl_sync(kAll, inc - mine, src);
+          break;
+        }
+        rem -= __shfl_sync(kAll, inc, 31);
+      }
+      at = rem;
+    }
+    if (lane == 0) {
+      st.b = fb;
+      st.h = fh;
+      st.i = fi;
+      st.off = (int)at;
+      st.first = g0;
+      st.left = g1 - g0;
+      st.total = total;
+      st.ctas = n;
+    }
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&st.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  fence_proxy();  // the prologue's writes to the ring come before the TMA's
+  const uint32_t tmem = st.tmem;
+  const Wait wait{&st, a.status};
+  const float c2 = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-30f);  // log2 units; the sign is in the MMA
+
+  // Two groups: 384 threads start with 168 registers each; the softmax groups
+  // take 208, the other four warps keep 88 (256 * 208 + 128 * 88 = 384 * 168).
+  if (warp >= kWarpLoad) {
+    if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == kWarpLoad) {
+      // ---- keys and values by TMA, a box per (page, 64 columns)
+      const int ps = a.kv.page_size;
+      const int box_rows = min(ps, kN);
+      const uint32_t box_bytes = (uint32_t)box_rows * 128;
+      const int part = lane % C::kSub, box = lane / C::kSub;  // this lane's box of a tile
+      uint32_t n_ops = 0;
+      bool ok = true;
+      for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0 && ok;) {
+        const int len = walk_len(w);
+        const int m = w.it.tiles ? len : 0;
+        const bool two = kGroups == 2 && w.it.rows > 128;
+        const int32_t* table = a.table + (int64_t)w.it.b * a.kv.table_stride;
+        for (int o = 0; o < 2 * m; ++o) {
+          bool value;
+          const int tile = w.it.t0 + w.off + ring_op(o, m, two, value);
+          const int k0 = tile * kN, from = max(w.it.lo, k0), to = min(w.it.hi, k0 + kN);
+          // boxes of the tile that hold a visible key
+          const int b0 = (from - k0) / box_rows, b1 = (to - k0 + box_rows - 1) / box_rows;
+          const bool mine = box >= b0 && box < b1;
+          int page = 0;
+          if (mine) {
+            page = __ldg(table + (k0 + box * box_rows) / ps);
+            if (page < 0 || page >= a.kv.num_pages) {
+              set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+              page = a.kv.num_pages;  // out of range: reads as zeros
+            }
+          }
+          const int slot = n_ops % kStages;
+          const uint32_t round = n_ops / kStages;
+          if (round > 0) {
+            if (lane == 0) ok = wait(empty(slot), (round - 1) & 1);
+            ok = __shfl_sync(kAll, (int)ok, 0);
+            if (!ok) break;
+          }
+          if (lane == 0) bar_expect(full(slot), box_bytes * (uint32_t)((b1 - b0) * C::kSub));
+          __syncwarp();
+          if (mine)
+            tma_4d(base + C::kSmemRing + slot * C::kSlot + part * (kN * 128) + box * box_bytes, value ? &vmap : &kmap,
+                   part * 64, (k0 + box * box_rows) % ps, w.it.h, page, full(slot));
+          ++n_ops;
+        }
+        walk_next<kN, kRows>(a, G, w, len);
+      }
+      if (!ok && lane == 0) {  // given up: the copies in flight still land before the CTA ends
+        for (uint32_t o = n_ops > (uint32_t)kStages ? n_ops - kStages : 0; o < n_ops; ++o) {
+          const long long t0 = clock64();
+          while (!bar_try(full(o % kStages), (o / kStages) & 1) && clock64() - t0 < kWaitCycles / 8) {
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == kWarpMma) {
+      // ---- the products
+      const uint32_t id_s = idesc(BF16, kN, false, a.scale < 0.0f), id_o = idesc(BF16, D, true, false);
+      uint32_t n_ops = 0, n_q = 0, n_u[2] = {0, 0};
+      bool ok = true;
+      const auto leader_wait = [&](uint32_t bar, uint32_t parity) {
+        bool r = true;
+        if (lane == 0) r = wait(bar, parity);
+        ok = ok && __shfl_sync(kAll, (int)r, 0);
+        return ok;
+      };
+      for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0 && ok;) {
+        const int len = walk_len(w);
+        const int m = w.it.tiles ? len : 0;
+        const bool two = kGroups == 2 && w.it.rows > 128;
+        const int U = two ? 2 * m : m;
+        if (m > 0 && leader_wait(q_full, n_q & 1)) {
+          ++n_q;
+          fence_after();
+          int k_slot = 0, v_slot = 0;
+          const auto scores = [&](int u) {  // S(u) = Q K^T
+            if (!two || !(u & 1)) {
+              k_slot = n_ops % kStages;
+              if (!leader_wait(full(k_slot), (n_ops / kStages) & 1)) return;
+              ++n_ops;
+            }
+            if (lane == 0) {
+              const uint32_t q = base + C::kSmemQ + (two && (u & 1) ? C::kQ : 0), k = base + C::kSmemRing + k_slot * C::kSlot;
+              const uint32_t d = tmem + C::kColS + (u & 1) * kN;
+#pragma unroll
+              for (int x = 0; x < D / 16; ++x)
+                mma_ss(d, desc_k(q + (x / 4) * 16384 + (x % 4) * 32), desc_k(k + (x / 4) * (kN * 128) + (x % 4) * 32),
+                       id_s, x > 0);
+              mma_commit(s_full(u & 1));
+              if (!two || (u & 1)) mma_commit(empty(k_slot));
+              if (u == U - 1) mma_commit(q_empty);
+            }
+            __syncwarp();
+          };
+          scores(0);
+          if (U > 1 && ok) scores(1);
+          for (int u = 0; u < U && ok; ++u) {
+            const int buf = u & 1, acc_group = kGroups == 2 ? buf : 0;
+            if (!leader_wait(p_full(buf), n_u[buf] & 1)) break;
+            ++n_u[buf];
+            const int tile = w.it.t0 + w.off + (two ? u >> 1 : u), k0 = tile * kN;
+            const int from = max(w.it.lo, k0) - k0, to = min(w.it.hi, k0 + kN) - k0;
+            const int x0 = from / 16, x1 = (to + 15) / 16;
+            if (!two || !(u & 1)) {
+              v_slot = n_ops % kStages;
+              if (!leader_wait(full(v_slot), (n_ops / kStages) & 1)) break;
+              ++n_ops;
+              if (to & 15) {
+                // values past the last visible key: whatever the page holds there, even NaN, must not reach a sum
+                for (int i = lane; i < (x1 * 16 - to) * C::kSub * 8; i += 32) {
+                  const int row = to + i / (C::kSub * 8), part = (i / 8) % C::kSub;
+                  *reinterpret_cast<uint4*>(smem + C::kSmemRing + v_slot * C::kSlot + part * (kN * 128) + row * 128 +
+                                            (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy();
+                __syncwarp();
+              }
+            }
+            fence_after();
+            if (lane == 0) {
+              const uint32_t v = base + C::kSmemRing + v_slot * C::kSlot;
+              const uint32_t d = tmem + C::kColO + acc_group * D, p = tmem + C::kColS + buf * kN;
+              const bool first = u < kGroups;  // the first product of this accumulator
+              for (int x = x0; x < x1; ++x)
+                mma_ts(d, p + x * 8, desc_mn(v + x * 2048, kN * 128), id_o, !(first && x == x0));
+              mma_commit(o_full(buf));
+              if (!two || (u & 1)) mma_commit(empty(v_slot));
+            }
+            __syncwarp();
+            if (u + 2 < U) scores(u + 2);
+          }
+        }
+        walk_next<kN, kRows>(a, G, w, len);
+      }
+      if (!ok && lane == 0) {  // given up: the products in flight end before tensor memory is freed
+        mma_commit(drain);
+        const long long t0 = clock64();
+        while (!bar_try(drain, 0) && clock64() - t0 < kWaitCycles / 8) {
+        }
+      }
+      __syncwarp();
+    } else {
+      // ---- query rows, gathered by 16-byte copies into the swizzled tiles
+      const int t = tid - kWarpQ * 32;
+      uint32_t n_q = 0;
+      bool ok = true;
+      for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0 && ok;) {
+        const int len = walk_len(w);
+        if (w.it.tiles) {
+          if (n_q > 0) ok = wait(q_empty, (n_q - 1) & 1);
+          if (!ok) break;
+          ++n_q;
+          constexpr int kChunks = D / 8;
+          const uint16_t* q = static_cast<const uint16_t*>(a.q);
+          for (int x = t; x < w.it.rows * kChunks; x += 64) {
+            const int row = x / kChunks, ch = x % kChunks, R = w.it.r0 + row, tok = R / G, g = R - tok * G;
+            const int r = row & 127;
+            cp_async16(base + C::kSmemQ + (row >> 7) * C::kQ + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                       q + (int64_t)(w.it.s.q0 + tok) * a.q_stride + (int64_t)(w.it.h * G + g) * a.q_head_stride + ch * 8);
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy();
+          bar_arrive(q_full);
+        }
+        walk_next<kN, kRows>(a, G, w, len);
+      }
+    }
+  } else {
+    if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---- softmax: thread = row
+    const int grp = warp >> 2, r = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+    const uint32_t o_addr = lanes + C::kColO + grp * D;
+    uint32_t n_u[2] = {0, 0}, n_p[2] = {0, 0};  // score tiles taken, weights handed over, per buffer
+    float* const part0 = reinterpret_cast<float*>(a.ws + kWsHead);
+    constexpr size_t kPartFloats = (size_t)kRows * (D + 2);
+    int* const counters = reinterpret_cast<int*>(a.ws + 16);
+    long long g_seg = st.first;  // unit at which the segment starts
+    for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0;) {
+      const int len = walk_len(w);
+      const int m = w.it.tiles ? len : 0;
+      const bool two = kGroups == 2 && w.it.rows > 128;
+      const int U = two ? 2 * m : m;
+      const int row = (two ? grp * 128 : 0) + r;  // row of the item
+      const bool valid = row < w.it.rows;
+      const bool busy = (row & ~31) < w.it.rows;  // some row of the warp exists
+      const int R = w.it.r0 + row, tok = valid ? R / G : 0, g = valid ? R - tok * G : 0;
+      const int pos = w.it.s.kv - w.it.s.n + tok;
+      const int hi = pos + 1, lo = a.window > 0 ? max(0, hi - a.window) : 0;
+      float ref = -INFINITY, sum = 0.0f;  // reference (raw score units) and sum of the row
+      bool acc = false;                   // the accumulator holds something
+
+      for (int u = kGroups == 2 ? grp : 0; u < U; u += kGroups) {
+        const int buf = u & 1;
+        warp_wait(wait, s_full(buf), n_u[buf] & 1);
+        ++n_u[buf];
+        fence_after();
+        if (u == 0 && (two || kGroups == 1) && tid == 0) bar_arrive(q_empty);
+        if (busy) {
+          const uint32_t s_addr = lanes + C::kColS + buf * kN;
+          uint32_t s[kN];
+#pragma unroll
+          for (int x = 0; x < kN / 32; ++x) tmem_ld32(s_addr + 32 * x, s + 32 * x);
+          wait_ld();
+          const int k0 = (w.it.t0 + w.off + (two ? u >> 1 : u)) * kN;
+          if (__any_sync(kAll, valid && (hi < k0 + kN || lo > k0))) {
+            const int j1 = hi - k0, j0 = lo - k0;
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              if (j >= j1 || j < j0) s[j] = 0xff800000u;
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < kN; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          float f = 1.0f;
+          const bool grow = ref == -INFINITY ? top > -INFINITY : (top - ref) * c2 > kGrow;
+          if (grow) {
+            f = ref == -INFINITY ? 0.0f : ex2((ref - top) * c2);
+            ref = top;
+            sum *= f;
+          }
+          if (acc && __any_sync(kAll, grow && valid)) {
+            const int pb = kGroups == 2 ? buf : buf ^ 1;  // the buffer of the group's previous tile
+            warp_wait(wait, o_full(pb), (n_p[pb] - 1) & 1);
+            fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + 32 * x, o);
+              wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(o_addr + 32 * x, o);
+            }
+          }
+          const float shift = ref == -INFINITY ? 0.0f : -ref * c2;
+          const uint64_t cc = f2(c2, c2), sh = f2(shift, shift);
+          uint64_t acc2[2] = {0, 0};
+#pragma unroll
+          for (int j = 0; j < kN; j += 2) {
+            const uint64_t t = f2_fma((uint64_t)s[j] | (uint64_t)s[j + 1] << 32, cc, sh);
+            const float p0 = ex2(f2_lo(t)), p1 = ex2(f2_hi(t));
+            acc2[(j >> 1) & 1] = f2_add(acc2[(j >> 1) & 1], f2(p0, p1));
+            s[j >> 1] = pack16<BF16>(p0, p1);
+          }
+          const uint64_t both = f2_add(acc2[0], acc2[1]);
+          sum += f2_lo(both) + f2_hi(both);
+#pragma unroll
+          for (int x = 0; x < kN / 64; ++x) tmem_st32(s_addr + 32 * x, s + 32 * x);
+          wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(p_full(buf));
+        acc = true;
+        ++n_p[buf];
+      }
+
+      // ---- the segment's result
+      const bool whole = w.off == 0 && len == w.it.cost();
+      const bool join = kGroups == 2 && !two && U > 1;  // two groups hold sums of the same rows
+      if (acc) {
+        const int lb = kGroups == 2 ? grp : (U - 1) & 1;
+        warp_wait(wait, o_full(lb), (n_p[lb] - 1) & 1);
+        fence_after();
+      }
+      float m2 = ref == -INFINITY ? -INFINITY : ref * c2;  // log2 units from here on
+      float f_own = 1.0f, f_other = 0.0f;
+      float* xch = reinterpret_cast<float*>(smem + C::kSmemQ + C::kQ);  // the second row tile of q: free in such items
+      const bool writes = two || grp == 0;                              // this group puts out the rows
+      // partial sums: slot 0 if the CTA's first unit is in this item, else 1
+      const long long g_item = g_seg - w.off;
+      const int slot = g_seg == st.first ? 0 : 1;
+      float* part = part0 + ((size_t)blockIdx.x * 2 + slot) * kPartFloats;
+      if (join) {
+        if (grp == 1) {
+          xch[r] = m2;
+          xch[128 + r] = sum;
+        }
+        named_sync(1, 256);
+        if (grp == 0) {
+          const float om = xch[r], os = xch[128 + r];
+          const float M = fmaxf(m2, om);
+          f_own = m2 == -INFINITY ? 0.0f : ex2(m2 - M);
+          f_other = om == -INFINITY ? 0.0f : ex2(om - M);
+          sum = sum * f_own + os * f_other;
+          m2 = M;
+        }
+        named_sync(1, 256);
+      }
+      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      constexpr int kX = D / 2;  // columns that the exchange buffer (kQ bytes) holds for 128 rows
+#pragma unroll 1
+      for (int x0 = 0; x0 < D; x0 += 32) {
+        uint32_t o[32];
+        if (busy && acc) {
+          tmem_ld32(o_addr + x0, o);
+          wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = 0u;
+        }
+        if (join) {
+          float* x = xch + (x0 % kX) * 128 + r;
+          if (x0 % kX == 0 && x0 > 0) named_sync(1, 256);  // the columns before have been read
+          if (grp == 1) {
+            if (busy) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j * 128] = __uint_as_float(o[j]);
+            }
+            if (x0 % kX == kX - 32) named_sync(1, 256);  // the other group's columns are there
+          } else {
+            if (x0 % kX == 0) named_sync(1, 256);
+            if (valid) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * f_own + x[j * 128] * f_other);
+            }
+          }
+        }
+        if (writes && valid) {
+          if (whole) {
+            uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tok) * a.o_stride +
+                            (int64_t)(w.it.h * G + g) * a.o_head_stride + x0;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              const auto at = [&](int i) { return __uint_as_float(o[j + i]) * inv; };
+              *reinterpret_cast<uint4*>(out + j) =
+                  make_uint4(pack16<BF16>(at(0), at(1)), pack16<BF16>(at(2), at(3)), pack16<BF16>(at(4), at(5)),
+                             pack16<BF16>(at(6), at(7)));
+            }
+          } else {
+            uint32_t* dst = reinterpret_cast<uint32_t*>(part) + 2 * kRows + (size_t)row * D + x0;
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<uint4*>(dst + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+          }
+        }
+        __syncwarp();
+      }
+      fence_before();
+      if (join) {
+        named_sync(1, 256);  // the exchange buffer has been read
+        if (tid == 0) bar_arrive(q_empty);
+      } else if (kGroups == 2 && !two && U == 1 && tid == 0) {
+        bar_arrive(q_empty);
+      }
+      if (writes && whole && valid && a.lse)
+        a.lse[(int64_t)(w.it.s.q0 + tok) * a.Hq + w.it.h * G + g] =
+            sum > 0.0f ? (m2 + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+      if (writes && !whole) {
+        if (valid) {
+          part[row] = m2;
+          part[kRows + row] = sum;
+        }
+        // the last of the item's CTAs to arrive joins the parts, in the order of the CTAs
+        const int c0 = owner(st.total, st.ctas, g_item), c1 = owner(st.total, st.ctas, g_item + w.it.cost() - 1);
+        const int slot0 = share(st.total, st.ctas, c0) == g_item ? 0 : 1;
+        int* cnt = counters + c0 * 2 + grp;
+        __threadfence();
+        named_sync(2 + grp, 128);
+        if (r == 0) {
+          const int before = atomicAdd(cnt, 1);
+          st.last[grp] = before == c1 - c0;
+          if (before == c1 - c0) *cnt = 0;
+        }
+        named_sync(2 + grp, 128);
+        if (st.last[grp]) {
+          __threadfence();
+          const int np = c1 - c0 + 1;
+          const int rows = min(128, w.it.rows - (two ? grp * 128 : 0));
+          const int row_base = two ? grp * 128 : 0;
+          const auto part_of = [&](int p) {
+            return part0 + ((size_t)(c0 + p) * 2 + (p == 0 ? slot0 : 0)) * kPartFloats;
+          };
+          for (int rr = warp & 3; rr < rows; rr += 4) {
+            const int pr = row_base + rr;
+            float M = -INFINITY;
+            for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(part_of(p) + pr));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+            float L = 0.0f;
+            constexpr int kV = D / 32;  // columns per lane
+            float v[kV] = {};
+            for (int p0 = 0; p0 < np; p0 += 32) {
+              const int p = p0 + lane;
+              float wgt = 0.0f, lp = 0.0f;
+              if (p < np) {
+                const float mp = __ldcg(part_of(p) + pr);
+                wgt = mp == -INFINITY ? 0.0f : ex2(mp - M);
+                lp = wgt * __ldcg(part_of(p) + kRows + pr);
+              }
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) lp += __shfl_xor_sync(kAll, lp, o);
+              L += lp;
+              const int cnt_p = min(32, np - p0);
+#pragma unroll 4
+              for (int x = 0; x < cnt_p; ++x) {
+                const float f = __shfl_sync(kAll, wgt, x);
+                const float* src = part_of(p0 + x) + 2 * kRows + (size_t)pr * D + lane * kV;
+                float e[kV];
+                if constexpr (kV == 2) {
+                  const float2 t2 = __ldcg(reinterpret_cast<const float2*>(src));
+                  e[0] = t2.x, e[1] = t2.y;
+                } else {
+#pragma unroll
+                  for (int j = 0; j < kV; j += 4) {
+                    const float4 t4 = __ldcg(reinterpret_cast<const float4*>(src + j));
+                    e[j] = t4.x, e[j + 1] = t4.y, e[j + 2] = t4.z, e[j + 3] = t4.w;
+                  }
+                }
+                // a part without keys for this row has weight 0 and an accumulator of zeros
+#pragma unroll
+                for (int j = 0; j < kV; ++j) v[j] = fmaf(f, e[j], v[j]);
+              }
+            }
+            const int Rr = w.it.r0 + pr, tk = Rr / G, gg = Rr - tk * G;
+            const float il = L > 0.0f ? 1.0f / L : 0.0f;
+            uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tk) * a.o_stride +
+                            (int64_t)(w.it.h * G + gg) * a.o_head_stride + lane * kV;
+            uint32_t pk[kV / 2];
+#pragma unroll
+            for (int j = 0; j < kV; j += 2) pk[j / 2] = pack16<BF16>(v[j] * il, v[j + 1] * il);
+            if constexpr (kV == 2) *reinterpret_cast<uint32_t*>(out) = pk[0];
+            else if constexpr (kV == 4) *reinterpret_cast<uint2*>(out) = make_uint2(pk[0], pk[1]);
+            else *reinterpret_cast<uint4*>(out) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            if (a.lse && lane == 0)
+              a.lse[(int64_t)(w.it.s.q0 + tk) * a.Hq + w.it.h * G + gg] =
+                  L > 0.0f ? (M + log2f(L)) * 0.693147180559945309f : -INFINITY;
+          }
+        }
+      }
+      g_seg += len;
+      walk_next<kN, kRows>(a, G, w, len);
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// ---------------------------------------------------------------- host side
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// a cache as [page][head][row][D]: boxes of 64 columns x `rows` rows of one head of one page
+bool make_cache_map(CUtensorMap* map, const moe_kv_desc& kv, const void* cache, int64_t row, int64_t head, int64_t page,
+                    int rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const auto bytes = [&](int64_t stride) { return (cuuint64_t)(stride ? stride * 2 : kv.D * 2); };  // 0: one entry
+  const cuuint64_t dims[4] = {(cuuint64_t)kv.D, (cuuint64_t)kv.page_size, (cuuint64_t)kv.Hkv, (cuuint64_t)kv.num_pages};
+  const cuuint64_t strides[3] = {bytes(row), bytes(head), bytes(page)};
+  const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(map, kv.dtype == MOE_DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+            const_cast<void*>(cache), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF16>
+cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
+  using C = Cfg<D>;
+  auto kern = attn_kernel<D, BF16>;
+  static bool opted = false;
+  if (!opted) {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (err != cudaSuccess) return err;
+    opted = true;
+  }
+  CUtensorMap km, vm;
+  const int rows = std::min(a.kv.page_size, (int)C::kN);
+  if (!make_cache_map(&km, a.kv, a.k_cache, a.kv.k_row_stride, a.kv.k_head_stride, a.kv.k_page_stride, rows) ||
+      !make_cache_map(&vm, a.kv, a.v_cache, a.kv.v_row_stride, a.kv.v_head_stride, a.kv.v_page_stride, rows))
+    return cudaErrorInvalidValue;
+  const int grid = std::min(num_sms(), kMaxCtas);
+  note_launch();
+  kern<<<grid, C::kThreads, C::kSmem, s>>>(a, km, vm);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_tensor_core(const moe_kv_desc& kv) {
+  const bool one_stride = (kv.k_row_stride || kv.page_size == 1) && (kv.v_row_stride || kv.page_size == 1) &&
+                          (kv.k_head_stride || kv.Hkv == 1) && (kv.v_head_stride || kv.Hkv == 1) &&
+                          (kv.k_page_stride || kv.num_pages == 1) && (kv.v_page_stride || kv.num_pages == 1);
+  return (kv.D == 64 || kv.D == 128 || kv.D == 256) && kv.page_size >= 16 && !(kv.page_size & (kv.page_size - 1)) &&
+         one_stride;
+}
+
+size_t attn_workspace(int, int, int D) {
+  if (D != 64 && D != 128 && D != 256) return 256;
+  return kWsHead + (size_t)kMaxCtas * 2 * (D == 256 ? 128 : 256) * (D + 2) * 4;
+}
+
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  const bool bf16 = a.kv.dtype == MOE_DT_BF16;
+  switch (a.kv.D) {
+    case 64: return bf16 ? launch_t<64, true>(a, s) : launch_t<64, false>(a, s);
+    case 128: return bf16 ? launch_t<128, true>(a, s) : launch_t<128, false>(a, s);
+    default: return bf16 ? launch_t<256, true>(a, s) : launch_t<256, false>(a, s);
+  }
+}
+
+}  // namespace moe

@@ -104,8 +104,6 @@ __global__ void __launch_bounds__(32 * kWarps) attn_general_kernel(const AttnArg
 
 }  // namespace
 
-size_t attn_workspace(int, int, int) { return 256; }
-
 cudaError_t launch_attn_general(const AttnArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
   const dim3 grid((unsigned)(a.T < 65536 ? a.T : 65536), (unsigned)a.Hq);

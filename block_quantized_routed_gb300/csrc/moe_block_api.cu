@@ -213,7 +213,8 @@ int moe_paged_attention(const moe_kv_desc* kv, const void* q, int64_t q_stride, 
   a.lse = lse;
   a.ws = static_cast<char*>(ws);
   a.status = static_cast<int*>(ws);
-  return done(launch_attn_general(a, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return done(attn_tensor_core(a.kv) ? launch_attn(a, s) : launch_attn_general(a, s));
 }
 
 }  // extern "C"
