@@ -14,8 +14,8 @@
 // Work split.  All items of a call, laid end to end in tiles, are divided
 // evenly over the CTAs (one per SM): every CTA gets the same number of key
 // tiles whatever the lengths.  An item cut by a CTA boundary leaves partial
-// sums in the workspace; the CTA that arrives last joins them in a fixed
-// order, so results do not depend on timing.  The division is found by each
+// sums in the workspace; when all of them are there, its CTAs join a slice of
+// its rows each, in a fixed order, so results do not depend on timing.  The division is found by each
 // CTA from cu_q and kv_len in a short prologue: no planning launch, no host
 // knowledge of the lengths.
 //
@@ -76,6 +76,7 @@ struct Cfg {
   static constexpr int kSmemRing = kGroups * kQ;
   static constexpr int kSmemMisc = kSmemRing + kStages * kSlot;
   static constexpr int kSmem = kSmemMisc + 1024 + 1024;  // barriers and the prologue's results; alignment slack
+  static constexpr size_t kPartFloats = (size_t)kRows * (D + 2);  // m, sum and accumulator of an item's rows
   static constexpr uint32_t kColO = 0, kColS = 256;      // tensor memory columns: O per group, two score buffers
 };
 static_assert(Cfg<128>::kSmem <= 232448 && Cfg<64>::kSmem <= 232448 && Cfg<256>::kSmem <= 232448, "shared memory");
@@ -237,6 +238,13 @@ struct Walk {
   long long left;
 };
 
+// An item whose units several CTAs share (this CTA holds at most two of them).
+struct Cut {
+  int c0, parts, slot0;  // first CTA, number of CTAs, the first one's slot (the others use slot 0)
+  int arrivals;          // of the counter once every part is written
+  int rows, r0, q0, h;
+};
+
 // what the prologue leaves in shared memory for every role
 struct Start {
   int b, h, i, off;
@@ -244,7 +252,8 @@ struct Start {
   int ctas;
   volatile int abort;
   uint32_t tmem;
-  int last[2];  // combine: this group arrived last
+  int n_cut;
+  Cut cut[2];
 };
 
 template <int kN, int kRows>
@@ -335,6 +344,144 @@ __device__ __forceinline__ void warp_wait(const Wait& w, uint32_t bar, uint32_t 
   __syncwarp();
 }
 
+// Joins one item's parts.  Every one of its CTAs takes a slice of the rows,
+// once all parts have arrived; the softmax threads of the CTA take part.
+//   M = max_p m_p,  L = sum_p 2^(m_p - M) l_p,  out = sum_p 2^(m_p - M) o_p / L
+// in the order of the parts.  (One CTA joining all rows of an item took up to
+// 250 us for 128 rows in 30 parts; in slices it is bound by the L2 reads.)
+template <int D, bool BF16>
+__device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, const Cut& cut, const float* part0,
+                                           int* counters, uint8_t* smem, const Wait& wait) {
+  using C = Cfg<D>;
+  constexpr int kThreads = 128 * C::kGroups, kVecs = D / 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int np = cut.parts;
+  int* arrived = counters + cut.c0 * 2;
+  if (tid == 0) {
+    const long long t0 = clock64();
+    while (*(volatile int*)arrived < cut.arrivals && !st.abort) {
+      if (clock64() - t0 > kWaitCycles) {
+        st.abort = 1;
+        set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+      }
+    }
+    __threadfence();
+  }
+  named_sync(4, kThreads);
+  const int per = (cut.rows + np - 1) / np, lo = ((int)blockIdx.x - cut.c0) * per;
+  const int nr = min(per, cut.rows - lo);
+  const auto part = [&](int p) { return part0 + ((size_t)(cut.c0 + p) * 2 + (p == 0 ? cut.slot0 : 0)) * C::kPartFloats; };
+  float* wgt = reinterpret_cast<float*>(smem);               // [np][per] weights over L: at most rows + np of them
+  float4* red = reinterpret_cast<float4*>(smem + 4096);      // [thread] partial sums
+  const auto finish = [&](int row, float M, float L) {
+    if (a.lse) {
+      const int R = cut.r0 + lo + row, tok = R / G;
+      a.lse[(int64_t)(cut.q0 + tok) * a.Hq + cut.h * G + (R - tok * G)] =
+          L > 0.0f ? (M + log2f(L)) * 0.693147180559945309f : -INFINITY;
+    }
+  };
+  if (np <= 8) {  // many rows each: a thread per row, its loads together
+    for (int row = tid; row < nr; row += kThreads) {
+      float m[8], l[8], M = -INFINITY, L = 0.0f;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        m[p] = p < np ? __ldcg(part(p) + lo + row) : -INFINITY;
+        l[p] = p < np ? __ldcg(part(p) + C::kRows + lo + row) : 0.0f;
+        M = fmaxf(M, m[p]);
+      }
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        m[p] = m[p] == -INFINITY ? 0.0f : ex2(m[p] - M);
+        L += m[p] * l[p];
+      }
+      const float il = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p < np) wgt[p * per + row] = m[p] * il;
+      finish(row, M, L);
+    }
+  } else {  // few rows each: a warp per row, a lane per part
+    constexpr int kPer = (kMaxCtas + 31) / 32;
+    for (int row = warp; row < nr; row += kThreads / 32) {
+      float m[kPer], M = -INFINITY, L = 0.0f;
+      float l[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int p = i * 32 + lane;
+        m[i] = p < np ? __ldcg(part(p) + lo + row) : -INFINITY;
+        l[i] = p < np ? __ldcg(part(p) + C::kRows + lo + row) : 0.0f;
+        M = fmaxf(M, m[i]);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        m[i] = m[i] == -INFINITY ? 0.0f : ex2(m[i] - M);
+        L += m[i] * l[i];
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kAll, L, o);
+      const float il = L > 0.0f ? 1.0f / L : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int p = i * 32 + lane;
+        if (p < np) wgt[p * per + row] = m[i] * il;
+      }
+      if (lane == 0) finish(row, M, L);
+    }
+  }
+  named_sync(4, kThreads);
+  if (nr > 0) {  // uniform over the CTA
+    const int n = nr * kVecs;  // vectors of 4 columns
+    int teams = 1;             // teams of threads share the parts where there are few vectors
+    while (teams * 2 * n <= kThreads && teams * 2 <= np) teams *= 2;
+    const int width = kThreads / teams, team = tid / width;
+    for (int e = tid % width; e < n; e += width) {
+      const int row = e / kVecs, c = (e % kVecs) * 4;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+      for (int p = team; p < np; p += teams) {
+        const float f = wgt[p * per + row];
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(p) + 2 * C::kRows + (size_t)(lo + row) * D + c));
+        acc.x = fmaf(f, v.x, acc.x);
+        acc.y = fmaf(f, v.y, acc.y);
+        acc.z = fmaf(f, v.z, acc.z);
+        acc.w = fmaf(f, v.w, acc.w);
+      }
+      if (teams > 1) {  // one vector per thread
+        red[tid] = acc;
+      } else {
+        const int R = cut.r0 + lo + row, tok = R / G;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(cut.q0 + tok) * a.o_stride +
+                                  (int64_t)(cut.h * G + R - tok * G) * a.o_head_stride + c) =
+            make_uint2(pack16<BF16>(acc.x, acc.y), pack16<BF16>(acc.z, acc.w));
+      }
+    }
+    if (teams > 1) {
+      named_sync(4, kThreads);
+      if (tid < n) {
+        float4 acc = red[tid];
+        for (int t = 1; t < teams; ++t) {
+          const float4 v = red[t * width + tid];
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+        const int row = tid / kVecs, c = (tid % kVecs) * 4, R = cut.r0 + lo + row, tok = R / G;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(cut.q0 + tok) * a.o_stride +
+                                  (int64_t)(cut.h * G + R - tok * G) * a.o_head_stride + c) =
+            make_uint2(pack16<BF16>(acc.x, acc.y), pack16<BF16>(acc.z, acc.w));
+      }
+    }
+  }
+  named_sync(4, kThreads);  // every read of the parts and of shared memory is done
+  if (tid == 0) {
+    __threadfence();
+    if (atomicAdd(arrived + 1, 1) == np - 1) {  // the last of the item's CTAs leaves the counters as they were
+      arrived[0] = 0;
+      arrived[1] = 0;
+    }
+  }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -386,6 +533,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     st.abort = 0;
+    st.n_cut = 0;
   }
   __syncthreads();
   if (warp == 0) {
@@ -624,15 +772,21 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           if (n_q > 0) ok = wait(q_empty, (n_q - 1) & 1);
           if (!ok) break;
           ++n_q;
-          constexpr int kChunks = D / 8;
-          const uint16_t* q = static_cast<const uint16_t*>(a.q);
-          for (int x = t; x < w.it.rows * kChunks; x += 64) {
-            const int row = x / kChunks, ch = x % kChunks, R = w.it.r0 + row, tok = R / G, g = R - tok * G;
-            const int r = row & 127;
-            cp_async16(base + C::kSmemQ + (row >> 7) * C::kQ + (ch >> 3) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
-                       q + (int64_t)(w.it.s.q0 + tok) * a.q_stride + (int64_t)(w.it.h * G + g) * a.q_head_stride + ch * 8);
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
+          // a thread keeps its 16-byte column and steps down the rows: no division per copy
+        constexpr int kChunks = D / 8, kStep = 64 / kChunks;
+        const int ch = t % kChunks;
+        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)w.it.s.q0 * a.q_stride +
+                            (int64_t)w.it.h * G * a.q_head_stride + ch * 8;
+        const uint32_t dst = base + C::kSmemQ + (ch >> 3) * 16384;
+        int row = t / kChunks;
+        int tok = (w.it.r0 + row) / G, g = w.it.r0 + row - tok * G;
+#pragma unroll 4
+        for (; row < w.it.rows; row += kStep) {
+          cp_async16(dst + (row >> 7) * C::kQ + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
+                     q + tok * a.q_stride + g * a.q_head_stride);
+          for (g += kStep; g >= G; g -= G) ++tok;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy();
           bar_arrive(q_full);
         }
@@ -647,7 +801,8 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     const uint32_t o_addr = lanes + C::kColO + grp * D;
     uint32_t n_u[2] = {0, 0}, n_p[2] = {0, 0};  // score tiles taken, weights handed over, per buffer
     float* const part0 = reinterpret_cast<float*>(a.ws + kWsHead);
-    constexpr size_t kPartFloats = (size_t)kRows * (D + 2);
+    constexpr size_t kPartFloats = C::kPartFloats;
+    constexpr int kJoin = 128 * kGroups;
     int* const counters = reinterpret_cast<int*>(a.ws + 16);
     long long g_seg = st.first;  // unit at which the segment starts
     for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0;) {
@@ -823,91 +978,35 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       if (writes && whole && valid && a.lse)
         a.lse[(int64_t)(w.it.s.q0 + tok) * a.Hq + w.it.h * G + g] =
             sum > 0.0f ? (m2 + log2f(sum)) * 0.693147180559945309f : -INFINITY;
-      if (writes && !whole) {
-        if (valid) {
+      if (!whole) {
+        // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
+        const int c0 = owner(st.total, st.ctas, g_item), c1 = owner(st.total, st.ctas, g_item + w.it.cost() - 1);
+        if (writes && valid) {
           part[row] = m2;
           part[kRows + row] = sum;
         }
-        // the last of the item's CTAs to arrive joins the parts, in the order of the CTAs
-        const int c0 = owner(st.total, st.ctas, g_item), c1 = owner(st.total, st.ctas, g_item + w.it.cost() - 1);
-        const int slot0 = share(st.total, st.ctas, c0) == g_item ? 0 : 1;
-        int* cnt = counters + c0 * 2 + grp;
-        __threadfence();
-        named_sync(2 + grp, 128);
-        if (r == 0) {
-          const int before = atomicAdd(cnt, 1);
-          st.last[grp] = before == c1 - c0;
-          if (before == c1 - c0) *cnt = 0;
+        if (tid == 0) {
+          Cut& cut = st.cut[st.n_cut++];
+          cut.c0 = c0;
+          cut.parts = c1 - c0 + 1;
+          cut.slot0 = share(st.total, st.ctas, c0) == g_item ? 0 : 1;
+          cut.arrivals = cut.parts * (two ? 2 : 1);
+          cut.rows = w.it.rows;
+          cut.r0 = w.it.r0;
+          cut.q0 = w.it.s.q0;
+          cut.h = w.it.h;
         }
-        named_sync(2 + grp, 128);
-        if (st.last[grp]) {
+        if (writes) {
           __threadfence();
-          const int np = c1 - c0 + 1;
-          const int rows = min(128, w.it.rows - (two ? grp * 128 : 0));
-          const int row_base = two ? grp * 128 : 0;
-          const auto part_of = [&](int p) {
-            return part0 + ((size_t)(c0 + p) * 2 + (p == 0 ? slot0 : 0)) * kPartFloats;
-          };
-          for (int rr = warp & 3; rr < rows; rr += 4) {
-            const int pr = row_base + rr;
-            float M = -INFINITY;
-            for (int p = lane; p < np; p += 32) M = fmaxf(M, __ldcg(part_of(p) + pr));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-            float L = 0.0f;
-            constexpr int kV = D / 32;  // columns per lane
-            float v[kV] = {};
-            for (int p0 = 0; p0 < np; p0 += 32) {
-              const int p = p0 + lane;
-              float wgt = 0.0f, lp = 0.0f;
-              if (p < np) {
-                const float mp = __ldcg(part_of(p) + pr);
-                wgt = mp == -INFINITY ? 0.0f : ex2(mp - M);
-                lp = wgt * __ldcg(part_of(p) + kRows + pr);
-              }
-#pragma unroll
-              for (int o = 16; o > 0; o >>= 1) lp += __shfl_xor_sync(kAll, lp, o);
-              L += lp;
-              const int cnt_p = min(32, np - p0);
-#pragma unroll 4
-              for (int x = 0; x < cnt_p; ++x) {
-                const float f = __shfl_sync(kAll, wgt, x);
-                const float* src = part_of(p0 + x) + 2 * kRows + (size_t)pr * D + lane * kV;
-                float e[kV];
-                if constexpr (kV == 2) {
-                  const float2 t2 = __ldcg(reinterpret_cast<const float2*>(src));
-                  e[0] = t2.x, e[1] = t2.y;
-                } else {
-#pragma unroll
-                  for (int j = 0; j < kV; j += 4) {
-                    const float4 t4 = __ldcg(reinterpret_cast<const float4*>(src + j));
-                    e[j] = t4.x, e[j + 1] = t4.y, e[j + 2] = t4.z, e[j + 3] = t4.w;
-                  }
-                }
-                // a part without keys for this row has weight 0 and an accumulator of zeros
-#pragma unroll
-                for (int j = 0; j < kV; ++j) v[j] = fmaf(f, e[j], v[j]);
-              }
-            }
-            const int Rr = w.it.r0 + pr, tk = Rr / G, gg = Rr - tk * G;
-            const float il = L > 0.0f ? 1.0f / L : 0.0f;
-            uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tk) * a.o_stride +
-                            (int64_t)(w.it.h * G + gg) * a.o_head_stride + lane * kV;
-            uint32_t pk[kV / 2];
-#pragma unroll
-            for (int j = 0; j < kV; j += 2) pk[j / 2] = pack16<BF16>(v[j] * il, v[j + 1] * il);
-            if constexpr (kV == 2) *reinterpret_cast<uint32_t*>(out) = pk[0];
-            else if constexpr (kV == 4) *reinterpret_cast<uint2*>(out) = make_uint2(pk[0], pk[1]);
-            else *reinterpret_cast<uint4*>(out) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            if (a.lse && lane == 0)
-              a.lse[(int64_t)(w.it.s.q0 + tk) * a.Hq + w.it.h * G + gg] =
-                  L > 0.0f ? (M + log2f(L)) * 0.693147180559945309f : -INFINITY;
-          }
+          named_sync(2 + grp, 128);
+          if (r == 0) atomicAdd(counters + c0 * 2, 1);
         }
       }
       g_seg += len;
       walk_next<kN, kRows>(a, G, w, len);
     }
+    named_sync(4, kJoin);
+    for (int x = 0; x < st.n_cut; ++x) join_parts<D, BF16>(a, G, st, st.cut[x], part0, counters, smem + C::kSmemRing, wait);
   }
   fence_before();
   __syncthreads();
@@ -964,8 +1063,18 @@ cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const int grid = std::min(num_sms(), kMaxCtas);
   note_launch();
-  kern<<<grid, C::kThreads, C::kSmem, s>>>(a, km, vm);
-  return cudaGetLastError();
+  // cooperative: CTAs that share an item wait for one another's parts, so all of them have to be resident
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, km, vm);
 }
 
 }  // namespace
