@@ -56,9 +56,9 @@ namespace {
 constexpr unsigned kAll = 0xffffffffu;
 constexpr long long kWaitCycles = 2000000000ll;  // ~1 s at 2 GHz
 constexpr int kMaxCtas = 160;                    // the workspace holds the partial sums of this many
-constexpr int kCounters = kMaxCtas * 2;
-constexpr size_t kWsHead = 16 + (size_t)kCounters * 4 + 240;  // status, counters; a multiple of 256
-static_assert(kWsHead % 256 == 0, "partials start aligned");
+constexpr size_t kWsHead = 1024;                 // status (16 bytes), a counter per CTA
+static_assert(kWsHead >= 16 + 4 * kMaxCtas, "counters");
+constexpr int kColMajor = 32;                    // parts of which each CTA joins at least so many rows lie column by column
 constexpr float kGrow = 8.0f;                    // log2 of the growth that forces a rescale
 
 template <int D_>
@@ -75,7 +75,8 @@ struct Cfg {
   static constexpr int kSmemQ = 0;
   static constexpr int kSmemRing = kGroups * kQ;
   static constexpr int kSmemMisc = kSmemRing + kStages * kSlot;
-  static constexpr int kSmem = kSmemMisc + 1024 + 1024;  // barriers and the prologue's results; alignment slack
+  static constexpr int kSmemXch = kSmemMisc + 1024;       // after barriers and the prologue's results
+  static constexpr int kSmem = kSmemXch + 2 * 128 * 8;   // per group and row: maximum and sum, for joining the groups
   static constexpr size_t kPartFloats = (size_t)kRows * (D + 2);  // m, sum and accumulator of an item's rows
   static constexpr uint32_t kColO = 0, kColS = 256;      // tensor memory columns: O per group, two score buffers
 };
@@ -115,19 +116,24 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// one K step of 16: A and B from shared memory / A from tensor memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((int)acc)
-      : "memory");
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((int)acc));
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((int)acc)
-      : "memory");
+      "{\n .reg .pred p;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(hi), "r"(idesc), "r"((int)acc));
+}
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -175,6 +181,11 @@ __device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
 __device__ __forceinline__ float ex2(float x) {  // 2^x, within 2 ulp; 2^-inf = 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -189,17 +200,15 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
-// Shared-memory matrix descriptors, 128-byte swizzle.  K-major: 8-row groups
-// 1024 bytes apart, K advances by 32 bytes per step of 16 inside the 128.
-__device__ __forceinline__ uint64_t desc_k(uint32_t addr) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-         (uint64_t)2 << 61;
-}
-// MN-major: 64 columns (128 bytes) of one K row per line, 8-row groups 1024
-// bytes apart along K, the next 64 columns `next` bytes further.
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t next) {
-  return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(next >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// Shared-memory matrix descriptors, 128-byte swizzle; only the start address
+// (bits 0-13, in 16 bytes) varies, so a step is an addition to the low word.
+// K-major: 8-row groups 1024 bytes apart, K advances by 32 bytes per step of
+// 16 inside the 128.  MN-major: 64 columns (128 bytes) of one K row per line,
+// 8-row groups 1024 bytes apart along K, the next 64 columns `next` bytes on.
+constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3FFFF) >> 4) | 1u << 16; }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t addr, uint32_t next) {
+  return ((addr & 0x3FFFF) >> 4) | (next >> 4) << 16;
 }
 // kind::f16, fp32 accumulation, M = 128
 __host__ __device__ constexpr uint32_t idesc(bool bf16, int N, bool b_mn, bool neg_a) {
@@ -241,7 +250,6 @@ struct Walk {
 // An item whose units several CTAs share (this CTA holds at most two of them).
 struct Cut {
   int c0, parts, slot0;  // first CTA, number of CTAs, the first one's slot (the others use slot 0)
-  int arrivals;          // of the counter once every part is written
   int rows, r0, q0, h;
 };
 
@@ -252,7 +260,7 @@ struct Start {
   int ctas;
   volatile int abort;
   uint32_t tmem;
-  int n_cut;
+  int n_cut, arrived;
   Cut cut[2];
 };
 
@@ -344,6 +352,22 @@ __device__ __forceinline__ void warp_wait(const Wait& w, uint32_t bar, uint32_t 
   __syncwarp();
 }
 
+__device__ __forceinline__ void fma4(float4& acc, float f, float4 v) {
+  acc.x = fmaf(f, v.x, acc.x);
+  acc.y = fmaf(f, v.y, acc.y);
+  acc.z = fmaf(f, v.z, acc.z);
+  acc.w = fmaf(f, v.w, acc.w);
+}
+// release / acquire at GPU scope; the CTA's other threads are ordered by the barriers around them
+__device__ __forceinline__ void count_up(unsigned* counter, int wrap) {
+  asm volatile("fence.acq_rel.gpu;\n red.relaxed.gpu.global.inc.u32 [%0], %1;" ::"l"(counter), "r"(wrap) : "memory");
+}
+__device__ __forceinline__ unsigned count_read(const unsigned* counter) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+  return v;
+}
+
 // Joins one item's parts.  Every one of its CTAs takes a slice of the rows,
 // once all parts have arrived; the softmax threads of the CTA take part.
 //   M = max_p m_p,  L = sum_p 2^(m_p - M) l_p,  out = sum_p 2^(m_p - M) o_p / L
@@ -351,23 +375,26 @@ __device__ __forceinline__ void warp_wait(const Wait& w, uint32_t bar, uint32_t 
 // 250 us for 128 rows in 30 parts; in slices it is bound by the L2 reads.)
 template <int D, bool BF16>
 __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, const Cut& cut, const float* part0,
-                                           int* counters, uint8_t* smem, const Wait& wait) {
+                                           unsigned* counters, uint8_t* smem) {
   using C = Cfg<D>;
   constexpr int kThreads = 128 * C::kGroups, kVecs = D / 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int np = cut.parts;
-  int* arrived = counters + cut.c0 * 2;
+  // One counter per item, named by its first CTA: up to np as the parts are
+  // written, up to 2 np as the CTAs have read them, where it wraps to 0.
+  unsigned* counter = counters + cut.c0;
   if (tid == 0) {
     const long long t0 = clock64();
-    while (*(volatile int*)arrived < cut.arrivals && !st.abort) {
+    while (count_read(counter) < (unsigned)np && !st.abort) {
       if (clock64() - t0 > kWaitCycles) {
         st.abort = 1;
         set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
       }
     }
-    __threadfence();
+    st.arrived = count_read(counter) >= (unsigned)np;
   }
   named_sync(4, kThreads);
+  if (!st.arrived) return;  // given up: the call is void
   const int per = (cut.rows + np - 1) / np, lo = ((int)blockIdx.x - cut.c0) * per;
   const int nr = min(per, cut.rows - lo);
   const auto part = [&](int p) { return part0 + ((size_t)(cut.c0 + p) * 2 + (p == 0 ? cut.slot0 : 0)) * C::kPartFloats; };
@@ -436,25 +463,49 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
     int teams = 1;             // teams of threads share the parts where there are few vectors
     while (teams * 2 * n <= kThreads && teams * 2 <= np) teams *= 2;
     const int width = kThreads / teams, team = tid / width;
-    for (int e = tid % width; e < n; e += width) {
-      const int row = e / kVecs, c = (e % kVecs) * 4;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool by_col = per >= kColMajor;
+    const auto put = [&](int row, int c, float4 v) {
+      const int R = cut.r0 + lo + row, tok = R / G;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(cut.q0 + tok) * a.o_stride +
+                                (int64_t)(cut.h * G + R - tok * G) * a.o_head_stride + c) =
+          make_uint2(pack16<BF16>(v.x, v.y), pack16<BF16>(v.z, v.w));
+    };
+    const auto load = [&](const float* src, int row, int c) {
+      if (!by_col) return __ldcg(reinterpret_cast<const float4*>(src + (size_t)(lo + row) * D + c));
+      const float* q = src + (size_t)c * C::kRows + lo + row;
+      return make_float4(__ldcg(q), __ldcg(q + C::kRows), __ldcg(q + 2 * C::kRows), __ldcg(q + 3 * C::kRows));
+    };
+    if (n <= width) {  // one vector per thread: several parts in flight
+      const int e = tid % width;
+      if (e < n) {
+        const int row = by_col ? e % nr : e / kVecs, c = (by_col ? e / nr : e % kVecs) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-      for (int p = team; p < np; p += teams) {
-        const float f = wgt[p * per + row];
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(part(p) + 2 * C::kRows + (size_t)(lo + row) * D + c));
-        acc.x = fmaf(f, v.x, acc.x);
-        acc.y = fmaf(f, v.y, acc.y);
-        acc.z = fmaf(f, v.z, acc.z);
-        acc.w = fmaf(f, v.w, acc.w);
+        for (int p = team; p < np; p += teams) fma4(acc, wgt[p * per + row], load(part(p) + 2 * C::kRows, row, c));
+        if (teams > 1) red[tid] = acc;
+        else put(row, c, acc);
       }
-      if (teams > 1) {  // one vector per thread
-        red[tid] = acc;
-      } else {
-        const int R = cut.r0 + lo + row, tok = R / G;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(cut.q0 + tok) * a.o_stride +
-                                  (int64_t)(cut.h * G + R - tok * G) * a.o_head_stride + c) =
-            make_uint2(pack16<BF16>(acc.x, acc.y), pack16<BF16>(acc.z, acc.w));
+    } else {  // several vectors of a thread in flight
+      constexpr int kB = 4;
+      for (int e0 = tid; e0 < n; e0 += kB * width) {
+        float4 acc[kB];
+        int row[kB], c[kB];
+#pragma unroll
+        for (int i = 0; i < kB; ++i) {
+          const int e = min(e0 + i * width, n - 1);  // the last vector again where there is none
+          acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          row[i] = by_col ? e % nr : e / kVecs;
+          c[i] = (by_col ? e / nr : e % kVecs) * 4;
+        }
+#pragma unroll 2
+        for (int p = 0; p < np; ++p) {
+          const float* src = part(p) + 2 * C::kRows;
+#pragma unroll
+          for (int i = 0; i < kB; ++i) fma4(acc[i], wgt[p * per + row[i]], load(src, row[i], c[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+          if (e0 + i * width < n) put(row[i], c[i], acc[i]);
       }
     }
     if (teams > 1) {
@@ -465,21 +516,12 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
           const float4 v = red[t * width + tid];
           acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
-        const int row = tid / kVecs, c = (tid % kVecs) * 4, R = cut.r0 + lo + row, tok = R / G;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(cut.q0 + tok) * a.o_stride +
-                                  (int64_t)(cut.h * G + R - tok * G) * a.o_head_stride + c) =
-            make_uint2(pack16<BF16>(acc.x, acc.y), pack16<BF16>(acc.z, acc.w));
+        put(by_col ? tid % nr : tid / kVecs, (by_col ? tid / nr : tid % kVecs) * 4, acc);
       }
     }
   }
   named_sync(4, kThreads);  // every read of the parts and of shared memory is done
-  if (tid == 0) {
-    __threadfence();
-    if (atomicAdd(arrived + 1, 1) == np - 1) {  // the last of the item's CTAs leaves the counters as they were
-      arrived[0] = 0;
-      arrived[1] = 0;
-    }
-  }
+  if (tid == 0) count_up(counter, np * 2 - 1);
 }
 
 template <int D, bool BF16>
@@ -487,16 +529,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
   using C = Cfg<D>;
   constexpr int kN = C::kN, kRows = C::kRows, kGroups = C::kGroups, kStages = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t base = smem_u32(smem);
+  if (base & 1023) {  // the swizzled tiles need it; no static shared memory comes before
+    if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+    return;
+  }
   const uint32_t bars = base + C::kSmemMisc;
   const auto full = [&](int s) { return bars + 8 * s; };
   const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-  const uint32_t q_full = bars + 8 * (2 * kStages), q_empty = q_full + 8, drain = q_full + 16;
-  const auto s_full = [&](int b) { return q_full + 24 + 8 * b; };
-  const auto p_full = [&](int b) { return q_full + 40 + 8 * b; };
-  const auto o_full = [&](int b) { return q_full + 56 + 8 * b; };
+  const uint32_t drain = bars + 8 * (2 * kStages);
+  const auto q_full = [&](int t) { return drain + 8 + 8 * t; };    // row tile t of q is there
+  const auto q_empty = [&](int t) { return drain + 24 + 8 * t; };  // its last product is done
+  const auto s_full = [&](int b) { return drain + 40 + 8 * b; };   // scores of buffer b
+  const auto p_full = [&](int b) { return drain + 56 + 8 * b; };   // weights of buffer b
+  const auto o_full = [&](int b) { return drain + 72 + 8 * b; };   // buffer b's product with the values
   Start& st = *reinterpret_cast<Start*>(smem + C::kSmemMisc + 512);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarpLoad = 4 * kGroups, kWarpMma = kWarpLoad + 1, kWarpQ = kWarpLoad + 2;
@@ -504,29 +551,46 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
 
   // ---- prologue: the call's work in units, and this CTA's share
   long long* cost = reinterpret_cast<long long*>(smem + C::kSmemRing);  // per sequence; the ring is not in use yet
-  for (int b = warp; b < a.kv.n_seqs; b += C::kThreads / 32) {
+  for (int b0 = warp * 32; b0 < a.kv.n_seqs; b0 += C::kThreads) {
+    // a lane per sequence; one of more than four row tiles is counted by the warp
+    const int b = b0 + lane;
     Item it;
-    it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, b);
-    if (!it.s.ok && blockIdx.x == 0 && lane == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+    it.s = SeqInfo{0, 0, 0, true};
+    if (b < a.kv.n_seqs) it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, b);
+    if (!it.s.ok && blockIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     const int nt = (it.s.n * G + kRows - 1) / kRows;
-    long long sum = 0;
-    for (it.i = lane; it.i < nt; it.i += 32) {
-      item_range<kN, kRows>(a, G, it);
-      sum += it.cost();
+    long long mine = 0;
+    if (nt <= 4) {
+      for (it.i = 0; it.i < nt; ++it.i) {
+        item_range<kN, kRows>(a, G, it);
+        mine += it.cost();
+      }
     }
+    for (unsigned many = __ballot_sync(kAll, nt > 4); many; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      Item x;
+      x.s = SeqInfo{0, __shfl_sync(kAll, it.s.n, src), __shfl_sync(kAll, it.s.kv, src), true};
+      const int nx = __shfl_sync(kAll, nt, src);
+      long long sum = 0;
+      for (x.i = lane; x.i < nx; x.i += 32) {
+        item_range<kN, kRows>(a, G, x);
+        sum += x.cost();
+      }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    if (lane == 0) cost[b] = sum * a.kv.Hkv;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+      if (lane == src) mine = sum;
+    }
+    if (b < a.kv.n_seqs) cost[b] = mine * a.kv.Hkv;
   }
   if (warp == kWarpMma && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       bar_init(full(s), 1);
       bar_init(empty(s), 1);
     }
-    bar_init(q_full, 64);
-    bar_init(q_empty, 2);
     bar_init(drain, 1);
     for (int b = 0; b < 2; ++b) {
+      bar_init(q_full(b), 64);
+      bar_init(q_empty(b), 1);
       bar_init(s_full(b), 1);
       bar_init(p_full(b), 4);
       bar_init(o_full(b), 1);
@@ -654,8 +718,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           const int slot = n_ops % kStages;
           const uint32_t round = n_ops / kStages;
           if (round > 0) {
-            if (lane == 0) ok = wait(empty(slot), (round - 1) & 1);
-            ok = __shfl_sync(kAll, (int)ok, 0);
+            ok = __all_sync(kAll, wait(empty(slot), (round - 1) & 1));
             if (!ok) break;
           }
           if (lane == 0) bar_expect(full(slot), box_bytes * (uint32_t)((b1 - b0) * C::kSub));
@@ -676,119 +739,132 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       }
       __syncwarp();
     } else if (warp == kWarpMma) {
-      // ---- the products
-      const uint32_t id_s = idesc(BF16, kN, false, a.scale < 0.0f), id_o = idesc(BF16, D, true, false);
-      uint32_t n_ops = 0, n_q = 0, n_u[2] = {0, 0};
-      bool ok = true;
-      const auto leader_wait = [&](uint32_t bar, uint32_t parity) {
-        bool r = true;
-        if (lane == 0) r = wait(bar, parity);
-        ok = ok && __shfl_sync(kAll, (int)r, 0);
-        return ok;
-      };
-      for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0 && ok;) {
-        const int len = walk_len(w);
-        const int m = w.it.tiles ? len : 0;
-        const bool two = kGroups == 2 && w.it.rows > 128;
-        const int U = two ? 2 * m : m;
-        if (m > 0 && leader_wait(q_full, n_q & 1)) {
-          ++n_q;
-          fence_after();
-          int k_slot = 0, v_slot = 0;
+      // ---- the products: one thread issues them.  (With the whole warp in the
+      // loop, its votes and reconvergence cost as much as the issue itself.)
+      if (elect_one()) {
+        const uint32_t id_s = idesc(BF16, kN, false, a.scale < 0.0f), id_o = idesc(BF16, D, true, false);
+        const uint32_t q_desc = desc_k(base + C::kSmemQ), k_desc = desc_k(base + C::kSmemRing);
+        const uint32_t v_desc = desc_mn(base + C::kSmemRing, kN * 128);
+        uint32_t slot = 0, phase = 0;  // of the ring
+        uint32_t p_phase = 0, q_phase = 0;  // bit b: parity of buffer / row tile b
+        int q_tile = 0;
+        uint32_t k_slot = 0, v_slot = 0;
+        const auto take = [&](uint32_t& got) {  // the ring's next tile
+          wait(full(slot), phase);
+          got = slot;
+          if (++slot == kStages) slot = 0, phase ^= 1;
+        };
+        for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0;) {
+          const int len = walk_len(w);
+          const int m = w.it.tiles ? len : 0;
+          const bool two = kGroups == 2 && w.it.rows > 128;
+          const int U = two ? 2 * m : m;
           const auto scores = [&](int u) {  // S(u) = Q K^T
-            if (!two || !(u & 1)) {
-              k_slot = n_ops % kStages;
-              if (!leader_wait(full(k_slot), (n_ops / kStages) & 1)) return;
-              ++n_ops;
+            const int odd = u & 1, qt = two ? odd : q_tile;
+            if (u == 0 || (two && u == 1)) {
+              wait(q_full(qt), q_phase >> qt & 1);
+              q_phase ^= 1u << qt;
             }
-            if (lane == 0) {
-              const uint32_t q = base + C::kSmemQ + (two && (u & 1) ? C::kQ : 0), k = base + C::kSmemRing + k_slot * C::kSlot;
-              const uint32_t d = tmem + C::kColS + (u & 1) * kN;
+            if (!two || !odd) take(k_slot);
+            fence_after();
+            const uint32_t q = q_desc + qt * (C::kQ / 16), k = k_desc + k_slot * (C::kSlot / 16);
+            const uint32_t d = tmem + C::kColS + odd * kN;
 #pragma unroll
-              for (int x = 0; x < D / 16; ++x)
-                mma_ss(d, desc_k(q + (x / 4) * 16384 + (x % 4) * 32), desc_k(k + (x / 4) * (kN * 128) + (x % 4) * 32),
-                       id_s, x > 0);
-              mma_commit(s_full(u & 1));
-              if (!two || (u & 1)) mma_commit(empty(k_slot));
-              if (u == U - 1) mma_commit(q_empty);
-            }
-            __syncwarp();
+            for (int x = 0; x < D / 16; ++x)
+              mma_ss(d, q + ((x / 4) * 16384 + (x % 4) * 32) / 16, k + ((x / 4) * (kN * 128) + (x % 4) * 32) / 16, kDescHi,
+                     id_s, x > 0);
+            mma_commit(s_full(odd));
+            if (!two || odd) mma_commit(empty(k_slot));
+            if (u >= U - (two ? 2 : 1)) mma_commit(q_empty(qt));
           };
-          scores(0);
-          if (U > 1 && ok) scores(1);
-          for (int u = 0; u < U && ok; ++u) {
+          if (U > 0) scores(0);
+          if (U > 1) scores(1);
+          for (int u = 0; u < U; ++u) {
             const int buf = u & 1, acc_group = kGroups == 2 ? buf : 0;
-            if (!leader_wait(p_full(buf), n_u[buf] & 1)) break;
-            ++n_u[buf];
-            const int tile = w.it.t0 + w.off + (two ? u >> 1 : u), k0 = tile * kN;
-            const int from = max(w.it.lo, k0) - k0, to = min(w.it.hi, k0 + kN) - k0;
-            const int x0 = from / 16, x1 = (to + 15) / 16;
-            if (!two || !(u & 1)) {
-              v_slot = n_ops % kStages;
-              if (!leader_wait(full(v_slot), (n_ops / kStages) & 1)) break;
-              ++n_ops;
-              if (to & 15) {
-                // values past the last visible key: whatever the page holds there, even NaN, must not reach a sum
-                for (int i = lane; i < (x1 * 16 - to) * C::kSub * 8; i += 32) {
-                  const int row = to + i / (C::kSub * 8), part = (i / 8) % C::kSub;
-                  *reinterpret_cast<uint4*>(smem + C::kSmemRing + v_slot * C::kSlot + part * (kN * 128) + row * 128 +
-                                            (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+            int x0 = 0, x1 = kN / 16;  // K steps that hold a visible key
+            const int tile = two ? u >> 1 : u;
+            if (!two || !buf) {
+              take(v_slot);
+              if (tile == m - 1) {
+                // Values past the sequence's last key: whatever the page holds there, even NaN, must not reach a sum.
+                const int k0 = (w.it.t0 + w.off + tile) * kN, to = min(w.it.hi, k0 + kN) - k0;
+                const int end = (to + 15) / 16 * 16;
+                for (int row = max(0, w.it.s.kv - k0); row < end; ++row) {
+                  uint8_t* line = smem + C::kSmemRing + v_slot * C::kSlot + row * 128;
+#pragma unroll
+                  for (int i = 0; i < C::kSub * 8; ++i)
+                    *reinterpret_cast<uint4*>(line + (i / 8) * (kN * 128) + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
                 }
-                fence_proxy();
-                __syncwarp();
+                if (w.it.s.kv - k0 < end) fence_proxy();
               }
             }
-            fence_after();
-            if (lane == 0) {
-              const uint32_t v = base + C::kSmemRing + v_slot * C::kSlot;
-              const uint32_t d = tmem + C::kColO + acc_group * D, p = tmem + C::kColS + buf * kN;
-              const bool first = u < kGroups;  // the first product of this accumulator
-              for (int x = x0; x < x1; ++x)
-                mma_ts(d, p + x * 8, desc_mn(v + x * 2048, kN * 128), id_o, !(first && x == x0));
-              mma_commit(o_full(buf));
-              if (!two || (u & 1)) mma_commit(empty(v_slot));
+            if (tile == 0 || tile == m - 1) {
+              const int k0 = (w.it.t0 + w.off + tile) * kN;
+              x0 = (max(w.it.lo, k0) - k0) / 16;
+              x1 = (min(w.it.hi, k0 + kN) - k0 + 15) / 16;
             }
-            __syncwarp();
+            wait(p_full(buf), p_phase >> buf & 1);
+            p_phase ^= 1u << buf;
+            fence_after();
+            const uint32_t v = v_desc + v_slot * (C::kSlot / 16);
+            const uint32_t d = tmem + C::kColO + acc_group * D, p = tmem + C::kColS + buf * kN;
+            const bool first = u < kGroups;  // the first product of this accumulator
+            if (x0 == 0 && x1 == kN / 16) {
+#pragma unroll
+              for (int x = 0; x < kN / 16; ++x) mma_ts(d, p + x * 8, v + x * 128, kDescHi, id_o, !first || x > 0);
+            } else {
+              for (int x = x0; x < x1; ++x) mma_ts(d, p + x * 8, v + x * 128, kDescHi, id_o, !first || x > x0);
+            }
+            mma_commit(o_full(buf));
+            if (!two || buf) mma_commit(empty(v_slot));
             if (u + 2 < U) scores(u + 2);
           }
+          if (kGroups == 2 && U > 0 && !two) q_tile ^= 1;
+          walk_next<kN, kRows>(a, G, w, len);
         }
-        walk_next<kN, kRows>(a, G, w, len);
-      }
-      if (!ok && lane == 0) {  // given up: the products in flight end before tensor memory is freed
-        mma_commit(drain);
-        const long long t0 = clock64();
-        while (!bar_try(drain, 0) && clock64() - t0 < kWaitCycles / 8) {
+        if (st.abort) {  // given up: the products in flight end before tensor memory is freed
+          mma_commit(drain);
+          const long long t0 = clock64();
+          while (!bar_try(drain, 0) && clock64() - t0 < kWaitCycles / 8) {
+          }
         }
       }
       __syncwarp();
     } else {
       // ---- query rows, gathered by 16-byte copies into the swizzled tiles
       const int t = tid - kWarpQ * 32;
-      uint32_t n_q = 0;
-      bool ok = true;
-      for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0 && ok;) {
+      uint32_t used = 0, q_phase = 0;  // bit t: row tile t was filled before; parity of its next release
+      int q_tile = 0;
+      // a thread keeps its 16-byte column and steps down the rows: no division per copy
+      constexpr int kChunks = D / 8, kStep = 64 / kChunks;
+      const int ch = t % kChunks;
+      for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0;) {
         const int len = walk_len(w);
         if (w.it.tiles) {
-          if (n_q > 0) ok = wait(q_empty, (n_q - 1) & 1);
-          if (!ok) break;
-          ++n_q;
-          // a thread keeps its 16-byte column and steps down the rows: no division per copy
-        constexpr int kChunks = D / 8, kStep = 64 / kChunks;
-        const int ch = t % kChunks;
-        const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)w.it.s.q0 * a.q_stride +
-                            (int64_t)w.it.h * G * a.q_head_stride + ch * 8;
-        const uint32_t dst = base + C::kSmemQ + (ch >> 3) * 16384;
-        int row = t / kChunks;
-        int tok = (w.it.r0 + row) / G, g = w.it.r0 + row - tok * G;
+          const bool two = kGroups == 2 && w.it.rows > 128;
+          const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)w.it.s.q0 * a.q_stride +
+                              (int64_t)w.it.h * G * a.q_head_stride + ch * 8;
+          for (int half = 0; half < (two ? 2 : 1); ++half) {
+            const int qt = two ? half : q_tile;
+            if (used >> qt & 1) {
+              wait(q_empty(qt), q_phase >> qt & 1);
+              q_phase ^= 1u << qt;
+            }
+            used |= 1u << qt;
+            const int rows = min(128, w.it.rows - half * 128);
+            const uint32_t dst = base + C::kSmemQ + qt * C::kQ + (ch >> 3) * 16384;
+            int row = t / kChunks;
+            int tok = (w.it.r0 + half * 128 + row) / G, g = w.it.r0 + half * 128 + row - tok * G;
 #pragma unroll 4
-        for (; row < w.it.rows; row += kStep) {
-          cp_async16(dst + (row >> 7) * C::kQ + (row & 127) * 128 + (((ch & 7) ^ (row & 7)) << 4),
-                     q + tok * a.q_stride + g * a.q_head_stride);
-          for (g += kStep; g >= G; g -= G) ++tok;
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy();
-          bar_arrive(q_full);
+            for (; row < rows; row += kStep) {
+              cp_async16(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4), q + tok * a.q_stride + g * a.q_head_stride);
+              for (g += kStep; g >= G; g -= G) ++tok;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy();
+            bar_arrive(q_full(qt));
+          }
+          if (kGroups == 2 && !two) q_tile ^= 1;
         }
         walk_next<kN, kRows>(a, G, w, len);
       }
@@ -799,11 +875,12 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     const int grp = warp >> 2, r = tid & 127;
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
     const uint32_t o_addr = lanes + C::kColO + grp * D;
-    uint32_t n_u[2] = {0, 0}, n_p[2] = {0, 0};  // score tiles taken, weights handed over, per buffer
+    uint32_t s_phase = 0, o_phase = 0;  // bit b: parity of buffer b's next scores / of its last product
     float* const part0 = reinterpret_cast<float*>(a.ws + kWsHead);
     constexpr size_t kPartFloats = C::kPartFloats;
     constexpr int kJoin = 128 * kGroups;
-    int* const counters = reinterpret_cast<int*>(a.ws + 16);
+    float2* const xch = reinterpret_cast<float2*>(smem + C::kSmemXch);
+    unsigned* const counters = reinterpret_cast<unsigned*>(a.ws + 16);
     long long g_seg = st.first;  // unit at which the segment starts
     for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0;) {
       const int len = walk_len(w);
@@ -821,10 +898,9 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
 
       for (int u = kGroups == 2 ? grp : 0; u < U; u += kGroups) {
         const int buf = u & 1;
-        warp_wait(wait, s_full(buf), n_u[buf] & 1);
-        ++n_u[buf];
+        warp_wait(wait, s_full(buf), s_phase >> buf & 1);
+        s_phase ^= 1u << buf;
         fence_after();
-        if (u == 0 && (two || kGroups == 1) && tid == 0) bar_arrive(q_empty);
         if (busy) {
           const uint32_t s_addr = lanes + C::kColS + buf * kN;
           uint32_t s[kN];
@@ -838,10 +914,13 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
             for (int j = 0; j < kN; ++j)
               if (j >= j1 || j < j0) s[j] = 0xff800000u;
           }
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx[4];
 #pragma unroll
-          for (int j = 0; j < kN; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[j]));
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+#pragma unroll
+          for (int j = 8; j < kN; j += 2)
+            mx[j / 2 & 3] = max3(mx[j / 2 & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+          const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
           float f = 1.0f;
           const bool grow = ref == -INFINITY ? top > -INFINITY : (top - ref) * c2 > kGrow;
           if (grow) {
@@ -851,7 +930,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           }
           if (acc && __any_sync(kAll, grow && valid)) {
             const int pb = kGroups == 2 ? buf : buf ^ 1;  // the buffer of the group's previous tile
-            warp_wait(wait, o_full(pb), (n_p[pb] - 1) & 1);
+            warp_wait(wait, o_full(pb), o_phase >> pb & 1 ^ 1);
             fence_after();
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
@@ -883,7 +962,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         __syncwarp();
         if (lane == 0) bar_arrive(p_full(buf));
         acc = true;
-        ++n_p[buf];
+        o_phase ^= 1u << buf;
       }
 
       // ---- the segment's result
@@ -891,96 +970,92 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       const bool join = kGroups == 2 && !two && U > 1;  // two groups hold sums of the same rows
       if (acc) {
         const int lb = kGroups == 2 ? grp : (U - 1) & 1;
-        warp_wait(wait, o_full(lb), (n_p[lb] - 1) & 1);
+        warp_wait(wait, o_full(lb), o_phase >> lb & 1 ^ 1);
         fence_after();
       }
       float m2 = ref == -INFINITY ? -INFINITY : ref * c2;  // log2 units from here on
-      float f_own = 1.0f, f_other = 0.0f;
-      float* xch = reinterpret_cast<float*>(smem + C::kSmemQ + C::kQ);  // the second row tile of q: free in such items
-      const bool writes = two || grp == 0;                              // this group puts out the rows
       // partial sums: slot 0 if the CTA's first unit is in this item, else 1
       const long long g_item = g_seg - w.off;
       const int slot = g_seg == st.first ? 0 : 1;
       float* part = part0 + ((size_t)blockIdx.x * 2 + slot) * kPartFloats;
-      if (join) {
-        if (grp == 1) {
-          xch[r] = m2;
-          xch[128 + r] = sum;
-        }
+      bool writes = two || grp == 0;  // this group puts out columns
+      int col0 = 0, col1 = D;
+      float f_own = 1.0f, f_other = 0.0f;
+      if (join) {  // both groups' accumulators are in reach of either: each puts out half of the columns
+        xch[grp * 128 + r] = make_float2(m2, sum);
+        fence_before();
         named_sync(1, 256);
-        if (grp == 0) {
-          const float om = xch[r], os = xch[128 + r];
-          const float M = fmaxf(m2, om);
-          f_own = m2 == -INFINITY ? 0.0f : ex2(m2 - M);
-          f_other = om == -INFINITY ? 0.0f : ex2(om - M);
-          sum = sum * f_own + os * f_other;
-          m2 = M;
-        }
-        named_sync(1, 256);
+        fence_after();
+        const float2 other = xch[(grp ^ 1) * 128 + r];
+        const float M = fmaxf(m2, other.x);
+        f_own = m2 == -INFINITY ? 0.0f : ex2(m2 - M);
+        f_other = other.x == -INFINITY ? 0.0f : ex2(other.x - M);
+        // the same sum in both groups, to the bit
+        const float a0 = grp ? other.y : sum, b0 = grp ? f_other : f_own, a1 = grp ? sum : other.y, b1 = grp ? f_own : f_other;
+        sum = a0 * b0 + a1 * b1;
+        m2 = M;
+        writes = true;
+        col0 = grp * (D / 2);
+        col1 = col0 + D / 2;
       }
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-      constexpr int kX = D / 2;  // columns that the exchange buffer (kQ bytes) holds for 128 rows
+      // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
+      const int c0 = whole ? 0 : owner(st.total, st.ctas, g_item);
+      const int parts = whole ? 1 : owner(st.total, st.ctas, g_item + w.it.cost() - 1) - c0 + 1;
+      const bool by_col = w.it.rows > (kColMajor - 1) * parts;
+      const uint32_t other_addr = lanes + C::kColO + (grp ^ 1) * D;
+      if (writes) {
+        constexpr int kW = 32;
 #pragma unroll 1
-      for (int x0 = 0; x0 < D; x0 += 32) {
-        uint32_t o[32];
-        if (busy && acc) {
-          tmem_ld32(o_addr + x0, o);
-          wait_ld();
-        } else {
+        for (int x0 = col0; x0 < col1; x0 += kW) {
+          uint32_t o[kW];
+          if (busy && acc) {
+            tmem_ld32(o_addr + x0, o);
+            if (join) {
+              uint32_t e[kW];
+              tmem_ld32(other_addr + x0, e);
+              wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = 0u;
-        }
-        if (join) {
-          float* x = xch + (x0 % kX) * 128 + r;
-          if (x0 % kX == 0 && x0 > 0) named_sync(1, 256);  // the columns before have been read
-          if (grp == 1) {
-            if (busy) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[j * 128] = __uint_as_float(o[j]);
-            }
-            if (x0 % kX == kX - 32) named_sync(1, 256);  // the other group's columns are there
-          } else {
-            if (x0 % kX == 0) named_sync(1, 256);
-            if (valid) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                o[j] = __float_as_uint(__uint_as_float(o[j]) * f_own + x[j * 128] * f_other);
-            }
-          }
-        }
-        if (writes && valid) {
-          if (whole) {
-            uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tok) * a.o_stride +
-                            (int64_t)(w.it.h * G + g) * a.o_head_stride + x0;
-#pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              const auto at = [&](int i) { return __uint_as_float(o[j + i]) * inv; };
-              *reinterpret_cast<uint4*>(out + j) =
-                  make_uint4(pack16<BF16>(at(0), at(1)), pack16<BF16>(at(2), at(3)), pack16<BF16>(at(4), at(5)),
-                             pack16<BF16>(at(6), at(7)));
+              for (int j = 0; j < kW; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * f_own + __uint_as_float(e[j]) * f_other);
+            } else {
+              wait_ld();
             }
           } else {
-            uint32_t* dst = reinterpret_cast<uint32_t*>(part) + 2 * kRows + (size_t)row * D + x0;
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<uint4*>(dst + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            for (int j = 0; j < kW; ++j) o[j] = 0u;
           }
+          if (valid) {
+            if (whole) {
+              uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tok) * a.o_stride +
+                              (int64_t)(w.it.h * G + g) * a.o_head_stride + x0;
+#pragma unroll
+              for (int j = 0; j < kW; j += 8) {
+                const auto at = [&](int i) { return __uint_as_float(o[j + i]) * inv; };
+                *reinterpret_cast<uint4*>(out + j) =
+                    make_uint4(pack16<BF16>(at(0), at(1)), pack16<BF16>(at(2), at(3)), pack16<BF16>(at(4), at(5)),
+                               pack16<BF16>(at(6), at(7)));
+              }
+            } else if (by_col) {  // a warp's stores of one column are contiguous
+              uint32_t* dst = reinterpret_cast<uint32_t*>(part) + 2 * kRows + (size_t)x0 * kRows + row;
+#pragma unroll
+              for (int j = 0; j < kW; ++j) dst[j * kRows] = o[j];
+            } else {
+              uint32_t* dst = reinterpret_cast<uint32_t*>(part) + 2 * kRows + (size_t)row * D + x0;
+#pragma unroll
+              for (int j = 0; j < kW; j += 4)
+                *reinterpret_cast<uint4*>(dst + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
       }
       fence_before();
-      if (join) {
-        named_sync(1, 256);  // the exchange buffer has been read
-        if (tid == 0) bar_arrive(q_empty);
-      } else if (kGroups == 2 && !two && U == 1 && tid == 0) {
-        bar_arrive(q_empty);
-      }
+      writes = two || grp == 0;  // the row's statistics are written once
       if (writes && whole && valid && a.lse)
         a.lse[(int64_t)(w.it.s.q0 + tok) * a.Hq + w.it.h * G + g] =
             sum > 0.0f ? (m2 + log2f(sum)) * 0.693147180559945309f : -INFINITY;
       if (!whole) {
-        // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
-        const int c0 = owner(st.total, st.ctas, g_item), c1 = owner(st.total, st.ctas, g_item + w.it.cost() - 1);
         if (writes && valid) {
           part[row] = m2;
           part[kRows + row] = sum;
@@ -988,25 +1063,23 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         if (tid == 0) {
           Cut& cut = st.cut[st.n_cut++];
           cut.c0 = c0;
-          cut.parts = c1 - c0 + 1;
+          cut.parts = parts;
           cut.slot0 = share(st.total, st.ctas, c0) == g_item ? 0 : 1;
-          cut.arrivals = cut.parts * (two ? 2 : 1);
           cut.rows = w.it.rows;
           cut.r0 = w.it.r0;
           cut.q0 = w.it.s.q0;
           cut.h = w.it.h;
         }
-        if (writes) {
-          __threadfence();
-          named_sync(2 + grp, 128);
-          if (r == 0) atomicAdd(counters + c0 * 2, 1);
-        }
       }
+      // every group's columns are read before the next item's products, and written before the part is announced
+      if (kGroups == 2 && (join || !whole)) named_sync(1, 256);
+      else if (!whole) named_sync(2, 128);
+      if (!whole && tid == 0) count_up(counters + c0, parts * 2 - 1);
       g_seg += len;
       walk_next<kN, kRows>(a, G, w, len);
     }
     named_sync(4, kJoin);
-    for (int x = 0; x < st.n_cut; ++x) join_parts<D, BF16>(a, G, st, st.cut[x], part0, counters, smem + C::kSmemRing, wait);
+    for (int x = 0; x < st.n_cut; ++x) join_parts<D, BF16>(a, G, st, st.cut[x], part0, counters, smem + C::kSmemRing);
   }
   fence_before();
   __syncthreads();
