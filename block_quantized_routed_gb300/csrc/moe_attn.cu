@@ -255,7 +255,8 @@ struct Cut {
 
 // what the prologue leaves in shared memory for every role
 struct Start {
-  int b, h, i, off;
+  Item item;  // the CTA's first, and the unit it starts with
+  int off;
   long long first, left, total;
   int ctas;
   volatile int abort;
@@ -264,19 +265,11 @@ struct Start {
   Cut cut[2];
 };
 
-template <int kN, int kRows>
-__device__ __forceinline__ Walk walk_begin(const AttnArgs& a, int G, const Start& st) {
+__device__ __forceinline__ Walk walk_begin(const Start& st) {
   Walk w;
-  w.it.b = st.b;
-  w.it.h = st.h;
-  w.it.i = st.i;
+  w.it = st.item;
   w.off = st.off;
   w.left = st.left;
-  if (w.left > 0) {
-    w.it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, w.it.b);
-    w.it.tiles_q = (w.it.s.n * G + kRows - 1) / kRows;
-    item_range<kN, kRows>(a, G, w.it);
-  }
   return w;
 }
 // past the current item, if work is left
@@ -362,6 +355,9 @@ __device__ __forceinline__ void fma4(float4& acc, float f, float4 v) {
 __device__ __forceinline__ void count_up(unsigned* counter, int wrap) {
   asm volatile("fence.acq_rel.gpu;\n red.relaxed.gpu.global.inc.u32 [%0], %1;" ::"l"(counter), "r"(wrap) : "memory");
 }
+__device__ __forceinline__ void count_gone(unsigned* counter, int wrap) {  // what was read has been used already
+  asm volatile("red.relaxed.gpu.global.inc.u32 [%0], %1;" ::"l"(counter), "r"(wrap) : "memory");
+}
 __device__ __forceinline__ unsigned count_read(const unsigned* counter) {
   unsigned v;
   asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
@@ -407,6 +403,25 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
           L > 0.0f ? (M + log2f(L)) * 0.693147180559945309f : -INFINITY;
     }
   };
+  const int n = nr > 0 ? nr * kVecs : 0;  // vectors of 4 columns
+  int teams = 1;                          // teams of threads share the parts where there are few vectors
+  while (n && teams * 2 * n <= kThreads && teams * 2 <= np) teams *= 2;
+  const int width = kThreads / teams, team = tid / width;
+  const bool by_col = per >= kColMajor, single = n <= width;  // single: one vector per thread
+  const auto load = [&](const float* src, int row, int c) {
+    if (!by_col) return __ldcg(reinterpret_cast<const float4*>(src + (size_t)(lo + row) * D + c));
+    const float* q = src + (size_t)c * C::kRows + lo + row;
+    return make_float4(__ldcg(q), __ldcg(q + C::kRows), __ldcg(q + 2 * C::kRows), __ldcg(q + 3 * C::kRows));
+  };
+  // one vector per thread: the first parts are asked for before the weights are known
+  constexpr int kAhead = 8;
+  float4 ahead[kAhead];
+  const int my = tid % width, my_row = by_col ? my % max(nr, 1) : my / kVecs, my_c = (by_col ? my / max(nr, 1) : my % kVecs) * 4;
+  if (single && my < n) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (team + i * teams < np) ahead[i] = load(part(team + i * teams) + 2 * C::kRows, my_row, my_c);
+  }
   if (np <= 8) {  // many rows each: a thread per row, its loads together
     for (int row = tid; row < nr; row += kThreads) {
       float m[8], l[8], M = -INFINITY, L = 0.0f;
@@ -459,31 +474,23 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
   }
   named_sync(4, kThreads);
   if (nr > 0) {  // uniform over the CTA
-    const int n = nr * kVecs;  // vectors of 4 columns
-    int teams = 1;             // teams of threads share the parts where there are few vectors
-    while (teams * 2 * n <= kThreads && teams * 2 <= np) teams *= 2;
-    const int width = kThreads / teams, team = tid / width;
-    const bool by_col = per >= kColMajor;
     const auto put = [&](int row, int c, float4 v) {
       const int R = cut.r0 + lo + row, tok = R / G;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(cut.q0 + tok) * a.o_stride +
                                 (int64_t)(cut.h * G + R - tok * G) * a.o_head_stride + c) =
           make_uint2(pack16<BF16>(v.x, v.y), pack16<BF16>(v.z, v.w));
     };
-    const auto load = [&](const float* src, int row, int c) {
-      if (!by_col) return __ldcg(reinterpret_cast<const float4*>(src + (size_t)(lo + row) * D + c));
-      const float* q = src + (size_t)c * C::kRows + lo + row;
-      return make_float4(__ldcg(q), __ldcg(q + C::kRows), __ldcg(q + 2 * C::kRows), __ldcg(q + 3 * C::kRows));
-    };
-    if (n <= width) {  // one vector per thread: several parts in flight
-      const int e = tid % width;
-      if (e < n) {
-        const int row = by_col ? e % nr : e / kVecs, c = (by_col ? e / nr : e % kVecs) * 4;
+    if (single) {
+      if (my < n) {
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+          if (team + i * teams < np) fma4(acc, wgt[(team + i * teams) * per + my_row], ahead[i]);
 #pragma unroll 8
-        for (int p = team; p < np; p += teams) fma4(acc, wgt[p * per + row], load(part(p) + 2 * C::kRows, row, c));
+        for (int p = team + kAhead * teams; p < np; p += teams)
+          fma4(acc, wgt[p * per + my_row], load(part(p) + 2 * C::kRows, my_row, my_c));
         if (teams > 1) red[tid] = acc;
-        else put(row, c, acc);
+        else put(my_row, my_c, acc);
       }
     } else {  // several vectors of a thread in flight
       constexpr int kB = 4;
@@ -516,12 +523,12 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
           const float4 v = red[t * width + tid];
           acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
-        put(by_col ? tid % nr : tid / kVecs, (by_col ? tid / nr : tid % kVecs) * 4, acc);
+        put(my_row, my_c, acc);
       }
     }
   }
   named_sync(4, kThreads);  // every read of the parts and of shared memory is done
-  if (tid == 0) count_up(counter, np * 2 - 1);
+  if (tid == 0) count_gone(counter, np * 2 - 1);
 }
 
 template <int D, bool BF16>
@@ -609,7 +616,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     const int c = blockIdx.x;
     const bool work = c < n && total > 0;
     const long long g0 = work ? share(total, n, c) : 0, g1 = work ? share(total, n, c + 1) : 0;
-    int fb = 0, fh = 0, fi = 0;
+    int fb = 0;
     long long at = 0;  // units before sequence fb
     if (work) {
       for (int b0 = 0; b0 < a.kv.n_seqs; b0 += 32) {
@@ -631,12 +638,13 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         at += __shfl_sync(kAll, inc, 31);
       }
       Item it;
+      it.b = fb;
       it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, fb);
-      const int nt = (it.s.n * G + kRows - 1) / kRows;
+      const int nt = it.tiles_q = (it.s.n * G + kRows - 1) / kRows;
       const long long per = cost[fb] / a.kv.Hkv;
       long long rem = g0 - at;
-      fh = (int)(rem / per);
-      rem -= fh * per;
+      it.h = (int)(rem / per);
+      rem -= it.h * per;
       for (int i0 = 0; i0 < nt; i0 += 32) {
         it.i = i0 + lane;
         long long mine = 0;
@@ -653,8 +661,8 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         const unsigned hit = __ballot_sync(kAll, inc > rem);
         if (hit) {
           const int src = __ffs(hit) - 1;
-          fi = i0 + src;
           rem -= __shfl_sync(kAll, inc - mine, src);
+          if (lane == src) st.item = it;
           break;
         }
         rem -= __shfl_sync(kAll, inc, 31);
@@ -662,16 +670,13 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       at = rem;
     }
     if (lane == 0) {
-      st.b = fb;
-      st.h = fh;
-      st.i = fi;
       st.off = (int)at;
       st.first = g0;
       st.left = g1 - g0;
       st.total = total;
       st.ctas = n;
     }
-    __syncwarp();
+  } else if (warp == kWarpMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&st.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -695,7 +700,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       const int part = lane % C::kSub, box = lane / C::kSub;  // this lane's box of a tile
       uint32_t n_ops = 0;
       bool ok = true;
-      for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0 && ok;) {
+      for (Walk w = walk_begin(st); w.left > 0 && ok;) {
         const int len = walk_len(w);
         const int m = w.it.tiles ? len : 0;
         const bool two = kGroups == 2 && w.it.rows > 128;
@@ -754,7 +759,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           got = slot;
           if (++slot == kStages) slot = 0, phase ^= 1;
         };
-        for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0;) {
+        for (Walk w = walk_begin(st); w.left > 0;) {
           const int len = walk_len(w);
           const int m = w.it.tiles ? len : 0;
           const bool two = kGroups == 2 && w.it.rows > 128;
@@ -815,7 +820,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
             } else {
               for (int x = x0; x < x1; ++x) mma_ts(d, p + x * 8, v + x * 128, kDescHi, id_o, !first || x > x0);
             }
-            mma_commit(o_full(buf));
+            if (kGroups == 1 || u >= U - 2) mma_commit(o_full(buf));
             if (!two || buf) mma_commit(empty(v_slot));
             if (u + 2 < U) scores(u + 2);
           }
@@ -838,7 +843,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       // a thread keeps its 16-byte column and steps down the rows: no division per copy
       constexpr int kChunks = D / 8, kStep = 64 / kChunks;
       const int ch = t % kChunks;
-      for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0;) {
+      for (Walk w = walk_begin(st); w.left > 0;) {
         const int len = walk_len(w);
         if (w.it.tiles) {
           const bool two = kGroups == 2 && w.it.rows > 128;
@@ -882,7 +887,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     float2* const xch = reinterpret_cast<float2*>(smem + C::kSmemXch);
     unsigned* const counters = reinterpret_cast<unsigned*>(a.ws + 16);
     long long g_seg = st.first;  // unit at which the segment starts
-    for (Walk w = walk_begin<kN, kRows>(a, G, st); w.left > 0;) {
+    for (Walk w = walk_begin(st); w.left > 0;) {
       const int len = walk_len(w);
       const int m = w.it.tiles ? len : 0;
       const bool two = kGroups == 2 && w.it.rows > 128;
@@ -929,9 +934,12 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
             sum *= f;
           }
           if (acc && __any_sync(kAll, grow && valid)) {
-            const int pb = kGroups == 2 ? buf : buf ^ 1;  // the buffer of the group's previous tile
-            warp_wait(wait, o_full(pb), o_phase >> pb & 1 ^ 1);
-            fence_after();
+            // The accumulator's last product has to be done.  Two groups: it was issued before this tile's scores,
+            // so it is.  One group: it may still run.
+            if (kGroups == 1) {
+              warp_wait(wait, o_full(buf ^ 1), o_phase >> (buf ^ 1) & 1 ^ 1);
+              fence_after();
+            }
 #pragma unroll 1
             for (int x = 0; x < D / 32; ++x) {
               uint32_t o[32];
@@ -962,7 +970,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         __syncwarp();
         if (lane == 0) bar_arrive(p_full(buf));
         acc = true;
-        o_phase ^= 1u << buf;
+        if (kGroups == 1) o_phase ^= 1u << buf;
       }
 
       // ---- the segment's result
@@ -970,6 +978,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       const bool join = kGroups == 2 && !two && U > 1;  // two groups hold sums of the same rows
       if (acc) {
         const int lb = kGroups == 2 ? grp : (U - 1) & 1;
+        if (kGroups == 2) o_phase ^= 1u << lb;  // two groups: told once per segment
         warp_wait(wait, o_full(lb), o_phase >> lb & 1 ^ 1);
         fence_after();
       }

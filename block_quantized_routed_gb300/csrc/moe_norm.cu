@@ -116,9 +116,13 @@ __device__ __forceinline__ float block_reduce(float v, float* buf) {
   return v;
 }
 
-// the q8_K rounding: half away from zero, clamped; 0 when the scale is 0
-__device__ __forceinline__ int q8k_code(float z, float d) {
-  return d != 0.0f ? (int)fminf(127.0f, fmaxf(-127.0f, roundf(__fdiv_rn(z, d)))) : 0;
+// The q8_K rounding of z / d: half away from zero, clamped.  The product with
+// the reciprocal is within 2 ulp of the IEEE quotient (at most 127: 2^-16), so
+// both round alike unless it is that near a half; only there it is divided.
+__device__ __forceinline__ int q8k_code(float z, float d, float inv) {
+  float x = z * inv;
+  if (fabsf(fabsf(x - truncf(x)) - 0.5f) < 3.1e-5f) x = __fdiv_rn(z, d);
+  return (int)fminf(127.0f, fmaxf(-127.0f, roundf(x)));
 }
 
 template <typename XT, typename RT, int NV, bool WIDE>
@@ -155,6 +159,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
   }
   sq = block_reduce<false>(sq, buf[0]);
   const float r = 1.0f / sqrtf(sq / (float)a.H + a.eps);
+  const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
   float peak = 0.0f;  // of the row, for the row-scaled outputs
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -166,13 +171,14 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
       for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * r * (w[j] + a.w_offset);
       if (a.y) store8_dt<WIDE>(a.y, a.y_dtype, row * a.y_stride + c, n, s[i]);
     }
+    if (per_row) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
+      for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
+    }
   }
   if (a.q_fmt == MOE_NORM_Q_NONE) return;
 
   const bool fp8 = a.q_fmt == MOE_NORM_Q_E4M3_G128 || a.q_fmt == MOE_NORM_Q_E4M3_ROW;
-  const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
   const float top = fp8 ? 448.0f : 127.0f;
   float d = 0.0f;
   if (per_row) {
@@ -195,19 +201,26 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
       d = __fdiv_rn(m, top);
       if (n > 0 && c % group == 0) a.d[row * groups + c / group] = d;
     }
+    // d = 0 only where every z of the group is 0 (or too small for its quotient to exist).  A reciprocal beyond
+    // fp32 (d below 2^-127) is not used: such groups are divided.
+    float inv = d > 0.0f ? 1.0f / d : 0.0f, dq = d;
+    if (inv > 3e38f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = __fdiv_rn(s[i][j], d);
+      inv = dq = 1.0f;
+    }
     uint8_t q[8];
     int sum = 0;
     if (fp8) {
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
-        // d = 0 only where every z of the group is 0 (or too small for z / 448 to exist)
-        const float2 z = d > 0.0f ? make_float2(__fdiv_rn(s[i][j], d), __fdiv_rn(s[i][j + 1], d)) : make_float2(0.f, 0.f);
-        *reinterpret_cast<__nv_fp8x2_storage_t*>(q + j) = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
+        *reinterpret_cast<__nv_fp8x2_storage_t*>(q + j) = __nv_cvt_float2_to_fp8x2(
+            make_float2(s[i][j] * inv, s[i][j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int code = q8k_code(s[i][j], d);
+        const int code = q8k_code(s[i][j], dq, inv);
         q[j] = (uint8_t)(int8_t)code;
         sum += code;
       }

@@ -117,17 +117,54 @@ __device__ __noinline__ int select64(const RouteArgs& a, int64_t row, int lane, 
   return mine;
 }
 
-// NP >= ceil(E / 32): elements per lane
-template <int NP>
+// the two largest of two pairs, each in order
+__device__ __forceinline__ void top2_join(float& first, float& second, float f, float s) {
+  second = fmaxf(fminf(first, f), fmaxf(second, s));
+  first = fmaxf(first, f);
+}
+
+// NP >= ceil(E / 32): elements per lane; lane i holds elements i * npl on.
+// VEC: npl = NP, E = 32 * NP and the rows are 16-byte aligned (wide loads).
+template <int NP, bool VEC>
 __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  __shared__ float s_key[4][NP * 32 + 1];  // groups that do not fall on lane boundaries
+  __shared__ int2 s_pick[4][MOE_MAX_TOPK + 1];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int t = blockIdx.x * (blockDim.x >> 5) + wid;
   if (t >= a.T) return;
   const int64_t row = (int64_t)t * a.stride;
-  const int npl = (a.E + 31) / 32, e0 = lane * npl;
+  const int npl = VEC ? NP : (a.E + 31) / 32, e0 = lane * npl;
+  const int have = VEC ? NP : max(0, min(npl, a.E - e0));  // elements of this lane
   float l[NP];
+  if constexpr (VEC) {
+    if (a.dtype == MOE_DT_F32) {
+      const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row + e0);
 #pragma unroll
-  for (int j = 0; j < NP; ++j) l[j] = j < npl && e0 + j < a.E ? load_logit(a, row + e0 + j) : -INFINITY;
+      for (int j = 0; j < NP / 4; ++j) {
+        const float4 v = __ldg(src + j);
+        l[4 * j] = v.x, l[4 * j + 1] = v.y, l[4 * j + 2] = v.z, l[4 * j + 3] = v.w;
+      }
+    } else {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.logits) + row + e0);
+#pragma unroll
+      for (int j = 0; j < NP / 8; ++j) {
+        const uint4 v = __ldg(src + j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float2 f;
+          if (a.dtype == MOE_DT_BF16) f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+          else f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+          l[8 * j + 2 * i] = f.x, l[8 * j + 2 * i + 1] = f.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NP; ++j) l[j] = l[j] != l[j] ? -INFINITY : l[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) l[j] = j < have ? load_logit(a, row + e0 + j) : -INFINITY;
+  }
 
   Stats st{0.0f, 1.0f};
   if (a.route == MOE_ROUTE_SOFTMAX) {
@@ -146,92 +183,113 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   }
   const float bound = a.route == MOE_ROUTE_SIGMOID ? 6.0f : (float)(npl + 130);
 
-  // ordering keys: p + b with a bias, the logits themselves without
+  // ordering keys: p + b with a bias, the logits themselves without; a group's
+  // score takes p (+ b) where it adds two keys
+  const bool scored = a.bias != nullptr;
   uint32_t key[NP];
 #pragma unroll
   for (int j = 0; j < NP; ++j) {
-    const bool in = j < npl && e0 + j < a.E;
-    const float v = in && a.bias ? score32(l[j], a.route, st) + a.bias[e0 + j] : l[j];
-    key[j] = in ? order_key(v) : 0u;
+    float v = l[j];
+    if (scored && j < have) v = score32(v, a.route, st) + __ldg(a.bias + e0 + j);
+    key[j] = j < have ? order_key(v) : 0u;
   }
 
   bool unsure = false;
   if (a.n_group > 1) {
-    const int gs = a.E / a.n_group;
-    // the two largest keys of each group, lane g keeping group g's
-    float my_score = -INFINITY, my_err = 0.0f;
-    for (int g = 0; g < a.n_group; ++g) {
-      float first = -INFINITY, second = -INFINITY;
+    const int gs = a.E / a.n_group, per = gs / npl;  // lanes per group, where groups are whole lanes
+    const bool on_lanes = gs == per * npl && (per & (per - 1)) == 0;
+    const bool add = a.group_score == MOE_GROUP_TOP2 && gs > 1;
+    float first = -INFINITY, second = -INFINITY;
+    const auto value = [&](int j) { return scored ? key_logit(key[j]) : add ? score32(l[j], a.route, st) : l[j]; };
+    if (on_lanes) {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const int e = e0 + j;
-        if (j < npl && e < a.E && e / gs == g) {
-          const float v = a.bias ? key_logit(key[j]) : a.group_score == MOE_GROUP_TOP2 ? score32(l[j], a.route, st) : l[j];
-          if (v > first) second = first, first = v;
-          else if (v > second) second = v;
+      for (int j = 0; j < NP; ++j)
+        if (j < have) top2_join(first, second, value(j), -INFINITY);
+      for (int o = 1; o < per; o <<= 1) {
+        const float f = __shfl_xor_sync(kAll, first, o), s2 = __shfl_xor_sync(kAll, second, o);
+        top2_join(first, second, f, s2);
+      }
+      // lane g takes group g's
+      first = __shfl_sync(kAll, first, lane * per & 31);
+      second = __shfl_sync(kAll, second, lane * per & 31);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; ++j)
+        if (j < have) s_key[wid][e0 + j] = value(j);
+      __syncwarp();
+      if (lane < a.n_group) {
+        int i = lane % gs;  // groups start at different elements: different banks
+        for (int j = 0; j < gs; ++j) {
+          top2_join(first, second, s_key[wid][lane * gs + i], -INFINITY);
+          if (++i == gs) i = 0;
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float f = __shfl_xor_sync(kAll, first, o), s2 = __shfl_xor_sync(kAll, second, o);
-        second = fmaxf(fminf(first, f), fmaxf(second, s2));
-        first = fmaxf(first, f);
-      }
-      if (lane == g) {
-        const bool two = a.group_score == MOE_GROUP_TOP2 && gs > 1;
-        my_score = two ? first + second : first;
-        // each key within (bound * p + |key|) ulp, p <= 1; without a bias a single logit is exact
-        my_err = a.bias || two ? kUlp * (fabsf(my_score) + fabsf(first) + fabsf(second == -INFINITY ? 0.0f : second) +
-                                         (two ? 2.0f : 1.0f) * bound)
-                               : 0.0f;
-      }
+    }
+    float score = -INFINITY, err = 0.0f;
+    if (lane < a.n_group) {
+      score = add ? first + second : first;
+      // each key within (bound * p + |key|) ulp, p <= 1; without a bias a single logit is exact
+      if (scored || add)
+        err = kUlp * (fabsf(score) + fabsf(first) + (add ? fabsf(second) : 0.0f) + (add ? 2.0f : 1.0f) * bound);
     }
     int rank = 0;
     for (int g = 0; g < a.n_group; ++g) {
-      const float other = __shfl_sync(kAll, my_score, g);
-      rank += other > my_score || (other == my_score && g < lane);
+      const float other = __shfl_sync(kAll, score, g);
+      rank += other > score || (other == score && g < lane);
     }
-    const bool in = lane < a.n_group && rank < a.topk_group;
-    const uint32_t kept = __ballot_sync(kAll, in);
+    if (lane >= a.n_group) rank = 64;
+    const uint32_t kept = __ballot_sync(kAll, rank < a.topk_group);
     // the last kept against the first dropped group
-    if (a.topk_group < a.n_group) {
-      const unsigned last = __ballot_sync(kAll, lane < a.n_group && rank == a.topk_group - 1);
-      const unsigned next = __ballot_sync(kAll, lane < a.n_group && rank == a.topk_group);
-      const float s0 = __shfl_sync(kAll, my_score, __ffs(last) - 1), s1 = __shfl_sync(kAll, my_score, __ffs(next) - 1);
-      const float x0 = __shfl_sync(kAll, my_err, __ffs(last) - 1), x1 = __shfl_sync(kAll, my_err, __ffs(next) - 1);
-      unsure = x0 + x1 > 0.0f && s0 - s1 <= x0 + x1;
-    }
+    const int last = __ffs(__ballot_sync(kAll, rank == a.topk_group - 1)) - 1;
+    const int next = __ffs(__ballot_sync(kAll, rank == a.topk_group)) - 1;
+    const float gap = __shfl_sync(kAll, score, last) - __shfl_sync(kAll, score, next);
+    const float tol = __shfl_sync(kAll, err, last) + __shfl_sync(kAll, err, next);
+    unsure = tol > 0.0f && gap <= tol;
+    int g = e0 / gs, left = (g + 1) * gs - e0;  // elements of the lane until the next group
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
-      if (key[j] && !(kept >> ((e0 + j) / gs) & 1)) key[j] = 0u;
+    for (int j = 0; j < NP; ++j) {
+      if (left == 0) ++g, left = gs;
+      --left;
+      if (!(kept >> (g & 31) & 1)) key[j] = 0u;
+    }
   }
 
-  // the k largest, and with a bias the one after them
+  // the k largest, and with a bias the one after them; only the lane that owns
+  // a choice looks for it and for its next largest
   const int avail = a.n_group > 1 ? a.topk_group * (a.E / a.n_group) : a.E;
-  const int rounds = a.bias && a.k < avail ? a.k + 1 : a.k;
-  int mine = 0;
-  for (int r = 0; r < rounds; ++r) {
-    uint32_t best = 0;
+  const int rounds = scored && a.k < avail ? a.k + 1 : a.k;
+  uint32_t best = 0;
 #pragma unroll
-    for (int j = 0; j < NP; ++j) best = max(best, key[j]);
+  for (int j = 0; j < NP; ++j) best = max(best, key[j]);
+  for (int r = 0; r < rounds; ++r) {
     const uint32_t top = __reduce_max_sync(kAll, best);
     const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-    int at = 0;
     if (lane == owner) {
-      bool done = false;
+      int at = 0;
+      float lv = 0.0f;
+      best = 0;
 #pragma unroll
-      for (int j = 0; j < NP; ++j)
-        if (!done && key[j] == top) done = true, key[j] = 0u, at = e0 + j;
+      for (int j = NP - 1; j >= 0; --j)  // ends with the lowest index
+        if (key[j] == top) at = j, lv = l[j];
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        if (j == at) key[j] = 0u;
+        best = max(best, key[j]);
+      }
+      s_pick[wid][r] = make_int2(e0 + at, __float_as_int(lv));
     }
-    at = __shfl_sync(kAll, at, owner);
-    if (lane == r) mine = at;
+    __syncwarp();
   }
-
+  int mine = 0;
   float lg = 0.0f;
-  if (lane < rounds) lg = load_logit(a, row + mine);
-  if (a.bias) {
-    const float b = lane < rounds ? a.bias[mine] : 0.0f;
-    const float p = score32(lg, a.route, st), v = p + b;
+  if (lane < rounds) {
+    const int2 pick = s_pick[wid][lane];
+    mine = pick.x;
+    lg = __int_as_float(pick.y);
+  }
+  float p = score32(lg, a.route, st);
+  if (scored) {
+    const float b = lane < rounds ? __ldg(a.bias + mine) : 0.0f, v = p + b;
     const float err = kUlp * (bound * p + fabsf(v));
     const float v1 = __shfl_down_sync(kAll, v, 1), err1 = __shfl_down_sync(kAll, err, 1);
     const float l1 = __shfl_down_sync(kAll, lg, 1), b1 = __shfl_down_sync(kAll, b, 1);
@@ -241,9 +299,9 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   if (unsure) {
     mine = select64(a, row, lane, st.m);
     if (lane < a.k) lg = load_logit(a, row + mine);
+    p = score32(lg, a.route, st);
   }
-
-  const float p = lane < a.k ? score32(lg, a.route, st) : 0.0f;
+  if (lane >= a.k) p = 0.0f;
   float g = p;
   if (a.renorm) {
     float sum = p;
@@ -257,6 +315,20 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   }
 }
 
+template <int NP>
+void launch_np(const RouteArgs& a, unsigned grid, int warps, cudaStream_t s) {
+  const int size = a.dtype == MOE_DT_F32 ? 4 : 2;
+  const bool vec = a.E == 32 * NP && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
+                   (a.T == 1 || a.stride * size % 16 == 0);
+  if constexpr (NP >= 8) {
+    if (vec) {
+      route_grouped_kernel<NP, true><<<grid, 32 * warps, 0, s>>>(a);
+      return;
+    }
+  }
+  route_grouped_kernel<NP, false><<<grid, 32 * warps, 0, s>>>(a);
+}
+
 }  // namespace
 
 cudaError_t launch_route_grouped(const RouteArgs& a, cudaStream_t s) {
@@ -265,11 +337,11 @@ cudaError_t launch_route_grouped(const RouteArgs& a, cudaStream_t s) {
   const int warps = a.T <= 4 * num_sms() ? 1 : 4;  // few tokens: one CTA each
   const unsigned grid = (unsigned)((a.T + warps - 1) / warps);
   note_launch();
-  if (npl <= 2) route_grouped_kernel<2><<<grid, 32 * warps, 0, s>>>(a);
-  else if (npl <= 4) route_grouped_kernel<4><<<grid, 32 * warps, 0, s>>>(a);
-  else if (npl <= 8) route_grouped_kernel<8><<<grid, 32 * warps, 0, s>>>(a);
-  else if (npl <= 16) route_grouped_kernel<16><<<grid, 32 * warps, 0, s>>>(a);
-  else route_grouped_kernel<32><<<grid, 32 * warps, 0, s>>>(a);
+  if (npl <= 2) launch_np<2>(a, grid, warps, s);
+  else if (npl <= 4) launch_np<4>(a, grid, warps, s);
+  else if (npl <= 8) launch_np<8>(a, grid, warps, s);
+  else if (npl <= 16) launch_np<16>(a, grid, warps, s);
+  else launch_np<32>(a, grid, warps, s);
   return cudaGetLastError();
 }
 
