@@ -13,12 +13,25 @@
 // columns a half-warp's, and neither needs shared memory.  Rows that are not
 // 16-byte aligned (odd H, odd strides) run the same mapping with element-wise
 // guarded loads (WIDE = false).
+#include <algorithm>
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "moe_device.cuh"
 #include "moe_internal.h"
+
+#ifndef MOE_NORM_THREADS
+#define MOE_NORM_THREADS 1024
+#endif
+#ifndef MOE_NORM_STAGES
+#define MOE_NORM_STAGES 3
+#endif
+#ifndef MOE_NORM_NV
+#define MOE_NORM_NV 2
+#endif
 
 namespace moe {
 namespace {
@@ -125,64 +138,17 @@ __device__ __forceinline__ int q8k_code(float z, float d, float inv) {
   return (int)fminf(127.0f, fmaxf(-127.0f, roundf(x)));
 }
 
-template <typename XT, typename RT, int NV, bool WIDE>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
-  __shared__ float buf[2][32];
-  const int64_t row = blockIdx.x;
+// Scales z (s[NV][8]) into y and the 8-bit output of one row; `peak` is the
+// thread's largest |z| (row-scaled outputs only), buf one block_reduce buffer.
+template <int NV, bool WIDE>
+__device__ __forceinline__ void put_codes(const NormArgs& a, int64_t row, float (&s)[NV][8], float peak, float* buf) {
   const int tid = threadIdx.x, nt = blockDim.x;
-  const XT* x = static_cast<const XT*>(a.x) + row * a.x_stride;
-  const RT* res = static_cast<const RT*>(a.residual) + row * a.r_stride;
-  float s[NV][8];
-  float sq = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + tid) * 8, n = a.H - c;
-    if (n > 0) {
-      load8<XT, WIDE>(x + c, n, s[i]);
-      if (a.residual) {
-        float r[8];
-        load8<RT, WIDE>(res + c, n, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[i][j] += r[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + tid) * 8, n = a.H - c;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
-    if (a.sum_out && n > 0) store8<RT, WIDE>(static_cast<RT*>(a.sum_out) + row * a.sum_stride + c, n, s[i]);
-  }
-  sq = block_reduce<false>(sq, buf[0]);
-  const float r = 1.0f / sqrtf(sq / (float)a.H + a.eps);
   const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
-  float peak = 0.0f;  // of the row, for the row-scaled outputs
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + tid) * 8, n = a.H - c;
-    float w[8];
-    if (n > 0) {
-      load8_dt<WIDE>(a.w, a.w_dtype, c, n, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * r * (w[j] + a.w_offset);
-      if (a.y) store8_dt<WIDE>(a.y, a.y_dtype, row * a.y_stride + c, n, s[i]);
-    }
-    if (per_row) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
-    }
-  }
-  if (a.q_fmt == MOE_NORM_Q_NONE) return;
-
   const bool fp8 = a.q_fmt == MOE_NORM_Q_E4M3_G128 || a.q_fmt == MOE_NORM_Q_E4M3_ROW;
   const float top = fp8 ? 448.0f : 127.0f;
   float d = 0.0f;
   if (per_row) {
-    peak = block_reduce<true>(peak, buf[1]);
+    peak = block_reduce<true>(peak, buf);
     d = __fdiv_rn(peak, top);
     if (tid == 0) a.d[row] = d;
   }
@@ -240,9 +206,205 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
   }
 }
 
+template <typename XT, typename RT, int NV, bool WIDE>
+__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
+  __shared__ float buf[2][32];
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const XT* x = static_cast<const XT*>(a.x) + row * a.x_stride;
+  const RT* res = static_cast<const RT*>(a.residual) + row * a.r_stride;
+  float s[NV][8];
+  float sq = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8, n = a.H - c;
+    if (n > 0) {
+      load8<XT, WIDE>(x + c, n, s[i]);
+      if (a.residual) {
+        float r[8];
+        load8<RT, WIDE>(res + c, n, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8, n = a.H - c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
+    if (a.sum_out && n > 0) store8<RT, WIDE>(static_cast<RT*>(a.sum_out) + row * a.sum_stride + c, n, s[i]);
+  }
+  sq = block_reduce<false>(sq, buf[0]);
+  const float r = 1.0f / sqrtf(sq / (float)a.H + a.eps);
+  const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
+  float peak = 0.0f;  // of the row, for the row-scaled outputs
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8, n = a.H - c;
+    float w[8];
+    if (n > 0) {
+      load8_dt<WIDE>(a.w, a.w_dtype, c, n, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * r * (w[j] + a.w_offset);
+      if (a.y) store8_dt<WIDE>(a.y, a.y_dtype, row * a.y_stride + c, n, s[i]);
+    }
+    if (per_row) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
+    }
+  }
+  if (a.q_fmt == MOE_NORM_Q_NONE) return;
+  put_codes<NV, WIDE>(a, row, s, peak, buf[1]);
+}
+
+// The same for many rows: a CTA stays on its SM and walks the rows.  The
+// weights are kept in registers; the rows ahead come by asynchronous copies
+// into shared memory, where each thread reads back only what it asked for
+// itself (no barrier), so the loads of the next rows are under way through
+// both reductions of this one.
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4* v, float* f) {
+  if constexpr (sizeof(T) == 4) {
+    const uint4 x = v[0], y = v[1];
+    f[0] = __uint_as_float(x.x), f[1] = __uint_as_float(x.y), f[2] = __uint_as_float(x.z), f[3] = __uint_as_float(x.w);
+    f[4] = __uint_as_float(y.x), f[5] = __uint_as_float(y.y), f[6] = __uint_as_float(y.z), f[7] = __uint_as_float(y.w);
+  } else {
+    const uint4 x = v[0];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      } else {
+        const float2 t = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+        f[2 * i] = t.x, f[2 * i + 1] = t.y;
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void copy8(uint4* dst, const T* src) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + i)),
+                 "l"(reinterpret_cast<const uint4*>(src) + i)
+                 : "memory");
+}
+
+template <typename XT, typename RT>
+constexpr int row_vec_bytes() { return 8 * (int)(sizeof(XT) + sizeof(RT)); }  // x and residual of one vector
+
+template <typename XT, typename RT, int NV, int STAGES>
+__global__ void __launch_bounds__(512, NV > 2 ? 1 : 2) add_rmsnorm_rows_kernel(const NormArgs a) {
+  __shared__ float buf[2][2][32];
+  extern __shared__ uint4 ring[];  // [stage][vector][x | residual][thread]
+  constexpr int kX = sizeof(XT) / 2, kR = sizeof(RT) / 2;
+  const int tid = threadIdx.x, nt = blockDim.x;
+  const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
+  const bool res = a.residual != nullptr;
+  const auto slot = [&](int stage, int i) { return ring + ((size_t)(stage * NV + i) * nt + tid) * (kX + kR); };
+  const auto fetch = [&](int64_t r, int stage) {
+    if (r < a.T) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * nt + tid) * 8;
+        if (c < a.H) {
+          copy8<XT>(slot(stage, i), static_cast<const XT*>(a.x) + r * a.x_stride + c);
+          if (res) copy8<RT>(slot(stage, i) + kX, static_cast<const RT*>(a.residual) + r * a.r_stride + c);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int64_t row = blockIdx.x;
+#pragma unroll
+  for (int k = 0; k < STAGES - 1; ++k) fetch(row + (int64_t)k * gridDim.x, k);
+  float w[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8;
+    if (c < a.H) {
+      load8_dt<true>(a.w, a.w_dtype, c, 8, w[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[i][j] += a.w_offset;
+    }
+  }
+  int stage = 0;
+  for (int odd = 0; row < a.T; row += gridDim.x, odd ^= 1) {
+    fetch(row + (int64_t)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+    float s[NV][8];
+    float sq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * nt + tid) * 8;
+      if (c < a.H) {
+        unpack8<XT>(slot(stage, i), s[i]);
+        if (res) {
+          float r[8];
+          unpack8<RT>(slot(stage, i) + kX, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+        }
+        if (a.sum_out) store8<RT, true>(static_cast<RT*>(a.sum_out) + row * a.sum_stride + c, 8, s[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
+    }
+    stage = stage == STAGES - 1 ? 0 : stage + 1;
+    sq = block_reduce<false>(sq, buf[odd][0]);
+    const float r = 1.0f / sqrtf(sq / (float)a.H + a.eps);
+    float peak = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * nt + tid) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = c < a.H ? s[i][j] * r * w[i][j] : 0.0f;
+      if (a.y && c < a.H) store8_dt<true>(a.y, a.y_dtype, row * a.y_stride + c, 8, s[i]);
+      if (per_row) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
+      }
+    }
+    if (a.q_fmt != MOE_NORM_Q_NONE) put_codes<NV, true>(a, row, s, peak, buf[odd][1]);
+  }
+}
+
+template <typename XT, typename RT, int NV>
+cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
+  constexpr int kStages = MOE_NORM_STAGES;
+  const int vecs = a.H / 8, threads = ((vecs + NV - 1) / NV + 31) / 32 * 32;
+  const int smem = kStages * NV * threads * row_vec_bytes<XT, RT>();
+  auto kern = add_rmsnorm_rows_kernel<XT, RT, NV, kStages>;
+  static bool opted = false;
+  if (!opted) {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+    if (err != cudaSuccess) return err;
+    opted = true;
+  }
+  const int per_sm = std::max(1, std::min(MOE_NORM_THREADS / threads, 220 * 1024 / (smem + 2048)));
+  const unsigned grid = (unsigned)std::min<int64_t>(a.T, (int64_t)num_sms() * per_sm);
+  note_launch();
+  kern<<<grid, threads, smem, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename XT, typename RT, bool WIDE>
 cudaError_t launch_nv(const NormArgs& a, cudaStream_t s) {
   const int vecs = (a.H + 7) / 8;
+  if constexpr (WIDE) {
+    // rows of up to 64 KB in, three of which fit an SM's shared memory
+    if (a.T >= 8 * num_sms() && a.H / 8 * row_vec_bytes<XT, RT>() <= 64 * 1024)
+      return vecs <= 1024 ? launch_rows<XT, RT, MOE_NORM_NV>(a, s) : launch_rows<XT, RT, 4>(a, s);
+  }
   // Few rows: latency counts, one vector per thread.  Many rows: two to eight
   // vectors per thread, so that a CTA is small and its loads are in flight together.
   int nv = 1;

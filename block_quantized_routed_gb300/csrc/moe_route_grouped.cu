@@ -7,8 +7,9 @@
 // with a bound on their error; lane s re-derives the key of the s-th choice
 // and compares it with the next one.  Where a gap (between neighbours of the
 // result, or between the last kept and the first dropped group) is within the
-// two bounds, fp32 cannot tell, and the warp decides that token again with
-// fp64 keys.  Without a bias the order of the keys is that of the logits,
+// two bounds, fp32 cannot tell: the choices in question, and those that might
+// displace the last of them, are ranked again by fp64 keys, one per lane (an
+// fp64 exp costs a warp about 500 cycles here, so as few as possible).  Without a bias the order of the keys is that of the logits,
 // which are compared exactly.  A gap of exactly equal inputs (same logit, same
 // bias) is a tie in any precision and goes to the lower index.
 //
@@ -59,29 +60,35 @@ __device__ __forceinline__ double score64(float l, int route, float m, double su
 
 __device__ __forceinline__ double shfl_xor_d(double v, int o) { return __shfl_xor_sync(kAll, v, o); }
 
-// The token decided with fp64 keys: rare, so written for size.  Lane r returns
-// the r-th choice.  Keys are recomputed from the logits in
-// global memory, one element at a time.
-__device__ __noinline__ int select64(const RouteArgs& a, int64_t row, int lane, float m) {
-  const int npl = (a.E + 31) / 32, e0 = lane * npl;
+// the softmax's denominator in fp64 (1 for the sigmoid)
+__device__ __noinline__ double sum64(const RouteArgs& a, int64_t row, int lane, float m) {
+  if (a.route != MOE_ROUTE_SOFTMAX || m == -INFINITY) return 1.0;
   double sum = 0.0;
-  if (a.route == MOE_ROUTE_SOFTMAX && m != -INFINITY) {
-    for (int j = 0; j < npl; ++j)
-      if (e0 + j < a.E) {
-        const float l = load_logit(a, row + e0 + j);
-        sum += l == m ? 1.0 : exp((double)l - (double)m);
-      }
-    for (int o = 16; o > 0; o >>= 1) sum += shfl_xor_d(sum, o);
+  for (int e = lane; e < a.E; e += 32) {
+    const float l = load_logit(a, row + e);
+    sum += l == m ? 1.0 : exp((double)l - (double)m);
   }
+  for (int o = 16; o > 0; o >>= 1) sum += shfl_xor_d(sum, o);
+  return sum;
+}
+
+// The token decided with fp64 keys throughout (its groups, or more than 32
+// candidates, are too near to one another): lane r returns the r-th choice.
+// buf: E doubles of the warp's shared memory.
+__device__ __noinline__ int select64(const RouteArgs& a, int64_t row, int lane, float m, double* buf) {
+  const double sum = sum64(a, row, lane, m);
   const int gs = a.E / a.n_group;
+  __syncwarp();
+  for (int e = lane; e < a.E; e += 32)
+    buf[e] = score64(load_logit(a, row + e), a.route, m, sum) + (a.bias ? (double)a.bias[e] : 0.0);
+  __syncwarp();
   uint32_t kept = kAll;  // bit g: group g may be used
   if (a.n_group > 1) {
-    // lane g scores group g
-    double score = -INFINITY;
+    double score = -INFINITY;  // lane g scores group g
     if (lane < a.n_group) {
       double first = -INFINITY, second = -INFINITY;
-      for (int e = lane * gs; e < lane * gs + gs; ++e) {
-        const double key = score64(load_logit(a, row + e), a.route, m, sum) + (a.bias ? (double)a.bias[e] : 0.0);
+      for (int j = 0; j < gs; ++j) {
+        const double key = buf[lane * gs + j];
         if (key > first) second = first, first = key;
         else if (key > second) second = key;
       }
@@ -94,16 +101,14 @@ __device__ __noinline__ int select64(const RouteArgs& a, int64_t row, int lane, 
     }
     kept = __ballot_sync(kAll, lane < a.n_group && rank < a.topk_group);
   }
-  uint32_t used = 0;  // bit j: the lane's element j was chosen
+  uint32_t used = 0;  // bit j: element lane + 32 j was chosen
   int mine = 0;
   for (int r = 0; r < a.k; ++r) {
     double best = -INFINITY;
     int at = INT_MAX;
-    for (int j = 0; j < npl; ++j) {
-      const int e = e0 + j;
-      if (e >= a.E || (used >> j & 1) || !(kept >> (e / gs) & 1)) continue;
-      const float l = load_logit(a, row + e);
-      const double key = a.bias ? score64(l, a.route, m, sum) + (double)a.bias[e] : (double)l;
+    for (int j = 0, e = lane; e < a.E; ++j, e += 32) {
+      if ((used >> j & 1) || !(kept >> (e / gs) & 1)) continue;
+      const double key = a.bias ? buf[e] : (double)load_logit(a, row + e);
       if (at == INT_MAX || key > best) best = key, at = e;
     }
     for (int o = 16; o > 0; o >>= 1) {
@@ -111,8 +116,29 @@ __device__ __noinline__ int select64(const RouteArgs& a, int64_t row, int lane, 
       const int oa = __shfl_xor_sync(kAll, at, o);
       if (oa != INT_MAX && (at == INT_MAX || ob > best || (ob == best && oa < at))) best = ob, at = oa;
     }
-    if (at / npl == lane) used |= 1u << (at - e0);
+    if ((at & 31) == lane) used |= 1u << (at >> 5);
     if (lane == r) mine = at;
+  }
+  return mine;
+}
+
+// The choices among n <= 32 candidates, lane i holding candidate e (logit l),
+// by fp64 keys: one key per lane.  Lane r returns the r-th choice.
+__device__ __noinline__ int rank64(const RouteArgs& a, int64_t row, int lane, float m, int n, int e, float l) {
+  const double sum = sum64(a, row, lane, m);
+  double key = -INFINITY;
+  if (lane < n) key = score64(l, a.route, m, sum) + (double)a.bias[e];
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const double other = __shfl_sync(kAll, key, i);
+    const int oe = __shfl_sync(kAll, e, i);
+    rank += other > key || (other == key && oe < e);
+  }
+  if (lane >= n) rank = 64;
+  int mine = 0;
+  for (int i = 0; i < n; ++i) {
+    const int ri = __shfl_sync(kAll, rank, i), oe = __shfl_sync(kAll, e, i);
+    if (ri == lane) mine = oe;
   }
   return mine;
 }
@@ -127,8 +153,8 @@ __device__ __forceinline__ void top2_join(float& first, float& second, float f, 
 // VEC: npl = NP, E = 32 * NP and the rows are 16-byte aligned (wide loads).
 template <int NP, bool VEC>
 __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
-  __shared__ float s_key[4][NP * 32 + 1];  // groups that do not fall on lane boundaries
-  __shared__ int2 s_pick[4][MOE_MAX_TOPK + 1];
+  __shared__ double s_buf[4][NP * 32];  // keys: of groups that do not fall on lane boundaries (fp32); of select64
+  __shared__ int2 s_pick[4][32];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + wid;
   if (t >= a.T) return;
@@ -196,6 +222,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
 
   bool unsure = false;
   if (a.n_group > 1) {
+    float* s_key = reinterpret_cast<float*>(s_buf[wid]);
     const int gs = a.E / a.n_group, per = gs / npl;  // lanes per group, where groups are whole lanes
     const bool on_lanes = gs == per * npl && (per & (per - 1)) == 0;
     const bool add = a.group_score == MOE_GROUP_TOP2 && gs > 1;
@@ -215,12 +242,12 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     } else {
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        if (j < have) s_key[wid][e0 + j] = value(j);
+        if (j < have) s_key[e0 + j] = value(j);
       __syncwarp();
       if (lane < a.n_group) {
         int i = lane % gs;  // groups start at different elements: different banks
         for (int j = 0; j < gs; ++j) {
-          top2_join(first, second, s_key[wid][lane * gs + i], -INFINITY);
+          top2_join(first, second, s_key[lane * gs + i], -INFINITY);
           if (++i == gs) i = 0;
         }
       }
@@ -261,8 +288,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   uint32_t best = 0;
 #pragma unroll
   for (int j = 0; j < NP; ++j) best = max(best, key[j]);
-  for (int r = 0; r < rounds; ++r) {
-    const uint32_t top = __reduce_max_sync(kAll, best);
+  const auto pick = [&](int r, uint32_t top) {
     const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
     if (lane == owner) {
       int at = 0;
@@ -279,13 +305,14 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
       s_pick[wid][r] = make_int2(e0 + at, __float_as_int(lv));
     }
     __syncwarp();
-  }
+  };
+  for (int r = 0; r < rounds; ++r) pick(r, __reduce_max_sync(kAll, best));
   int mine = 0;
   float lg = 0.0f;
   if (lane < rounds) {
-    const int2 pick = s_pick[wid][lane];
-    mine = pick.x;
-    lg = __int_as_float(pick.y);
+    const int2 choice = s_pick[wid][lane];
+    mine = choice.x;
+    lg = __int_as_float(choice.y);
   }
   float p = score32(lg, a.route, st);
   if (scored) {
@@ -294,10 +321,38 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     const float v1 = __shfl_down_sync(kAll, v, 1), err1 = __shfl_down_sync(kAll, err, 1);
     const float l1 = __shfl_down_sync(kAll, lg, 1), b1 = __shfl_down_sync(kAll, b, 1);
     const bool same = lg == l1 && b == b1;
-    unsure |= __any_sync(kAll, lane + 1 < rounds && !same && v - v1 <= err + err1);
+    const bool near = __any_sync(kAll, lane + 1 < rounds && !same && v - v1 <= err + err1);
+    if (near && !unsure) {
+      // choices that fp32 cannot order: take more until one is certainly below the k-th, and rank them in fp64
+      const float vk = __shfl_sync(kAll, v, a.k - 1);
+      int n = rounds;
+      bool enough = n == avail;
+      while (!enough && n < 32) {
+        const uint32_t top = __reduce_max_sync(kAll, best);
+        if (top == 0) break;
+        const float vn = key_logit(top);
+        enough = vk - vn > kUlp * (2.0f * bound + fabsf(vk) + fabsf(vn));
+        if (!enough) pick(n++, top);
+        else break;
+      }
+      enough |= n < 32;
+      if (enough) {
+        int e = 0;
+        float le = 0.0f;
+        if (lane < n) {
+          e = s_pick[wid][lane].x;
+          le = __int_as_float(s_pick[wid][lane].y);
+        }
+        mine = rank64(a, row, lane, st.m, n, e, le);
+        if (lane < a.k) lg = load_logit(a, row + mine);
+        p = score32(lg, a.route, st);
+      } else {
+        unsure = true;
+      }
+    }
   }
   if (unsure) {
-    mine = select64(a, row, lane, st.m);
+    mine = select64(a, row, lane, st.m, s_buf[wid]);
     if (lane < a.k) lg = load_logit(a, row + mine);
     p = score32(lg, a.route, st);
   }

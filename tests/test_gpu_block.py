@@ -75,7 +75,7 @@ def check_norm(x, res, w, eps, offset, s_got, y, q, d, bs, fmt):
 
 
 @pytest.mark.parametrize("T,H", [(1, 1), (1, 2048), (3, 7), (5, 129), (37, 6144), (700, 640), (2, 16384), (400, 8192),
-                                 (1000, 33)])
+                                 (1000, 33), (1300, 2048), (1217, 12288), (1500, 5000)])
 @pytest.mark.parametrize("xt,rt", [(BF16, None), (BF16, BF16), (BF16, F32), (F16, F16), (F16, F32), (F32, F32)])
 def test_norm_types_and_sizes(T, H, xt, rt):
     x, w = rnd((T, H), 1, xt), 1 + 0.2 * rnd((H,), 2)
@@ -88,7 +88,8 @@ def test_norm_types_and_sizes(T, H, xt, rt):
 
 
 @pytest.mark.parametrize("fmt", list(FMTS))
-@pytest.mark.parametrize("T,H", [(1, 256), (3, 2048), (600, 4096), (2, 16384), (4, 1), (5, 200), (9, 1027)])
+@pytest.mark.parametrize("T,H", [(1, 256), (3, 2048), (600, 4096), (2, 16384), (4, 1), (5, 200), (9, 1027),
+                                 (1500, 2304), (1234, 10240)])
 def test_norm_codes(fmt, T, H):
     code, group, _ = FMTS[fmt]
     if fmt == "q8k" and H % 256:
@@ -204,6 +205,22 @@ def test_route_keys_closer_than_fp32():
     check_route(l, bias, 8)
     check_route(l, bias, 8, n_group=4, topk_group=2)
     check_route(l, bias, 8, n_group=4, topk_group=2, top2=False)
+
+
+@pytest.mark.parametrize("E,n_group,topk_group", [(256, 1, 1), (1024, 1, 1), (256, 8, 3), (90, 5, 2)])
+def test_route_whole_rows_closer_than_fp32(E, n_group, topk_group):
+    """Every expert's key within fp32 rounding of every other's: more candidates than fit a warp."""
+    rng = np.random.default_rng(E + n_group)
+    bias = rng.uniform(0, 0.2, E).astype(np.float32)
+    l = np.empty((6, E), np.float32)
+    for t in range(6):
+        p = 0.7 - bias.astype(np.float64) + rng.uniform(-1, 1, E) * 1e-8
+        l[t] = np.log(p / (1 - p)).astype(np.float32)
+    check_route(l, bias, 8, True, n_group, topk_group)
+    check_route(l, bias, 8, True, n_group, topk_group, top2=False)
+    # softmax: equal logits but for the last bits, and a bias that undoes what they differ by
+    l = (1.0 + rng.integers(0, 3, (6, E)) * 2.0 ** -23).astype(np.float32)
+    check_route(l, (rng.integers(0, 3, E) * 1e-10).astype(np.float32), 8, False, n_group, topk_group)
 
 
 def test_route_masked_and_special_logits():
