@@ -388,36 +388,32 @@ def moe_debug_prefill_sums(fmt, w, N, K, q, d, bsum16, S, M, ws, stream=None):
 
 # ----------------------------------------------------------------- decoder-block operators
 
-_dtypes = {}
+_ext = None
 
 
-def _dt(t, where):
-    """moe_dtype of a tensor."""
-    if not _dtypes:
-        import torch
-        _dtypes.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16})
-    code = _dtypes.get(t.dtype)
-    if code is None:
-        raise MoeError(MOE_ERR_UNSUPPORTED, f"{where}: element type {t.dtype}")
-    return code
+def _raise(status, text):
+    raise MoeError(status, text)
 
 
-def _need(ok, where, what):
-    if not ok:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{where}: {what}")
+def _binding():
+    """The native binding of these operators (csrc/binding.cpp): tensors in, checks, the C call."""
+    global _ext
+    if _ext is None:
+        import importlib.machinery
+        import importlib.util
 
-
-def _rows(t, T, H, where, what):
-    """Row stride of a [T, H] tensor whose rows are contiguous."""
-    _need(t.shape == (T, H) and (t.stride(1) == 1 or H == 1), where, f"{what} must be [{T}, {H}] with contiguous rows")
-    return t.stride(0)
-
-
-def _raw_stream(stream):
-    if stream is None:
-        import torch
-        stream = torch.cuda.current_stream()
-    return stream.cuda_stream
+        import torch  # noqa: F401  (the binding links against torch's libraries)
+        load()
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError(f"{_build.BINDING} is missing: build the CUDA library first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        loader = importlib.machinery.ExtensionFileLoader("moe_binding", _build.BINDING)
+        spec = importlib.util.spec_from_file_location("moe_binding", _build.BINDING, loader=loader)
+        ext = importlib.util.module_from_spec(spec)
+        loader.exec_module(ext)
+        ext.on_error(_raise)
+        _ext = ext
+    return _ext
 
 
 def moe_add_rmsnorm(x, weight, eps, residual=None, sum_out=None, y=None, q_fmt=NORM_Q_NONE, q=None, d=None,
@@ -425,93 +421,21 @@ def moe_add_rmsnorm(x, weight, eps, residual=None, sum_out=None, y=None, q_fmt=N
     """Residual addition and RMS norm of x [T, H] with an optional 8-bit output
     (NORM_Q_*): sum_out = x + residual, y = norm * (weight + weight_offset), q/d/bsum16 = the codes of the
     unrounded y.  See include/moe_q8k.h."""
-    w = "moe_add_rmsnorm"
-    _need(x.dim() == 2, w, "x must be [T, H]")
-    T, H = x.shape
-    xs, xt = _rows(x, T, H, w, "x"), _dt(x, w)
-    _need(weight.shape == (H,) and weight.is_contiguous(), w, "weight must be [H]")
-    rs = ss = ys = rt = yt = 0
-    if residual is not None:
-        rs, rt = _rows(residual, T, H, w, "residual"), _dt(residual, w)
-    if sum_out is not None:
-        ss = _rows(sum_out, T, H, w, "sum_out")
-        _need(_dt(sum_out, w) == (rt if residual is not None else xt), w, "sum_out must have the residual's type")
-    if y is not None:
-        ys, yt = _rows(y, T, H, w, "y"), _dt(y, w)
-    qp = dp = bp = None
-    if q_fmt != NORM_Q_NONE:
-        _need(q is not None and d is not None, w, "q_fmt needs q and d")
-        _need(q.shape == (T, H) and q.element_size() == 1 and q.is_contiguous(), w, "q must be [T, H] of 8 bits")
-        g = 256 if q_fmt == NORM_Q_Q8K else 128 if q_fmt == NORM_Q_E4M3_G128 else max(H, 1)
-        _need(d.numel() == T * -(-H // g) and d.is_contiguous() and _dt(d, w) == DT_F32, w,
-              "d must hold one fp32 scale per group")
-        qp, dp = q.data_ptr(), d.data_ptr()
-        if bsum16 is not None:
-            _need(bsum16.numel() == T * (H // 16) and bsum16.element_size() == 2 and bsum16.is_contiguous(), w,
-                  "bsum16 must be int16 [T, H/16]")
-            bp = bsum16.data_ptr()
-    _check(load().moe_add_rmsnorm(x.data_ptr(), xt, xs, None if residual is None else residual.data_ptr(), rt, rs,
-                                  weight.data_ptr(), _dt(weight, w), weight_offset, eps, T, H,
-                                  None if sum_out is None else sum_out.data_ptr(), ss,
-                                  None if y is None else y.data_ptr(), yt, ys, q_fmt, qp, dp, bp,
-                                  _raw_stream(stream)), w)
+    (_ext or _binding()).add_rmsnorm(x, weight, eps, residual, sum_out, y, q_fmt, q, d, bsum16, weight_offset, stream)
 
 
 def moe_route_grouped(logits, k, ids, gates, bias=None, route=ROUTE_SIGMOID, n_group=1, topk_group=1,
                       group_score=GROUP_TOP2, renorm=True, scale=1.0, stream=None):
     """Routes given logits [T, E] to k experts: scores, a balance bias that only takes part in the selection,
     expert groups, renormalised gates.  ids int32 [T, k], gates fp32 [T, k].  See include/moe_q8k.h."""
-    w = "moe_route_grouped"
-    _need(logits.dim() == 2, w, "logits must be [T, E]")
-    T, E = logits.shape
-    stride = _rows(logits, T, E, w, "logits")
-    _need(ids.shape == (T, k) and ids.is_contiguous() and ids.element_size() == 4, w, "ids must be int32 [T, k]")
-    _need(gates.shape == (T, k) and gates.is_contiguous() and _dt(gates, w) == DT_F32, w, "gates must be fp32 [T, k]")
-    if bias is not None:
-        _need(bias.shape == (E,) and bias.is_contiguous() and _dt(bias, w) == DT_F32, w, "bias must be fp32 [E]")
-        bias = bias.data_ptr()
-    _check(load().moe_route_grouped(logits.data_ptr(), _dt(logits, w), stride, bias, T, E, k, route, n_group,
-                                    topk_group, group_score, 1 if renorm else 0, scale, ids.data_ptr(),
-                                    gates.data_ptr(), _raw_stream(stream)), w)
-
-
-def _kv_desc(k_cache, v_cache, page_table, cu_q, kv_len, w):
-    """moe_kv_desc of caches [pages, page_size, Hkv, D] (any strides over the first three)."""
-    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype, w,
-          "caches must be [pages, page_size, Hkv, D] of one type")
-    pages, page, hkv, D = k_cache.shape
-    ks, vs = k_cache.stride(), v_cache.stride()
-    _need(ks[3] == 1 and vs[3] == 1, w, "a head's elements must be contiguous")
-    _need(page_table.dim() == 2 and page_table.stride(1) == 1 and page_table.element_size() == 4, w,
-          "page_table must be int32 [n_seqs, max_pages]")
-    n, most = page_table.shape
-    _need(cu_q.shape == (n + 1,) and cu_q.element_size() == 4 and cu_q.is_contiguous(), w,
-          "cu_q must be int32 [n_seqs + 1]")
-    _need(kv_len.shape == (n,) and kv_len.element_size() == 4 and kv_len.is_contiguous(), w,
-          "kv_len must be int32 [n_seqs]")
-    return KvDesc(n, hkv, D, _dt(k_cache, w), page, pages, most, 0, page_table.stride(0), ks[0], ks[1], ks[2], vs[0],
-                  vs[1], vs[2])
-
-
-def _heads(t, Hn, D, dtype, w, what):
-    """Token and head strides of a [T, Hn, D] tensor."""
-    _need(t.dim() == 3 and t.shape[1] == Hn and t.shape[2] == D and t.stride(2) == 1 and t.dtype == dtype, w,
-          f"{what} must be [T, {Hn}, {D}] of the cache's type")
-    return t.stride(0), t.stride(1)
+    (_ext or _binding()).route_grouped(logits, k, ids, gates, bias, route, n_group, topk_group, group_score, renorm,
+                                       scale, stream)
 
 
 def moe_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, ws, stream=None):
     """Writes new keys and values [T, Hkv, D] into the pages of a cache [pages, page_size, Hkv, D]; kv_len counts
     them already.  ws: zeroed uint8 tensor of at least 16 bytes (status word).  See include/moe_q8k.h."""
-    w = "moe_kv_append"
-    kv = _kv_desc(k_cache, v_cache, page_table, cu_q, kv_len, w)
-    ks, kh = _heads(k, kv.Hkv, kv.D, k_cache.dtype, w, "k")
-    vs, vh = _heads(v, kv.Hkv, kv.D, k_cache.dtype, w, "v")
-    T = k.shape[0]
-    _need(v.shape[0] == T, w, "k and v must have the same tokens")
-    _check(load().moe_kv_append(kv, k.data_ptr(), ks, kh, v.data_ptr(), vs, vh, k_cache.data_ptr(),
-                                v_cache.data_ptr(), page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), T,
-                                ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)), w)
+    (_ext or _binding()).kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, ws, stream)
 
 
 def moe_paged_attention_workspace_size(Hq, Hkv, D) -> int:
@@ -523,20 +447,8 @@ def moe_paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_len, scale, ou
     """Attention of new tokens q [T, Hq, D] over a paged cache that holds their keys already: causal, grouped
     heads, optional sliding window; lse fp32 [T, Hq] optional.  ws: zeroed uint8 tensor of
     moe_paged_attention_workspace_size bytes.  See include/moe_q8k.h."""
-    w = "moe_paged_attention"
-    kv = _kv_desc(k_cache, v_cache, page_table, cu_q, kv_len, w)
-    _need(q.dim() == 3, w, "q must be [T, Hq, D]")
-    T, Hq, _ = q.shape
-    qs, qh = _heads(q, Hq, kv.D, k_cache.dtype, w, "q")
-    os_, oh = _heads(out, Hq, kv.D, k_cache.dtype, w, "out")
-    _need(out.shape[0] == T, w, "out must have q's tokens")
-    if lse is not None:
-        _need(lse.shape == (T, Hq) and lse.is_contiguous() and _dt(lse, w) == DT_F32, w, "lse must be fp32 [T, Hq]")
-        lse = lse.data_ptr()
-    _check(load().moe_paged_attention(kv, q.data_ptr(), qs, qh, Hq, T, k_cache.data_ptr(), v_cache.data_ptr(),
-                                      page_table.data_ptr(), cu_q.data_ptr(), kv_len.data_ptr(), scale, window,
-                                      out.data_ptr(), os_, oh, lse, ws.data_ptr(), ws.numel() * ws.element_size(),
-                                      _raw_stream(stream)), w)
+    (_ext or _binding()).paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_len, scale, out, ws, lse, window,
+                                         stream)
 
 
 # ----------------------------------------------------------------- convenience

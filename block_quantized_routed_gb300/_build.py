@@ -1,5 +1,7 @@
 """In-tree build of the CUDA library (sm_103a) with nvcc: every .cu file in
-csrc/ is compiled in parallel, then linked into _build/libmoe_q8k.so."""
+csrc/ is compiled in parallel, then linked into _build/libmoe_q8k.so; beside
+it the host compiler builds the tensor binding (csrc/binding.cpp) against
+torch's headers into _build/moe_binding.so."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -12,6 +14,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libmoe_q8k.so")
+BINDING = os.path.join(BUILD, "moe_binding.so")
 INCLUDE = os.path.join(ROOT, "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
@@ -29,16 +32,40 @@ def _sources():
 
 
 def _deps():
-    files = _sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    files = _sources() + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".cpp"))]
     files.append(os.path.join(INCLUDE, "moe_q8k.h"))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _binding_commands(out: str):
+    """Compile and link commands of csrc/binding.cpp; the link needs LIB."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [INCLUDE, os.path.join(cuda, "include"), sysconfig.get_paths()["include"], *cpp_extension.include_paths()]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    obj = os.path.join(BUILD, "binding.o")
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
+    return ([cxx, "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+             *["-I" + i for i in inc], "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj],
+            [cxx, "-shared", "-o", out, obj, "-L" + BUILD, "-l:libmoe_q8k.so", "-L" + lib, "-lc10", "-lc10_cuda",
+             "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -59,14 +86,20 @@ def build(force: bool = False, verbose: bool = False) -> str:
             print(r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    btmp = BINDING + f".tmp{os.getpid()}"
+    bind_compile, bind_link = _binding_commands(btmp)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        bound = ex.submit(_run, bind_compile, "the compilation of csrc/binding.cpp")
         list(ex.map(compile_one, zip(srcs, objs)))
+        bound.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _run(bind_link, "the link of the binding")
+    os.replace(btmp, BINDING)
     return LIB
 
 

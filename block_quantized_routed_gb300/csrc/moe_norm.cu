@@ -23,12 +23,6 @@
 #include "moe_device.cuh"
 #include "moe_internal.h"
 
-#ifndef MOE_NORM_THREADS
-#define MOE_NORM_THREADS 1024
-#endif
-#ifndef MOE_NORM_STAGES
-#define MOE_NORM_STAGES 3
-#endif
 #ifndef MOE_NORM_NV
 #define MOE_NORM_NV 2
 #endif
@@ -73,6 +67,13 @@ template <>
 __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <>
 __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 template <typename T, bool WIDE>
 __device__ __forceinline__ void store8(T* p, int n, const float* v) {
@@ -81,10 +82,8 @@ __device__ __forceinline__ void store8(T* p, int n, const float* v) {
       *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
       *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-      T e[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) e[i] = from_f<T>(v[i]);
-      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+      *reinterpret_cast<uint4*>(p) =
+          make_uint4(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]), pack2<T>(v[4], v[5]), pack2<T>(v[6], v[7]));
     }
   } else {
 #pragma unroll
@@ -129,143 +128,136 @@ __device__ __forceinline__ float block_reduce(float v, float* buf) {
   return v;
 }
 
-// The q8_K rounding of z / d: half away from zero, clamped.  The product with
-// the reciprocal is within 2 ulp of the IEEE quotient (at most 127: 2^-16), so
-// both round alike unless it is that near a half; only there it is divided.
-__device__ __forceinline__ int q8k_code(float z, float d, float inv) {
-  float x = z * inv;
-  if (fabsf(fabsf(x - truncf(x)) - 0.5f) < 3.1e-5f) x = __fdiv_rn(z, d);
-  return (int)fminf(127.0f, fmaxf(-127.0f, roundf(x)));
+// The q8_K rounding of z / d: half away from zero, clamped.  The product x
+// with the reciprocal (1 ulp) is within 2 ulp of the IEEE quotient, which is at
+// most 127: 2^-15.  Both round alike unless they are that near a half, and away
+// from a half adding 1.5 * 2^23 rounds to the nearest, the code in the low byte.
+// Near a half, or beyond the range, it is divided and rounded as written.
+// Returns the bits of code + 1.5 * 2^23.
+constexpr float kMagic = 12582912.0f;
+__device__ __forceinline__ int q8k_bits(float z, float d, float inv) {
+  const float x = z * inv;
+  float y = x + kMagic;
+  if (!(fabsf(x - (y - kMagic)) < 0.49996f)) y = fminf(127.0f, fmaxf(-127.0f, roundf(__fdiv_rn(z, d)))) + kMagic;
+  return __float_as_int(y);
 }
 
-// Scales z (s[NV][8]) into y and the 8-bit output of one row; `peak` is the
-// thread's largest |z| (row-scaled outputs only), buf one block_reduce buffer.
-template <int NV, bool WIDE>
+__device__ __forceinline__ float rcp(float x) {  // within 1 ulp
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The 8-bit output of one row z (s[NV][8]); `peak` is the thread's largest |z|
+// (row-scaled outputs only), buf one block_reduce buffer.  FMT: the format, or
+// -1 for a.q_fmt.  The scale d is an IEEE quotient; z / d is the product with
+// d's reciprocal (2 ulp), which for int8 codes is put right near a half.
+template <int NV, bool WIDE, int FMT>
 __device__ __forceinline__ void put_codes(const NormArgs& a, int64_t row, float (&s)[NV][8], float peak, float* buf) {
   const int tid = threadIdx.x, nt = blockDim.x;
-  const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
-  const bool fp8 = a.q_fmt == MOE_NORM_Q_E4M3_G128 || a.q_fmt == MOE_NORM_Q_E4M3_ROW;
-  const float top = fp8 ? 448.0f : 127.0f;
+  const int fmt = FMT >= 0 ? FMT : a.q_fmt;
+  const bool fp8 = fmt == MOE_NORM_Q_E4M3_G128 || fmt == MOE_NORM_Q_E4M3_ROW;
+  const bool per_row = fmt == MOE_NORM_Q_E4M3_ROW || fmt == MOE_NORM_Q_INT8_ROW;
   float d = 0.0f;
   if (per_row) {
     peak = block_reduce<true>(peak, buf);
-    d = __fdiv_rn(peak, top);
+    d = fp8 ? peak * (1.0f / 448.0f) : __fdiv_rn(peak, 127.0f);
     if (tid == 0) a.d[row] = d;
   }
-  const int group = a.q_fmt == MOE_NORM_Q_Q8K ? 256 : 128;
-  const int groups = (a.H + group - 1) / group;
+  const int group = fmt == MOE_NORM_Q_Q8K ? 256 : 128;
+  uint8_t* const out = static_cast<uint8_t*>(a.q) + row * a.H;
+  float* const dout = a.d + row * ((a.H + group - 1) / group);
+  float m[NV];
+  if (!per_row) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      m[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[i] = fmaxf(m[i], fabsf(s[i][j]));
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], o));
+    if (group == 256) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], 16));
+    }
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * nt + tid) * 8, n = a.H - c;
     if (!per_row) {
-      float m = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(s[i][j]));
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (group == 256) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-      d = __fdiv_rn(m, top);
-      if (n > 0 && c % group == 0) a.d[row * groups + c / group] = d;
+      d = fp8 ? m[i] * (1.0f / 448.0f) : __fdiv_rn(m[i], 127.0f);
+      if (n > 0 && c % group == 0) dout[c / group] = d;
     }
     // d = 0 only where every z of the group is 0 (or too small for its quotient to exist).  A reciprocal beyond
-    // fp32 (d below 2^-127) is not used: such groups are divided.
-    float inv = d > 0.0f ? 1.0f / d : 0.0f, dq = d;
-    if (inv > 3e38f) {
+    // fp32 (d below 2^-126) is not used: such groups are divided.
+    float inv = d > 0.0f ? rcp(d) : 0.0f, dq = d;
+    if (d < 1.2e-38f && d > 0.0f) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[i][j] = __fdiv_rn(s[i][j], d);
       inv = dq = 1.0f;
     }
-    uint8_t q[8];
+    uint32_t lo, hi;
     int sum = 0;
     if (fp8) {
+      uint32_t h[4];
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        *reinterpret_cast<__nv_fp8x2_storage_t*>(q + j) = __nv_cvt_float2_to_fp8x2(
-            make_float2(s[i][j] * inv, s[i][j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-      }
+      for (int j = 0; j < 8; j += 2)
+        h[j / 2] = __nv_cvt_float2_to_fp8x2(make_float2(s[i][j] * inv, s[i][j + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+      lo = h[0] | h[1] << 16;
+      hi = h[2] | h[3] << 16;
     } else {
+      int code[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int code = q8k_code(s[i][j], dq, inv);
-        q[j] = (uint8_t)(int8_t)code;
-        sum += code;
+        code[j] = q8k_bits(s[i][j], dq, inv);
+        sum += code[j];
       }
+      sum -= 8 * __float_as_int(kMagic);
+      lo = __byte_perm(__byte_perm(code[0], code[1], 0x0040), __byte_perm(code[2], code[3], 0x0040), 0x5410);
+      hi = __byte_perm(__byte_perm(code[4], code[5], 0x0040), __byte_perm(code[6], code[7], 0x0040), 0x5410);
     }
-    uint8_t* out = static_cast<uint8_t*>(a.q) + row * a.H + c;
     if constexpr (WIDE) {
-      if (n > 0) *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(q);
+      if (n > 0) *reinterpret_cast<uint2*>(out + c) = make_uint2(lo, hi);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (j < n) out[j] = q[j];
+        if (j < n) out[c + j] = (uint8_t)((j < 4 ? lo : hi) >> 8 * (j & 3));
     }
-    if (a.bsum16) {  // q8_K: two lanes hold the 16 codes
+    if (fmt == MOE_NORM_Q_Q8K && a.bsum16) {  // two lanes hold the 16 codes
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       if (n > 0 && (tid & 1) == 0) a.bsum16[row * (a.H / 16) + c / 16] = (int16_t)sum;
     }
   }
 }
 
-template <typename XT, typename RT, int NV, bool WIDE>
-__global__ void __launch_bounds__(1024) add_rmsnorm_kernel(const NormArgs a) {
-  __shared__ float buf[2][32];
-  const int64_t row = blockIdx.x;
-  const int tid = threadIdx.x, nt = blockDim.x;
-  const XT* x = static_cast<const XT*>(a.x) + row * a.x_stride;
-  const RT* res = static_cast<const RT*>(a.residual) + row * a.r_stride;
-  float s[NV][8];
-  float sq = 0.0f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + tid) * 8, n = a.H - c;
-    if (n > 0) {
-      load8<XT, WIDE>(x + c, n, s[i]);
-      if (a.residual) {
-        float r[8];
-        load8<RT, WIDE>(res + c, n, r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[i][j] += r[j];
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + tid) * 8, n = a.H - c;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
-    if (a.sum_out && n > 0) store8<RT, WIDE>(static_cast<RT*>(a.sum_out) + row * a.sum_stride + c, n, s[i]);
-  }
-  sq = block_reduce<false>(sq, buf[0]);
-  const float r = 1.0f / sqrtf(sq / (float)a.H + a.eps);
-  const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
-  float peak = 0.0f;  // of the row, for the row-scaled outputs
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + tid) * 8, n = a.H - c;
-    float w[8];
-    if (n > 0) {
-      load8_dt<WIDE>(a.w, a.w_dtype, c, n, w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] = s[i][j] * r * (w[j] + a.w_offset);
-      if (a.y) store8_dt<WIDE>(a.y, a.y_dtype, row * a.y_stride + c, n, s[i]);
-    }
-    if (per_row) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
-    }
-  }
-  if (a.q_fmt == MOE_NORM_Q_NONE) return;
-  put_codes<NV, WIDE>(a, row, s, peak, buf[1]);
+// two fp32 operations in one instruction (each rounded as the scalar one)
+__device__ __forceinline__ uint64_t bits2(float2 v) {
+  return (uint64_t)__float_as_uint(v.x) | (uint64_t)__float_as_uint(v.y) << 32;
+}
+__device__ __forceinline__ float2 unbits2(uint64_t v) {
+  return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+  return unbits2(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(a)), "l"(bits2(b)));
+  return unbits2(d);
+}
+__device__ __forceinline__ void add2(float* a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits2(make_float2(a[0], a[1]))), "l"(bits2(b)));
+  const float2 r = unbits2(d);
+  a[0] = r.x;
+  a[1] = r.y;
 }
 
-// The same for many rows: a CTA stays on its SM and walks the rows.  The
-// weights are kept in registers; the rows ahead come by asynchronous copies
-// into shared memory, where each thread reads back only what it asked for
-// itself (no barrier), so the loads of the next rows are under way through
-// both reductions of this one.
 template <typename T>
 __device__ __forceinline__ void unpack8(const uint4* v, float* f) {
   if constexpr (sizeof(T) == 4) {
@@ -287,138 +279,129 @@ __device__ __forceinline__ void unpack8(const uint4* v, float* f) {
     }
   }
 }
-template <typename T>
-__device__ __forceinline__ void copy8(uint4* dst, const T* src) {
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst + i)),
-                 "l"(reinterpret_cast<const uint4*>(src) + i)
-                 : "memory");
-}
-
-template <typename XT, typename RT>
-constexpr int row_vec_bytes() { return 8 * (int)(sizeof(XT) + sizeof(RT)); }  // x and residual of one vector
-
-template <typename XT, typename RT, int NV, int STAGES>
-__global__ void __launch_bounds__(512, NV > 2 ? 1 : 2) add_rmsnorm_rows_kernel(const NormArgs a) {
-  __shared__ float buf[2][2][32];
-  extern __shared__ uint4 ring[];  // [stage][vector][x | residual][thread]
-  constexpr int kX = sizeof(XT) / 2, kR = sizeof(RT) / 2;
+// FMT: the 8-bit format, or -1 for a.q_fmt (rows that are not WIDE)
+template <typename XT, typename RT, int NV, bool WIDE, int FMT>
+__global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 2 ? 2 : 1) add_rmsnorm_kernel(const NormArgs a) {
+  __shared__ float buf[2][32];
+  const int64_t row = blockIdx.x;
   const int tid = threadIdx.x, nt = blockDim.x;
-  const bool per_row = a.q_fmt == MOE_NORM_Q_E4M3_ROW || a.q_fmt == MOE_NORM_Q_INT8_ROW;
-  const bool res = a.residual != nullptr;
-  const auto slot = [&](int stage, int i) { return ring + ((size_t)(stage * NV + i) * nt + tid) * (kX + kR); };
-  const auto fetch = [&](int64_t r, int stage) {
-    if (r < a.T) {
+  const int fmt = FMT >= 0 ? FMT : a.q_fmt;
+  const bool per_row = fmt == MOE_NORM_Q_E4M3_ROW || fmt == MOE_NORM_Q_INT8_ROW;
+  const XT* x = static_cast<const XT*>(a.x) + row * a.x_stride;
+  const RT* res = static_cast<const RT*>(a.residual) + row * a.r_stride;
+  RT* sum = static_cast<RT*>(a.sum_out) + row * a.sum_stride;
+  float s[NV][8];
+  float2 sq2 = make_float2(0.f, 0.f);
+  if constexpr (WIDE) {
+    // every load of the row is under way before the first is used
+    constexpr int kX = sizeof(XT) / 2, kR = sizeof(RT) / 2;
+    uint4 rx[NV][kX], rr[NV][kR];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * nt + tid) * 8;
+#pragma unroll
+      for (int k = 0; k < kX; ++k)
+        rx[i][k] = c < a.H ? reinterpret_cast<const uint4*>(x + c)[k] : make_uint4(0, 0, 0, 0);
+    }
+    if (a.residual) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * nt + tid) * 8;
-        if (c < a.H) {
-          copy8<XT>(slot(stage, i), static_cast<const XT*>(a.x) + r * a.x_stride + c);
-          if (res) copy8<RT>(slot(stage, i) + kX, static_cast<const RT*>(a.residual) + r * a.r_stride + c);
-        }
+#pragma unroll
+        for (int k = 0; k < kR; ++k)
+          rr[i][k] = c < a.H ? reinterpret_cast<const uint4*>(res + c)[k] : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float r[8];
+        unpack8<XT>(rx[i], s[i]);
+        unpack8<RT>(rr[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) add2(s[i] + j, make_float2(r[j], r[j + 1]));
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) unpack8<XT>(rx[i], s[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * nt + tid) * 8, n = a.H - c;
+      load8<XT, false>(x + c, n, s[i]);
+      if (a.residual) {
+        float r[8];
+        load8<RT, false>(res + c, n, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] += r[j];
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-  int64_t row = blockIdx.x;
-#pragma unroll
-  for (int k = 0; k < STAGES - 1; ++k) fetch(row + (int64_t)k * gridDim.x, k);
-  float w[NV][8];
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * nt + tid) * 8;
-    if (c < a.H) {
-      load8_dt<true>(a.w, a.w_dtype, c, 8, w[i]);
+    const int c = (i * nt + tid) * 8, n = a.H - c;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[i][j] += a.w_offset;
+    for (int j = 0; j < 8; j += 2)
+      sq2 = fma2(make_float2(s[i][j], s[i][j + 1]), make_float2(s[i][j], s[i][j + 1]), sq2);
+    if (a.sum_out && n > 0) store8<RT, WIDE>(sum + c, n, s[i]);
+  }
+  const float sq = block_reduce<false>(sq2.x + sq2.y, buf[0]);
+  const float r = rsqrtf(fmaf(sq, 1.0f / (float)a.H, a.eps));
+  float peak = 0.0f;  // of the row, for the row-scaled outputs
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * nt + tid) * 8, n = a.H - c;
+    if (n > 0) {
+      float w[8];
+      load8_dt<WIDE>(a.w, a.w_dtype, c, n, w);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const float2 z = mul2(mul2(make_float2(s[i][j], s[i][j + 1]), make_float2(r, r)),
+                              make_float2(w[j] + a.w_offset, w[j + 1] + a.w_offset));
+        s[i][j] = z.x;
+        s[i][j + 1] = z.y;
+      }
+      if (a.y) store8_dt<WIDE>(a.y, a.y_dtype, row * a.y_stride + c, n, s[i]);
+    }
+    if (per_row) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
     }
   }
-  int stage = 0;
-  for (int odd = 0; row < a.T; row += gridDim.x, odd ^= 1) {
-    fetch(row + (int64_t)(STAGES - 1) * gridDim.x, stage == 0 ? STAGES - 1 : stage - 1);
-    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
-    float s[NV][8];
-    float sq = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * nt + tid) * 8;
-      if (c < a.H) {
-        unpack8<XT>(slot(stage, i), s[i]);
-        if (res) {
-          float r[8];
-          unpack8<RT>(slot(stage, i) + kX, r);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s[i][j] += r[j];
-        }
-        if (a.sum_out) store8<RT, true>(static_cast<RT*>(a.sum_out) + row * a.sum_stride + c, 8, s[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sq = fmaf(s[i][j], s[i][j], sq);
-    }
-    stage = stage == STAGES - 1 ? 0 : stage + 1;
-    sq = block_reduce<false>(sq, buf[odd][0]);
-    const float r = 1.0f / sqrtf(sq / (float)a.H + a.eps);
-    float peak = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * nt + tid) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] = c < a.H ? s[i][j] * r * w[i][j] : 0.0f;
-      if (a.y && c < a.H) store8_dt<true>(a.y, a.y_dtype, row * a.y_stride + c, 8, s[i]);
-      if (per_row) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) peak = fmaxf(peak, fabsf(s[i][j]));
-      }
-    }
-    if (a.q_fmt != MOE_NORM_Q_NONE) put_codes<NV, true>(a, row, s, peak, buf[odd][1]);
-  }
+  if (fmt != MOE_NORM_Q_NONE) put_codes<NV, WIDE, FMT>(a, row, s, peak, buf[1]);
 }
 
-template <typename XT, typename RT, int NV>
-cudaError_t launch_rows(const NormArgs& a, cudaStream_t s) {
-  constexpr int kStages = MOE_NORM_STAGES;
-  const int vecs = a.H / 8, threads = ((vecs + NV - 1) / NV + 31) / 32 * 32;
-  const int smem = kStages * NV * threads * row_vec_bytes<XT, RT>();
-  auto kern = add_rmsnorm_rows_kernel<XT, RT, NV, kStages>;
-  static bool opted = false;
-  if (!opted) {
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    if (err != cudaSuccess) return err;
-    opted = true;
+template <typename XT, typename RT, int NV, bool WIDE>
+void launch_fmt(const NormArgs& a, int threads, cudaStream_t s) {
+  const dim3 grid((unsigned)a.T);
+  if constexpr (WIDE) {
+    switch (a.q_fmt) {
+      case MOE_NORM_Q_NONE: add_rmsnorm_kernel<XT, RT, NV, true, MOE_NORM_Q_NONE><<<grid, threads, 0, s>>>(a); break;
+      case MOE_NORM_Q_Q8K: add_rmsnorm_kernel<XT, RT, NV, true, MOE_NORM_Q_Q8K><<<grid, threads, 0, s>>>(a); break;
+      case MOE_NORM_Q_E4M3_G128:
+        add_rmsnorm_kernel<XT, RT, NV, true, MOE_NORM_Q_E4M3_G128><<<grid, threads, 0, s>>>(a);
+        break;
+      case MOE_NORM_Q_E4M3_ROW:
+        add_rmsnorm_kernel<XT, RT, NV, true, MOE_NORM_Q_E4M3_ROW><<<grid, threads, 0, s>>>(a);
+        break;
+      default: add_rmsnorm_kernel<XT, RT, NV, true, MOE_NORM_Q_INT8_ROW><<<grid, threads, 0, s>>>(a);
+    }
+  } else {
+    add_rmsnorm_kernel<XT, RT, NV, false, -1><<<grid, threads, 0, s>>>(a);
   }
-  const int per_sm = std::max(1, std::min(MOE_NORM_THREADS / threads, 220 * 1024 / (smem + 2048)));
-  const unsigned grid = (unsigned)std::min<int64_t>(a.T, (int64_t)num_sms() * per_sm);
-  note_launch();
-  kern<<<grid, threads, smem, s>>>(a);
-  return cudaGetLastError();
 }
 
 template <typename XT, typename RT, bool WIDE>
 cudaError_t launch_nv(const NormArgs& a, cudaStream_t s) {
   const int vecs = (a.H + 7) / 8;
-  if constexpr (WIDE) {
-    // rows of up to 64 KB in, three of which fit an SM's shared memory
-    if (a.T >= 8 * num_sms() && a.H / 8 * row_vec_bytes<XT, RT>() <= 64 * 1024)
-      return vecs <= 1024 ? launch_rows<XT, RT, MOE_NORM_NV>(a, s) : launch_rows<XT, RT, 4>(a, s);
-  }
-  // Few rows: latency counts, one vector per thread.  Many rows: two to eight
-  // vectors per thread, so that a CTA is small and its loads are in flight together.
-  int nv = 1;
-  if (a.T > 2 * num_sms())
-    while (nv < 4 && vecs > 128 * nv) nv *= 2;
-  while (nv < 8 && vecs > 1024 * nv) nv *= 2;
+  // Few rows: latency counts, one vector per thread.  Many rows: two, so that a CTA's loads are larger and its two
+  // reductions are shared by more columns.  Rows of more than 8192 columns: four.
+  int nv = a.T > 2 * num_sms() ? MOE_NORM_NV : 1;
+  while (nv < 4 && vecs > (nv == 1 ? 1024 : 512) * nv) nv *= 2;
   const int threads = ((vecs + nv - 1) / nv + 31) / 32 * 32;
   note_launch();
-  const dim3 grid((unsigned)a.T);
-  switch (nv) {
-    case 1: add_rmsnorm_kernel<XT, RT, 1, WIDE><<<grid, threads, 0, s>>>(a); break;
-    case 2: add_rmsnorm_kernel<XT, RT, 2, WIDE><<<grid, threads, 0, s>>>(a); break;
-    default: add_rmsnorm_kernel<XT, RT, 4, WIDE><<<grid, threads, 0, s>>>(a); break;
-  }
+  if (nv == 1) launch_fmt<XT, RT, 1, WIDE>(a, threads, s);
+  else if (nv == 2) launch_fmt<XT, RT, 2, WIDE>(a, threads, s);
+  else launch_fmt<XT, RT, 4, WIDE>(a, threads, s);
   return cudaGetLastError();
 }
 
