@@ -59,6 +59,13 @@ constexpr int kMaxCtas = 160;                    // the workspace holds the part
 constexpr size_t kWsHead = 1024;                 // status (16 bytes), a counter per CTA
 static_assert(kWsHead >= 16 + 4 * kMaxCtas, "counters");
 constexpr int kColMajor = 32;                    // parts of which each CTA joins at least so many rows lie column by column
+// Units of work: a key tile counts 1, an item kItemUnits more (loading its
+// queries, filling the pipeline, writing its rows).  With 0, 2 and 4 units an
+// 8192-token prompt (32 heads over 4, 128 wide) took 549, 422 and 402 us, 48
+// decoded tokens over up to 8192 keys 82, 77 and 78 us.  (Fewer CTAs of 2 or 4
+// units at least, where the work does not fill the SMs, were slower: one token
+// over 777 keys 12 us, 14 and 19.)
+constexpr int kItemUnits = 3;
 constexpr float kGrow = 8.0f;                    // log2 of the growth that forces a rescale
 
 template <int D_>
@@ -225,7 +232,8 @@ struct Item {
   int r0, rows;      // first row, rows (1 .. kRows)
   int lo, hi;        // keys that some row sees
   int t0, tiles;     // first key tile, number of key tiles
-  __device__ __forceinline__ int cost() const { return max(1, tiles); }
+  __device__ __forceinline__ int payload() const { return max(1, tiles); }  // an item without keys still writes its rows
+  __device__ __forceinline__ int cost() const { return kItemUnits + payload(); }
 };
 
 template <int kN, int kRows>
@@ -291,7 +299,20 @@ __device__ __forceinline__ void walk_next(const AttnArgs& a, int G, Walk& w, int
   }
   item_range<kN, kRows>(a, G, w.it);
 }
-__device__ __forceinline__ int walk_len(const Walk& w) { return (int)min((long long)(w.it.cost() - w.off), w.left); }
+// What of the current item is this CTA's: `len` units, of which the payload
+// [first, last) (none: the CTA's boundary fell into the item's overhead, and
+// the item is the next CTA's), `tiles` key tiles of it.
+struct Seg {
+  int len, first, last, tiles;
+};
+__device__ __forceinline__ Seg walk_seg(const Walk& w) {
+  Seg s;
+  s.len = (int)min((long long)(w.it.cost() - w.off), w.left);
+  s.first = max(w.off - kItemUnits, 0);
+  s.last = max(w.off + s.len - kItemUnits, 0);
+  s.tiles = w.it.tiles ? s.last - s.first : 0;
+  return s;
+}
 
 // units before CTA c of n
 __device__ __forceinline__ long long share(long long total, int n, int c) { return total * c / n; }
@@ -701,13 +722,13 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       uint32_t n_ops = 0;
       bool ok = true;
       for (Walk w = walk_begin(st); w.left > 0 && ok;) {
-        const int len = walk_len(w);
-        const int m = w.it.tiles ? len : 0;
+        const Seg sg = walk_seg(w);
+        const int m = sg.tiles;
         const bool two = kGroups == 2 && w.it.rows > 128;
         const int32_t* table = a.table + (int64_t)w.it.b * a.kv.table_stride;
         for (int o = 0; o < 2 * m; ++o) {
           bool value;
-          const int tile = w.it.t0 + w.off + ring_op(o, m, two, value);
+          const int tile = w.it.t0 + sg.first + ring_op(o, m, two, value);
           const int k0 = tile * kN, from = max(w.it.lo, k0), to = min(w.it.hi, k0 + kN);
           // boxes of the tile that hold a visible key
           const int b0 = (from - k0) / box_rows, b1 = (to - k0 + box_rows - 1) / box_rows;
@@ -733,7 +754,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
                    part * 64, (k0 + box * box_rows) % ps, w.it.h, page, full(slot));
           ++n_ops;
         }
-        walk_next<kN, kRows>(a, G, w, len);
+        walk_next<kN, kRows>(a, G, w, sg.len);
       }
       if (!ok && lane == 0) {  // given up: the copies in flight still land before the CTA ends
         for (uint32_t o = n_ops > (uint32_t)kStages ? n_ops - kStages : 0; o < n_ops; ++o) {
@@ -760,8 +781,8 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           if (++slot == kStages) slot = 0, phase ^= 1;
         };
         for (Walk w = walk_begin(st); w.left > 0;) {
-          const int len = walk_len(w);
-          const int m = w.it.tiles ? len : 0;
+          const Seg sg = walk_seg(w);
+          const int m = sg.tiles;
           const bool two = kGroups == 2 && w.it.rows > 128;
           const int U = two ? 2 * m : m;
           const auto scores = [&](int u) {  // S(u) = Q K^T
@@ -792,7 +813,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
               take(v_slot);
               if (tile == m - 1) {
                 // Values past the sequence's last key: whatever the page holds there, even NaN, must not reach a sum.
-                const int k0 = (w.it.t0 + w.off + tile) * kN, to = min(w.it.hi, k0 + kN) - k0;
+                const int k0 = (w.it.t0 + sg.first + tile) * kN, to = min(w.it.hi, k0 + kN) - k0;
                 const int end = (to + 15) / 16 * 16;
                 for (int row = max(0, w.it.s.kv - k0); row < end; ++row) {
                   uint8_t* line = smem + C::kSmemRing + v_slot * C::kSlot + row * 128;
@@ -804,7 +825,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
               }
             }
             if (tile == 0 || tile == m - 1) {
-              const int k0 = (w.it.t0 + w.off + tile) * kN;
+              const int k0 = (w.it.t0 + sg.first + tile) * kN;
               x0 = (max(w.it.lo, k0) - k0) / 16;
               x1 = (min(w.it.hi, k0 + kN) - k0 + 15) / 16;
             }
@@ -825,7 +846,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
             if (u + 2 < U) scores(u + 2);
           }
           if (kGroups == 2 && U > 0 && !two) q_tile ^= 1;
-          walk_next<kN, kRows>(a, G, w, len);
+          walk_next<kN, kRows>(a, G, w, sg.len);
         }
         if (st.abort) {  // given up: the products in flight end before tensor memory is freed
           mma_commit(drain);
@@ -844,8 +865,8 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       constexpr int kChunks = D / 8, kStep = 64 / kChunks;
       const int ch = t % kChunks;
       for (Walk w = walk_begin(st); w.left > 0;) {
-        const int len = walk_len(w);
-        if (w.it.tiles) {
+        const Seg sg = walk_seg(w);
+        if (sg.tiles) {
           const bool two = kGroups == 2 && w.it.rows > 128;
           const uint16_t* q = static_cast<const uint16_t*>(a.q) + (int64_t)w.it.s.q0 * a.q_stride +
                               (int64_t)w.it.h * G * a.q_head_stride + ch * 8;
@@ -871,7 +892,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           }
           if (kGroups == 2 && !two) q_tile ^= 1;
         }
-        walk_next<kN, kRows>(a, G, w, len);
+        walk_next<kN, kRows>(a, G, w, sg.len);
       }
     }
   } else {
@@ -888,8 +909,13 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     unsigned* const counters = reinterpret_cast<unsigned*>(a.ws + 16);
     long long g_seg = st.first;  // unit at which the segment starts
     for (Walk w = walk_begin(st); w.left > 0;) {
-      const int len = walk_len(w);
-      const int m = w.it.tiles ? len : 0;
+      const Seg sg = walk_seg(w);
+      if (sg.first == sg.last) {
+        g_seg += sg.len;
+        walk_next<kN, kRows>(a, G, w, sg.len);
+        continue;
+      }
+      const int m = sg.tiles;
       const bool two = kGroups == 2 && w.it.rows > 128;
       const int U = two ? 2 * m : m;
       const int row = (two ? grp * 128 : 0) + r;  // row of the item
@@ -912,7 +938,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
 #pragma unroll
           for (int x = 0; x < kN / 32; ++x) tmem_ld32(s_addr + 32 * x, s + 32 * x);
           wait_ld();
-          const int k0 = (w.it.t0 + w.off + (two ? u >> 1 : u)) * kN;
+          const int k0 = (w.it.t0 + sg.first + (two ? u >> 1 : u)) * kN;
           if (__any_sync(kAll, valid && (hi < k0 + kN || lo > k0))) {
             const int j1 = hi - k0, j0 = lo - k0;
 #pragma unroll
@@ -974,7 +1000,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       }
 
       // ---- the segment's result
-      const bool whole = w.off == 0 && len == w.it.cost();
+      const bool whole = sg.first == 0 && sg.last == w.it.payload();
       const bool join = kGroups == 2 && !two && U > 1;  // two groups hold sums of the same rows
       if (acc) {
         const int lb = kGroups == 2 ? grp : (U - 1) & 1;
@@ -1009,7 +1035,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       }
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
       // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
-      const int c0 = whole ? 0 : owner(st.total, st.ctas, g_item);
+      const int c0 = whole ? 0 : owner(st.total, st.ctas, g_item + kItemUnits);
       const int parts = whole ? 1 : owner(st.total, st.ctas, g_item + w.it.cost() - 1) - c0 + 1;
       const bool by_col = w.it.rows > (kColMajor - 1) * parts;
       const uint32_t other_addr = lanes + C::kColO + (grp ^ 1) * D;
@@ -1073,7 +1099,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           Cut& cut = st.cut[st.n_cut++];
           cut.c0 = c0;
           cut.parts = parts;
-          cut.slot0 = share(st.total, st.ctas, c0) == g_item ? 0 : 1;
+          cut.slot0 = share(st.total, st.ctas, c0) >= g_item ? 0 : 1;
           cut.rows = w.it.rows;
           cut.r0 = w.it.r0;
           cut.q0 = w.it.s.q0;
@@ -1084,8 +1110,8 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       if (kGroups == 2 && (join || !whole)) named_sync(1, 256);
       else if (!whole) named_sync(2, 128);
       if (!whole && tid == 0) count_up(counters + c0, parts * 2 - 1);
-      g_seg += len;
-      walk_next<kN, kRows>(a, G, w, len);
+      g_seg += sg.len;
+      walk_next<kN, kRows>(a, G, w, sg.len);
     }
     named_sync(4, kJoin);
     for (int x = 0; x < st.n_cut; ++x) join_parts<D, BF16>(a, G, st, st.cut[x], part0, counters, smem + C::kSmemRing);

@@ -13,10 +13,12 @@
 // which are compared exactly.  A gap of exactly equal inputs (same logit, same
 // bias) is a tie in any precision and goes to the lower index.
 //
-// Error bound of a key p + b, in units of 2^-24: expf is within 2 ulp, so the
-// sigmoid (one addition, one division) is within 6 p; the softmax adds the
-// rounding of l - m (|l - m| p, below 104 p for any p that fp32 can hold) and
-// the sum's (one rounding per element of a lane and per shuffle).
+// Error bound of a key p + b, in units of 2^-24.  exp32 is within 4 (2 ulp) and
+// 1.5 |x| (its argument is scaled and rounded).  Sigmoid: the error of e^-l
+// reaches p times 1 - p, and p (1 - p) |l| < 0.3, so with the addition and the
+// reciprocal 8 p + 1 covers it.  Softmax: |l - m| stays below 88 where p is not
+// 0, and the sum adds one rounding per element of a lane and per shuffle:
+// (npl + 136) p covers it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -37,19 +39,32 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t at) {
   return v != v ? -INFINITY : v;
 }
 
-__device__ __forceinline__ uint32_t order_key(float v) {  // as logit_key; never 0, which marks a taken entry
-  return logit_key(v);
+// as logit_key, for a v that is no NaN: larger v, larger key; never 0, which marks a taken entry
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);  // -0 and +0 are the same logit
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 
 // softmax statistics of a token; sigmoid uses neither
 struct Stats {
-  float m, sum;
+  float m, inv_sum;
 };
 
+__device__ __forceinline__ float exp32(float x) {  // 2 ulp, and the rounding of the argument: |x| ulp
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504088896341f));
+  return y;
+}
+__device__ __forceinline__ float rcp32(float x) {  // 1 ulp; 0 at infinity
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// sigmoid: m and inv_sum unused; softmax: the row's maximum and the reciprocal of its sum
 __device__ __forceinline__ float score32(float l, int route, Stats st) {
-  if (route == MOE_ROUTE_SIGMOID) return 1.0f / (1.0f + expf(-l));
+  if (route == MOE_ROUTE_SIGMOID) return rcp32(1.0f + exp32(-l));
   if (st.m == -INFINITY) return 0.0f;
-  return (l == st.m ? 1.0f : expf(l - st.m)) / st.sum;
+  return (l == st.m ? 1.0f : exp32(l - st.m)) * st.inv_sum;
 }
 
 __device__ __forceinline__ double score64(float l, int route, float m, double sum) {
@@ -149,6 +164,11 @@ __device__ __forceinline__ void top2_join(float& first, float& second, float f, 
   first = fmaxf(first, f);
 }
 
+__device__ __forceinline__ void top2_add(float& first, float& second, float v) {
+  second = fmaxf(second, fminf(first, v));
+  first = fmaxf(first, v);
+}
+
 // NP >= ceil(E / 32): elements per lane; lane i holds elements i * npl on.
 // VEC: npl = NP, E = 32 * NP and the rows are 16-byte aligned (wide loads).
 template <int NP, bool VEC>
@@ -192,7 +212,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     for (int j = 0; j < NP; ++j) l[j] = j < have ? load_logit(a, row + e0 + j) : -INFINITY;
   }
 
-  Stats st{0.0f, 1.0f};
+  Stats st{0.0f, 1.0f};  // of the softmax
   if (a.route == MOE_ROUTE_SOFTMAX) {
     float m = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -201,13 +221,13 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
     if (m != -INFINITY) {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) sum += l[j] == m ? 1.0f : expf(l[j] - m);
+      for (int j = 0; j < NP; ++j) sum += l[j] == m ? 1.0f : exp32(l[j] - m);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    st = Stats{m, sum};
+    st = Stats{m, 1.0f / sum};
   }
-  const float bound = a.route == MOE_ROUTE_SIGMOID ? 6.0f : (float)(npl + 130);
+  const float bound = a.route == MOE_ROUTE_SIGMOID ? 8.0f : (float)(npl + 136);
 
   // ordering keys: p + b with a bias, the logits themselves without; a group's
   // score takes p (+ b) where it adds two keys
@@ -231,7 +251,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     if (on_lanes) {
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        if (j < have) top2_join(first, second, value(j), -INFINITY);
+        if (j < have) top2_add(first, second, value(j));
       for (int o = 1; o < per; o <<= 1) {
         const float f = __shfl_xor_sync(kAll, first, o), s2 = __shfl_xor_sync(kAll, second, o);
         top2_join(first, second, f, s2);
@@ -247,7 +267,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
       if (lane < a.n_group) {
         int i = lane % gs;  // groups start at different elements: different banks
         for (int j = 0; j < gs; ++j) {
-          top2_join(first, second, s_key[lane * gs + i], -INFINITY);
+          top2_add(first, second, s_key[lane * gs + i]);
           if (++i == gs) i = 0;
         }
       }
@@ -257,7 +277,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
       score = add ? first + second : first;
       // each key within (bound * p + |key|) ulp, p <= 1; without a bias a single logit is exact
       if (scored || add)
-        err = kUlp * (fabsf(score) + fabsf(first) + (add ? fabsf(second) : 0.0f) + (add ? 2.0f : 1.0f) * bound);
+        err = kUlp * (fabsf(score) + fabsf(first) + (add ? fabsf(second) : 0.0f) + (add ? 2.0f : 1.0f) * (bound + 1.0f));
     }
     int rank = 0;
     for (int g = 0; g < a.n_group; ++g) {
@@ -291,22 +311,22 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   const auto pick = [&](int r, uint32_t top) {
     const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
     if (lane == owner) {
-      int at = 0;
+      int at = -1;
       float lv = 0.0f;
       best = 0;
 #pragma unroll
-      for (int j = NP - 1; j >= 0; --j)  // ends with the lowest index
-        if (key[j] == top) at = j, lv = l[j];
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        if (j == at) key[j] = 0u;
+      for (int j = 0; j < NP; ++j) {  // the lowest index of equals
+        const bool hit = key[j] == top && at < 0;
+        at = hit ? j : at;
+        lv = hit ? l[j] : lv;
+        key[j] = hit ? 0u : key[j];
         best = max(best, key[j]);
       }
       s_pick[wid][r] = make_int2(e0 + at, __float_as_int(lv));
     }
-    __syncwarp();
   };
   for (int r = 0; r < rounds; ++r) pick(r, __reduce_max_sync(kAll, best));
+  __syncwarp();
   int mine = 0;
   float lg = 0.0f;
   if (lane < rounds) {
@@ -317,7 +337,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   float p = score32(lg, a.route, st);
   if (scored) {
     const float b = lane < rounds ? __ldg(a.bias + mine) : 0.0f, v = p + b;
-    const float err = kUlp * (bound * p + fabsf(v));
+    const float err = kUlp * (bound * p + 1.0f + fabsf(v));
     const float v1 = __shfl_down_sync(kAll, v, 1), err1 = __shfl_down_sync(kAll, err, 1);
     const float l1 = __shfl_down_sync(kAll, lg, 1), b1 = __shfl_down_sync(kAll, b, 1);
     const bool same = lg == l1 && b == b1;
@@ -331,10 +351,11 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
         const uint32_t top = __reduce_max_sync(kAll, best);
         if (top == 0) break;
         const float vn = key_logit(top);
-        enough = vk - vn > kUlp * (2.0f * bound + fabsf(vk) + fabsf(vn));
+        enough = vk - vn > kUlp * (2.0f * bound + 2.0f + fabsf(vk) + fabsf(vn));
         if (!enough) pick(n++, top);
         else break;
       }
+      __syncwarp();
       enough |= n < 32;
       if (enough) {
         int e = 0;
