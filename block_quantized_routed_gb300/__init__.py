@@ -30,7 +30,7 @@ __all__ = [
     "ws_view", "moe_debug_prefill_sums", "moe_debug_prefill_sums_workspace_size", "moe_prefill_tile_tokens",
     "NORM_Q_NONE", "NORM_Q_Q8K", "NORM_Q_E4M3_G128", "NORM_Q_E4M3_ROW", "NORM_Q_INT8_ROW", "GROUP_MAX", "GROUP_TOP2",
     "KvDesc", "moe_add_rmsnorm", "moe_route_grouped", "moe_kv_append", "moe_paged_attention",
-    "moe_paged_attention_workspace_size",
+    "moe_paged_attention_workspace_size", "MoeDecoderBlock",
 ]
 
 FMT_Q4K = 0
@@ -507,3 +507,6 @@ class MoeLayer:
             n *= s
         itemsize = torch.empty((), dtype=dtype).element_size()
         return ws[off:off + n * itemsize].view(dtype).view(*shape)
+
+
+from .block import MoeDecoderBlock  # noqa: E402

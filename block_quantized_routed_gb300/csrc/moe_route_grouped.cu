@@ -8,17 +8,24 @@
 // and compares it with the next one.  Where a gap (between neighbours of the
 // result, or between the last kept and the first dropped group) is within the
 // two bounds, fp32 cannot tell: the choices in question, and those that might
-// displace the last of them, are ranked again by fp64 keys, one per lane (an
-// fp64 exp costs a warp about 500 cycles here, so as few as possible).  Without a bias the order of the keys is that of the logits,
-// which are compared exactly.  A gap of exactly equal inputs (same logit, same
-// bias) is a tie in any precision and goes to the lower index.
+// displace the last of them, are ranked again by fp64 keys, and likewise the
+// elements that make up the groups' scores, one key per lane.  (Deciding such a
+// token with fp64 keys of all its experts takes a warp tens of microseconds on
+// this part's few fp64 units: it is left for more than 32 such elements.)
+// Without a bias the order of the keys is that of the logits, which are
+// compared exactly.  A gap of exactly equal inputs (same logit, same bias) is a
+// tie in any precision and goes to the lower index.
+//
+// What bounds it: instruction issue, about 900 warp instructions a token at
+// 256 experts and k = 8 (8192 tokens: 17 us in 8 groups with a bias, 10 us
+// without either; their 8 MB take 1.3 us).
 //
 // Error bound of a key p + b, in units of 2^-24.  exp32 is within 4 (2 ulp) and
 // 1.5 |x| (its argument is scaled and rounded).  Sigmoid: the error of e^-l
 // reaches p times 1 - p, and p (1 - p) |l| < 0.3, so with the addition and the
-// reciprocal 8 p + 1 covers it.  Softmax: |l - m| stays below 88 where p is not
-// 0, and the sum adds one rounding per element of a lane and per shuffle:
-// (npl + 136) p covers it.
+// reciprocal 8 p + 1 covers it.  Softmax, x = l - m: p 1.5 |x| < 0.6 for the
+// element itself; in the sum the errors' weighted mean is 1.5 (ln E + 1) < 12,
+// and each addition in a lane and each shuffle rounds: (npl + 32) p + 1 covers it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -42,7 +49,7 @@ __device__ __forceinline__ float load_logit(const RouteArgs& a, int64_t at) {
 // as logit_key, for a v that is no NaN: larger v, larger key; never 0, which marks a taken entry
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);  // -0 and +0 are the same logit
-  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return max(b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u), 1u);  // (a NaN bias: some key, never 0)
 }
 
 // softmax statistics of a token; sigmoid uses neither
@@ -158,6 +165,32 @@ __device__ __noinline__ int rank64(const RouteArgs& a, int64_t row, int lane, fl
   return mine;
 }
 
+// The groups' scores by fp64 keys of the n <= 32 elements `list` that may be
+// among a group's two largest, one per lane: bit g of the result is set for
+// the topk_group best groups.
+__device__ __noinline__ uint32_t groups64(const RouteArgs& a, int64_t row, int lane, float m, int n, const int* list) {
+  const double sum = sum64(a, row, lane, m);
+  const int e = lane < n ? list[lane] : 0, gs = a.E / a.n_group;
+  double key = -INFINITY;
+  if (lane < n) key = score64(load_logit(a, row + e), a.route, m, sum) + (a.bias ? (double)a.bias[e] : 0.0);
+  double first = -INFINITY, second = -INFINITY;  // lane g: of group g
+  for (int i = 0; i < n; ++i) {
+    const double k = __shfl_sync(kAll, key, i);
+    const int g = __shfl_sync(kAll, e, i) / gs;
+    if (g != lane) continue;
+    if (k > first) second = first, first = k;
+    else if (k > second) second = k;
+  }
+  const double score = lane >= a.n_group ? -INFINITY
+                       : a.group_score == MOE_GROUP_TOP2 && gs > 1 ? first + second : first;
+  int rank = 0;
+  for (int g = 0; g < a.n_group; ++g) {
+    const double other = __shfl_sync(kAll, score, g);
+    rank += other > score || (other == score && g < lane);
+  }
+  return __ballot_sync(kAll, lane < a.n_group && rank < a.topk_group);
+}
+
 // the two largest of two pairs, each in order
 __device__ __forceinline__ void top2_join(float& first, float& second, float f, float s) {
   second = fmaxf(fminf(first, f), fmaxf(second, s));
@@ -227,7 +260,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
     st = Stats{m, 1.0f / sum};
   }
-  const float bound = a.route == MOE_ROUTE_SIGMOID ? 8.0f : (float)(npl + 136);
+  const float bound = a.route == MOE_ROUTE_SIGMOID ? 8.0f : (float)(npl + 32);
 
   // ordering keys: p + b with a bias, the logits themselves without; a group's
   // score takes p (+ b) where it adds two keys
@@ -285,14 +318,34 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
       rank += other > score || (other == score && g < lane);
     }
     if (lane >= a.n_group) rank = 64;
-    const uint32_t kept = __ballot_sync(kAll, rank < a.topk_group);
+    uint32_t kept = __ballot_sync(kAll, rank < a.topk_group);
     // the last kept against the first dropped group
     const int last = __ffs(__ballot_sync(kAll, rank == a.topk_group - 1)) - 1;
     const int next = __ffs(__ballot_sync(kAll, rank == a.topk_group)) - 1;
     const float gap = __shfl_sync(kAll, score, last) - __shfl_sync(kAll, score, next);
     const float tol = __shfl_sync(kAll, err, last) + __shfl_sync(kAll, err, next);
-    unsure = tol > 0.0f && gap <= tol;
     int g = e0 / gs, left = (g + 1) * gs - e0;  // elements of the lane until the next group
+    if (tol > 0.0f && gap <= tol) {
+      // decided by fp64 keys of the elements that may count for a group
+      int* list = reinterpret_cast<int*>(s_pick[wid]);
+      int n = 0, gg = g, ll = left;
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        if (ll == 0) ++gg, ll = gs;
+        --ll;
+        const float low = __shfl_sync(kAll, add ? second : first, gg & 31);  // lane g holds group g's
+        const float v = value(j);
+        const bool may = j < have && v >= low - kUlp * (2.0f * bound + 2.0f + fabsf(v) + fabsf(low));
+        const uint32_t who = __ballot_sync(kAll, may);
+        const int at = n + __popc(who & ((1u << lane) - 1u));
+        if (may && at < 32) list[at] = e0 + j;
+        n += __popc(who);
+      }
+      __syncwarp();
+      if (n <= 32) kept = groups64(a, row, lane, st.m, n, list);
+      else unsure = true;
+      __syncwarp();
+    }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
       if (left == 0) ++g, left = gs;
