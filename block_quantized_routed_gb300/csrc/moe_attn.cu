@@ -315,9 +315,14 @@ __device__ __forceinline__ Seg walk_seg(const Walk& w) {
 }
 
 // units before CTA c of n
-__device__ __forceinline__ long long share(long long total, int n, int c) { return total * c / n; }
+__device__ __forceinline__ long long divide(long long x, long long y) {  // of two numbers >= 0, y > 0
+  return (unsigned long long)(x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
+}
+__device__ __forceinline__ long long share(long long total, int n, int c) { return divide(total * c, n); }
 // the CTA that holds unit g
-__device__ __forceinline__ int owner(long long total, int n, long long g) { return (int)(((g + 1) * n - 1) / total); }
+__device__ __forceinline__ int owner(long long total, int n, long long g) {
+  return (int)divide((g + 1) * n - 1, total);
+}
 
 // The ring's order: pair(o) is the o-th load of a segment of m tiles, a key
 // tile (value = false) or a value tile.  Items of two row tiles consume K0 V0
@@ -578,38 +583,6 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
   const int G = a.Hq / a.kv.Hkv;
 
   // ---- prologue: the call's work in units, and this CTA's share
-  long long* cost = reinterpret_cast<long long*>(smem + C::kSmemRing);  // per sequence; the ring is not in use yet
-  for (int b0 = warp * 32; b0 < a.kv.n_seqs; b0 += C::kThreads) {
-    // a lane per sequence; one of more than four row tiles is counted by the warp
-    const int b = b0 + lane;
-    Item it;
-    it.s = SeqInfo{0, 0, 0, true};
-    if (b < a.kv.n_seqs) it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, b);
-    if (!it.s.ok && blockIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-    const int nt = (it.s.n * G + kRows - 1) / kRows;
-    long long mine = 0;
-    if (nt <= 4) {
-      for (it.i = 0; it.i < nt; ++it.i) {
-        item_range<kN, kRows>(a, G, it);
-        mine += it.cost();
-      }
-    }
-    for (unsigned many = __ballot_sync(kAll, nt > 4); many; many &= many - 1) {
-      const int src = __ffs(many) - 1;
-      Item x;
-      x.s = SeqInfo{0, __shfl_sync(kAll, it.s.n, src), __shfl_sync(kAll, it.s.kv, src), true};
-      const int nx = __shfl_sync(kAll, nt, src);
-      long long sum = 0;
-      for (x.i = lane; x.i < nx; x.i += 32) {
-        item_range<kN, kRows>(a, G, x);
-        sum += x.cost();
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-      if (lane == src) mine = sum;
-    }
-    if (b < a.kv.n_seqs) cost[b] = mine * a.kv.Hkv;
-  }
   if (warp == kWarpMma && lane == 0) {
     for (int s = 0; s < kStages; ++s) {
       bar_init(full(s), 1);
@@ -627,79 +600,144 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     st.abort = 0;
     st.n_cut = 0;
   }
-  __syncthreads();
-  if (warp == 0) {
-    long long total = 0;
-    for (int b = lane; b < a.kv.n_seqs; b += 32) total += cost[b];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-    const int n = (int)max(1ll, min((long long)gridDim.x, total));
-    const int c = blockIdx.x;
-    const bool work = c < n && total > 0;
-    const long long g0 = work ? share(total, n, c) : 0, g1 = work ? share(total, n, c + 1) : 0;
-    int fb = 0;
-    long long at = 0;  // units before sequence fb
-    if (work) {
-      for (int b0 = 0; b0 < a.kv.n_seqs; b0 += 32) {
-        const int b = b0 + lane;
-        const long long mine = b < a.kv.n_seqs ? cost[b] : 0;
-        long long inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(kAll, inc, o);
-          if (lane >= o) inc += v;
-        }
-        const unsigned hit = __ballot_sync(kAll, at + inc > g0);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          fb = b0 + src;
-          at += __shfl_sync(kAll, inc - mine, src);
-          break;
-        }
-        at += __shfl_sync(kAll, inc, 31);
+  if (warp == kWarpMma) {
+    __syncwarp();
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&st.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  // The units of 32 sequences, a lane per sequence (one of more than four row tiles is counted by the warp).
+  const auto count = [&](int b, SeqInfo& s) {
+    Item it;
+    s = SeqInfo{0, 0, 0, true};
+    if (b < a.kv.n_seqs) s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, b);
+    if (!s.ok && blockIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+    it.s = s;
+    const int nt = (s.n * G + kRows - 1) / kRows;
+    long long mine = 0;
+    if (nt <= 4) {
+      int sum = 0;
+      for (it.i = 0; it.i < nt; ++it.i) {
+        item_range<kN, kRows>(a, G, it);
+        sum += it.cost();
       }
-      Item it;
-      it.b = fb;
-      it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, fb);
-      const int nt = it.tiles_q = (it.s.n * G + kRows - 1) / kRows;
-      const long long per = cost[fb] / a.kv.Hkv;
-      long long rem = g0 - at;
-      it.h = (int)(rem / per);
-      rem -= it.h * per;
-      for (int i0 = 0; i0 < nt; i0 += 32) {
-        it.i = i0 + lane;
-        long long mine = 0;
-        if (it.i < nt) {
-          item_range<kN, kRows>(a, G, it);
-          mine = it.cost();
-        }
-        long long inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long v = __shfl_up_sync(kAll, inc, o);
-          if (lane >= o) inc += v;
-        }
-        const unsigned hit = __ballot_sync(kAll, inc > rem);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          rem -= __shfl_sync(kAll, inc - mine, src);
-          if (lane == src) st.item = it;
-          break;
-        }
-        rem -= __shfl_sync(kAll, inc, 31);
-      }
-      at = rem;
+      mine = sum;
     }
+    for (unsigned many = __ballot_sync(kAll, nt > 4); many; many &= many - 1) {
+      const int src = __ffs(many) - 1;
+      Item x;
+      x.s = SeqInfo{0, __shfl_sync(kAll, s.n, src), __shfl_sync(kAll, s.kv, src), true};
+      const int nx = __shfl_sync(kAll, nt, src);
+      long long sum = 0;
+      for (x.i = lane; x.i < nx; x.i += 32) {
+        item_range<kN, kRows>(a, G, x);
+        sum += x.cost();
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+      if (lane == src) mine = sum;
+    }
+    return mine * a.kv.Hkv;
+  };
+  const auto scan = [&](auto v) {  // inclusive, over the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const auto u = __shfl_up_sync(kAll, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  // warp 0: the CTA's units [g0, g1) start `rem` units into sequence it.b, of `mine` units in all
+  const auto locate = [&](Item& it, long long mine, long long rem) {
+    const int nt = it.tiles_q = (it.s.n * G + kRows - 1) / kRows;
+    const long long per = divide(mine, a.kv.Hkv);
+    it.h = (int)divide(rem, per);
+    rem -= it.h * per;
+    for (int i0 = 0; i0 < nt; i0 += 32) {
+      it.i = i0 + lane;
+      int units = 0;
+      if (it.i < nt) {
+        item_range<kN, kRows>(a, G, it);
+        units = it.cost();
+      }
+      if (nt == 1) {  // a decode step
+        if (lane == 0) st.item = it;
+        return rem;
+      }
+      const long long inc = scan((long long)units);
+      const unsigned hit = __ballot_sync(kAll, inc > rem);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        rem -= __shfl_sync(kAll, inc - units, src);
+        if (lane == src) st.item = it;
+        return rem;
+      }
+      rem -= __shfl_sync(kAll, inc, 31);
+    }
+    return rem;
+  };
+  const auto begin = [&](long long total, long long& g0) {  // this CTA's share; false: none
+    const int n = (int)max(1ll, min((long long)gridDim.x, total));
+    const bool work = (int)blockIdx.x < n && total > 0;
+    g0 = work ? share(total, n, blockIdx.x) : 0;
     if (lane == 0) {
-      st.off = (int)at;
+      st.off = 0;
       st.first = g0;
-      st.left = g1 - g0;
+      st.left = work ? share(total, n, blockIdx.x + 1) - g0 : 0;
       st.total = total;
       st.ctas = n;
     }
-  } else if (warp == kWarpMma) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&st.tmem)));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    return work;
+  };
+  if (a.kv.n_seqs <= 32) {  // one warp's lanes hold all sequences
+    if (warp == 0) {
+      Item it;
+      const long long mine = count(lane, it.s);
+      const long long inc = scan(mine);
+      long long g0;
+      if (begin(__shfl_sync(kAll, inc, 31), g0)) {
+        const int src = __ffs(__ballot_sync(kAll, inc > g0)) - 1;
+        it.b = src;
+        it.s = SeqInfo{__shfl_sync(kAll, it.s.q0, src), __shfl_sync(kAll, it.s.n, src), __shfl_sync(kAll, it.s.kv, src),
+                       true};
+        const long long whole = __shfl_sync(kAll, mine, src), before = __shfl_sync(kAll, inc, src) - whole;
+        const long long off = locate(it, whole, g0 - before);
+        if (lane == 0) st.off = (int)off;
+      }
+    }
+  } else {
+    long long* cost = reinterpret_cast<long long*>(smem + C::kSmemRing);  // per sequence; the ring is not in use yet
+    for (int b0 = warp * 32; b0 < a.kv.n_seqs; b0 += C::kThreads) {
+      SeqInfo s;
+      const long long mine = count(b0 + lane, s);
+      if (b0 + lane < a.kv.n_seqs) cost[b0 + lane] = mine;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      long long total = 0;
+      for (int b = lane; b < a.kv.n_seqs; b += 32) total += cost[b];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+      long long g0;
+      if (begin(total, g0)) {
+        long long at = 0;  // units before the 32 sequences
+        for (int b0 = 0; b0 < a.kv.n_seqs; b0 += 32) {
+          const int b = b0 + lane;
+          const long long mine = b < a.kv.n_seqs ? cost[b] : 0, inc = scan(mine);
+          const unsigned hit = __ballot_sync(kAll, at + inc > g0);
+          if (hit) {
+            const int src = __ffs(hit) - 1;
+            Item it;
+            it.b = b0 + src;
+            it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, it.b);
+            const long long whole = __shfl_sync(kAll, mine, src), before = at + __shfl_sync(kAll, inc, src) - whole;
+            const long long off = locate(it, whole, g0 - before);
+            if (lane == 0) st.off = (int)off;
+            break;
+          }
+          at += __shfl_sync(kAll, inc, 31);
+        }
+      }
+    }
   }
   fence_before();
   __syncthreads();
@@ -1040,15 +1078,17 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       const bool by_col = w.it.rows > (kColMajor - 1) * parts;
       const uint32_t other_addr = lanes + C::kColO + (grp ^ 1) * D;
       if (writes) {
-        constexpr int kW = 32;
+        constexpr int kW = kGroups == 1 ? 64 : 32;  // columns at a time
 #pragma unroll 1
         for (int x0 = col0; x0 < col1; x0 += kW) {
           uint32_t o[kW];
           if (busy && acc) {
-            tmem_ld32(o_addr + x0, o);
+#pragma unroll
+            for (int y = 0; y < kW; y += 32) tmem_ld32(o_addr + x0 + y, o + y);
             if (join) {
               uint32_t e[kW];
-              tmem_ld32(other_addr + x0, e);
+#pragma unroll
+              for (int y = 0; y < kW; y += 32) tmem_ld32(other_addr + x0 + y, e + y);
               wait_ld();
 #pragma unroll
               for (int j = 0; j < kW; ++j)
