@@ -142,26 +142,27 @@ __device__ __forceinline__ int q8k_bits(float z, float d, float inv) {
   return __float_as_int(y);
 }
 
-__device__ __forceinline__ float rcp(float x) {  // within 1 ulp
+__device__ __forceinline__ float rcp(float x) {  // the approximation (1 ulp) and one Newton step: little over half an ulp
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  return fmaf(y, fmaf(-x, y, 1.0f), y);
 }
 
 // The 8-bit output of one row z (s[NV][8]); `peak` is the thread's largest |z|
 // (row-scaled outputs only), buf one block_reduce buffer.  FMT: the format, or
 // -1 for a.q_fmt.  The scale d is an IEEE quotient; z / d is the product with
-// d's reciprocal (2 ulp), which for int8 codes is put right near a half.
+// d's reciprocal, which for int8 codes is put right near a half.
 template <int NV, bool WIDE, int FMT>
 __device__ __forceinline__ void put_codes(const NormArgs& a, int64_t row, float (&s)[NV][8], float peak, float* buf) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int fmt = FMT >= 0 ? FMT : a.q_fmt;
   const bool fp8 = fmt == MOE_NORM_Q_E4M3_G128 || fmt == MOE_NORM_Q_E4M3_ROW;
   const bool per_row = fmt == MOE_NORM_Q_E4M3_ROW || fmt == MOE_NORM_Q_INT8_ROW;
+  const float top = fp8 ? 448.0f : 127.0f;
   float d = 0.0f;
   if (per_row) {
     peak = block_reduce<true>(peak, buf);
-    d = fp8 ? peak * (1.0f / 448.0f) : __fdiv_rn(peak, 127.0f);
+    d = __fdiv_rn(peak, top);
     if (tid == 0) a.d[row] = d;
   }
   const int group = fmt == MOE_NORM_Q_Q8K ? 256 : 128;
@@ -188,7 +189,7 @@ __device__ __forceinline__ void put_codes(const NormArgs& a, int64_t row, float 
   for (int i = 0; i < NV; ++i) {
     const int c = (i * nt + tid) * 8, n = a.H - c;
     if (!per_row) {
-      d = fp8 ? m[i] * (1.0f / 448.0f) : __fdiv_rn(m[i], 127.0f);
+      d = __fdiv_rn(m[i], top);
       if (n > 0 && c % group == 0) dout[c / group] = d;
     }
     // d = 0 only where every z of the group is 0 (or too small for its quotient to exist).  A reciprocal beyond

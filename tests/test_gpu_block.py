@@ -483,6 +483,34 @@ def test_attention_bad_tables_are_reported(D, page):
     assert ((out.cpu().double() - want).abs() <= tol)[:5].all() and (out[5] == 5).all()
 
 
+@pytest.mark.parametrize("D,page", [(128, 64), (256, 16), (80, 16)])
+def test_cache_offsets_beyond_32_bits(D, page):
+    """Pages whose first element lies past 2^31: appended to, then attended over."""
+    hkv, hq, n, kv = 4, 8, 3, 100
+    pages = (1 << 31) // (page * hkv * D) + 40
+    kc = torch.empty(pages, page, hkv, D, dtype=BF16, device="cuda")
+    vc = torch.empty(pages, page, hkv, D, dtype=BF16, device="cuda")
+    need = -(-kv // page)
+    ids = torch.arange(pages - need, pages, dtype=torch.int32)
+    small_k, small_v = rnd((need, page, hkv, D), 90, BF16), rnd((need, page, hkv, D), 91, BF16)
+    kc[pages - need:], vc[pages - need:] = small_k.cuda(), small_v.cuda()
+    q, kn, vn = rnd((n, hq, D), 92, BF16), rnd((n, hkv, D), 93, BF16), rnd((n, hkv, D), 94, BF16)
+    table, cu = ids.view(1, -1).cuda(), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([kv], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(moe.moe_paged_attention_workspace_size(hq, hkv, D), dtype=torch.uint8, device="cuda")
+    moe.moe_kv_append(kn.cuda(), vn.cuda(), kc, vc, table, cu, lens, ws)
+    out = torch.empty(n, hq, D, dtype=BF16, device="cuda")
+    moe.moe_paged_attention(q.cuda(), kc, vc, table, cu, lens, 0.1, out, ws)
+    assert status(ws) == 0
+    for i in range(n):
+        j = kv - n + i
+        small_k[j // page, j % page], small_v[j // page, j % page] = kn[i], vn[i]
+    assert torch.equal(kc[pages - need:].cpu(), small_k) and torch.equal(vc[pages - need:].cpu(), small_v)
+    local = torch.arange(need, dtype=torch.int32).view(1, -1)
+    want, _, tol, _ = block_ref.attention(q, small_k, small_v, local, [n], [kv], 0.1, 0, BF16)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
 # ------------------------------------------------------------------ streams and graphs
 
 def test_other_stream_and_graph():
