@@ -453,8 +453,9 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
       float m[8], l[8], M = -INFINITY, L = 0.0f;
 #pragma unroll
       for (int p = 0; p < 8; ++p) {
-        m[p] = p < np ? __ldcg(part(p) + lo + row) : -INFINITY;
-        l[p] = p < np ? __ldcg(part(p) + C::kRows + lo + row) : 0.0f;
+        const float2 ml = p < np ? __ldcg(reinterpret_cast<const float2*>(part(p)) + lo + row) : make_float2(-INFINITY, 0.0f);
+        m[p] = ml.x;
+        l[p] = ml.y;
         M = fmaxf(M, m[p]);
       }
 #pragma unroll
@@ -476,8 +477,9 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int p = i * 32 + lane;
-        m[i] = p < np ? __ldcg(part(p) + lo + row) : -INFINITY;
-        l[i] = p < np ? __ldcg(part(p) + C::kRows + lo + row) : 0.0f;
+        const float2 ml = p < np ? __ldcg(reinterpret_cast<const float2*>(part(p)) + lo + row) : make_float2(-INFINITY, 0.0f);
+        m[i] = ml.x;
+        l[i] = ml.y;
         M = fmaxf(M, m[i]);
       }
 #pragma unroll
@@ -1132,8 +1134,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
             sum > 0.0f ? (m2 + log2f(sum)) * 0.693147180559945309f : -INFINITY;
       if (!whole) {
         if (writes && valid) {
-          part[row] = m2;
-          part[kRows + row] = sum;
+          reinterpret_cast<float2*>(part)[row] = make_float2(m2, sum);
         }
         if (tid == 0) {
           Cut& cut = st.cut[st.n_cut++];

@@ -291,8 +291,11 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 2 ? 2 : 1) add_rms
   const XT* x = static_cast<const XT*>(a.x) + row * a.x_stride;
   const RT* res = static_cast<const RT*>(a.residual) + row * a.r_stride;
   RT* sum = static_cast<RT*>(a.sum_out) + row * a.sum_stride;
-  float s[NV][8];
+  float s[NV][8], w1[8];  // w1: with one vector per thread the weights too are asked for before the reduction
   float2 sq2 = make_float2(0.f, 0.f);
+  if constexpr (WIDE && NV == 1) {
+    if (tid * 8 < a.H) load8_dt<true>(a.w, a.w_dtype, tid * 8, 8, w1);
+  }
   if constexpr (WIDE) {
     // every load of the row is under way before the first is used
     constexpr int kX = sizeof(XT) / 2, kR = sizeof(RT) / 2;
@@ -353,7 +356,12 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 2 ? 2 : 1) add_rms
     const int c = (i * nt + tid) * 8, n = a.H - c;
     if (n > 0) {
       float w[8];
-      load8_dt<WIDE>(a.w, a.w_dtype, c, n, w);
+      if constexpr (WIDE && NV == 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = w1[j];
+      } else {
+        load8_dt<WIDE>(a.w, a.w_dtype, c, n, w);
+      }
 #pragma unroll
       for (int j = 0; j < 8; j += 2) {
         const float2 z = mul2(mul2(make_float2(s[i][j], s[i][j + 1]), make_float2(r, r)),

@@ -202,12 +202,29 @@ __device__ __forceinline__ void top2_add(float& first, float& second, float v) {
   first = fmaxf(first, v);
 }
 
+// Batcher's odd-even merge sort of N (a power of two) keys, largest first.
+// (P, Q: the step, as template arguments so that every index is a constant.)
+template <int N, int P, int Q>
+__device__ __forceinline__ void sort_step(uint32_t (&k)[N]) {
+#pragma unroll
+  for (int j = Q % P; j + Q < N; j += 2 * Q)
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+      if (i + j + Q < N && (i + j) / (2 * P) == (i + j + Q) / (2 * P)) {
+        const uint32_t x = k[i + j], y = k[i + j + Q];
+        k[i + j] = max(x, y);
+        k[i + j + Q] = min(x, y);
+      }
+  if constexpr (Q > 1) sort_step<N, P, Q / 2>(k);
+  else if constexpr (2 * P < N) sort_step<N, 2 * P, 2 * P>(k);
+}
+
 // NP >= ceil(E / 32): elements per lane; lane i holds elements i * npl on.
 // VEC: npl = NP, E = 32 * NP and the rows are 16-byte aligned (wide loads).
 template <int NP, bool VEC>
 __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   __shared__ double s_buf[4][NP * 32];  // keys: of groups that do not fall on lane boundaries (fp32); of select64
-  __shared__ int2 s_pick[4][32];
+  __shared__ int s_list[4][32];
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int t = blockIdx.x * (blockDim.x >> 5) + wid;
   if (t >= a.T) return;
@@ -275,7 +292,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
 
   bool unsure = false;
   if (a.n_group > 1) {
-    float* s_key = reinterpret_cast<float*>(s_buf[wid]);
+    float* s_val = reinterpret_cast<float*>(s_buf[wid]);
     const int gs = a.E / a.n_group, per = gs / npl;  // lanes per group, where groups are whole lanes
     const bool on_lanes = gs == per * npl && (per & (per - 1)) == 0;
     const bool add = a.group_score == MOE_GROUP_TOP2 && gs > 1;
@@ -295,12 +312,12 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     } else {
 #pragma unroll
       for (int j = 0; j < NP; ++j)
-        if (j < have) s_key[e0 + j] = value(j);
+        if (j < have) s_val[e0 + j] = value(j);
       __syncwarp();
       if (lane < a.n_group) {
         int i = lane % gs;  // groups start at different elements: different banks
         for (int j = 0; j < gs; ++j) {
-          top2_add(first, second, s_key[lane * gs + i]);
+          top2_add(first, second, s_val[lane * gs + i]);
           if (++i == gs) i = 0;
         }
       }
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     int g = e0 / gs, left = (g + 1) * gs - e0;  // elements of the lane until the next group
     if (tol > 0.0f && gap <= tol) {
       // decided by fp64 keys of the elements that may count for a group
-      int* list = reinterpret_cast<int*>(s_pick[wid]);
+      int* list = s_list[wid];
       int n = 0, gg = g, ll = left;
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
@@ -346,47 +363,58 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
       else unsure = true;
       __syncwarp();
     }
+    if (on_lanes) {
+      if (!(kept >> (g & 31) & 1)) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      if (left == 0) ++g, left = gs;
-      --left;
-      if (!(kept >> (g & 31) & 1)) key[j] = 0u;
+        for (int j = 0; j < NP; ++j) key[j] = 0u;
+      }
+    } else {
+      __syncwarp();  // s_val has been read
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        if (left == 0) ++g, left = gs;
+        --left;
+        if (!(kept >> (g & 31) & 1)) key[j] = 0u;
+      }
     }
   }
 
-  // the k largest, and with a bias the one after them; only the lane that owns
-  // a choice looks for it and for its next largest
+  // The k largest, and with a bias the one after them.  Each lane sorts its keys; a round takes the largest head, and
+  // the lane that owned it moves its keys up.  Lane r keeps the r-th key and its owner.
+  uint32_t* const s_key = reinterpret_cast<uint32_t*>(s_buf[wid]);
+#pragma unroll
+  for (int j = 0; j < NP; ++j) s_key[j * 32 + lane] = key[j];
+  sort_step<NP, 1, 1>(key);
   const int avail = a.n_group > 1 ? a.topk_group * (a.E / a.n_group) : a.E;
   const int rounds = scored && a.k < avail ? a.k + 1 : a.k;
-  uint32_t best = 0;
-#pragma unroll
-  for (int j = 0; j < NP; ++j) best = max(best, key[j]);
+  uint32_t my_key = 0;
+  int my_owner = 0;
   const auto pick = [&](int r, uint32_t top) {
-    const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
+    const int owner = __ffs(__ballot_sync(kAll, key[0] == top)) - 1;  // equal keys: the lower lane first
+    if (lane == r) my_key = top, my_owner = owner;
     if (lane == owner) {
-      int at = -1;
-      float lv = 0.0f;
-      best = 0;
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {  // the lowest index of equals
-        const bool hit = key[j] == top && at < 0;
-        at = hit ? j : at;
-        lv = hit ? l[j] : lv;
-        key[j] = hit ? 0u : key[j];
-        best = max(best, key[j]);
-      }
-      s_pick[wid][r] = make_int2(e0 + at, __float_as_int(lv));
+      for (int j = 0; j + 1 < NP; ++j) key[j] = key[j + 1];
+      key[NP - 1] = 0u;
     }
   };
-  for (int r = 0; r < rounds; ++r) pick(r, __reduce_max_sync(kAll, best));
+  // the element that lane r's choice was: among its owner's equal keys, the one after those of earlier rounds
+  const auto element = [&](int n) {
+    const uint32_t same = __match_any_sync(kAll, lane < n ? my_key : 0u) & __match_any_sync(kAll, my_owner);
+    int skip = __popc(same & ((1u << lane) - 1u)), at = 0;
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+      const bool hit = s_key[j * 32 + my_owner] == my_key;
+      if (hit && !found && skip-- == 0) at = j, found = true;
+    }
+    return my_owner * npl + at;
+  };
+  for (int r = 0; r < rounds; ++r) pick(r, __reduce_max_sync(kAll, key[0]));
   __syncwarp();
-  int mine = 0;
-  float lg = 0.0f;
-  if (lane < rounds) {
-    const int2 choice = s_pick[wid][lane];
-    mine = choice.x;
-    lg = __int_as_float(choice.y);
-  }
+  int mine = element(rounds);
+  if (lane >= rounds) mine = 0;
+  float lg = lane < rounds ? load_logit(a, row + mine) : 0.0f;
   float p = score32(lg, a.route, st);
   if (scored) {
     const float b = lane < rounds ? __ldg(a.bias + mine) : 0.0f, v = p + b;
@@ -401,23 +429,17 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
       int n = rounds;
       bool enough = n == avail;
       while (!enough && n < 32) {
-        const uint32_t top = __reduce_max_sync(kAll, best);
+        const uint32_t top = __reduce_max_sync(kAll, key[0]);
         if (top == 0) break;
         const float vn = key_logit(top);
         enough = vk - vn > kUlp * (2.0f * bound + 2.0f + fabsf(vk) + fabsf(vn));
         if (!enough) pick(n++, top);
         else break;
       }
-      __syncwarp();
       enough |= n < 32;
       if (enough) {
-        int e = 0;
-        float le = 0.0f;
-        if (lane < n) {
-          e = s_pick[wid][lane].x;
-          le = __int_as_float(s_pick[wid][lane].y);
-        }
-        mine = rank64(a, row, lane, st.m, n, e, le);
+        const int e = element(n);
+        mine = rank64(a, row, lane, st.m, n, e, lane < n ? load_logit(a, row + e) : 0.0f);
         if (lane < a.k) lg = load_logit(a, row + mine);
         p = score32(lg, a.route, st);
       } else {
