@@ -1,8 +1,8 @@
 """block_quantized_routed_gb300 — the block-quantized routed MoE layer on GB300.
 
-A thin ctypes binding of the C ABI in include/moe_q8k.h (libmoe_q8k.so, built
-in-tree for sm_103a).  Every function has the name of its C entry point and
-only marshals arguments: device tensors go in as raw pointers, the stream is
+A thin binding of the C ABI in include/moe_q8k.h (libmoe_q8k.so, built in-tree
+for sm_103a): ctypes, and csrc/binding.cpp for the decoder-block operators.
+Every function has the name of its C entry point and only marshals arguments: device tensors go in as raw pointers, the stream is
 torch's current CUDA stream, and a negative status raises MoeError.  Every
 step of the layer runs in the library's CUDA kernels; there is no other
 implementation behind these names, and loading fails loudly when the library

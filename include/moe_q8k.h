@@ -550,7 +550,8 @@ int moe_kv_append(const moe_kv_desc* kv, const void* k, int64_t k_stride, int64_
 
 /* Workspace bytes of moe_paged_attention (0 for unsupported sizes): a status
  * word and counters, zero before the first call, and partial results of
- * sequences that several CTAs share. */
+ * sequences that several CTAs share.  Calls leave the counters at zero; after
+ * MOE_ERR_DEVICE_TIMEOUT zero the workspace again. */
 size_t moe_paged_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D);
 
 /* Attention of a chunk of new tokens over a paged cache that already holds
@@ -570,7 +571,8 @@ size_t moe_paged_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D);
  * does, have to be finite: they are multiplied by a zero weight.  The cache
  * beyond kv_len is never used.  Head sizes 64, 128 and 256 with a page size
  * that is a power of two >= 16 run on the tensor cores; other sizes run on a
- * general kernel.  Sequences with cu_q out of order or out of range, or
+ * general kernel.  The tensor-core form is one cooperative launch of a CTA per
+ * SM.  Sequences with cu_q out of order or out of range, or
  * kv_len outside 0..max_pages*page_size, are skipped and recorded as
  * MOE_ERR_DEVICE_BOUNDS in the status word of ws, as are page numbers outside
  * 0..num_pages (their keys read as zeros). */
