@@ -199,6 +199,11 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, within 2 ulp; 2^-inf = 
   return y;
 }
 
+__device__ __forceinline__ void store32(void* p, const uint32_t* v) {  // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   uint32_t r;
@@ -926,10 +931,16 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
               cp_async16(dst + row * 128 + (((ch & 7) ^ (row & 7)) << 4), q + tok * a.q_stride + g * a.q_head_stride);
               for (g += kStep; g >= G; g -= G) ++tok;
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_proxy();
-            bar_arrive(q_full(qt));
+            asm volatile("cp.async.commit_group;" ::: "memory");
           }
+          if (two) {  // both tiles' copies are under way before the first is waited for
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            fence_proxy();
+            bar_arrive(q_full(0));
+          }
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+          fence_proxy();
+          bar_arrive(q_full(two ? 1 : q_tile));
           if (kGroups == 2 && !two) q_tile ^= 1;
         }
         walk_next<kN, kRows>(a, G, w, sg.len);
@@ -948,6 +959,8 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     float2* const xch = reinterpret_cast<float2*>(smem + C::kSmemXch);
     unsigned* const counters = reinterpret_cast<unsigned*>(a.ws + 16);
     long long g_seg = st.first;  // unit at which the segment starts
+    // rows of out on 32-byte boundaries: whole sectors at a time
+    const bool wide_out = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.o_stride * 2) | (uintptr_t)(a.o_head_stride * 2)) & 31) == 0;
     for (Walk w = walk_begin(st); w.left > 0;) {
       const Seg sg = walk_seg(w);
       if (sg.first == sg.last) {
@@ -1107,11 +1120,15 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
               uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tok) * a.o_stride +
                               (int64_t)(w.it.h * G + g) * a.o_head_stride + x0;
 #pragma unroll
-              for (int j = 0; j < kW; j += 8) {
-                const auto at = [&](int i) { return __uint_as_float(o[j + i]) * inv; };
-                *reinterpret_cast<uint4*>(out + j) =
-                    make_uint4(pack16<BF16>(at(0), at(1)), pack16<BF16>(at(2), at(3)), pack16<BF16>(at(4), at(5)),
-                               pack16<BF16>(at(6), at(7)));
+              for (int j = 0; j < kW / 2; ++j)
+                o[j] = pack16<BF16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+              if (wide_out) {
+#pragma unroll
+                for (int j = 0; j < kW / 2; j += 8) store32(out + 2 * j, o + j);
+              } else {
+#pragma unroll
+                for (int j = 0; j < kW / 2; j += 4)
+                  *reinterpret_cast<uint4*>(out + 2 * j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
               }
             } else if (by_col) {  // a warp's stores of one column are contiguous
               uint32_t* dst = reinterpret_cast<uint32_t*>(part) + 2 * kRows + (size_t)x0 * kRows + row;

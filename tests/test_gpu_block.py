@@ -327,7 +327,8 @@ def attend(c, hq, D, scale, window, dtype, seed, strided=False, ws=None, lse=Tru
     q = rnd((c.T, hq + 2, D), seed, dtype)
     q = q[:, 1:1 + hq] if strided else q[:, :hq].contiguous()
     dq = q.cuda() if not strided else rnd((c.T, hq + 2, D), seed, dtype).cuda()[:, 1:1 + hq]
-    out = torch.full((c.T, hq + (1 if strided else 0), D), 5.0, dtype=dtype, device="cuda")[:, :hq]
+    pad = 8 if strided else 0                      # heads of out on 16-byte, not on 32-byte boundaries
+    out = torch.full((c.T, hq + (1 if strided else 0), D + pad), 5.0, dtype=dtype, device="cuda")[:, :hq, :D]
     l = torch.full((c.T, hq), NAN, device="cuda") if lse else None
     if ws is None:
         ws = torch.zeros(moe.moe_paged_attention_workspace_size(hq, c.k.shape[2], D), dtype=torch.uint8, device="cuda")
