@@ -257,7 +257,7 @@ __device__ __forceinline__ void item_range(const AttnArgs& a, int G, Item& it) {
 struct Walk {
   Item it;
   int off;
-  long long left;
+  int left;
 };
 
 // An item whose units several CTAs share (this CTA holds at most two of them).
@@ -270,7 +270,8 @@ struct Cut {
 struct Start {
   Item item;  // the CTA's first, and the unit it starts with
   int off;
-  long long first, left, total;
+  int first, left;  // units
+  int per, extra;   // units per CTA of the call, and how many CTAs' worth of remainder (see share)
   int ctas;
   volatile int abort;
   uint32_t tmem;
@@ -312,21 +313,22 @@ struct Seg {
 };
 __device__ __forceinline__ Seg walk_seg(const Walk& w) {
   Seg s;
-  s.len = (int)min((long long)(w.it.cost() - w.off), w.left);
+  s.len = min(w.it.cost() - w.off, w.left);
   s.first = max(w.off - kItemUnits, 0);
   s.last = max(w.off + s.len - kItemUnits, 0);
   s.tiles = w.it.tiles ? s.last - s.first : 0;
   return s;
 }
 
-// units before CTA c of n
-__device__ __forceinline__ long long divide(long long x, long long y) {  // of two numbers >= 0, y > 0
-  return (unsigned long long)(x | y) >> 32 ? x / y : (long long)((uint32_t)x / (uint32_t)y);
-}
-__device__ __forceinline__ long long share(long long total, int n, int c) { return divide(total * c, n); }
-// the CTA that holds unit g
-__device__ __forceinline__ int owner(long long total, int n, long long g) {
-  return (int)divide((g + 1) * n - 1, total);
+// units before CTA c
+// (A call has fewer than 2^31 units: attn_units_fit.)
+__device__ __forceinline__ int share(const Start& st, int c) { return c * st.per + c * st.extra / st.ctas; }
+// the CTA that holds unit g: a guess, put right
+__device__ __forceinline__ int owner(const Start& st, int g) {
+  int c = min((int)(((float)g + 0.5f) / ((float)st.per + (float)st.extra / (float)st.ctas)), st.ctas - 1);
+  while (share(st, c) > g) --c;
+  while (c + 1 < st.ctas && share(st, c + 1) <= g) ++c;
+  return c;
 }
 
 // The ring's order: pair(o) is the o-th load of a segment of m tiles, a key
@@ -620,21 +622,19 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     if (!s.ok && blockIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     it.s = s;
     const int nt = (s.n * G + kRows - 1) / kRows;
-    long long mine = 0;
+    int mine = 0;
     if (nt <= 4) {
-      int sum = 0;
       for (it.i = 0; it.i < nt; ++it.i) {
         item_range<kN, kRows>(a, G, it);
-        sum += it.cost();
+        mine += it.cost();
       }
-      mine = sum;
     }
     for (unsigned many = __ballot_sync(kAll, nt > 4); many; many &= many - 1) {
       const int src = __ffs(many) - 1;
       Item x;
       x.s = SeqInfo{0, __shfl_sync(kAll, s.n, src), __shfl_sync(kAll, s.kv, src), true};
       const int nx = __shfl_sync(kAll, nt, src);
-      long long sum = 0;
+      int sum = 0;
       for (x.i = lane; x.i < nx; x.i += 32) {
         item_range<kN, kRows>(a, G, x);
         sum += x.cost();
@@ -654,10 +654,10 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     return v;
   };
   // warp 0: the CTA's units [g0, g1) start `rem` units into sequence it.b, of `mine` units in all
-  const auto locate = [&](Item& it, long long mine, long long rem) {
+  const auto locate = [&](Item& it, int mine, int rem) {
     const int nt = it.tiles_q = (it.s.n * G + kRows - 1) / kRows;
-    const long long per = divide(mine, a.kv.Hkv);
-    it.h = (int)divide(rem, per);
+    const int per = mine / a.kv.Hkv;
+    it.h = rem / per;
     rem -= it.h * per;
     for (int i0 = 0; i0 < nt; i0 += 32) {
       it.i = i0 + lane;
@@ -670,7 +670,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         if (lane == 0) st.item = it;
         return rem;
       }
-      const long long inc = scan((long long)units);
+      const int inc = scan(units);
       const unsigned hit = __ballot_sync(kAll, inc > rem);
       if (hit) {
         const int src = __ffs(hit) - 1;
@@ -682,15 +682,17 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     }
     return rem;
   };
-  const auto begin = [&](long long total, long long& g0) {  // this CTA's share; false: none
-    const int n = (int)max(1ll, min((long long)gridDim.x, total));
+  const auto begin = [&](int total, int& g0) {  // this CTA's share; false: none
+    const int n = max(1, min((int)gridDim.x, total));
     const bool work = (int)blockIdx.x < n && total > 0;
-    g0 = work ? share(total, n, blockIdx.x) : 0;
+    const int per = total / n, extra = total - per * n, c = blockIdx.x;
+    g0 = work ? c * per + c * extra / n : 0;
     if (lane == 0) {
       st.off = 0;
       st.first = g0;
-      st.left = work ? share(total, n, blockIdx.x + 1) - g0 : 0;
-      st.total = total;
+      st.left = work ? (c + 1) * per + (c + 1) * extra / n - g0 : 0;
+      st.per = per;
+      st.extra = extra;
       st.ctas = n;
     }
     return work;
@@ -698,47 +700,46 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
   if (a.kv.n_seqs <= 32) {  // one warp's lanes hold all sequences
     if (warp == 0) {
       Item it;
-      const long long mine = count(lane, it.s);
-      const long long inc = scan(mine);
-      long long g0;
+      const int mine = count(lane, it.s), inc = scan(mine);
+      int g0;
       if (begin(__shfl_sync(kAll, inc, 31), g0)) {
         const int src = __ffs(__ballot_sync(kAll, inc > g0)) - 1;
         it.b = src;
         it.s = SeqInfo{__shfl_sync(kAll, it.s.q0, src), __shfl_sync(kAll, it.s.n, src), __shfl_sync(kAll, it.s.kv, src),
                        true};
-        const long long whole = __shfl_sync(kAll, mine, src), before = __shfl_sync(kAll, inc, src) - whole;
-        const long long off = locate(it, whole, g0 - before);
-        if (lane == 0) st.off = (int)off;
+        const int whole = __shfl_sync(kAll, mine, src), before = __shfl_sync(kAll, inc, src) - whole;
+        const int off = locate(it, whole, g0 - before);
+        if (lane == 0) st.off = off;
       }
     }
   } else {
-    long long* cost = reinterpret_cast<long long*>(smem + C::kSmemRing);  // per sequence; the ring is not in use yet
+    int* cost = reinterpret_cast<int*>(smem + C::kSmemRing);  // per sequence; the ring is not in use yet
     for (int b0 = warp * 32; b0 < a.kv.n_seqs; b0 += C::kThreads) {
       SeqInfo s;
-      const long long mine = count(b0 + lane, s);
+      const int mine = count(b0 + lane, s);
       if (b0 + lane < a.kv.n_seqs) cost[b0 + lane] = mine;
     }
     __syncthreads();
     if (warp == 0) {
-      long long total = 0;
+      int total = 0;
       for (int b = lane; b < a.kv.n_seqs; b += 32) total += cost[b];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-      long long g0;
+      int g0;
       if (begin(total, g0)) {
-        long long at = 0;  // units before the 32 sequences
+        int at = 0;  // units before the 32 sequences
         for (int b0 = 0; b0 < a.kv.n_seqs; b0 += 32) {
           const int b = b0 + lane;
-          const long long mine = b < a.kv.n_seqs ? cost[b] : 0, inc = scan(mine);
+          const int mine = b < a.kv.n_seqs ? cost[b] : 0, inc = scan(mine);
           const unsigned hit = __ballot_sync(kAll, at + inc > g0);
           if (hit) {
             const int src = __ffs(hit) - 1;
             Item it;
             it.b = b0 + src;
             it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, it.b);
-            const long long whole = __shfl_sync(kAll, mine, src), before = at + __shfl_sync(kAll, inc, src) - whole;
-            const long long off = locate(it, whole, g0 - before);
-            if (lane == 0) st.off = (int)off;
+            const int whole = __shfl_sync(kAll, mine, src), before = at + __shfl_sync(kAll, inc, src) - whole;
+            const int off = locate(it, whole, g0 - before);
+            if (lane == 0) st.off = off;
             break;
           }
           at += __shfl_sync(kAll, inc, 31);
@@ -958,7 +959,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     constexpr int kJoin = 128 * kGroups;
     float2* const xch = reinterpret_cast<float2*>(smem + C::kSmemXch);
     unsigned* const counters = reinterpret_cast<unsigned*>(a.ws + 16);
-    long long g_seg = st.first;  // unit at which the segment starts
+    int g_seg = st.first;  // unit at which the segment starts
     // rows of out on 32-byte boundaries: whole sectors at a time
     const bool wide_out = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.o_stride * 2) | (uintptr_t)(a.o_head_stride * 2)) & 31) == 0;
     for (Walk w = walk_begin(st); w.left > 0;) {
@@ -1063,7 +1064,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       }
       float m2 = ref == -INFINITY ? -INFINITY : ref * c2;  // log2 units from here on
       // partial sums: slot 0 if the CTA's first unit is in this item, else 1
-      const long long g_item = g_seg - w.off;
+      const int g_item = g_seg - w.off;
       const int slot = g_seg == st.first ? 0 : 1;
       float* part = part0 + ((size_t)blockIdx.x * 2 + slot) * kPartFloats;
       bool writes = two || grp == 0;  // this group puts out columns
@@ -1088,8 +1089,8 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       }
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
       // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
-      const int c0 = whole ? 0 : owner(st.total, st.ctas, g_item + kItemUnits);
-      const int parts = whole ? 1 : owner(st.total, st.ctas, g_item + w.it.cost() - 1) - c0 + 1;
+      const int c0 = whole ? 0 : owner(st, g_item + kItemUnits);
+      const int parts = whole ? 1 : owner(st, g_item + w.it.cost() - 1) - c0 + 1;
       const bool by_col = w.it.rows > (kColMajor - 1) * parts;
       const uint32_t other_addr = lanes + C::kColO + (grp ^ 1) * D;
       if (writes) {
@@ -1157,7 +1158,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           Cut& cut = st.cut[st.n_cut++];
           cut.c0 = c0;
           cut.parts = parts;
-          cut.slot0 = share(st.total, st.ctas, c0) >= g_item ? 0 : 1;
+          cut.slot0 = share(st, c0) >= g_item ? 0 : 1;
           cut.rows = w.it.rows;
           cut.r0 = w.it.r0;
           cut.q0 = w.it.s.q0;
@@ -1251,6 +1252,12 @@ bool attn_tensor_core(const moe_kv_desc& kv) {
                           (kv.k_page_stride || kv.num_pages == 1) && (kv.v_page_stride || kv.num_pages == 1);
   return (kv.D == 64 || kv.D == 128 || kv.D == 256) && kv.page_size >= 16 && !(kv.page_size & (kv.page_size - 1)) &&
          one_stride;
+}
+
+bool attn_units_fit(const moe_kv_desc& kv, int Hq, int T) {
+  const int64_t kn = kv.D == 256 ? 64 : 128, rows = kv.D == 256 ? 128 : 256;
+  const int64_t tiles = ((int64_t)T * (Hq / kv.Hkv) / rows + kv.n_seqs) * kv.Hkv;
+  return tiles * ((int64_t)kv.max_pages * kv.page_size / kn + 2 + kItemUnits) < (int64_t)1 << 31;
 }
 
 size_t attn_workspace(int, int, int D) {

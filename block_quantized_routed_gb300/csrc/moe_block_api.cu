@@ -193,6 +193,7 @@ int moe_paged_attention(const moe_kv_desc* kv, const void* q, int64_t q_stride, 
   if (!kv_strides16(tidy(*kv)) || q_stride % 8 || q_head_stride % 8 || o_stride % 8 || o_head_stride % 8)
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < attn_workspace(Hq, kv->Hkv, kv->D)) return MOE_ERR_WORKSPACE;
+  if (attn_tensor_core(*kv) && !attn_units_fit(*kv, Hq, T)) return MOE_ERR_UNSUPPORTED;
   AttnArgs a{};
   a.kv = tidy(*kv);
   a.q = q;

@@ -328,6 +328,7 @@ struct AttnArgs {
 };
 size_t attn_workspace(int Hq, int Hkv, int D);
 bool attn_tensor_core(const moe_kv_desc& kv);  // the sizes that launch_attn takes
+bool attn_units_fit(const moe_kv_desc& kv, int Hq, int T);  // the largest possible work of a call stays below 2^31 tiles
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_general(const AttnArgs& a, cudaStream_t s);
 

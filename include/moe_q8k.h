@@ -572,7 +572,8 @@ size_t moe_paged_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D);
  * beyond kv_len is never used.  Head sizes 64, 128 and 256 with a page size
  * that is a power of two >= 16 run on the tensor cores; other sizes run on a
  * general kernel.  The tensor-core form is one cooperative launch of a CTA per
- * SM.  Sequences with cu_q out of order or out of range, or
+ * SM; calls that could hold 2^31 (row tile, key tile) pairs by T, n_seqs and
+ * max_pages alone are refused (MOE_ERR_UNSUPPORTED): cut them.  Sequences with cu_q out of order or out of range, or
  * kv_len outside 0..max_pages*page_size, are skipped and recorded as
  * MOE_ERR_DEVICE_BOUNDS in the status word of ws, as are page numbers outside
  * 0..num_pages (their keys read as zeros). */

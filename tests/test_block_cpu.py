@@ -114,6 +114,12 @@ def test_attention_cache_strides_refused(lib):
         assert attn_rc(lib, kv(**{name: 2052})) == INV      # rows off 16-byte boundaries
 
 
+def test_attention_work_limit(lib):
+    """A million tokens of 128 heads over a table of a million keys could be 2^31 tiles and more: refused."""
+    d = kv(n_seqs=1, Hkv=8, D=128, page_size=64, max_pages=1 << 14, num_pages=1 << 14, table_stride=1 << 14)
+    assert attn_rc(lib, d, Hq=128, qs=16384, os=16384, T=1 << 20) == UNS
+
+
 def test_attention_workspace_size(lib):
     assert moe.moe_paged_attention_workspace_size(32, 8, 128) >= 256
     for bad in [(0, 1, 64), (3, 2, 64), (4, 2, 60), (4, 2, 512), (4, 0, 64)]:
