@@ -253,11 +253,13 @@ __device__ __forceinline__ void item_range(const AttnArgs& a, int G, Item& it) {
   it.tiles = it.hi > it.lo ? (it.hi + kN - 1) / kN - it.t0 : 0;
 }
 
-// The CTA's run of work: `left` units from unit `off` of the current item on.
+// The CTA's run of work: `left` units from unit `off` of the current item on
+// (by_item: a unit is a whole item, off = 0).
 struct Walk {
   Item it;
   int off;
   int left;
+  bool by_item;
 };
 
 // An item whose units several CTAs share (this CTA holds at most two of them).
@@ -273,6 +275,7 @@ struct Start {
   int first, left;  // units
   int per, extra;   // units per CTA of the call, and how many CTAs' worth of remainder (see share)
   int ctas;
+  bool by_item;     // units are whole items (see plan)
   volatile int abort;
   uint32_t tmem;
   int n_cut, arrived;
@@ -284,6 +287,7 @@ __device__ __forceinline__ Walk walk_begin(const Start& st) {
   w.it = st.item;
   w.off = st.off;
   w.left = st.left;
+  w.by_item = st.by_item;
   return w;
 }
 // past the current item, if work is left
@@ -313,16 +317,55 @@ struct Seg {
 };
 __device__ __forceinline__ Seg walk_seg(const Walk& w) {
   Seg s;
-  s.len = min(w.it.cost() - w.off, w.left);
+  s.len = w.by_item ? 1 : min(w.it.cost() - w.off, w.left);
   s.first = max(w.off - kItemUnits, 0);
-  s.last = max(w.off + s.len - kItemUnits, 0);
+  s.last = w.by_item ? w.it.payload() : max(w.off + s.len - kItemUnits, 0);
   s.tiles = w.it.tiles ? s.last - s.first : 0;
   return s;
 }
 
+// a / b for 0 <= a < 2^16, 0 < b <= kMaxCtas: the quotient of a + 1/2 lies at
+// least 1 / (2 b) from a whole number, far more than its error
+__device__ __forceinline__ int small_div(int a, int b) { return (int)__fdividef((float)a + 0.5f, (float)b); }
+
+// How a call's work is divided.  Even shares of units finish together, but an
+// item that is cut costs its parts' way through the workspace and their join:
+// about 6 units, and X = rows * D / 4096 for what they write and read; a CTA
+// that holds parts of two items takes about X again.  So
+//   - whole items, as even in number as they go, if no CTA can then have more
+//     than 6 + X units above its even share,
+//   - else, where all items are alike and fewer than the CTAs, equal numbers
+//     of CTAs for each, if no CTA then has more than X units above it,
+//   - else even shares of units.
+// With 152 CTAs and head size 128, in us:       even shares  equal numbers  whole
+//   64 items of   8 rows over  512 keys                14.7           12.5   12.3
+//   64 items of   8 rows over 2048 keys                24.7           25.2   29.3
+//   32 items of   8 rows over 8192 keys                32.0           34.9   95.2
+//   64 items of 128 rows over 1024 keys                27.7           22.6   19.3
+//   32 items of 128 rows over 8192 keys                43.5           37.3   95.9
+//  128 items of 256 rows over 2048 keys                59.2              -   37.9
+struct Plan {
+  bool by_item;
+  int units, ctas;
+};
+template <int D, int kRows>
+__device__ __forceinline__ Plan plan(int units, int items, int most, int rows) {  // most: units of the largest item
+  // (fp32 will do: every CTA comes to the same plan, and any plan is right.)
+  const int grid = gridDim.x;
+  const float even = __fdividef((float)units, (float)grid), x = (float)(min(rows, kRows) * D) * (1.0f / 4096);
+  if (items && (float)most * ceilf(__fdividef((float)items, (float)grid)) <= even + 6.0f + x)
+    return Plan{true, items, min(grid, items)};
+  int n = grid;
+  if (items && items < grid && (unsigned)most * items == (unsigned)units) {
+    const int each = small_div(grid, items);
+    if ((float)most <= (even + x) * (float)each) n = items * each;
+  }
+  return Plan{false, units, max(1, min(n, units))};
+}
+
 // units before CTA c
 // (A call has fewer than 2^31 units: attn_units_fit.)
-__device__ __forceinline__ int share(const Start& st, int c) { return c * st.per + c * st.extra / st.ctas; }
+__device__ __forceinline__ int share(const Start& st, int c) { return c * st.per + small_div(c * st.extra, st.ctas); }
 // the CTA that holds unit g: a guess, put right
 __device__ __forceinline__ int owner(const Start& st, int g) {
   int c = min((int)(((float)g + 0.5f) / ((float)st.per + (float)st.extra / (float)st.ctas)), st.ctas - 1);
@@ -615,6 +658,9 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   // The units of 32 sequences, a lane per sequence (one of more than four row tiles is counted by the warp).
+  struct Count {
+    int units, items, most;  // most: units of the largest item
+  };
   const auto count = [&](int b, SeqInfo& s) {
     Item it;
     s = SeqInfo{0, 0, 0, true};
@@ -622,11 +668,12 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     if (!s.ok && blockIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     it.s = s;
     const int nt = (s.n * G + kRows - 1) / kRows;
-    int mine = 0;
+    Count mine{0, nt * a.kv.Hkv, 0};
     if (nt <= 4) {
       for (it.i = 0; it.i < nt; ++it.i) {
         item_range<kN, kRows>(a, G, it);
-        mine += it.cost();
+        mine.units += it.cost();
+        mine.most = max(mine.most, it.cost());
       }
     }
     for (unsigned many = __ballot_sync(kAll, nt > 4); many; many &= many - 1) {
@@ -634,16 +681,18 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       Item x;
       x.s = SeqInfo{0, __shfl_sync(kAll, s.n, src), __shfl_sync(kAll, s.kv, src), true};
       const int nx = __shfl_sync(kAll, nt, src);
-      int sum = 0;
+      int sum = 0, most = 0;
       for (x.i = lane; x.i < nx; x.i += 32) {
         item_range<kN, kRows>(a, G, x);
         sum += x.cost();
+        most = max(most, x.cost());
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-      if (lane == src) mine = sum;
+      sum = __reduce_add_sync(kAll, sum);
+      most = __reduce_max_sync(kAll, most);
+      if (lane == src) mine.units = sum, mine.most = most;
     }
-    return mine * a.kv.Hkv;
+    mine.units *= a.kv.Hkv;
+    return mine;
   };
   const auto scan = [&](auto v) {  // inclusive, over the warp
 #pragma unroll
@@ -654,11 +703,17 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     return v;
   };
   // warp 0: the CTA's units [g0, g1) start `rem` units into sequence it.b, of `mine` units in all
-  const auto locate = [&](Item& it, int mine, int rem) {
+  const auto locate = [&](Item& it, bool by_item, int mine, int rem) {
     const int nt = it.tiles_q = (it.s.n * G + kRows - 1) / kRows;
     const int per = mine / a.kv.Hkv;
     it.h = rem / per;
     rem -= it.h * per;
+    if (by_item) {
+      it.i = rem;
+      item_range<kN, kRows>(a, G, it);
+      if (lane == 0) st.item = it;
+      return 0;
+    }
     for (int i0 = 0; i0 < nt; i0 += 32) {
       it.i = i0 + lane;
       int units = 0;
@@ -682,51 +737,67 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     }
     return rem;
   };
-  const auto begin = [&](int total, int& g0) {  // this CTA's share; false: none
-    const int n = max(1, min((int)gridDim.x, total));
+  const auto begin = [&](const Plan& pl, int& g0) {  // this CTA's share; false: none
+    const int total = pl.units, n = pl.ctas;
     const bool work = (int)blockIdx.x < n && total > 0;
     const int per = total / n, extra = total - per * n, c = blockIdx.x;
-    g0 = work ? c * per + c * extra / n : 0;
+    g0 = work ? c * per + small_div(c * extra, n) : 0;
     if (lane == 0) {
       st.off = 0;
       st.first = g0;
-      st.left = work ? (c + 1) * per + (c + 1) * extra / n - g0 : 0;
+      st.left = work ? (c + 1) * per + small_div((c + 1) * extra, n) - g0 : 0;
       st.per = per;
       st.extra = extra;
       st.ctas = n;
+      st.by_item = pl.by_item;
     }
     return work;
   };
   if (a.kv.n_seqs <= 32) {  // one warp's lanes hold all sequences
     if (warp == 0) {
       Item it;
-      const int mine = count(lane, it.s), inc = scan(mine);
+      const Count my = count(lane, it.s);
+      const Plan pl = plan<D, kRows>(__reduce_add_sync(kAll, my.units), __reduce_add_sync(kAll, my.items),
+                                     __reduce_max_sync(kAll, my.most), __reduce_max_sync(kAll, it.s.n) * G);
+      const int mine = pl.by_item ? my.items : my.units, inc = scan(mine);
       int g0;
-      if (begin(__shfl_sync(kAll, inc, 31), g0)) {
+      if (begin(pl, g0)) {
         const int src = __ffs(__ballot_sync(kAll, inc > g0)) - 1;
         it.b = src;
         it.s = SeqInfo{__shfl_sync(kAll, it.s.q0, src), __shfl_sync(kAll, it.s.n, src), __shfl_sync(kAll, it.s.kv, src),
                        true};
         const int whole = __shfl_sync(kAll, mine, src), before = __shfl_sync(kAll, inc, src) - whole;
-        const int off = locate(it, whole, g0 - before);
+        const int off = locate(it, pl.by_item, whole, g0 - before);
         if (lane == 0) st.off = off;
       }
     }
   } else {
-    int* cost = reinterpret_cast<int*>(smem + C::kSmemRing);  // per sequence; the ring is not in use yet
+    // per sequence its units, its items; then per warp the largest item and the most tokens; the ring is not in use yet
+    int* units = reinterpret_cast<int*>(smem + C::kSmemRing);
+    int *items = units + MOE_MAX_SEQS, *peaks = items + MOE_MAX_SEQS;
+    static_assert(C::kStages * C::kSlot >= 4 * (2 * MOE_MAX_SEQS + 2 * C::kThreads / 32), "counts of the sequences");
+    int most = 0, tokens = 0;
     for (int b0 = warp * 32; b0 < a.kv.n_seqs; b0 += C::kThreads) {
       SeqInfo s;
-      const int mine = count(b0 + lane, s);
-      if (b0 + lane < a.kv.n_seqs) cost[b0 + lane] = mine;
+      const Count my = count(b0 + lane, s);
+      if (b0 + lane < a.kv.n_seqs) units[b0 + lane] = my.units, items[b0 + lane] = my.items;
+      most = max(most, my.most);
+      tokens = max(tokens, s.n);
     }
+    most = __reduce_max_sync(kAll, most);
+    tokens = __reduce_max_sync(kAll, tokens);
+    if (lane == 0) peaks[2 * warp] = most, peaks[2 * warp + 1] = tokens;
     __syncthreads();
     if (warp == 0) {
-      int total = 0;
-      for (int b = lane; b < a.kv.n_seqs; b += 32) total += cost[b];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+      int all_units = 0, all_items = 0;
+      for (int b = lane; b < a.kv.n_seqs; b += 32) all_units += units[b], all_items += items[b];
+      most = lane < C::kThreads / 32 ? peaks[2 * lane] : 0;
+      tokens = lane < C::kThreads / 32 ? peaks[2 * lane + 1] : 0;
+      const Plan pl = plan<D, kRows>(__reduce_add_sync(kAll, all_units), __reduce_add_sync(kAll, all_items),
+                                     __reduce_max_sync(kAll, most), __reduce_max_sync(kAll, tokens) * G);
+      const int* cost = pl.by_item ? items : units;
       int g0;
-      if (begin(total, g0)) {
+      if (begin(pl, g0)) {
         int at = 0;  // units before the 32 sequences
         for (int b0 = 0; b0 < a.kv.n_seqs; b0 += 32) {
           const int b = b0 + lane;
@@ -738,7 +809,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
             it.b = b0 + src;
             it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, it.b);
             const int whole = __shfl_sync(kAll, mine, src), before = at + __shfl_sync(kAll, inc, src) - whole;
-            const int off = locate(it, whole, g0 - before);
+            const int off = locate(it, pl.by_item, whole, g0 - before);
             if (lane == 0) st.off = off;
             break;
           }
