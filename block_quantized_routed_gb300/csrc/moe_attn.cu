@@ -11,13 +11,20 @@
 // head.  A work item is (sequence, key/value head, up to 256 rows) over its
 // visible range of keys, cut into tiles of kN keys.
 //
-// Work split.  All items of a call, laid end to end in tiles, are divided
-// evenly over the CTAs (one per SM): every CTA gets the same number of key
-// tiles whatever the lengths.  An item cut by a CTA boundary leaves partial
-// sums in the workspace; when all of them are there, its CTAs join a slice of
-// its rows each, in a fixed order, so results do not depend on timing.  The division is found by each
-// CTA from cu_q and kv_len in a short prologue: no planning launch, no host
-// knowledge of the lengths.
+// Work split.  Each CTA (one per SM) finds its share of the items' key tiles
+// from cu_q and kv_len in a short prologue: no planning launch, no host
+// knowledge of the lengths.  Items stay whole where cutting them costs more
+// than uneven work does; else equal numbers of CTAs share each item, or all
+// tiles, laid end to end, are divided evenly whatever the lengths (see plan).
+// A cut item leaves partial sums in the workspace; when all of them are there,
+// its CTAs join a slice of its rows each, in a fixed order, so results do not
+// depend on timing.
+//
+// What it measured: 2 prompts of up to 4096 new tokens over up to 16384 keys
+// (32 heads over 4 of 128) 700 us, 1500 TFLOP/s, bound by the chain of the
+// softmax and the products that feed it; 48 tokens over up to 8192 keys 77 us,
+// 5.4 TB/s (6.5 to 6.9 where the lengths are equal); one token over 777 keys
+// 10.9 us, latency.
 //
 // Inside a CTA (warp roles): one warp feeds a ring of key and value tiles by
 // TMA through the page table, one issues the MMAs, two gather the query rows,
@@ -58,7 +65,6 @@ constexpr long long kWaitCycles = 2000000000ll;  // ~1 s at 2 GHz
 constexpr int kMaxCtas = 160;                    // the workspace holds the partial sums of this many
 constexpr size_t kWsHead = 1024;                 // status (16 bytes), a counter per CTA
 static_assert(kWsHead >= 16 + 4 * kMaxCtas, "counters");
-constexpr int kColMajor = 32;                    // parts of which each CTA joins at least so many rows lie column by column
 // Units of work: a key tile counts 1, an item kItemUnits more (loading its
 // queries, filling the pipeline, writing its rows).  With 0, 2 and 4 units an
 // 8192-token prompt (32 heads over 4, 128 wide) took 549, 422 and 402 us, 48
@@ -276,6 +282,7 @@ struct Start {
   int per, extra;   // units per CTA of the call, and how many CTAs' worth of remainder (see share)
   int ctas;
   bool by_item;     // units are whole items (see plan)
+  int c0, parts;    // equal numbers of CTAs for the items: the first CTA of this item, and how many take part (else 0)
   volatile int abort;
   uint32_t tmem;
   int n_cut, arrived;
@@ -328,39 +335,43 @@ __device__ __forceinline__ Seg walk_seg(const Walk& w) {
 // least 1 / (2 b) from a whole number, far more than its error
 __device__ __forceinline__ int small_div(int a, int b) { return (int)__fdividef((float)a + 0.5f, (float)b); }
 
-// How a call's work is divided.  Even shares of units finish together, but an
-// item that is cut costs its parts' way through the workspace and their join:
-// about 6 units, and X = rows * D / 4096 for what they write and read; a CTA
-// that holds parts of two items takes about X again.  So
-//   - whole items, as even in number as they go, if no CTA can then have more
-//     than 6 + X units above its even share,
-//   - else, where all items are alike and fewer than the CTAs, equal numbers
-//     of CTAs for each, if no CTA then has more than X units above it,
-//   - else even shares of units.
-// With 152 CTAs and head size 128, in us:       even shares  equal numbers  whole
-//   64 items of   8 rows over  512 keys                14.7           12.5   12.3
-//   64 items of   8 rows over 2048 keys                24.7           25.2   29.3
-//   32 items of   8 rows over 8192 keys                32.0           34.9   95.2
-//   64 items of 128 rows over 1024 keys                27.7           22.6   19.3
-//   32 items of 128 rows over 8192 keys                43.5           37.3   95.9
-//  128 items of 256 rows over 2048 keys                59.2              -   37.9
+// How a call's work is divided: whole items, as even in number as they go; or,
+// where items are few, an equal number of CTAs for each; or even shares of all
+// units.  Even shares finish together, but an item that is cut costs its parts'
+// way through the workspace and their join, and the more, the more of the CTAs
+// hold parts of two items.  In units, with X = rows * D / (16 threads) for what
+// a thread of the softmax groups writes and reads of a part, a CTA is done after
+//   whole items       most * ceil(items / ctas)
+//   equal numbers     most / (ctas / items)  +  6 + X / 3
+//   even shares       units / ctas  +  6 + X / 3  +  (4 + 1.6 X) / max(2, ctas / items)
+// and the least is taken; the constants are fits to 500 measured shapes.  With
+// 152 CTAs, in us:                          whole items  equal numbers  even shares
+//   64 items of   8 rows of 128,  512 keys         12.3           12.9         14.5
+//   64 items of   8 rows of 128, 2048 keys         29.6           22.3         24.3
+//   32 items of   8 rows of 128, 8192 keys         95.0           34.2         32.4
+//   64 items of 128 rows of 128, 1024 keys         19.2           19.1         26.2
+//   32 items of 128 rows of 256, 4096 keys         90.8           39.4         48.6
+//  100 items of 128 rows of 256, 1024 keys         31.6              -         53.9
+//  200 items of   8 rows of  64,  512 keys         17.4              -         22.0
 struct Plan {
   bool by_item;
+  int each;  // CTAs of an item (by_item; 0: whole items, any number to a CTA)
   int units, ctas;
 };
 template <int D, int kRows>
 __device__ __forceinline__ Plan plan(int units, int items, int most, int rows) {  // most: units of the largest item
   // (fp32 will do: every CTA comes to the same plan, and any plan is right.)
   const int grid = gridDim.x;
-  const float even = __fdividef((float)units, (float)grid), x = (float)(min(rows, kRows) * D) * (1.0f / 4096);
-  if (items && (float)most * ceilf(__fdividef((float)items, (float)grid)) <= even + 6.0f + x)
-    return Plan{true, items, min(grid, items)};
-  int n = grid;
-  if (items && items < grid && (unsigned)most * items == (unsigned)units) {
-    const int each = small_div(grid, items);
-    if ((float)most <= (even + x) * (float)each) n = items * each;
-  }
-  return Plan{false, units, max(1, min(n, units))};
+  const float even = __fdividef((float)units, (float)grid), ratio = __fdividef((float)grid, (float)items);
+  const float x = (float)(min(rows, kRows) * D) * (1.0f / (16 * kRows));
+  const float joined = 6.0f + x * (1.0f / 3);
+  const int each = max(1, (int)(ratio + 0.01f));
+  const float whole = (float)most * ceilf(__fdividef((float)items, (float)grid));
+  const float equal = each > 1 ? __fdividef((float)most, (float)each) + joined : INFINITY;
+  const float shares = even + joined + __fdividef(4.0f + 1.6f * x, fmaxf(ratio, 2.0f));
+  if (items && whole <= fminf(equal, shares)) return Plan{true, 0, items, min(grid, items)};
+  if (items && equal <= shares) return Plan{true, each, items, items * each};
+  return Plan{false, 0, units, max(1, min(grid, units))};
 }
 
 // units before CTA c
@@ -440,6 +451,14 @@ __device__ __forceinline__ unsigned count_read(const unsigned* counter) {
   return v;
 }
 
+// A part's accumulator, in vectors of 4 columns: the rows of a vector next to
+// each other, so that a warp's stores (thread = row) and the loads of a slice
+// of rows both take whole sectors; the vectors of a row next to each other
+// where the CTAs join one row each and a part has few (one token of 8 heads of
+// 256 over 32768 keys: 26 against 29 us; a prompt of 78 tokens of 8 heads of
+// 256 over 7275 keys: 31 against 25).
+__device__ __forceinline__ bool part_by_row(int rows, int parts) { return rows <= min(parts, 32); }
+
 // Joins one item's parts.  Every one of its CTAs takes a slice of the rows,
 // once all parts have arrived; the softmax threads of the CTA take part.
 //   M = max_p m_p,  L = sum_p 2^(m_p - M) l_p,  out = sum_p 2^(m_p - M) o_p / L
@@ -483,20 +502,20 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
   int teams = 1;                          // teams of threads share the parts where there are few vectors
   while (n && teams * 2 * n <= kThreads && teams * 2 <= np) teams *= 2;
   const int width = kThreads / teams, team = tid / width;
-  const bool by_col = per >= kColMajor, single = n <= width;  // single: one vector per thread
-  const auto load = [&](const float* src, int row, int c) {
-    if (!by_col) return __ldcg(reinterpret_cast<const float4*>(src + (size_t)(lo + row) * D + c));
-    const float* q = src + (size_t)c * C::kRows + lo + row;
-    return make_float4(__ldcg(q), __ldcg(q + C::kRows), __ldcg(q + 2 * C::kRows), __ldcg(q + 3 * C::kRows));
+  const bool single = n <= width;  // one vector per thread
+  const bool by_row = part_by_row(cut.rows, np);
+  const int cs = by_row ? 1 : cut.rows, rs = by_row ? kVecs : 1;  // steps of a vector's column and row
+  const auto load = [&](const float* src, int row, int v) {
+    return __ldcg(reinterpret_cast<const float4*>(src) + v * cs + (lo + row) * rs);
   };
   // one vector per thread: the first parts are asked for before the weights are known
   constexpr int kAhead = 8;
   float4 ahead[kAhead];
-  const int my = tid % width, my_row = by_col ? my % max(nr, 1) : my / kVecs, my_c = (by_col ? my / max(nr, 1) : my % kVecs) * 4;
+  const int my = tid % width, my_v = small_div(my, max(nr, 1)), my_row = my - my_v * nr;
   if (single && my < n) {
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
-      if (team + i * teams < np) ahead[i] = load(part(team + i * teams) + 2 * C::kRows, my_row, my_c);
+      if (team + i * teams < np) ahead[i] = load(part(team + i * teams) + 2 * C::kRows, my_row, my_v);
   }
   if (np <= 8) {  // many rows each: a thread per row, its loads together
     for (int row = tid; row < nr; row += kThreads) {
@@ -552,10 +571,10 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
   }
   named_sync(4, kThreads);
   if (nr > 0) {  // uniform over the CTA
-    const auto put = [&](int row, int c, float4 v) {
+    const auto put = [&](int row, int col, float4 v) {
       const int R = cut.r0 + lo + row, tok = R / G;
       *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + (int64_t)(cut.q0 + tok) * a.o_stride +
-                                (int64_t)(cut.h * G + R - tok * G) * a.o_head_stride + c) =
+                                (int64_t)(cut.h * G + R - tok * G) * a.o_head_stride + 4 * col) =
           make_uint2(pack16<BF16>(v.x, v.y), pack16<BF16>(v.z, v.w));
     };
     if (single) {
@@ -566,9 +585,9 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
           if (team + i * teams < np) fma4(acc, wgt[(team + i * teams) * per + my_row], ahead[i]);
 #pragma unroll 8
         for (int p = team + kAhead * teams; p < np; p += teams)
-          fma4(acc, wgt[p * per + my_row], load(part(p) + 2 * C::kRows, my_row, my_c));
+          fma4(acc, wgt[p * per + my_row], load(part(p) + 2 * C::kRows, my_row, my_v));
         if (teams > 1) red[tid] = acc;
-        else put(my_row, my_c, acc);
+        else put(my_row, my_v, acc);
       }
     } else {  // several vectors of a thread in flight
       constexpr int kB = 4;
@@ -579,10 +598,10 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
         for (int i = 0; i < kB; ++i) {
           const int e = min(e0 + i * width, n - 1);  // the last vector again where there is none
           acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          row[i] = by_col ? e % nr : e / kVecs;
-          c[i] = (by_col ? e / nr : e % kVecs) * 4;
+          c[i] = small_div(e, nr);
+          row[i] = e - c[i] * nr;
         }
-#pragma unroll 2
+#pragma unroll (C::kGroups == 1 ? 4 : 2)  // a group of threads less: more loads of each in flight
         for (int p = 0; p < np; ++p) {
           const float* src = part(p) + 2 * C::kRows;
 #pragma unroll
@@ -601,7 +620,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
           const float4 v = red[t * width + tid];
           acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
         }
-        put(my_row, my_c, acc);
+        put(my_row, my_v, acc);
       }
     }
   }
@@ -703,16 +722,28 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     return v;
   };
   // warp 0: the CTA's units [g0, g1) start `rem` units into sequence it.b, of `mine` units in all
-  const auto locate = [&](Item& it, bool by_item, int mine, int rem) {
+  const auto locate = [&](Item& it, const Plan& pl, int mine, int rem) {
     const int nt = it.tiles_q = (it.s.n * G + kRows - 1) / kRows;
     const int per = mine / a.kv.Hkv;
     it.h = rem / per;
     rem -= it.h * per;
-    if (by_item) {
+    if (pl.by_item) {
       it.i = rem;
       item_range<kN, kRows>(a, G, it);
-      if (lane == 0) st.item = it;
-      return 0;
+      int off = 0;
+      if (lane == 0) {
+        st.item = it;
+        if (pl.each) {  // this CTA's part of the payload
+          const int parts = min(pl.each, it.payload()), part = blockIdx.x - st.first * pl.each;
+          const int q = it.payload() / parts, r = it.payload() - q * parts;
+          const int first = part * q + small_div(part * r, parts), last = (part + 1) * q + small_div((part + 1) * r, parts);
+          off = first ? kItemUnits + first : 0;
+          st.c0 = st.first * pl.each;
+          st.parts = parts;
+          st.left = part < parts ? kItemUnits + last - off : 0;
+        }
+      }
+      return off;
     }
     for (int i0 = 0; i0 < nt; i0 += 32) {
       it.i = i0 + lane;
@@ -738,10 +769,10 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     return rem;
   };
   const auto begin = [&](const Plan& pl, int& g0) {  // this CTA's share; false: none
-    const int total = pl.units, n = pl.ctas;
-    const bool work = (int)blockIdx.x < n && total > 0;
-    const int per = total / n, extra = total - per * n, c = blockIdx.x;
-    g0 = work ? c * per + small_div(c * extra, n) : 0;
+    const int total = pl.units, n = pl.ctas, c = blockIdx.x;
+    const bool work = c < n && total > 0;
+    const int per = pl.each ? 0 : total / n, extra = total - per * n;
+    g0 = !work ? 0 : pl.each ? small_div(c, pl.each) : c * per + small_div(c * extra, n);
     if (lane == 0) {
       st.off = 0;
       st.first = g0;
@@ -749,7 +780,8 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       st.per = per;
       st.extra = extra;
       st.ctas = n;
-      st.by_item = pl.by_item;
+      st.by_item = pl.by_item && !pl.each;
+      st.parts = 0;
     }
     return work;
   };
@@ -767,7 +799,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         it.s = SeqInfo{__shfl_sync(kAll, it.s.q0, src), __shfl_sync(kAll, it.s.n, src), __shfl_sync(kAll, it.s.kv, src),
                        true};
         const int whole = __shfl_sync(kAll, mine, src), before = __shfl_sync(kAll, inc, src) - whole;
-        const int off = locate(it, pl.by_item, whole, g0 - before);
+        const int off = locate(it, pl, whole, g0 - before);
         if (lane == 0) st.off = off;
       }
     }
@@ -809,7 +841,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
             it.b = b0 + src;
             it.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, it.b);
             const int whole = __shfl_sync(kAll, mine, src), before = at + __shfl_sync(kAll, inc, src) - whole;
-            const int off = locate(it, pl.by_item, whole, g0 - before);
+            const int off = locate(it, pl, whole, g0 - before);
             if (lane == 0) st.off = off;
             break;
           }
@@ -1160,9 +1192,10 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       }
       const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
       // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
-      const int c0 = whole ? 0 : owner(st, g_item + kItemUnits);
-      const int parts = whole ? 1 : owner(st, g_item + w.it.cost() - 1) - c0 + 1;
-      const bool by_col = w.it.rows > (kColMajor - 1) * parts;
+      const int c0 = whole ? 0 : st.parts ? st.c0 : owner(st, g_item + kItemUnits);
+      const int parts = whole ? 1 : st.parts ? st.parts : owner(st, g_item + w.it.cost() - 1) - c0 + 1;
+      const bool by_row = part_by_row(w.it.rows, parts);
+      const int part_cs = by_row ? 1 : w.it.rows, part_rs = by_row ? D / 4 : 1;
       const uint32_t other_addr = lanes + C::kColO + (grp ^ 1) * D;
       if (writes) {
         constexpr int kW = kGroups == 1 ? 64 : 32;  // columns at a time
@@ -1202,15 +1235,12 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
                 for (int j = 0; j < kW / 2; j += 4)
                   *reinterpret_cast<uint4*>(out + 2 * j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
               }
-            } else if (by_col) {  // a warp's stores of one column are contiguous
-              uint32_t* dst = reinterpret_cast<uint32_t*>(part) + 2 * kRows + (size_t)x0 * kRows + row;
-#pragma unroll
-              for (int j = 0; j < kW; ++j) dst[j * kRows] = o[j];
             } else {
-              uint32_t* dst = reinterpret_cast<uint32_t*>(part) + 2 * kRows + (size_t)row * D + x0;
+              float4* dst = reinterpret_cast<float4*>(part + 2 * kRows) + x0 / 4 * part_cs + row * part_rs;
 #pragma unroll
               for (int j = 0; j < kW; j += 4)
-                *reinterpret_cast<uint4*>(dst + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                dst[j / 4 * part_cs] = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                 __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
             }
           }
           __syncwarp();
@@ -1229,7 +1259,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           Cut& cut = st.cut[st.n_cut++];
           cut.c0 = c0;
           cut.parts = parts;
-          cut.slot0 = share(st, c0) >= g_item ? 0 : 1;
+          cut.slot0 = st.parts || share(st, c0) >= g_item ? 0 : 1;
           cut.rows = w.it.rows;
           cut.r0 = w.it.r0;
           cut.q0 = w.it.s.q0;

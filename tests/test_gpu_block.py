@@ -463,6 +463,34 @@ def test_attention_workspace_is_reused():
     assert status(ws) == 0
 
 
+DIVISIONS = [  # the ways in which a call's work is divided: new tokens, keys, query heads, key/value heads
+    ([1] * 90, [i * 53 % 250 + 1 for i in range(90)], 8, 4),         # whole items, several to a CTA, over 32 sequences
+    ([40] * 20, [40 + 9 * i for i in range(20)], 16, 2),             # whole items of several row tiles
+    ([4, 0, 4, 4], [3000, 0, 130, 4], 16, 2),                        # equal numbers; an item of fewer tiles than CTAs
+    ([60], [2500], 16, 2),                                           # equal numbers, many rows
+    ([1] * 40, [2000 - 25 * i for i in range(40)], 8, 1),            # equal numbers, over 32 sequences
+    ([1] * 100, [i * 131 % 4000 + 500 for i in range(100)], 8, 1),   # even shares, few rows
+    ([30] * 50, [1000 + 10 * i for i in range(50)], 8, 2),           # even shares, many rows
+]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv", DIVISIONS)
+def test_attention_division_of_work(q_lens, kv_lens, hq, hkv, D):
+    check_attention(q_lens, kv_lens, hq, hkv, D, 64)
+
+
+def test_attention_divisions_share_a_workspace():
+    """Calls that divide their work in different ways leave the counters as they found them."""
+    ws = torch.zeros(moe.moe_paged_attention_workspace_size(16, 2, 128), dtype=torch.uint8, device="cuda")
+    cs = [(Cache(q, kv, hkv, 128, 64, BF16, 90), hq) for q, kv, hq, hkv in DIVISIONS if hkv == 2]
+    first = [attend(c, hq, 128, 0.1, 0, BF16, 91)[1].clone() for c, hq in cs]
+    for _ in range(3):
+        for (c, hq), want in zip(cs, first):
+            assert torch.equal(attend(c, hq, 128, 0.1, 0, BF16, 91, ws=ws)[1].view(torch.int16), want.view(torch.int16))
+    assert status(ws) == 0
+
+
 @pytest.mark.parametrize("D,page", [(64, 32), (128, 16), (256, 64), (80, 16)])
 def test_attention_bad_tables_are_reported(D, page):
     c = Cache([2, 3, 1], [100, 90, 70], 2, D, page, BF16, 63)
