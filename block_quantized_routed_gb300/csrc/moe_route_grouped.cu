@@ -17,8 +17,10 @@
 // tie in any precision and goes to the lower index.
 //
 // What bounds it: instruction issue, about 900 warp instructions a token at
-// 256 experts and k = 8 (8192 tokens: 17 us in 8 groups with a bias, 10 us
-// without either; their 8 MB take 1.3 us).
+// 256 experts and k = 8 (8192 tokens: 14 us in 8 groups with a bias, their 8 MB
+// take 1.3 us); for few tokens the latency of the rounds, and more so of code
+// that is fetched for the first time.  So a lane holds no more keys than it has
+// to (528 experts in lanes of 20 and not 32, one warp per CTA: 12 to 6 us).
 //
 // Error bound of a key p + b, in units of 2^-24.  exp32 is within 4 (2 ulp) and
 // 1.5 |x| (its argument is scaled and rounded).  Sigmoid: the error of e^-l
@@ -202,7 +204,9 @@ __device__ __forceinline__ void top2_add(float& first, float& second, float v) {
   first = fmaxf(first, v);
 }
 
-// Batcher's odd-even merge sort of N (a power of two) keys, largest first.
+// Batcher's odd-even merge sort of N keys, largest first: that of the next
+// power of two without the comparisons that reach past N (where the smallest
+// keys would lie and stay).
 // (P, Q: the step, as template arguments so that every index is a constant.)
 template <int N, int P, int Q>
 __device__ __forceinline__ void sort_step(uint32_t (&k)[N]) {
@@ -220,7 +224,7 @@ __device__ __forceinline__ void sort_step(uint32_t (&k)[N]) {
 }
 
 // NP >= ceil(E / 32): elements per lane; lane i holds elements i * npl on.
-// VEC: npl = NP, E = 32 * NP and the rows are 16-byte aligned (wide loads).
+// VEC: npl = NP, E = 32 * NP, and the rows and the bias are 16-byte aligned (wide loads).
 template <int NP, bool VEC>
 __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   __shared__ double s_buf[4][NP * 32];  // keys: of groups that do not fall on lane boundaries (fp32); of select64
@@ -257,9 +261,31 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < NP; ++j) l[j] = l[j] != l[j] ? -INFINITY : l[j];
-  } else {
+  } else {  // (the type is looked at once, so that the loads are under way together)
+    const auto load = [&](auto* src, auto wide) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j) l[j] = j < have ? load_logit(a, row + e0 + j) : -INFINITY;
+      for (int j = 0; j < NP; ++j) l[j] = j < have ? wide(src[row + e0 + j]) : -INFINITY;
+    };
+    if (a.dtype == MOE_DT_F32) load(static_cast<const float*>(a.logits), [](float v) { return v; });
+    else if (a.dtype == MOE_DT_BF16)
+      load(static_cast<const __nv_bfloat16*>(a.logits), [](__nv_bfloat16 v) { return __bfloat162float(v); });
+    else load(static_cast<const __half*>(a.logits), [](__half v) { return __half2float(v); });
+#pragma unroll
+    for (int j = 0; j < NP; ++j) l[j] = l[j] != l[j] ? -INFINITY : l[j];
+  }
+
+  float b[NP];  // the bias
+  if (a.bias) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int j = 0; j < NP; j += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(a.bias + e0 + j));
+        b[j] = v.x, b[j + 1] = v.y, b[j + 2] = v.z, b[j + 3] = v.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) b[j] = j < have ? __ldg(a.bias + e0 + j) : 0.0f;
+    }
   }
 
   Stats st{0.0f, 1.0f};  // of the softmax
@@ -283,11 +309,12 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   // score takes p (+ b) where it adds two keys
   const bool scored = a.bias != nullptr;
   uint32_t key[NP];
+  if (scored) {
 #pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    float v = l[j];
-    if (scored && j < have) v = score32(v, a.route, st) + __ldg(a.bias + e0 + j);
-    key[j] = j < have ? order_key(v) : 0u;
+    for (int j = 0; j < NP; ++j) key[j] = j < have ? order_key(score32(l[j], a.route, st) + b[j]) : 0u;
+  } else {
+#pragma unroll
+    for (int j = 0; j < NP; ++j) key[j] = j < have ? order_key(l[j]) : 0u;
   }
 
   bool unsure = false;
@@ -314,13 +341,19 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
       for (int j = 0; j < NP; ++j)
         if (j < have) s_val[e0 + j] = value(j);
       __syncwarp();
-      if (lane < a.n_group) {
-        int i = lane % gs;  // groups start at different elements: different banks
-        for (int j = 0; j < gs; ++j) {
-          top2_add(first, second, s_val[lane * gs + i]);
-          if (++i == gs) i = 0;
-        }
+      // as many lanes per group as there are, a power of two
+      int share = 32;
+      while (share * a.n_group > 32) share >>= 1;
+      if (lane < share * a.n_group) {
+        const float* val = s_val + lane / share * gs;
+        for (int j = lane & (share - 1); j < gs; j += share) top2_add(first, second, val[j]);
       }
+      for (int o = 1; o < share; o <<= 1) {
+        const float f = __shfl_xor_sync(kAll, first, o), s2 = __shfl_xor_sync(kAll, second, o);
+        top2_join(first, second, f, s2);
+      }
+      first = __shfl_sync(kAll, first, lane * share & 31);
+      second = __shfl_sync(kAll, second, lane * share & 31);
     }
     float score = -INFINITY, err = 0.0f;
     if (lane < a.n_group) {
@@ -470,8 +503,8 @@ template <int NP>
 void launch_np(const RouteArgs& a, unsigned grid, int warps, cudaStream_t s) {
   const int size = a.dtype == MOE_DT_F32 ? 4 : 2;
   const bool vec = a.E == 32 * NP && reinterpret_cast<uintptr_t>(a.logits) % 16 == 0 &&
-                   (a.T == 1 || a.stride * size % 16 == 0);
-  if constexpr (NP >= 8) {
+                   (a.T == 1 || a.stride * size % 16 == 0) && reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
+  if constexpr (NP % 8 == 0) {
     if (vec) {
       route_grouped_kernel<NP, true><<<grid, 32 * warps, 0, s>>>(a);
       return;
@@ -491,7 +524,10 @@ cudaError_t launch_route_grouped(const RouteArgs& a, cudaStream_t s) {
   if (npl <= 2) launch_np<2>(a, grid, warps, s);
   else if (npl <= 4) launch_np<4>(a, grid, warps, s);
   else if (npl <= 8) launch_np<8>(a, grid, warps, s);
+  else if (npl <= 12) launch_np<12>(a, grid, warps, s);
   else if (npl <= 16) launch_np<16>(a, grid, warps, s);
+  else if (npl <= 20) launch_np<20>(a, grid, warps, s);
+  else if (npl <= 24) launch_np<24>(a, grid, warps, s);
   else launch_np<32>(a, grid, warps, s);
   return cudaGetLastError();
 }

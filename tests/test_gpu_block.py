@@ -183,6 +183,30 @@ def test_route_groups(E, n_group, topk_group, k, top2):
         check_route(l, None, k, sigmoid, n_group, topk_group, top2, dtype=BF16)
 
 
+@pytest.mark.parametrize("E", [65, 129, 257, 320, 384, 385, 512, 513, 600, 640, 641, 768, 769, 896])
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_numbers_of_experts(E, sigmoid):
+    """Sizes around those at which a lane's number of elements changes; groups that straddle lanes."""
+    rng = np.random.default_rng(E)
+    l = (1.5 * rng.standard_normal((77, E))).astype(np.float32)
+    bias = (0.05 * rng.standard_normal(E)).astype(np.float32)
+    for dtype in (F32, BF16, F16):
+        check_route(l, bias, 16, sigmoid, dtype=dtype)
+        check_route(l, None, 3, sigmoid, dtype=dtype)
+    for n_group in (n for n in (2, 3, 4, 5, 7, 8, 15, 16, 31, 32) if E % n == 0):
+        keep = max(1, n_group // 3)
+        for top2 in (True, False):
+            check_route(l, bias, min(6, keep * (E // n_group)), sigmoid, n_group, keep, top2)
+    shifted = torch.zeros(E + 1, device="cuda")[1:]         # a bias off the 16-byte boundary
+    shifted.copy_(torch.from_numpy(bias))
+    ids = torch.full((77, 8), -1, dtype=torch.int32, device="cuda")
+    gates = torch.full((77, 8), NAN, device="cuda")
+    moe.moe_route_grouped(torch.from_numpy(l).cuda(), 8, ids, gates, bias=shifted,
+                          route=moe.ROUTE_SIGMOID if sigmoid else moe.ROUTE_SOFTMAX)
+    want, _ = block_ref.route(l, bias, 8, sigmoid, 1, 1, False, True, 1.0)
+    np.testing.assert_array_equal(ids.cpu().numpy(), want)
+
+
 def test_route_ties_go_to_the_lower_index():
     l = np.tile(np.array([1.0, 1.0, 0.5, 1.0, -2.0, 0.5], np.float32), (40, 16))          # 96 experts, many equal
     for bias in (None, np.zeros(96, np.float32)):
