@@ -149,12 +149,13 @@ __device__ __forceinline__ float rcp(float x) {  // the approximation (1 ulp) an
   return fmaf(y, fmaf(-x, y, 1.0f), y);
 }
 
-// The 8-bit output of one row z (s[NV][8]); `peak` is the row's largest |z|
-// (row-scaled outputs only).  FMT: the format, or
-// -1 for a.q_fmt.  The scale d is an IEEE quotient; z / d is the product with
-// d's reciprocal, which for int8 codes is put right near a half.
+// The 8-bit output of one row z = v * r (v in s[NV][8]; r = 1 but for fp8
+// codes, which r does not change: they are v over the largest |v|, a rounding
+// less).  `peak` is the row's largest |v| (row-scaled outputs only).  FMT: the
+// format, or -1 for a.q_fmt.  The scale d is an IEEE quotient; v / d is the
+// product with d's reciprocal, which for int8 codes is put right near a half.
 template <int NV, bool WIDE, int FMT>
-__device__ __forceinline__ void put_codes(const NormArgs& a, int64_t row, float (&s)[NV][8], float peak) {
+__device__ __forceinline__ void put_codes(const NormArgs& a, int64_t row, float (&s)[NV][8], float peak, float r) {
   const int tid = threadIdx.x, nt = blockDim.x;
   const int fmt = FMT >= 0 ? FMT : a.q_fmt;
   const bool fp8 = fmt == MOE_NORM_Q_E4M3_G128 || fmt == MOE_NORM_Q_E4M3_ROW;
@@ -163,7 +164,7 @@ __device__ __forceinline__ void put_codes(const NormArgs& a, int64_t row, float 
   float d = 0.0f;
   if (per_row) {
     d = __fdiv_rn(peak, top);
-    if (tid == 0) a.d[row] = d;
+    if (tid == 0) a.d[row] = fp8 ? __fdiv_rn(peak * r, top) : d;
   }
   const int group = fmt == MOE_NORM_Q_Q8K ? 256 : 128;
   uint8_t* const out = static_cast<uint8_t*>(a.q) + row * a.H;
@@ -190,9 +191,9 @@ __device__ __forceinline__ void put_codes(const NormArgs& a, int64_t row, float 
     const int c = (i * nt + tid) * 8, n = a.H - c;
     if (!per_row) {
       d = __fdiv_rn(m[i], top);
-      if (n > 0 && c % group == 0) dout[c / group] = d;
+      if (n > 0 && c % group == 0) dout[c / group] = fp8 ? __fdiv_rn(m[i] * r, top) : d;
     }
-    // d = 0 only where every z of the group is 0 (or too small for its quotient to exist).  A reciprocal beyond
+    // d = 0 only where every v of the group is 0 (or too small for its quotient to exist).  A reciprocal beyond
     // fp32 (d below 2^-126) is not used: such groups are divided.
     float inv = d > 0.0f ? rcp(d) : 0.0f, dq = d;
     if (d < 1.2e-38f && d > 0.0f) {
@@ -372,7 +373,8 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 2 ? 2 : 1) add_rms
     block_reduce<true, false>(sq, peak, buf);
   }
   const float r = rsqrtf(fmaf(sq, 1.0f / (float)a.H, a.eps));
-  if constexpr (kEarly) peak = fmaxf(peak * r, 0.0f);  // (no number: 0, as the maximum of the |z| would be)
+  const bool fp8 = fmt == MOE_NORM_Q_E4M3_G128 || fmt == MOE_NORM_Q_E4M3_ROW;
+  if (kEarly && !fp8) peak = fmaxf(peak * r, 0.0f);  // (no number: 0, as the maximum of the |z| would be)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * nt + tid) * 8, n = a.H - c;
@@ -383,11 +385,16 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 2 ? 2 : 1) add_rms
       for (int j = 0; j < 8; j += 2) {
         float2 z = make_float2(s[i][j], s[i][j + 1]);
         if constexpr (!kEarly) z = mul2(z, make_float2(w[j] + a.w_offset, w[j + 1] + a.w_offset));
-        z = mul2(z, make_float2(r, r));
+        if (!fp8) z = mul2(z, make_float2(r, r));
         s[i][j] = z.x;
         s[i][j + 1] = z.y;
       }
-      if (a.y) store8_dt<WIDE>(a.y, a.y_dtype, row * a.y_stride + c, n, s[i]);
+      if (a.y) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = fp8 ? s[i][j] * r : s[i][j];
+        store8_dt<WIDE>(a.y, a.y_dtype, row * a.y_stride + c, n, y);
+      }
     }
     if (!kEarly && per_row) {
 #pragma unroll
@@ -395,7 +402,7 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 2 ? 2 : 1) add_rms
     }
   }
   if (!kEarly && per_row) block_reduce<false, true>(sq, peak, buf);
-  if (fmt != MOE_NORM_Q_NONE) put_codes<NV, WIDE, FMT>(a, row, s, peak);
+  if (fmt != MOE_NORM_Q_NONE) put_codes<NV, WIDE, FMT>(a, row, s, peak, r);
 }
 
 template <typename XT, typename RT, int NV, bool WIDE>
