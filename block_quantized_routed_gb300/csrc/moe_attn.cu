@@ -21,10 +21,10 @@
 // depend on timing.
 //
 // What it measured: 2 prompts of up to 4096 new tokens over up to 16384 keys
-// (32 heads over 4 of 128) 700 us, 1500 TFLOP/s, bound by the chain of the
-// softmax and the products that feed it; 48 tokens over up to 8192 keys 77 us,
-// 5.4 TB/s (6.5 to 6.9 where the lengths are equal); one token over 777 keys
-// 10.9 us, latency.
+// (32 heads over 4 of 128) 690 us, 1520 TFLOP/s, bound by the chain of the
+// softmax and the products that feed it; 48 tokens over up to 8192 keys 74 us,
+// 5.5 TB/s (6.6 to 6.9 where the lengths are equal); one token over 777 keys
+// 10.7 us, latency.
 //
 // Inside a CTA (warp roles): one warp feeds a ring of key and value tiles by
 // TMA through the page table, one issues the MMAs, two gather the query rows,
@@ -342,17 +342,17 @@ __device__ __forceinline__ int small_div(int a, int b) { return (int)__fdividef(
 // hold parts of two items.  In units, with X = rows * D / (16 threads) for what
 // a thread of the softmax groups writes and reads of a part, a CTA is done after
 //   whole items       most * ceil(items / ctas)
-//   equal numbers     most / (ctas / items)  +  6 + X / 3
-//   even shares       units / ctas  +  6 + X / 3  +  (4 + 1.6 X) / max(2, ctas / items)
-// and the least is taken; the constants are fits to 500 measured shapes.  With
+//   equal numbers     most / (ctas / items)  +  7 + X / 5
+//   even shares       units / ctas  +  7 + X / 5  +  (12 + X) / max(2, ctas / items)
+// and the least is taken; the constants are fits to 800 measured shapes.  With
 // 152 CTAs, in us:                          whole items  equal numbers  even shares
-//   64 items of   8 rows of 128,  512 keys         12.3           12.9         14.5
-//   64 items of   8 rows of 128, 2048 keys         29.6           22.3         24.3
-//   32 items of   8 rows of 128, 8192 keys         95.0           34.2         32.4
-//   64 items of 128 rows of 128, 1024 keys         19.2           19.1         26.2
-//   32 items of 128 rows of 256, 4096 keys         90.8           39.4         48.6
-//  100 items of 128 rows of 256, 1024 keys         31.6              -         53.9
-//  200 items of   8 rows of  64,  512 keys         17.4              -         22.0
+//   64 items of   8 rows of 128,  512 keys         11.2           12.7         14.1
+//   64 items of   8 rows of 128, 2048 keys         23.3           21.9         24.6
+//   32 items of   8 rows of 128, 8192 keys         67.8           32.4         32.9
+//   64 items of 128 rows of 128, 1024 keys         17.4           18.8         26.2
+//   32 items of 128 rows of 256, 4096 keys         65.5           39.2         48.2
+//  100 items of 128 rows of 256, 1024 keys         28.9              -         53.3
+//  200 items of   8 rows of  64,  512 keys         15.8              -         21.7
 struct Plan {
   bool by_item;
   int each;  // CTAs of an item (by_item; 0: whole items, any number to a CTA)
@@ -364,11 +364,11 @@ __device__ __forceinline__ Plan plan(int units, int items, int most, int rows) {
   const int grid = gridDim.x;
   const float even = __fdividef((float)units, (float)grid), ratio = __fdividef((float)grid, (float)items);
   const float x = (float)(min(rows, kRows) * D) * (1.0f / (16 * kRows));
-  const float joined = 6.0f + x * (1.0f / 3);
+  const float joined = 7.0f + 0.2f * x;
   const int each = max(1, (int)(ratio + 0.01f));
   const float whole = (float)most * ceilf(__fdividef((float)items, (float)grid));
   const float equal = each > 1 ? __fdividef((float)most, (float)each) + joined : INFINITY;
-  const float shares = even + joined + __fdividef(4.0f + 1.6f * x, fmaxf(ratio, 2.0f));
+  const float shares = even + joined + __fdividef(12.0f + x, fmaxf(ratio, 2.0f));
   if (items && whole <= fminf(equal, shares)) return Plan{true, 0, items, min(grid, items)};
   if (items && equal <= shares) return Plan{true, each, items, items * each};
   return Plan{false, 0, units, max(1, min(grid, units))};
@@ -864,8 +864,11 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpLoad) {
       // ---- keys and values by TMA, a box per (page, 64 columns)
-      const int ps = a.kv.page_size;
-      const int box_rows = min(ps, kN);
+      // (Page and box sizes are powers of two, and the next copy's page is asked for before this copy's slot is waited
+      // for: with divisions and the page on the spot the copies were the bound where a key tile serves 128 rows or fewer,
+      // an 8192-token prompt at head size 256 1175 us, now 950.)
+      const int ps = a.kv.page_size, page_log = 31 - __clz(ps);
+      const int box_rows = min(ps, kN), box_log = 31 - __clz(box_rows);
       const uint32_t box_bytes = (uint32_t)box_rows * 128;
       const int part = lane % C::kSub, box = lane / C::kSub;  // this lane's box of a tile
       uint32_t n_ops = 0;
@@ -875,32 +878,41 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         const int m = sg.tiles;
         const bool two = kGroups == 2 && w.it.rows > 128;
         const int32_t* table = a.table + (int64_t)w.it.b * a.kv.table_stride;
-        for (int o = 0; o < 2 * m; ++o) {
+        struct Copy {
+          int k0, b0, b1, page;  // its first key, the boxes that hold a visible key, this lane's page
           bool value;
-          const int tile = w.it.t0 + sg.first + ring_op(o, m, two, value);
-          const int k0 = tile * kN, from = max(w.it.lo, k0), to = min(w.it.hi, k0 + kN);
-          // boxes of the tile that hold a visible key
-          const int b0 = (from - k0) / box_rows, b1 = (to - k0 + box_rows - 1) / box_rows;
-          const bool mine = box >= b0 && box < b1;
-          int page = 0;
-          if (mine) {
-            page = __ldg(table + (k0 + box * box_rows) / ps);
-            if (page < 0 || page >= a.kv.num_pages) {
-              set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-              page = a.kv.num_pages;  // out of range: reads as zeros
-            }
-          }
+        };
+        const auto prepare = [&](int o) {
+          Copy c;
+          c.k0 = (w.it.t0 + sg.first + ring_op(o, m, two, c.value)) * kN;
+          c.b0 = (max(w.it.lo, c.k0) - c.k0) >> box_log;
+          c.b1 = (min(w.it.hi, c.k0 + kN) - c.k0 + box_rows - 1) >> box_log;
+          c.page = 0;
+          if (box >= c.b0 && box < c.b1) c.page = __ldg(table + ((c.k0 + (box << box_log)) >> page_log));
+          return c;
+        };
+        Copy next = m ? prepare(0) : Copy{0, 0, 0, 0, false};
+        for (int o = 0; o < 2 * m; ++o) {
+          const Copy c = next;
+          const bool mine = box >= c.b0 && box < c.b1;
+          if (o + 1 < 2 * m) next = prepare(o + 1);
           const int slot = n_ops % kStages;
           const uint32_t round = n_ops / kStages;
           if (round > 0) {
             ok = __all_sync(kAll, wait(empty(slot), (round - 1) & 1));
             if (!ok) break;
           }
-          if (lane == 0) bar_expect(full(slot), box_bytes * (uint32_t)((b1 - b0) * C::kSub));
+          if (lane == 0) bar_expect(full(slot), box_bytes * (uint32_t)((c.b1 - c.b0) * C::kSub));
           __syncwarp();
-          if (mine)
-            tma_4d(base + C::kSmemRing + slot * C::kSlot + part * (kN * 128) + box * box_bytes, value ? &vmap : &kmap,
-                   part * 64, (k0 + box * box_rows) % ps, w.it.h, page, full(slot));
+          if (mine) {
+            int page = c.page;
+            if (page < 0 || page >= a.kv.num_pages) {
+              set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+              page = a.kv.num_pages;  // out of range: reads as zeros
+            }
+            tma_4d(base + C::kSmemRing + slot * C::kSlot + part * (kN * 128) + box * box_bytes,
+                   c.value ? &vmap : &kmap, part * 64, (c.k0 + (box << box_log)) & (ps - 1), w.it.h, page, full(slot));
+          }
           ++n_ops;
         }
         walk_next<kN, kRows>(a, G, w, sg.len);
