@@ -385,26 +385,6 @@ __device__ __forceinline__ int owner(const Start& st, int g) {
   return c;
 }
 
-// The ring's order: pair(o) is the o-th load of a segment of m tiles, a key
-// tile (value = false) or a value tile.  Items of two row tiles consume K0 V0
-// K1 V1 ..; the others run one tile ahead: K0 K1 V0 K2 V1 .. V(m-1).
-__device__ __forceinline__ int ring_op(int o, int m, bool two, bool& value) {
-  if (two) {
-    value = o & 1;
-    return o >> 1;
-  }
-  if (o == 2 * m - 1) {
-    value = true;
-    return m - 1;
-  }
-  if (o < 2) {
-    value = false;
-    return o;
-  }
-  value = !(o & 1);
-  return value ? (o - 2) >> 1 : (o + 1) >> 1;
-}
-
 struct Wait {
   Start* st;
   int* status;
@@ -864,56 +844,64 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kWarpLoad) {
       // ---- keys and values by TMA, a box per (page, 64 columns)
-      // (Page and box sizes are powers of two, and the next copy's page is asked for before this copy's slot is waited
-      // for: with divisions and the page on the spot the copies were the bound where a key tile serves 128 rows or fewer,
-      // an 8192-token prompt at head size 256 1175 us, now 950.)
+      // (Page and box sizes are powers of two; what a tile's keys and values share is formed once, and the next tile's
+      // page is asked for before this one's slots are waited for: with divisions and the page on the spot the copies
+      // were the bound where a key tile serves 128 rows or fewer, an 8192-token prompt at head size 256 1175 us, now
+      // 950.  One thread for all boxes of a tile was slower: 38 decoded tokens over 8192 keys of 64 79 us against 60.)
       const int ps = a.kv.page_size, page_log = 31 - __clz(ps);
       const int box_rows = min(ps, kN), box_log = 31 - __clz(box_rows);
       const uint32_t box_bytes = (uint32_t)box_rows * 128;
       const int part = lane % C::kSub, box = lane / C::kSub;  // this lane's box of a tile
-      uint32_t n_ops = 0;
+      const uint32_t my_dst = base + C::kSmemRing + part * (kN * 128) + box * box_bytes;
+      uint32_t n_ops = 0, slot = 0, phase = 1;  // of the ring: the first round's slots are free
       bool ok = true;
+      struct Tile {
+        uint32_t bytes;  // of the boxes that hold a visible key
+        int row, page;   // this lane's box: first row of its page
+        bool mine;
+      };
       for (Walk w = walk_begin(st); w.left > 0 && ok;) {
         const Seg sg = walk_seg(w);
-        const int m = sg.tiles;
-        const bool two = kGroups == 2 && w.it.rows > 128;
+        // The ring's order: items of two row tiles consume K0 V0 K1 V1 .., the others run one tile ahead, K0 K1 V0 K2 V1
+        // .. V(m-1).
+        const int m = sg.tiles, lag = kGroups == 2 && w.it.rows > 128 ? 0 : 1;
         const int32_t* table = a.table + (int64_t)w.it.b * a.kv.table_stride;
-        struct Copy {
-          int k0, b0, b1, page;  // its first key, the boxes that hold a visible key, this lane's page
-          bool value;
+        const auto prepare = [&](int i) {
+          const int k0 = (w.it.t0 + sg.first + i) * kN, first = k0 + (box << box_log);
+          const int b0 = (max(w.it.lo, k0) - k0) >> box_log;
+          const int b1 = (min(w.it.hi, k0 + kN) - k0 + box_rows - 1) >> box_log;
+          Tile x;
+          x.bytes = box_bytes * (uint32_t)((b1 - b0) * C::kSub);
+          x.row = first & (ps - 1);
+          x.mine = box >= b0 && box < b1;
+          x.page = x.mine ? __ldg(table + (first >> page_log)) : 0;
+          return x;
         };
-        const auto prepare = [&](int o) {
-          Copy c;
-          c.k0 = (w.it.t0 + sg.first + ring_op(o, m, two, c.value)) * kN;
-          c.b0 = (max(w.it.lo, c.k0) - c.k0) >> box_log;
-          c.b1 = (min(w.it.hi, c.k0 + kN) - c.k0 + box_rows - 1) >> box_log;
-          c.page = 0;
-          if (box >= c.b0 && box < c.b1) c.page = __ldg(table + ((c.k0 + (box << box_log)) >> page_log));
-          return c;
-        };
-        Copy next = m ? prepare(0) : Copy{0, 0, 0, 0, false};
-        for (int o = 0; o < 2 * m; ++o) {
-          const Copy c = next;
-          const bool mine = box >= c.b0 && box < c.b1;
-          if (o + 1 < 2 * m) next = prepare(o + 1);
-          const int slot = n_ops % kStages;
-          const uint32_t round = n_ops / kStages;
-          if (round > 0) {
-            ok = __all_sync(kAll, wait(empty(slot), (round - 1) & 1));
-            if (!ok) break;
-          }
-          if (lane == 0) bar_expect(full(slot), box_bytes * (uint32_t)((c.b1 - c.b0) * C::kSub));
+        const auto copy = [&](const Tile& x, const CUtensorMap* map) {
+          ok = __all_sync(kAll, wait(empty(slot), phase));
+          if (!ok) return;
+          if (lane == 0) bar_expect(full(slot), x.bytes);
           __syncwarp();
-          if (mine) {
-            int page = c.page;
+          if (x.mine) {
+            int page = x.page;
             if (page < 0 || page >= a.kv.num_pages) {
               set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
               page = a.kv.num_pages;  // out of range: reads as zeros
             }
-            tma_4d(base + C::kSmemRing + slot * C::kSlot + part * (kN * 128) + box * box_bytes,
-                   c.value ? &vmap : &kmap, part * 64, (c.k0 + (box << box_log)) & (ps - 1), w.it.h, page, full(slot));
+            tma_4d(my_dst + slot * C::kSlot, map, part * 64, x.row, w.it.h, page, full(slot));
           }
           ++n_ops;
+          if (++slot == kStages) slot = 0, phase ^= 1;
+        };
+        Tile next{}, now{}, before{};
+        if (m) next = prepare(0);
+        for (int i = 0; i < m + lag && m; ++i) {
+          before = now;
+          now = next;
+          if (i + 1 < m) next = prepare(i + 1);
+          if (i < m) copy(now, &kmap);
+          if (ok && i >= lag) copy(lag ? before : now, &vmap);
+          if (!ok) break;
         }
         walk_next<kN, kRows>(a, G, w, sg.len);
       }
