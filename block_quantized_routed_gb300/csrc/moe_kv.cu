@@ -5,8 +5,8 @@
 // sequence with a 32-way search of cu_q (two rounds for up to 1024
 // sequences), forms the page address once, and copies the token's heads in
 // 16-byte vectors; several vectors per lane are in flight before the first
-// store.  5257 tokens of 8 heads of 128 (43 MB): 9.8 us, 4.4 TB/s with the
-// launch; 64 tokens: 3.1 us.
+// store.  5257 tokens of 8 heads of 128 (43 MB): 8.7 us, 4.9 TB/s with the
+// launch; 64 tokens: 2.8 us.
 #include "moe_kv.cuh"
 
 namespace moe {
@@ -32,6 +32,24 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.T) return;
+  // the first vectors are asked for before the token's page is looked up
+  constexpr int kPer = sizeof(V) / 2, kBatch = 4;
+  const int vecs = a.kv.D / kPer, total = a.kv.Hkv * vecs;
+  const uint16_t* k = static_cast<const uint16_t*>(a.k) + (int64_t)t * a.k_stride;
+  const uint16_t* v = static_cast<const uint16_t*>(a.v) + (int64_t)t * a.v_stride;
+  V kb[kBatch], vb[kBatch];
+  const auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + 32 * u;
+      if (i < total) {
+        const int h = i / vecs, c = (i - h * vecs) * kPer;
+        kb[u] = *reinterpret_cast<const V*>(k + h * a.k_head_stride + c);
+        vb[u] = *reinterpret_cast<const V*>(v + h * a.v_head_stride + c);
+      }
+    }
+  };
+  load(lane);
   const int b = find_seq(a.cu_q, a.kv.n_seqs, t, lane);
   const SeqInfo s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, b);
   if (!s.ok) {
@@ -46,24 +64,10 @@ __global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
     return;
   }
   const int slot = pos % a.kv.page_size;
-  constexpr int kPer = sizeof(V) / 2;
-  const int vecs = a.kv.D / kPer, total = a.kv.Hkv * vecs;
-  const uint16_t* k = static_cast<const uint16_t*>(a.k) + (int64_t)t * a.k_stride;
-  const uint16_t* v = static_cast<const uint16_t*>(a.v) + (int64_t)t * a.v_stride;
   uint16_t* kc = static_cast<uint16_t*>(a.k_cache) + (int64_t)page * a.kv.k_page_stride + slot * a.kv.k_row_stride;
   uint16_t* vc = static_cast<uint16_t*>(a.v_cache) + (int64_t)page * a.kv.v_page_stride + slot * a.kv.v_row_stride;
-  constexpr int kBatch = 4;
   for (int i0 = lane; i0 < total; i0 += 32 * kBatch) {
-    V kb[kBatch], vb[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + 32 * u;
-      if (i < total) {
-        const int h = i / vecs, c = (i - h * vecs) * kPer;
-        kb[u] = *reinterpret_cast<const V*>(k + h * a.k_head_stride + c);
-        vb[u] = *reinterpret_cast<const V*>(v + h * a.v_head_stride + c);
-      }
-    }
+    if (i0 != lane) load(i0);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const int i = i0 + 32 * u;
