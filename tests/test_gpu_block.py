@@ -111,6 +111,25 @@ def test_norm_codes(fmt, T, H):
         assert torch.equal(q, q2) and torch.equal(d, d2) and torch.equal(bs, bs2)
 
 
+@pytest.mark.parametrize("fmt", list(FMTS))
+@pytest.mark.parametrize("T,H", [(3, 256), (400, 1536), (5, 6400), (700, 10240)])
+def test_norm_codes_of_rows_off_the_boundary(fmt, T, H):
+    code, group, _ = FMTS[fmt]
+    x, res, w = rnd((T, H), 7, BF16), rnd((T, H), 8, F32, 3.0), 1 + 0.2 * rnd((H,), 9)
+    xb = torch.full((T, H + 3), NAN, dtype=BF16, device="cuda")
+    xb[:, 1:H + 1] = x.cuda()
+    q = torch.empty((T, H), dtype=torch.float8_e4m3fn if fmt in ("g128", "e4m3") else torch.int8, device="cuda")
+    d = torch.empty((T, -(-H // (group or H))), device="cuda")
+    bs = torch.empty((T, H // 16), dtype=torch.int16, device="cuda") if fmt == "q8k" else None
+    y = torch.empty((T, H), device="cuda")
+    moe.moe_add_rmsnorm(xb[:, 1:H + 1], w.cuda(), 1e-5, residual=res.cuda(), y=y, q_fmt=code, q=q, d=d, bsum16=bs)
+    check_norm(x, res, w, 1e-5, 0.0, None, y, q, d, bs, fmt)
+    if fmt == "q8k":
+        q2, d2, bs2 = torch.empty_like(q), torch.empty_like(d), torch.empty_like(bs)
+        moe.moe_q8k_quantize(y, q2, d2, bs2)
+        assert torch.equal(q, q2) and torch.equal(d, d2) and torch.equal(bs, bs2)
+
+
 @pytest.mark.parametrize("H,off,stride", [(512, 0, 640), (512, 1, 640), (512, 0, 643), (100, 3, 131)])
 def test_norm_strides_and_alignment(H, off, stride):
     T = 5
