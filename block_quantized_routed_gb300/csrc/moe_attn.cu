@@ -254,7 +254,7 @@ __device__ __forceinline__ void item_range(const AttnArgs& a, int G, Item& it) {
   it.rows = min(kRows, R - it.r0);
   const int off = it.s.kv - it.s.n;
   it.hi = max(0, off + (it.r0 + it.rows - 1) / G + 1);
-  it.lo = a.window > 0 ? min(it.hi, max(0, off + it.r0 / G + 1 - a.window)) : 0;
+  it.lo = min(it.hi, window_lo(off + it.r0 / G + 1, a.window));
   it.t0 = it.lo / kN;
   it.tiles = it.hi > it.lo ? (it.hi + kN - 1) / kN - it.t0 : 0;
 }
@@ -1080,7 +1080,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       const bool busy = (row & ~31) < w.it.rows;  // some row of the warp exists
       const int R = w.it.r0 + row, tok = valid ? R / G : 0, g = valid ? R - tok * G : 0;
       const int pos = w.it.s.kv - w.it.s.n + tok;
-      const int hi = pos + 1, lo = a.window > 0 ? max(0, hi - a.window) : 0;
+      const int hi = pos + 1, lo = window_lo(hi, a.window);
       float ref = -INFINITY, sum = 0.0f;  // reference (raw score units) and sum of the row
       bool acc = false;                   // the accumulator holds something
 

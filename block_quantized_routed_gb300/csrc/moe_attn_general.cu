@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(32 * kWarps) attn_general_kernel(const AttnArg
     }
     if (b == a.kv.n_seqs) continue;  // uniform over the CTA
     const int pos = s.kv - s.n + (t - s.q0);
-    const int hi = pos + 1, lo = a.window > 0 ? max(0, hi - a.window) : 0;
+    const int hi = pos + 1, lo = window_lo(hi, a.window);
     float q[8];
     if (act) {
       unpack8<T>(*reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + (int64_t)t * a.q_stride +

@@ -15,4 +15,9 @@ __device__ __forceinline__ SeqInfo seq_info(const moe_kv_desc& kv, const int32_t
   return ok ? SeqInfo{q0, q1 - q0, len, true} : SeqInfo{0, 0, 0, false};
 }
 
+// The first key that a row which may see the keys below `hi` does see.  hi is
+// at or below 0 for a row before the first key; the window is any int, so it
+// is not taken off a negative number.
+__device__ __forceinline__ int window_lo(int hi, int window) { return window > 0 ? max(max(hi, 0) - window, 0) : 0; }
+
 }  // namespace moe

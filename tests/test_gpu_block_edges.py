@@ -1,0 +1,33 @@
+"""The decoder-block operators where their inputs are degenerate: near-ties of unequal precision, non-finite numbers
+in hidden and in visible places, underflow, limits of integers.  Plain 64-bit forms as in test_gpu_block.py."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_routed_gb300 as moe
+from tests import block_ref
+from tests.test_gpu_block import BF16, F16, F32, Cache, attend, check_route, rnd, status
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    moe.load()
+
+
+# ------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("D", [64, 128, 256, 80])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3])
+def test_attention_largest_window(D, window):
+    """A window as large as its type, with tokens that stand before the first key."""
+    c = Cache([5, 40, 2], [2, 7, 50], 2, D, 16, BF16, 86)
+    q, out, lse, ws = attend(c, 4, D, 0.1, window, BF16, 87)
+    assert status(ws) == 0
+    want, wl, tol, ltol = block_ref.attention(q, c.k, c.v, c.table, c.q_lens, c.kv_lens, 0.1, 0, BF16)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+    none = torch.isneginf(wl)
+    gl = lse.cpu().double()
+    assert torch.equal(torch.isneginf(gl), none) and ((gl - wl).abs()[~none] <= ltol[~none]).all()
