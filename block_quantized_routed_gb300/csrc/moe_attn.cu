@@ -272,6 +272,7 @@ struct Walk {
 struct Cut {
   int c0, parts, slot0;  // first CTA, number of CTAs, the first one's slot (the others use slot 0)
   int rows, r0, q0, h;
+  int arrived;           // all parts are there (written once, before the barrier behind which it is read)
 };
 
 // what the prologue leaves in shared memory for every role
@@ -285,7 +286,7 @@ struct Start {
   int c0, parts;    // equal numbers of CTAs for the items: the first CTA of this item, and how many take part (else 0)
   volatile int abort;
   uint32_t tmem;
-  int n_cut, arrived;
+  int n_cut;
   Cut cut[2];
 };
 
@@ -445,7 +446,7 @@ __device__ __forceinline__ bool part_by_row(int rows, int parts) { return rows <
 // in the order of the parts.  (One CTA joining all rows of an item took up to
 // 250 us for 128 rows in 30 parts; in slices it is bound by the L2 reads.)
 template <int D, bool BF16>
-__device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, const Cut& cut, const float* part0,
+__device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, Cut& cut, const float* part0,
                                            unsigned* counters, uint8_t* smem) {
   using C = Cfg<D>;
   constexpr int kThreads = 128 * C::kGroups, kVecs = D / 4;
@@ -462,10 +463,12 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
         set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
       }
     }
-    st.arrived = count_read(counter) >= (unsigned)np;
+    cut.arrived = count_read(counter) >= (unsigned)np;
   }
   named_sync(4, kThreads);
-  if (!st.arrived) return;  // given up: the call is void
+  // Given up: the call is void.  Every thread reads the flag of this item, which no later item's wait writes, so all of
+  // them leave here or none does, and all meet the same barriers afterwards.
+  if (!cut.arrived) return;
   const int per = (cut.rows + np - 1) / np, lo = ((int)blockIdx.x - cut.c0) * per;
   const int nr = min(per, cut.rows - lo);
   const auto part = [&](int p) { return part0 + ((size_t)(cut.c0 + p) * 2 + (p == 0 ? cut.slot0 : 0)) * C::kPartFloats; };

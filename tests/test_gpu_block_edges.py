@@ -31,3 +31,25 @@ def test_attention_largest_window(D, window):
     none = torch.isneginf(wl)
     gl = lse.cpu().double()
     assert torch.equal(torch.isneginf(gl), none) and ((gl - wl).abs()[~none] <= ltol[~none]).all()
+
+
+# the division of work in which most CTAs hold parts of two items
+SHARED = ([1] * 100, [i * 131 % 4000 + 500 for i in range(100)], 8, 1)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hkv", [SHARED, ([1, 1], [3000, 50], 16, 2)])
+def test_attention_gives_up_waiting_for_parts(q_lens, kv_lens, hq, hkv, D):
+    """Counters that never reach the number of parts: every CTA's wait runs out after a second, on the first of its
+    items as on the second, the call ends with an error, and a zeroed workspace serves the next one."""
+    c = Cache(q_lens, kv_lens, hkv, D, 64, BF16, 90)
+    ws = torch.zeros(moe.moe_paged_attention_workspace_size(hq, hkv, D), dtype=torch.uint8, device="cuda")
+    q, out, lse, _ = attend(c, hq, D, 0.1, 0, BF16, 91, ws=ws)
+    good = out.clone()
+    assert status(ws) == 0
+    ws[16:16 + 4 * 160].view(torch.int32).fill_(2 ** 30)     # an increment takes these to 0, not on
+    attend(c, hq, D, 0.1, 0, BF16, 91, ws=ws)
+    assert status(ws) == moe.MOE_ERR_DEVICE_TIMEOUT
+    ws.zero_()
+    out = attend(c, hq, D, 0.1, 0, BF16, 91, ws=ws)[1]
+    assert status(ws) == 0 and torch.equal(out.view(torch.int16), good.view(torch.int16))
