@@ -696,6 +696,14 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     mine.units *= a.kv.Hkv;
     return mine;
   };
+  // Whether sequences share rows of q, by the number of tokens that this lane's name.  Sequences follow one another in
+  // cu_q, so only a cu_q out of order can make them overlap, and then their sum is no longer bounded by T, nor the
+  // units by what the host allowed: nothing is computed.  (One of the sequences is reported in any case.)
+  const auto overlap = [&](long long tokens) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) tokens += __shfl_xor_sync(kAll, tokens, o);
+    return tokens > a.T;
+  };
   const auto scan = [&](auto v) {  // inclusive, over the warp
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -772,8 +780,9 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     if (warp == 0) {
       Item it;
       const Count my = count(lane, it.s);
-      const Plan pl = plan<D, kRows>(__reduce_add_sync(kAll, my.units), __reduce_add_sync(kAll, my.items),
+      Plan pl = plan<D, kRows>(__reduce_add_sync(kAll, my.units), __reduce_add_sync(kAll, my.items),
                                      __reduce_max_sync(kAll, my.most), __reduce_max_sync(kAll, it.s.n) * G);
+      if (__any_sync(kAll, !it.s.ok) && overlap(it.s.n)) pl = Plan{false, 0, 0, 1};
       const int mine = pl.by_item ? my.items : my.units, inc = scan(mine);
       int g0;
       if (begin(pl, g0)) {
@@ -787,29 +796,37 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       }
     }
   } else {
-    // per sequence its units, its items; then per warp the largest item and the most tokens; the ring is not in use yet
+    // per sequence its units, its items; then per warp the largest item, the most tokens, whether one is bad; the ring is not in use yet
     int* units = reinterpret_cast<int*>(smem + C::kSmemRing);
     int *items = units + MOE_MAX_SEQS, *peaks = items + MOE_MAX_SEQS;
-    static_assert(C::kStages * C::kSlot >= 4 * (2 * MOE_MAX_SEQS + 2 * C::kThreads / 32), "counts of the sequences");
+    static_assert(C::kStages * C::kSlot >= 4 * (2 * MOE_MAX_SEQS + 3 * C::kThreads / 32), "counts of the sequences");
     int most = 0, tokens = 0;
+    bool bad = false;
     for (int b0 = warp * 32; b0 < a.kv.n_seqs; b0 += C::kThreads) {
       SeqInfo s;
       const Count my = count(b0 + lane, s);
       if (b0 + lane < a.kv.n_seqs) units[b0 + lane] = my.units, items[b0 + lane] = my.items;
       most = max(most, my.most);
       tokens = max(tokens, s.n);
+      bad |= __any_sync(kAll, !s.ok);
     }
     most = __reduce_max_sync(kAll, most);
     tokens = __reduce_max_sync(kAll, tokens);
-    if (lane == 0) peaks[2 * warp] = most, peaks[2 * warp + 1] = tokens;
+    if (lane == 0) peaks[3 * warp] = most, peaks[3 * warp + 1] = tokens, peaks[3 * warp + 2] = bad;
     __syncthreads();
     if (warp == 0) {
       int all_units = 0, all_items = 0;
       for (int b = lane; b < a.kv.n_seqs; b += 32) all_units += units[b], all_items += items[b];
-      most = lane < C::kThreads / 32 ? peaks[2 * lane] : 0;
-      tokens = lane < C::kThreads / 32 ? peaks[2 * lane + 1] : 0;
-      const Plan pl = plan<D, kRows>(__reduce_add_sync(kAll, all_units), __reduce_add_sync(kAll, all_items),
+      most = lane < C::kThreads / 32 ? peaks[3 * lane] : 0;
+      tokens = lane < C::kThreads / 32 ? peaks[3 * lane + 1] : 0;
+      bad = __any_sync(kAll, lane < C::kThreads / 32 && peaks[3 * lane + 2]);
+      Plan pl = plan<D, kRows>(__reduce_add_sync(kAll, all_units), __reduce_add_sync(kAll, all_items),
                                      __reduce_max_sync(kAll, most), __reduce_max_sync(kAll, tokens) * G);
+      if (bad) {
+        long long all = 0;
+        for (int b = lane; b < a.kv.n_seqs; b += 32) all += seq_info(a.kv, a.cu_q, a.kv_len, a.T, b).n;
+        if (overlap(all)) pl = Plan{false, 0, 0, 1};
+      }
       const int* cost = pl.by_item ? items : units;
       int g0;
       if (begin(pl, g0)) {

@@ -53,3 +53,26 @@ def test_attention_gives_up_waiting_for_parts(q_lens, kv_lens, hq, hkv, D):
     ws.zero_()
     out = attend(c, hq, D, 0.1, 0, BF16, 91, ws=ws)[1]
     assert status(ws) == 0 and torch.equal(out.view(torch.int16), good.view(torch.int16))
+
+
+@pytest.mark.parametrize("n,T,kv,hq", [(4, 40, 100, 4), (31, 300, 500, 16), (64, 40, 200, 4), (8192, 8192, 32768, 128),
+                                       (8192, 8192, 49152, 128)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_sequences_that_share_rows(n, T, kv, hq, D):
+    """cu_q goes up and down, so that every other sequence names all rows: far more work than the call's sizes allow,
+    up to more than 32 bits count.  Reported, and nothing is computed."""
+    hkv, page = (8, 64) if hq == 128 else (2, 64)
+    pages = -(-kv // page)
+    kc = torch.zeros(pages, page, hkv, D, dtype=BF16, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").repeat(n, 1)
+    cu = torch.tensor([0 if b % 2 == 0 else T for b in range(n + 1)], dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), kv, dtype=torch.int32, device="cuda")
+    q = torch.zeros(T, hq, D, dtype=BF16, device="cuda")
+    out = torch.full((T, hq, D), 5.0, dtype=BF16, device="cuda")
+    ws = torch.zeros(moe.moe_paged_attention_workspace_size(hq, hkv, D), dtype=torch.uint8, device="cuda")
+    moe.moe_paged_attention(q, kc, kc, table, cu, lens, 0.1, out, ws)
+    assert status(ws) == moe.MOE_ERR_DEVICE_BOUNDS
+    assert (out == 5.0).all()
+    cu = torch.tensor([0, T] + [T] * (n - 1), dtype=torch.int32, device="cuda")     # in order: the first has all rows
+    moe.moe_paged_attention(q, kc, kc, table, cu, lens, 0.1, out, ws)
+    assert status(ws) == 0 and (out == 0.0).all()
