@@ -7,7 +7,10 @@
 // before the launch.  Nothing is computed and nothing is kept between calls.
 #include <Python.h>
 
+#include <initializer_list>
+
 #include <ATen/core/Tensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -68,6 +71,17 @@ void* stream_of(PyObject* o) {
   Py_DECREF(h);
   if (PyErr_Occurred()) throw std::runtime_error("");
   return reinterpret_cast<void*>(v);
+}
+// every tensor of a call (null: not given) on the current device: a kernel takes them as bare pointers
+void on_device(std::initializer_list<const at::Tensor*> ts) {
+  int dev = -1;
+  for (const at::Tensor* t : ts) {
+    if (!t) continue;
+    need(t->is_cuda(), "every tensor must be on the GPU");
+    need(dev < 0 || t->get_device() == dev, "all tensors must be on one device");
+    dev = t->get_device();
+  }
+  need(dev < 0 || dev == c10::cuda::current_device(), "the tensors' device must be the current one");
 }
 size_t bytes_of(const at::Tensor& t) { return (size_t)t.numel() * t.element_size(); }
 
@@ -132,6 +146,7 @@ PyObject* add_rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       q = d = bs = nullptr;
     }
+    on_device({&x, &w, res, sum, y, q, d, bs});
     return moe_add_rmsnorm(x.data_ptr(), xt, xs, ptr(res), rt, rs, w.data_ptr(), dtype(w), (float)number(a[10]),
                            (float)number(a[2]), T, (int32_t)H, ptr(sum), ss, ptr(y), yt, ys, fmt, ptr(q),
                            static_cast<float*>(ptr(d)), static_cast<int16_t*>(ptr(bs)), stream_of(a[11]));
@@ -157,9 +172,12 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (bias)
       need(bias->dim() == 1 && bias->size(0) == E && bias->is_contiguous() && bias->scalar_type() == at::kFloat,
            "bias must be fp32 [E]");
+    const int renorm = PyObject_IsTrue(a[9]);
+    if (renorm < 0) throw std::runtime_error("");
+    on_device({&l, &ids, &gates, bias});
     return moe_route_grouped(l.data_ptr(), dtype(l), stride, static_cast<const float*>(ptr(bias)), (int32_t)T,
                              (int32_t)E, k, int32(a[5], "route"), int32(a[6], "n_group"), int32(a[7], "topk_group"),
-                             int32(a[8], "group_score"), PyObject_IsTrue(a[9]), (float)number(a[10]),
+                             int32(a[8], "group_score"), renorm, (float)number(a[10]),
                              ids.data_ptr<int32_t>(), gates.data_ptr<float>(), stream_of(a[11]));
   });
 }
@@ -213,6 +231,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     need(k.dim() == 3 && k.size(0) <= INT32_MAX, "k must be [T, Hkv, D] of the cache's type");
     heads(k, k.size(0), d.Hkv, kc, "k must be [T, Hkv, D] of the cache's type");
     heads(v, k.size(0), d.Hkv, kc, "v must be like k");
+    need(ws.is_contiguous(), "ws must be contiguous");
+    on_device({&k, &v, &kc, &vc, &table, &cu, &len, &ws});
     return moe_kv_append(&d, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
                          kc.data_ptr(), vc.data_ptr(), table.data_ptr<int32_t>(), cu.data_ptr<int32_t>(),
                          len.data_ptr<int32_t>(), (int32_t)k.size(0), ws.data_ptr(), bytes_of(ws), stream_of(a[8]));
@@ -236,6 +256,8 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
       need(lse->dim() == 2 && lse->size(0) == T && lse->size(1) == Hq && lse->is_contiguous() &&
                lse->scalar_type() == at::kFloat,
            "lse must be fp32 [T, Hq]");
+    need(ws.is_contiguous(), "ws must be contiguous");
+    on_device({&q, &kc, &vc, &table, &cu, &len, &out, &ws, lse});
     return moe_paged_attention(&d, q.data_ptr(), q.stride(0), q.stride(1), (int32_t)Hq, (int32_t)T, kc.data_ptr(),
                                vc.data_ptr(), table.data_ptr<int32_t>(), cu.data_ptr<int32_t>(),
                                len.data_ptr<int32_t>(), (float)number(a[6]), int32(a[10], "window"), out.data_ptr(),

@@ -1,0 +1,56 @@
+"""The binding and the build of the decoder-block operators on the CPU: what is refused before any launch."""
+import pytest
+import torch
+
+import block_quantized_routed_gb300 as moe
+from block_quantized_routed_gb300 import _build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    _build.build()
+    moe.load()
+
+
+def calls():
+    """Each operator with tensors that are right but for their device."""
+    x, w = torch.zeros(2, 256), torch.ones(256)
+    yield "norm", lambda: moe.moe_add_rmsnorm(x, w, 1e-6, residual=x, sum_out=x, y=x.clone(), q_fmt=moe.NORM_Q_Q8K,
+                                              q=torch.zeros(2, 256, dtype=torch.int8), d=torch.zeros(2, 1),
+                                              bsum16=torch.zeros(2, 16, dtype=torch.int16))
+    yield "route", lambda: moe.moe_route_grouped(x, 4, torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, 4),
+                                                 bias=torch.zeros(256))
+    kc = torch.zeros(8, 16, 2, 64, dtype=torch.bfloat16)
+    table, cu = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    n, kn = torch.zeros(2, dtype=torch.int32), torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    ws = torch.zeros(moe.moe_paged_attention_workspace_size(4, 2, 64), dtype=torch.uint8)
+    yield "append", lambda: moe.moe_kv_append(kn, kn, kc, kc, table, cu, n, ws)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    yield "attention", lambda: moe.moe_paged_attention(q, kc, kc, table, cu, n, 0.1, torch.empty_like(q), ws,
+                                                       lse=torch.zeros(3, 4))
+
+
+@pytest.mark.parametrize("name", ["norm", "route", "append", "attention"])
+def test_tensors_of_the_host_are_refused(name):
+    """A tensor that is right in every other way: its pointer would reach a kernel."""
+    with pytest.raises(moe.MoeError) as e:
+        dict(calls())[name]()
+    assert e.value.status == moe.MOE_ERR_INVALID_ARG and "GPU" in str(e.value)
+
+
+def test_workspaces_have_to_be_contiguous():
+    """An expanded workspace has fewer bytes than elements."""
+    kc = torch.zeros(8, 16, 2, 64, dtype=torch.bfloat16)
+    table, cu, n = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+    ws = torch.zeros(1, dtype=torch.uint8).expand(1 << 20)
+    with pytest.raises(moe.MoeError, match="contiguous"):
+        moe.moe_kv_append(q[:, :2], q[:, 2:], kc, kc, table, cu, n, ws)
+    with pytest.raises(moe.MoeError, match="contiguous"):
+        moe.moe_paged_attention(q, kc, kc, table, cu, n, 0.1, torch.empty_like(q), ws)
+
+
+def test_a_flag_without_a_truth_value_is_an_error():
+    x = torch.zeros(2, 256)
+    with pytest.raises(RuntimeError, match="ambiguous|Boolean"):
+        moe.moe_route_grouped(x, 4, torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, 4), renorm=torch.ones(2))
