@@ -5,11 +5,13 @@
 //
 // The selection is the one that 64-bit keys give.  Keys are formed in fp32
 // with a bound on their error; lane s re-derives the key of the s-th choice
-// and compares it with the next one.  Where a gap (between neighbours of the
-// result, or between the last kept and the first dropped group) is within the
-// two bounds, fp32 cannot tell: the choices in question, and those that might
-// displace the last of them, are ranked again by fp64 keys, and likewise the
-// elements that make up the groups' scores, one key per lane.  (Deciding such a
+// and compares it with the next one, the k-th with the first that is not its
+// equal, by a bound that holds for all that was not chosen.  Where a gap
+// (between neighbours of the result, below the k-th, or between the last kept
+// and the first dropped group) is within the two bounds, fp32 cannot tell: the
+// choices in question, and those that might displace the last of them, are
+// ranked again by fp64 keys, and likewise the elements that make up the
+// groups' scores, one key per lane.  (Deciding such a
 // token with fp64 keys of all its experts takes a warp tens of microseconds on
 // this part's few fp64 units: it is left for more than 32 such elements.)
 // Without a bias the order of the keys is that of the logits, which are
@@ -74,6 +76,13 @@ __device__ __forceinline__ float score32(float l, int route, Stats st) {
   if (route == MOE_ROUTE_SIGMOID) return rcp32(1.0f + exp32(-l));
   if (st.m == -INFINITY) return 0.0f;
   return (l == st.m ? 1.0f : exp32(l - st.m)) * st.inv_sum;
+}
+
+// An infinite key comes from an infinite bias and is exact.
+__device__ __forceinline__ float magnitude(float v) { return fabsf(v) < INFINITY ? fabsf(v) : 0.0f; }
+// v certainly comes before v1 (which it was not after in fp32)
+__device__ __forceinline__ bool above(float v, float v1, float tol) {
+  return v - v1 > tol || (v == v1 && fabsf(v) == INFINITY);
 }
 
 __device__ __forceinline__ double score64(float l, int route, float m, double sum) {
@@ -191,6 +200,20 @@ __device__ __noinline__ uint32_t groups64(const RouteArgs& a, int64_t row, int l
     rank += other > score || (other == score && g < lane);
   }
   return __ballot_sync(kAll, lane < a.n_group && rank < a.topk_group);
+}
+
+// The largest key at or below key_k of an element that is not the equal of e_k (another logit or bias); -inf: none.
+// s_key: [element of a lane][lane] keys.
+__device__ __noinline__ float next_other(const RouteArgs& a, int64_t row, int e_k, uint32_t key_k, const uint32_t* s_key) {
+  const int lane = threadIdx.x & 31, npl = (a.E + 31) / 32, e0 = lane * npl;
+  const float l = load_logit(a, row + e_k), b = __ldg(a.bias + e_k);
+  uint32_t top = 0;
+  for (int j = 0; j < npl && e0 + j < a.E; ++j) {
+    const uint32_t key = s_key[j * 32 + lane];
+    if (key > top && key <= key_k && !(load_logit(a, row + e0 + j) == l && __ldg(a.bias + e0 + j) == b)) top = key;
+  }
+  top = __reduce_max_sync(kAll, top);
+  return top ? key_logit(top) : -INFINITY;
 }
 
 // the two largest of two pairs, each in order
@@ -451,21 +474,34 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   float p = score32(lg, a.route, st);
   if (scored) {
     const float b = lane < rounds ? __ldg(a.bias + mine) : 0.0f, v = p + b;
-    const float err = kUlp * (bound * p + 1.0f + fabsf(v));
+    const float err = kUlp * (bound * p + 1.0f + magnitude(v));
     const float v1 = __shfl_down_sync(kAll, v, 1), err1 = __shfl_down_sync(kAll, err, 1);
     const float l1 = __shfl_down_sync(kAll, lg, 1), b1 = __shfl_down_sync(kAll, b, 1);
     const bool same = lg == l1 && b == b1;
-    const bool near = __any_sync(kAll, lane + 1 < rounds && !same && v - v1 <= err + err1);
+    // neighbours of the result, each with its own bound
+    bool near = __any_sync(kAll, lane + 1 < a.k && !same && !above(v, v1, err + err1));
+    const float vk = __shfl_sync(kAll, v, a.k - 1);
+    if (rounds > a.k) {
+      // The k-th against all that was not chosen: every one of those lies at or below the next key, but its score, and so
+      // its bound, may be anything up to the largest of the row.
+      float vn = __shfl_sync(kAll, v, a.k);
+      if (__shfl_sync(kAll, (int)same, a.k - 1)) {
+        // the next is the k-th's equal in any precision (and of a higher index)
+        vn = next_other(a, row, __shfl_sync(kAll, mine, a.k - 1), __shfl_sync(kAll, my_key, a.k - 1), s_key);
+      }
+      const float most = a.route == MOE_ROUTE_SIGMOID ? 1.0f : st.m == -INFINITY ? 0.0f : fminf(st.inv_sum, 1.0f);
+      const float tol = __shfl_sync(kAll, err, a.k - 1) + kUlp * (bound * most + 1.0f + magnitude(vn));
+      near |= !above(vk, vn, tol);
+    }
     if (near && !unsure) {
       // choices that fp32 cannot order: take more until one is certainly below the k-th, and rank them in fp64
-      const float vk = __shfl_sync(kAll, v, a.k - 1);
       int n = rounds;
       bool enough = n == avail;
       while (!enough && n < 32) {
         const uint32_t top = __reduce_max_sync(kAll, key[0]);
         if (top == 0) break;
         const float vn = key_logit(top);
-        enough = vk - vn > kUlp * (2.0f * bound + 2.0f + fabsf(vk) + fabsf(vn));
+        enough = above(vk, vn, kUlp * (2.0f * bound + 2.0f + magnitude(vk) + magnitude(vn)));
         if (!enough) pick(n++, top);
         else break;
       }

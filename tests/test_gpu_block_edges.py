@@ -17,6 +17,72 @@ def _lib():
     moe.load()
 
 
+# ------------------------------------------------------------------ routing: the border of the selection
+
+def test_route_a_tie_at_the_border_hides_no_rival():
+    """The k-th and the next key are the same in any precision; one further down is larger in 64 bits alone."""
+    l = np.array([[17.0, 17.0, 18.0]], np.float32)
+    check_route(l, np.zeros(3, np.float32), 1)
+    for E, k in [(64, 3), (256, 8), (700, 8), (1024, 16)]:
+        l = np.full((4, E), -5.0, np.float32)
+        for t in range(4):
+            l[t, 3 * t:3 * t + k + 1] = 17.0              # k + 1 equal keys, all 1 in fp32
+            l[t, E - 1 - t] = 18.0
+        check_route(l, np.zeros(E, np.float32), k)
+        check_route(l, np.full(E, 0.25, np.float32), k)
+
+
+@pytest.mark.parametrize("E,k", [(64, 4), (256, 8), (512, 10), (1024, 16)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_route_scores_of_few_values(E, k, sigmoid):
+    """Logits of a narrow type repeat: saturated scores, tiny scores, whole rows of one value, more than 32 of each."""
+    rng = np.random.default_rng(E + k)
+    zero, half = np.zeros(E, np.float32), np.full(E, 0.5, np.float32)
+    steps = rng.integers(0, 6, (24, E)).astype(np.float32) * 0.125
+    for bias in (zero, half):
+        check_route(17.0 + steps, bias, k, sigmoid)
+        check_route(-18.0 + steps, bias, k, sigmoid)
+        check_route(np.full((3, E), 2.0, np.float32), bias, k, sigmoid)
+        check_route(np.where(rng.random((24, E)) < 0.5, 20.0, 19.0).astype(np.float32), bias, k, sigmoid)
+        check_route(17.0 + steps, bias, min(k, 4), sigmoid, n_group=4, topk_group=2)
+
+
+@pytest.mark.parametrize("E", [128, 512, 1024])
+@pytest.mark.parametrize("at", [0, 77, 127])
+def test_route_large_scores_beside_small_ones(E, at):
+    """Softmax: the error of a score near 1 is far larger than that of one near 0, so a large one below both of the
+    keys at the border may belong above them."""
+    l = np.full((1, E), np.log(7e-8), np.float32)
+    l[0, at] = 0.0
+    p = np.exp(l[0].astype(np.float64))
+    p /= p.sum()
+    bias = np.full(E, -1.0, np.float32)
+    bias[at] = -0.99
+    top = p[at] + float(bias[at])
+    for below in [(2e-7, 1.2e-6), (1e-7, 9e-7), (3e-7, 2e-6)]:
+        b = bias.copy()
+        others = [e for e in (5, 60, 100) if e != at][:2]
+        for e, d in zip(others, below):
+            b[e] = np.float32(top - d - p[e])
+        check_route(l, b, 1, False)
+        check_route(l, b, 2, False)
+        check_route(l, b, 3, False)
+
+
+def test_route_masks_in_the_bias():
+    """Experts masked by a bias of -inf, up to leaving fewer than k; +inf forces a choice."""
+    rng = np.random.default_rng(9)
+    l = rng.standard_normal((40, 64)).astype(np.float32)
+    for n in (60, 20, 8, 5, 0):
+        bias = (0.05 * rng.standard_normal(64)).astype(np.float32)
+        bias[rng.permutation(64)[:64 - n]] = -np.inf
+        for sigmoid in (True, False):
+            check_route(l, bias, 8, sigmoid)
+    bias = np.zeros(64, np.float32)
+    bias[[7, 50]] = np.inf
+    check_route(l, bias, 4)
+
+
 # ------------------------------------------------------------------ attention
 
 @pytest.mark.parametrize("D", [64, 128, 256, 80])
