@@ -7,8 +7,8 @@
 // with a bound on their error; lane s re-derives the key of the s-th choice
 // and compares it with the next one, the k-th with the first that is not its
 // equal, by a bound that holds for all that was not chosen.  Where a gap
-// (between neighbours of the result, below the k-th, or between the last kept
-// and the first dropped group) is within the two bounds, fp32 cannot tell: the
+// (between neighbours of the result, below the k-th, or between any kept and
+// any dropped group) is within the two bounds, fp32 cannot tell: the
 // choices in question, and those that might displace the last of them, are
 // ranked again by fp64 keys, and likewise the elements that make up the
 // groups' scores, one key per lane.  (Deciding such a
@@ -381,8 +381,8 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     float score = -INFINITY, err = 0.0f;
     if (lane < a.n_group) {
       score = add ? first + second : first;
-      // each key within (bound * p + |key|) ulp, p <= 1; without a bias a single logit is exact
-      if (scored || add)
+      // each key within (bound * p + |key|) ulp, p <= 1; without a bias a single logit is exact, and so is an infinite sum
+      if ((scored || add) && fabsf(score) < INFINITY)
         err = kUlp * (fabsf(score) + fabsf(first) + (add ? fabsf(second) : 0.0f) + (add ? 2.0f : 1.0f) * (bound + 1.0f));
     }
     int rank = 0;
@@ -392,13 +392,15 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
     }
     if (lane >= a.n_group) rank = 64;
     uint32_t kept = __ballot_sync(kAll, rank < a.topk_group);
-    // the last kept against the first dropped group
-    const int last = __ffs(__ballot_sync(kAll, rank == a.topk_group - 1)) - 1;
-    const int next = __ffs(__ballot_sync(kAll, rank == a.topk_group)) - 1;
-    const float gap = __shfl_sync(kAll, score, last) - __shfl_sync(kAll, score, next);
-    const float tol = __shfl_sync(kAll, err, last) + __shfl_sync(kAll, err, next);
+    // Every kept group against every dropped one: their errors differ with the size of their keys, so it is not enough
+    // to look at the two scores next to one another.
+    const bool mine_kept = kept >> lane & 1;
+    const float low = key_logit(__reduce_min_sync(kAll, order_key(mine_kept ? score - err : INFINITY)));
+    const float high =
+        key_logit(__reduce_max_sync(kAll, order_key(lane < a.n_group && !mine_kept ? score + err : -INFINITY)));
+    const bool clear = above(low, high, 0.0f);
     int g = e0 / gs, left = (g + 1) * gs - e0;  // elements of the lane until the next group
-    if (tol > 0.0f && gap <= tol) {
+    if ((scored || add) && !clear) {
       // decided by fp64 keys of the elements that may count for a group
       int* list = s_list[wid];
       int n = 0, gg = g, ll = left;

@@ -83,6 +83,27 @@ def test_route_masks_in_the_bias():
     check_route(l, bias, 4)
 
 
+def test_route_groups_of_unequal_precision():
+    """A group whose two keys are large and of opposite sign has a score of far larger error than its neighbours': it
+    may belong above both groups at the border."""
+    rng = np.random.default_rng(12)
+    sig = lambda x: 1.0 / (1.0 + np.exp(-x.astype(np.float64)))
+    rows, bias = [], np.array([1000.0, -1000.0, 0.0, 0.0, 0.0, 0.0], np.float32)
+    while len(rows) < 40:
+        x = rng.uniform(-1, 1, 2).astype(np.float32)
+        true = sig(x).sum()
+        f32 = float(np.float32(1000.0) + np.float32(sig(x)[0])) + float(np.float32(-1000.0) + np.float32(sig(x)[1]))
+        if true - f32 < 4e-5:
+            continue
+        # the other two groups 2e-5 and 3e-5 below its true score, above its fp32 one
+        want = np.array([true - 2e-5, true - 3e-5]) / 2
+        y = np.log(want / (1 - want)).astype(np.float32)
+        rows.append([x[0], x[1], y[0], y[0], y[1], y[1]])
+    l = np.array(rows, np.float32)
+    check_route(l, bias, 2, True, 3, 1)
+    check_route(l, bias, 2, True, 3, 2)
+
+
 # ------------------------------------------------------------------ attention
 
 @pytest.mark.parametrize("D", [64, 128, 256, 80])
