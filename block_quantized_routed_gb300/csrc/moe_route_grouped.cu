@@ -202,6 +202,27 @@ __device__ __noinline__ uint32_t groups64(const RouteArgs& a, int64_t row, int l
   return __ballot_sync(kAll, lane < a.n_group && rank < a.topk_group);
 }
 
+// The gate of lane r's choice (logit l, r < k), before the scale.  Renormalised gates are ratios of scores, formed with
+// the largest exponential of the choices divided out, so that they hold where the scores themselves are below fp32's
+// range, and so that the approximate exponential sees small arguments: sigmoid(l) = e^min(l, 0) / (1 + e^-|l|),
+// softmax e^l / sum.
+__device__ __forceinline__ float gate(const RouteArgs& a, int lane, float l, Stats st) {
+  const bool chosen = lane < a.k, sigmoid = a.route == MOE_ROUTE_SIGMOID;
+  const float x = sigmoid ? fminf(l, 0.0f) : l;
+  float top = a.renorm ? chosen ? x : -INFINITY : sigmoid ? 0.0f : st.m;
+  if (a.renorm) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+  }
+  float w = !chosen || x == -INFINITY ? 0.0f : x == top ? 1.0f : exp32(x - top);
+  if (sigmoid) w *= rcp32(1.0f + exp32(-fabsf(l)));
+  if (!a.renorm) return sigmoid ? w : w > 0.0f ? w * st.inv_sum : 0.0f;  // (a row of -inf: no sum)
+  float sum = w;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  return sum > 0.0f ? w / sum : 0.0f;
+}
+
 // The largest key at or below key_k of an element that is not the equal of e_k (another logit or bias); -inf: none.
 // s_key: [element of a lane][lane] keys.
 __device__ __noinline__ float next_other(const RouteArgs& a, int64_t row, int e_k, uint32_t key_k, const uint32_t* s_key) {
@@ -473,8 +494,8 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   int mine = element(rounds);
   if (lane >= rounds) mine = 0;
   float lg = lane < rounds ? load_logit(a, row + mine) : 0.0f;
-  float p = score32(lg, a.route, st);
   if (scored) {
+    const float p = score32(lg, a.route, st);
     const float b = lane < rounds ? __ldg(a.bias + mine) : 0.0f, v = p + b;
     const float err = kUlp * (bound * p + 1.0f + magnitude(v));
     const float v1 = __shfl_down_sync(kAll, v, 1), err1 = __shfl_down_sync(kAll, err, 1);
@@ -512,7 +533,6 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
         const int e = element(n);
         mine = rank64(a, row, lane, st.m, n, e, lane < n ? load_logit(a, row + e) : 0.0f);
         if (lane < a.k) lg = load_logit(a, row + mine);
-        p = score32(lg, a.route, st);
       } else {
         unsure = true;
       }
@@ -521,16 +541,8 @@ __global__ void __launch_bounds__(128) route_grouped_kernel(const RouteArgs a) {
   if (unsure) {
     mine = select64(a, row, lane, st.m, s_buf[wid]);
     if (lane < a.k) lg = load_logit(a, row + mine);
-    p = score32(lg, a.route, st);
   }
-  if (lane >= a.k) p = 0.0f;
-  float g = p;
-  if (a.renorm) {
-    float sum = p;
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    g = sum > 0.0f ? p / sum : 0.0f;
-  }
+  const float g = gate(a, lane, lg, st);
   if (lane < a.k) {
     a.ids[(int64_t)t * a.k + lane] = mine;
     a.gates[(int64_t)t * a.k + lane] = g * a.scale;

@@ -104,6 +104,25 @@ def test_route_groups_of_unequal_precision():
     check_route(l, bias, 2, True, 3, 2)
 
 
+def test_route_gates_of_scores_below_fp32():
+    """Renormalised gates are ratios: they exist where the scores themselves are below fp32's range."""
+    rng = np.random.default_rng(10)
+    for base in (-80.0, -88.0, -95.0, -120.0, -700.0):
+        l = (base + rng.uniform(-3, 3, (20, 64))).astype(np.float32)
+        check_route(l, None, 8, True)
+        check_route(l, None, 8, True, scale=2.5, n_group=4, topk_group=2, top2=False)
+        check_route(l, None, 8, True, renorm=False)
+        l[:, 5] = 30.0                                     # softmax: one that takes all, kept out by its bias
+        bias = np.zeros(64, np.float32)
+        bias[5] = -5.0
+        check_route(l, bias, 8, False)
+        check_route(l, None, 8, False)
+    l = np.full((3, 64), -np.inf, np.float32)
+    l[1, 40] = 1.0
+    for sigmoid in (True, False):
+        check_route(l, None, 8, sigmoid, renorm=False)
+
+
 # ------------------------------------------------------------------ attention
 
 @pytest.mark.parametrize("D", [64, 128, 256, 80])
