@@ -205,6 +205,13 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x, within 2 ulp; 2^-inf = 
   return y;
 }
 
+// A row's results from its sum of weights, 2^m of them in all: 0 where it sees no key.  A sum that is no number (a NaN or
+// an overflow in its scores) stays one.
+__device__ __forceinline__ float inverse_of(float sum) { return sum == 0.0f ? 0.0f : 1.0f / sum; }
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  return sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
+}
+
 __device__ __forceinline__ void store32(void* p, const uint32_t* v) {  // 32-byte aligned
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
                "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
@@ -478,7 +485,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
     if (a.lse) {
       const int R = cut.r0 + lo + row, tok = R / G;
       a.lse[(int64_t)(cut.q0 + tok) * a.Hq + cut.h * G + (R - tok * G)] =
-          L > 0.0f ? (M + log2f(L)) * 0.693147180559945309f : -INFINITY;
+          lse_of(M, L);
     }
   };
   const int n = nr > 0 ? nr * kVecs : 0;  // vectors of 4 columns
@@ -515,7 +522,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
         m[p] = m[p] == -INFINITY ? 0.0f : ex2(m[p] - M);
         L += m[p] * l[p];
       }
-      const float il = L > 0.0f ? 1.0f / L : 0.0f;
+      const float il = inverse_of(L);
 #pragma unroll
       for (int p = 0; p < 8; ++p)
         if (p < np) wgt[p * per + row] = m[p] * il;
@@ -543,7 +550,7 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kAll, L, o);
-      const float il = L > 0.0f ? 1.0f / L : 0.0f;
+      const float il = inverse_of(L);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int p = i * 32 + lane;
@@ -1210,7 +1217,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         col0 = grp * (D / 2);
         col1 = col0 + D / 2;
       }
-      const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
+      const float inv = inverse_of(sum);
       // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
       const int c0 = whole ? 0 : st.parts ? st.c0 : owner(st, g_item + kItemUnits);
       const int parts = whole ? 1 : st.parts ? st.parts : owner(st, g_item + w.it.cost() - 1) - c0 + 1;
@@ -1270,7 +1277,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       writes = two || grp == 0;  // the row's statistics are written once
       if (writes && whole && valid && a.lse)
         a.lse[(int64_t)(w.it.s.q0 + tok) * a.Hq + w.it.h * G + g] =
-            sum > 0.0f ? (m2 + log2f(sum)) * 0.693147180559945309f : -INFINITY;
+            lse_of(m2, sum);
       if (!whole) {
         if (writes && valid) {
           reinterpret_cast<float2*>(part)[row] = make_float2(m2, sum);

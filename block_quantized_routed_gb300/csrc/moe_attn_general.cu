@@ -66,7 +66,8 @@ __global__ void __launch_bounds__(32 * kWarps) attn_general_kernel(const AttnArg
       for (int x = 16; x > 0; x >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, x);
       dot *= a.scale;
       const float m1 = fmaxf(m, dot);
-      const float f = m1 == -INFINITY ? 1.0f : expf(m - m1), p = m1 == -INFINITY ? 0.0f : expf(dot - m1);
+      const float f = m1 == -INFINITY ? 1.0f : expf(m - m1);
+      const float p = m1 == -INFINITY ? (dot == m1 ? 0.0f : dot) : expf(dot - m1);  // (a maximum skips NaN, the sum does not)
       m = m1;
       l = l * f + p;
       float v[8] = {};
@@ -96,9 +97,9 @@ __global__ void __launch_bounds__(32 * kWarps) attn_general_kernel(const AttnArg
       float v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) v = fmaf(f[w], s_o[w][c], v);
-      static_cast<T*>(a.out)[(int64_t)t * a.o_stride + head * a.o_head_stride + c] = (T)(ll > 0.0f ? v / ll : 0.0f);
+      static_cast<T*>(a.out)[(int64_t)t * a.o_stride + head * a.o_head_stride + c] = (T)(ll == 0.0f ? 0.0f : v / ll);
     }
-    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)t * a.Hq + head] = ll > 0.0f ? mm + logf(ll) : -INFINITY;
+    if (a.lse && threadIdx.x == 0) a.lse[(int64_t)t * a.Hq + head] = ll == 0.0f ? -INFINITY : mm + logf(ll);
   }
 }
 

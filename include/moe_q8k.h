@@ -566,7 +566,8 @@ size_t moe_paged_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D);
  * outside cu_q are ignored and their out is not written.  q and out
  * [T, Hq, D] have token and head strides in elements, multiples of 8; all
  * pointers are 16-byte aligned.  Scores and sums are fp32; the weights are
- * rounded to the cache's type before the product with the values.  The
+ * rounded to the cache's type before the product with the values.  A key that
+ * gives a row a score of NaN makes its out and lse NaN.  The
  * values of keys that a token does not see, but another token of its tile
  * does, have to be finite: they are multiplied by a zero weight.  The cache
  * beyond kv_len is never used.  Head sizes 64, 128 and 256 with a page size

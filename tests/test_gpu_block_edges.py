@@ -182,3 +182,65 @@ def test_attention_sequences_that_share_rows(n, T, kv, hq, D):
     cu = torch.tensor([0, T] + [T] * (n - 1), dtype=torch.int32, device="cuda")     # in order: the first has all rows
     moe.moe_paged_attention(q, kc, kc, table, cu, lens, 0.1, out, ws)
     assert status(ws) == 0 and (out == 0.0).all()
+
+
+def positions(c):
+    """Position of each token in its sequence, and the sequence."""
+    pos, seq = [], []
+    for b, (n, kv) in enumerate(zip(c.q_lens, c.kv_lens)):
+        pos += list(range(kv - n, kv))
+        seq += [b] * n
+    return pos, seq
+
+
+def check_special(c, hq, D, window, dtype, bad_v, bad_k=(), seed=81):
+    """bad_v: (sequence, key, head, column, value) that are not finite, bad_k: (sequence, key, head) whose key is NaN.
+    Rows that see none of them are as if they were 0; a row that sees a value has no finite number in its column; a
+    row that sees a key has NaN everywhere."""
+    page, hkv = c.k.shape[1], c.k.shape[2]
+    G = hq // hkv
+    clean_k, clean_v = c.k.clone(), c.v.clone()
+    for b, j, h, col, v in bad_v:
+        p = int(c.table[b, j // page])
+        c.v[p, j % page, h, col] = v
+        clean_v[p, j % page, h, col] = 0.0
+    for b, j, h in bad_k:
+        c.k[int(c.table[b, j // page]), j % page, h, D // 2] = NAN
+    c.dk.copy_(c.k), c.dv.copy_(c.v)
+    q, out, lse, ws = attend(c, hq, D, 0.1, window, dtype, seed)
+    assert status(ws) == 0
+    want, wl, tol, ltol = block_ref.attention(q, clean_k, clean_v, c.table, c.q_lens, c.kv_lens, 0.1, window, dtype)
+    pos, seq = positions(c)
+    got, gl = out.cpu().double(), lse.cpu().double()
+    extra = torch.zeros_like(want)
+    void = torch.zeros(c.T, hq, dtype=torch.bool)
+    for t in range(c.T):
+        sees = lambda b, j: seq[t] == b and j <= pos[t] and (not window or j > pos[t] - window)
+        for b, j, h, col, v in bad_v:
+            if sees(b, j):
+                extra[t, h * G:(h + 1) * G, col] += v
+        for b, j, h in bad_k:
+            if sees(b, j):
+                void[t, h * G:(h + 1) * G] = True
+    fine = torch.isfinite(extra) & ~void.unsqueeze(2)
+    assert (extra[fine] == 0).all()
+    assert torch.isnan(got[void]).all() and torch.isnan(gl[void]).all()
+    assert ((got - want).abs() <= tol)[fine].all()
+    none = torch.isneginf(wl) & ~void
+    assert torch.isneginf(gl[none]).all()
+    rest = ~none & ~void
+    assert ((gl - wl).abs()[rest] <= ltol[rest]).all()
+    # (not finite, not which: the weight of a far key may be 0 in 16 bits, and 0 times infinity is NaN)
+    assert not torch.isfinite(got[~torch.isfinite(extra) & ~void.unsqueeze(2)]).any()
+    return ws
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 80])
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("q_lens,kv_lens", [([1, 2], [40, 33]), ([1], [6000]), ([150, 3], [200, 60])])
+def test_attention_of_keys_and_values_that_are_not_finite(q_lens, kv_lens, D, dtype):
+    """What every row sees: NaN keys make rows NaN in out and in lse, values that are not finite reach their column."""
+    c = Cache(q_lens, kv_lens, 2, D, 32, dtype, 80)
+    check_special(c, 6, D, 0, dtype, [(0, 3, 0, 5, INF), (0, 20, 1, 7, -INF), (0, 2, 1, D - 1, NAN)])
+    c = Cache(q_lens, kv_lens, 2, D, 32, dtype, 82)
+    check_special(c, 6, D, 0, dtype, [], [(0, 7, 1)])
