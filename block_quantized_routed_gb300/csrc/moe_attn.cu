@@ -88,11 +88,14 @@ struct Cfg {
   static constexpr int kSmemQ = 0;
   static constexpr int kSmemRing = kGroups * kQ;
   static constexpr int kSmemMisc = kSmemRing + kStages * kSlot;
-  static constexpr int kSmemXch = kSmemMisc + 1024;       // after barriers and the prologue's results
+  static constexpr int kBars = 8 * (2 * kStages + 11);    // barriers of a pass
+  static constexpr int kSmemStart = kSmemMisc + 2 * kBars;  // after those of two passes: the prologue's results
+  static constexpr int kSmemXch = kSmemMisc + 1024;
   static constexpr int kSmem = kSmemXch + 2 * 128 * 8;   // per group and row: maximum and sum, for joining the groups
   static constexpr size_t kPartFloats = (size_t)kRows * (D + 2);  // m, sum and accumulator of an item's rows
   static constexpr uint32_t kColO = 0, kColS = 256;      // tensor memory columns: O per group, two score buffers
 };
+static_assert(Cfg<64>::kBars >= Cfg<128>::kBars && Cfg<64>::kBars >= Cfg<256>::kBars, "barriers");
 static_assert(Cfg<128>::kSmem <= 232448 && Cfg<64>::kSmem <= 232448 && Cfg<256>::kSmem <= 232448, "shared memory");
 
 // ---------------------------------------------------------------- PTX
@@ -125,6 +128,14 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t p) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t p, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -292,10 +303,21 @@ struct Start {
   bool by_item;     // units are whole items (see plan)
   int c0, parts;    // equal numbers of CTAs for the items: the first CTA of this item, and how many take part (else 0)
   volatile int abort;
+  volatile int again;  // some output was not finite: a second pass (see clean_values)
   uint32_t tmem;
   int n_cut;
   Cut cut[2];
 };
+
+// Keys that every row of an item sees; the others of the item's range some rows see and some do not.
+struct Shared {
+  int lo, hi;
+};
+__device__ __forceinline__ Shared shared_keys(const AttnArgs& a, int G, const Item& it) {
+  return Shared{window_lo(it.hi, a.window), max(it.lo, it.s.kv - it.s.n + it.r0 / G + 1)};
+}
+
+static_assert(2 * Cfg<64>::kBars + sizeof(Start) <= 1024 && Cfg<64>::kBars % 8 == 0, "shared memory after the barriers");
 
 __device__ __forceinline__ Walk walk_begin(const Start& st) {
   Walk w;
@@ -618,6 +640,78 @@ __device__ __forceinline__ void join_parts(const AttnArgs& a, int G, Start& st, 
   if (tid == 0) count_gone(counter, np * 2 - 1);
 }
 
+// All ones in each half of a word whose 16-bit number is not finite.
+template <bool BF16>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  constexpr uint32_t kExp = BF16 ? 0x7f807f80u : 0x7c007c00u;
+  return __vcmpeq2(w & kExp, kExp);
+}
+// Eight numbers times 0, added up: 0 (false) where all are finite, else NaN.
+template <bool BF16>
+__device__ __forceinline__ bool times_zero(uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w[i]), "r"(0u));
+    else asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(sum) : "r"(w[i]), "r"(0u));
+  }
+  return (sum & 0x7fff7fffu) != 0;
+}
+// Values that some row of an item multiplies by 0, because it does not see their key, have to be finite: 0 times infinity
+// is NaN.  The issuing thread clears what lies outside the item's range of keys.  Keys that some rows of an item see and
+// some do not (later tokens of the chunk, the far end of a window) are looked at only when a row's output turned out not
+// to be finite although its sum is: the CTA then does its work again, and in that pass the 128 threads of a softmax group
+// look through the values of the tile's rows [s0, e) and [b, s1), which are those keys, before they hand over the tile's
+// weights.  What is not finite is cleared, and the rows that do see it get it back with their results (see add_cleared).
+// With two row tiles both groups do so, each before its own product, on the same tile: they clear the same elements.
+// (Looking in the first pass made items of few tiles 5 to 15% longer: by the softmax groups, or by the warps that gather
+// the query rows.)
+template <int D, bool BF16>
+__device__ __forceinline__ void clean_values(uint32_t tile, int s0, int e, int b, int s1, int r) {
+  constexpr int kN = Cfg<D>::kN, kChunks = D / 8;
+  const int n0 = (e - s0) * kChunks, n = n0 + (s1 - b) * kChunks;
+#pragma unroll 1
+  for (int i = r; i < n; i += 128) {
+    const int row = (i < n0 ? s0 : b - (e - s0)) + i / kChunks, ch = i % kChunks;
+    const uint32_t p = tile + (ch / 8) * (kN * 128) + row * 128 + (ch % 8) * 16;
+    const auto keep = [](uint32_t w) { return w & ~not_finite<BF16>(w); };
+    const uint4 v = lds16(p);
+    if (times_zero<BF16>(v)) sts16(p, make_uint4(keep(v.x), keep(v.y), keep(v.z), keep(v.w)));
+  }
+  fence_proxy();  // the products read shared memory by the async proxy
+}
+// Adds the values that clean_values takes out to the columns [col0, col1) of a row that sees the keys [j0, j1) of a
+// segment: the infinity or NaN of the value, whatever the row's weight.  The row's result is in `out`, or where that is
+// null in `part`, vectors of four columns `cs` vectors apart.
+template <bool BF16>
+__device__ __forceinline__ void add_cleared(const AttnArgs& a, int b, int h, int j0, int j1, Shared all, int col0, int col1,
+                                            uint16_t* out, float* part, int cs) {
+#pragma unroll 1
+  for (int j = j0; j < j1; ++j) {
+    if (j >= all.lo && j < all.hi) {
+      j = all.hi - 1;
+      continue;
+    }
+    const int page = __ldg(a.table + (int64_t)b * a.kv.table_stride + j / a.kv.page_size);
+    if (page < 0 || page >= a.kv.num_pages) continue;
+    const uint16_t* v = static_cast<const uint16_t*>(a.v_cache) + page * a.kv.v_page_stride +
+                        (j % a.kv.page_size) * a.kv.v_row_stride + h * a.kv.v_head_stride;
+#pragma unroll 1
+    for (int c = col0; c < col1; ++c) {
+      const uint32_t x = __ldg(v + c);
+      if (!(not_finite<BF16>(x) & 1u)) continue;
+      const float f = BF16 ? __uint_as_float(x << 16) : __half2float(__ushort_as_half((unsigned short)x));
+      if (out) {
+        const float o = BF16 ? __uint_as_float((uint32_t)out[c] << 16) : __half2float(__ushort_as_half(out[c]));
+        out[c] = (uint16_t)pack16<BF16>(o + f, 0.0f);
+      } else {
+        part[(c / 4 * cs) * 4 + c % 4] += f;
+      }
+    }
+  }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -629,27 +723,27 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     if (threadIdx.x == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     return;
   }
-  const uint32_t bars = base + C::kSmemMisc;
+  uint32_t bars = base + C::kSmemMisc;
   const auto full = [&](int s) { return bars + 8 * s; };
   const auto empty = [&](int s) { return bars + 8 * (kStages + s); };
-  const uint32_t drain = bars + 8 * (2 * kStages);
-  const auto q_full = [&](int t) { return drain + 8 + 8 * t; };    // row tile t of q is there
-  const auto q_empty = [&](int t) { return drain + 24 + 8 * t; };  // its last product is done
-  const auto s_full = [&](int b) { return drain + 40 + 8 * b; };   // scores of buffer b
-  const auto p_full = [&](int b) { return drain + 56 + 8 * b; };   // weights of buffer b
-  const auto o_full = [&](int b) { return drain + 72 + 8 * b; };   // buffer b's product with the values
-  Start& st = *reinterpret_cast<Start*>(smem + C::kSmemMisc + 512);
+  const auto drain = [&] { return bars + 8 * (2 * kStages); };
+  const auto q_full = [&](int t) { return drain() + 8 + 8 * t; };    // row tile t of q is there
+  const auto q_empty = [&](int t) { return drain() + 24 + 8 * t; };  // its last product is done
+  const auto s_full = [&](int b) { return drain() + 40 + 8 * b; };   // scores of buffer b
+  const auto p_full = [&](int b) { return drain() + 56 + 8 * b; };   // weights of buffer b
+  const auto o_full = [&](int b) { return drain() + 72 + 8 * b; };   // buffer b's product with the values
+  Start& st = *reinterpret_cast<Start*>(smem + C::kSmemStart);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarpLoad = 4 * kGroups, kWarpMma = kWarpLoad + 1, kWarpQ = kWarpLoad + 2;
   const int G = a.Hq / a.kv.Hkv;
 
   // ---- prologue: the call's work in units, and this CTA's share
-  if (warp == kWarpMma && lane == 0) {
+  const auto init_barriers = [&] {
     for (int s = 0; s < kStages; ++s) {
       bar_init(full(s), 1);
       bar_init(empty(s), 1);
     }
-    bar_init(drain, 1);
+    bar_init(drain(), 1);
     for (int b = 0; b < 2; ++b) {
       bar_init(q_full(b), 64);
       bar_init(q_empty(b), 1);
@@ -658,7 +752,11 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
       bar_init(o_full(b), 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  };
+  if (warp == kWarpMma && lane == 0) {
+    init_barriers();
     st.abort = 0;
+    st.again = 0;
     st.n_cut = 0;
   }
   if (warp == kWarpMma) {
@@ -865,10 +963,275 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
   const Wait wait{&st, a.status};
   const float c2 = fmaxf(fabsf(a.scale) * 1.44269504088896341f, 1e-30f);  // log2 units; the sign is in the MMA
 
-  // Two groups: 384 threads start with 168 registers each; the softmax groups
-  // take 208, the other four warps keep 88 (256 * 208 + 128 * 88 = 384 * 168).
-  if (warp >= kWarpLoad) {
-    if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  // ---- softmax: thread = row
+  const auto softmax = [&](auto pass) {
+    constexpr bool kCareful = decltype(pass)::value;
+    const int grp = warp >> 2, r = tid & 127;
+    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
+    const uint32_t o_addr = lanes + C::kColO + grp * D;
+    uint32_t s_phase = 0, o_phase = 0;  // bit b: parity of buffer b's next scores / of its last product
+    float* const part0 = reinterpret_cast<float*>(a.ws + kWsHead);
+    constexpr size_t kPartFloats = C::kPartFloats;
+    float2* const xch = reinterpret_cast<float2*>(smem + C::kSmemXch);
+    int g_seg = st.first;  // unit at which the segment starts
+    int ring = 0;          // tiles that the segments before took from the ring (careful)
+    // rows of out on 32-byte boundaries: whole sectors at a time
+    const bool wide_out = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.o_stride * 2) | (uintptr_t)(a.o_head_stride * 2)) & 31) == 0;
+    for (Walk w = walk_begin(st); w.left > 0;) {
+      const Seg sg = walk_seg(w);
+      if (sg.first == sg.last) {
+        g_seg += sg.len;
+        walk_next<kN, kRows>(a, G, w, sg.len);
+        continue;
+      }
+      const int m = sg.tiles;
+      const bool two = kGroups == 2 && w.it.rows > 128;
+      const int U = two ? 2 * m : m;
+      const int row = (two ? grp * 128 : 0) + r;  // row of the item
+      const bool valid = row < w.it.rows;
+      const bool busy = (row & ~31) < w.it.rows;  // some row of the warp exists
+      const int R = w.it.r0 + row, tok = valid ? R / G : 0, g = valid ? R - tok * G : 0;
+      const int pos = w.it.s.kv - w.it.s.n + tok;
+      const int hi = pos + 1, lo = window_lo(hi, a.window);
+      float ref = -INFINITY, sum = 0.0f;  // reference (raw score units) and sum of the row
+      bool acc = false;                   // the accumulator holds something
+
+      for (int u = kGroups == 2 ? grp : 0; u < U; u += kGroups) {
+        const int buf = u & 1;
+        warp_wait(wait, s_full(buf), s_phase >> buf & 1);
+        s_phase ^= 1u << buf;
+        fence_after();
+        if (busy) {
+          const uint32_t s_addr = lanes + C::kColS + buf * kN;
+          uint32_t s[kN];
+#pragma unroll
+          for (int x = 0; x < kN / 32; ++x) tmem_ld32(s_addr + 32 * x, s + 32 * x);
+          wait_ld();
+          const int k0 = (w.it.t0 + sg.first + (two ? u >> 1 : u)) * kN;
+          if (__any_sync(kAll, valid && (hi < k0 + kN || lo > k0))) {
+            const int j1 = hi - k0, j0 = lo - k0;
+#pragma unroll
+            for (int j = 0; j < kN; ++j)
+              if (j >= j1 || j < j0) s[j] = 0xff800000u;
+          }
+          float mx[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
+#pragma unroll
+          for (int j = 8; j < kN; j += 2)
+            mx[j / 2 & 3] = max3(mx[j / 2 & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
+          const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
+          float f = 1.0f;
+          const bool grow = ref == -INFINITY ? top > -INFINITY : (top - ref) * c2 > kGrow;
+          if (grow) {
+            f = ref == -INFINITY ? 0.0f : ex2((ref - top) * c2);
+            ref = top;
+            sum *= f;
+          }
+          if (acc && __any_sync(kAll, grow && valid)) {
+            // The accumulator's last product has to be done.  Two groups: it was issued before this tile's scores,
+            // so it is.  One group: it may still run.
+            if (kGroups == 1) {
+              warp_wait(wait, o_full(buf ^ 1), o_phase >> (buf ^ 1) & 1 ^ 1);
+              fence_after();
+            }
+#pragma unroll 1
+            for (int x = 0; x < D / 32; ++x) {
+              uint32_t o[32];
+              tmem_ld32(o_addr + 32 * x, o);
+              wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tmem_st32(o_addr + 32 * x, o);
+            }
+          }
+          const float shift = ref == -INFINITY ? 0.0f : -ref * c2;
+          const uint64_t cc = f2(c2, c2), sh = f2(shift, shift);
+          uint64_t acc2[2] = {0, 0};
+#pragma unroll
+          for (int j = 0; j < kN; j += 2) {
+            const uint64_t t = f2_fma((uint64_t)s[j] | (uint64_t)s[j + 1] << 32, cc, sh);
+            const float p0 = ex2(f2_lo(t)), p1 = ex2(f2_hi(t));
+            acc2[(j >> 1) & 1] = f2_add(acc2[(j >> 1) & 1], f2(p0, p1));
+            s[j >> 1] = pack16<BF16>(p0, p1);
+          }
+          const uint64_t both = f2_add(acc2[0], acc2[1]);
+          sum += f2_lo(both) + f2_hi(both);
+#pragma unroll
+          for (int x = 0; x < kN / 64; ++x) tmem_st32(s_addr + 32 * x, s + 32 * x);
+          wait_st();
+        }
+        if constexpr (kCareful) {
+          const int tile = two ? u >> 1 : u, k0 = (w.it.t0 + sg.first + tile) * kN;
+          const Shared all = shared_keys(a, G, w.it);
+          const int s0 = max(w.it.lo - k0, 0), s1 = min(w.it.hi - k0, kN);
+          const int e = min(max(all.lo - k0, s0), s1), b = max(min(all.hi - k0, s1), e);
+          if (e > s0 || b < s1) {
+            const int op = ring + (two ? 2 * tile + 1 : min(2 * tile + 2, 2 * m - 1));  // its place in the ring's order
+            warp_wait(wait, full(op % kStages), op / kStages & 1);
+            clean_values<D, BF16>(base + C::kSmemRing + op % kStages * C::kSlot, s0, e, b, s1, r);
+          }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(p_full(buf));
+        acc = true;
+        if (kGroups == 1) o_phase ^= 1u << buf;
+      }
+
+      // ---- the segment's result
+      const bool whole = sg.first == 0 && sg.last == w.it.payload();
+      const bool join = kGroups == 2 && !two && U > 1;  // two groups hold sums of the same rows
+      if (acc) {
+        const int lb = kGroups == 2 ? grp : (U - 1) & 1;
+        if (kGroups == 2) o_phase ^= 1u << lb;  // two groups: told once per segment
+        warp_wait(wait, o_full(lb), o_phase >> lb & 1 ^ 1);
+        fence_after();
+      }
+      float m2 = ref == -INFINITY ? -INFINITY : ref * c2;  // log2 units from here on
+      // partial sums: slot 0 if the CTA's first unit is in this item, else 1
+      const int g_item = g_seg - w.off;
+      const int slot = g_seg == st.first ? 0 : 1;
+      float* part = part0 + ((size_t)blockIdx.x * 2 + slot) * kPartFloats;
+      bool writes = two || grp == 0;  // this group puts out columns
+      int col0 = 0, col1 = D;
+      float f_own = 1.0f, f_other = 0.0f;
+      if (join) {  // both groups' accumulators are in reach of either: each puts out half of the columns
+        xch[grp * 128 + r] = make_float2(m2, sum);
+        fence_before();
+        named_sync(1, 256);
+        fence_after();
+        const float2 other = xch[(grp ^ 1) * 128 + r];
+        const float M = fmaxf(m2, other.x);
+        f_own = m2 == -INFINITY ? 0.0f : ex2(m2 - M);
+        f_other = other.x == -INFINITY ? 0.0f : ex2(other.x - M);
+        // the same sum in both groups, to the bit
+        const float a0 = grp ? other.y : sum, b0 = grp ? f_other : f_own, a1 = grp ? sum : other.y, b1 = grp ? f_own : f_other;
+        sum = a0 * b0 + a1 * b1;
+        m2 = M;
+        writes = true;
+        col0 = grp * (D / 2);
+        col1 = col0 + D / 2;
+      }
+      const float inv = inverse_of(sum);
+      // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
+      const int c0 = whole ? 0 : st.parts ? st.c0 : owner(st, g_item + kItemUnits);
+      const int parts = whole ? 1 : st.parts ? st.parts : owner(st, g_item + w.it.cost() - 1) - c0 + 1;
+      const bool by_row = part_by_row(w.it.rows, parts);
+      const int part_cs = by_row ? 1 : w.it.rows, part_rs = by_row ? D / 4 : 1;
+      const uint32_t other_addr = lanes + C::kColO + (grp ^ 1) * D;
+      const bool mixed = !kCareful && w.it.s.n > 1;  // keys that not every row sees
+      uint64_t zero = 0;                             // 0 while every output is finite
+      if (writes) {
+        constexpr int kW = kGroups == 1 ? 64 : 32;  // columns at a time
+#pragma unroll 1
+        for (int x0 = col0; x0 < col1; x0 += kW) {
+          uint32_t o[kW];
+          if (busy && acc) {
+#pragma unroll
+            for (int y = 0; y < kW; y += 32) tmem_ld32(o_addr + x0 + y, o + y);
+            if (join) {
+              uint32_t e[kW];
+#pragma unroll
+              for (int y = 0; y < kW; y += 32) tmem_ld32(other_addr + x0 + y, e + y);
+              wait_ld();
+#pragma unroll
+              for (int j = 0; j < kW; ++j)
+                o[j] = __float_as_uint(__uint_as_float(o[j]) * f_own + __uint_as_float(e[j]) * f_other);
+            } else {
+              wait_ld();
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kW; ++j) o[j] = 0u;
+          }
+          if (mixed) {
+#pragma unroll
+            for (int j = 0; j < kW; j += 2) zero = f2_fma((uint64_t)o[j] | (uint64_t)o[j + 1] << 32, 0, zero);
+          }
+          if (valid) {
+            if (whole) {
+              uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tok) * a.o_stride +
+                              (int64_t)(w.it.h * G + g) * a.o_head_stride + x0;
+#pragma unroll
+              for (int j = 0; j < kW / 2; ++j)
+                o[j] = pack16<BF16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+              if (wide_out) {
+#pragma unroll
+                for (int j = 0; j < kW / 2; j += 8) store32(out + 2 * j, o + j);
+              } else {
+#pragma unroll
+                for (int j = 0; j < kW / 2; j += 4)
+                  *reinterpret_cast<uint4*>(out + 2 * j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+              }
+            } else {
+              float4* dst = reinterpret_cast<float4*>(part + 2 * kRows) + x0 / 4 * part_cs + row * part_rs;
+#pragma unroll
+              for (int j = 0; j < kW; j += 4)
+                dst[j / 4 * part_cs] = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
+                                                 __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+            }
+          }
+          __syncwarp();
+        }
+        if constexpr (kCareful) {
+          const int key0 = (w.it.t0 + sg.first) * kN;
+          if (valid)
+            add_cleared<BF16>(a, w.it.b, w.it.h, max(lo, key0), min(hi, key0 + m * kN), shared_keys(a, G, w.it), col0, col1,
+                              whole ? static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tok) * a.o_stride +
+                                          (int64_t)(w.it.h * G + g) * a.o_head_stride
+                                    : nullptr,
+                              part + 2 * kRows + (size_t)row * part_rs * 4, part_cs);
+        } else if (mixed && valid && f2_lo(zero) + f2_hi(zero) != 0.0f && sum - sum == 0.0f) {
+          st.again = 1;  // not finite, though the weights are
+        }
+      }
+      ring += 2 * m;
+      fence_before();
+      writes = two || grp == 0;  // the row's statistics are written once
+      if (writes && whole && valid && a.lse)
+        a.lse[(int64_t)(w.it.s.q0 + tok) * a.Hq + w.it.h * G + g] =
+            lse_of(m2, sum);
+      if (!whole) {
+        if (writes && valid) {
+          reinterpret_cast<float2*>(part)[row] = make_float2(m2, sum);
+        }
+        if (tid == 0) {
+          Cut& cut = st.cut[st.n_cut++];
+          cut.c0 = c0;
+          cut.parts = parts;
+          cut.slot0 = st.parts || share(st, c0) >= g_item ? 0 : 1;
+          cut.rows = w.it.rows;
+          cut.r0 = w.it.r0;
+          cut.q0 = w.it.s.q0;
+          cut.h = w.it.h;
+        }
+      }
+      if (join) named_sync(1, 256);  // both groups' columns are read before the next item's products
+      g_seg += sg.len;
+      walk_next<kN, kRows>(a, G, w, sg.len);
+    }
+  };
+
+  // The end of a pass, for every warp: whether there is another one, on barriers of its own (the last arrivals on this
+  // pass's may still be under way).
+  const auto another = [&](bool careful) {
+    __syncwarp();
+    fence_before();
+    named_sync(0, C::kThreads);
+    fence_after();
+    if (careful || !st.again || st.abort) return false;
+    named_sync(0, C::kThreads);
+    bars += C::kBars;
+    if (warp == kWarpMma && lane == 0) {
+      init_barriers();
+      st.n_cut = 0;
+    }
+    named_sync(0, C::kThreads);
+    return true;
+  };
+  // ---- the warps that feed the softmax groups
+  const auto feed = [&] {
     if (warp == kWarpLoad) {
       // ---- keys and values by TMA, a box per (page, 64 columns)
       // (Page and box sizes are powers of two; what a tile's keys and values share is formed once, and the next tile's
@@ -987,17 +1350,20 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
             const int tile = two ? u >> 1 : u;
             if (!two || !buf) {
               take(v_slot);
-              if (tile == m - 1) {
-                // Values past the sequence's last key: whatever the page holds there, even NaN, must not reach a sum.
-                const int k0 = (w.it.t0 + sg.first + tile) * kN, to = min(w.it.hi, k0 + kN) - k0;
-                const int end = (to + 15) / 16 * 16;
-                for (int row = max(0, w.it.s.kv - k0); row < end; ++row) {
+              if (tile == 0 || tile == m - 1) {
+                // Values next to the item's keys, in the first and the last K step: whatever they are, even NaN, they must
+                // not reach a sum.
+                const int k0 = (w.it.t0 + sg.first + tile) * kN, from = max(w.it.lo - k0, 0), to = min(w.it.hi - k0, kN);
+                const int begin = from & ~15, end = (to + 15) & ~15;
+                for (int row = begin; row < end; ++row) {
+                  if (row == from) row = to;
+                  if (row == end) break;
                   uint8_t* line = smem + C::kSmemRing + v_slot * C::kSlot + row * 128;
 #pragma unroll
                   for (int i = 0; i < C::kSub * 8; ++i)
                     *reinterpret_cast<uint4*>(line + (i / 8) * (kN * 128) + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
                 }
-                if (w.it.s.kv - k0 < end) fence_proxy();
+                if (begin < from || to < end) fence_proxy();
               }
             }
             if (tile == 0 || tile == m - 1) {
@@ -1025,9 +1391,9 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
           walk_next<kN, kRows>(a, G, w, sg.len);
         }
         if (st.abort) {  // given up: the products in flight end before tensor memory is freed
-          mma_commit(drain);
+          mma_commit(drain());
           const long long t0 = clock64();
-          while (!bar_try(drain, 0) && clock64() - t0 < kWaitCycles / 8) {
+          while (!bar_try(drain(), 0) && clock64() - t0 < kWaitCycles / 8) {
           }
         }
       }
@@ -1077,231 +1443,28 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         walk_next<kN, kRows>(a, G, w, sg.len);
       }
     }
+  };
+
+  // Two groups: 384 threads start with 168 registers each; the softmax groups
+  // take 208, the other four warps keep 88 (256 * 208 + 128 * 88 = 384 * 168).
+  if (warp >= kWarpLoad) {
+    if constexpr (kGroups == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    for (bool careful = false;; careful = true) {
+      feed();
+      if (!another(careful)) break;
+    }
   } else {
     if constexpr (kGroups == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    // ---- softmax: thread = row
-    const int grp = warp >> 2, r = tid & 127;
-    const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
-    const uint32_t o_addr = lanes + C::kColO + grp * D;
-    uint32_t s_phase = 0, o_phase = 0;  // bit b: parity of buffer b's next scores / of its last product
-    float* const part0 = reinterpret_cast<float*>(a.ws + kWsHead);
-    constexpr size_t kPartFloats = C::kPartFloats;
-    constexpr int kJoin = 128 * kGroups;
-    float2* const xch = reinterpret_cast<float2*>(smem + C::kSmemXch);
-    unsigned* const counters = reinterpret_cast<unsigned*>(a.ws + 16);
-    int g_seg = st.first;  // unit at which the segment starts
-    // rows of out on 32-byte boundaries: whole sectors at a time
-    const bool wide_out = ((reinterpret_cast<uintptr_t>(a.out) | (uintptr_t)(a.o_stride * 2) | (uintptr_t)(a.o_head_stride * 2)) & 31) == 0;
-    for (Walk w = walk_begin(st); w.left > 0;) {
-      const Seg sg = walk_seg(w);
-      if (sg.first == sg.last) {
-        g_seg += sg.len;
-        walk_next<kN, kRows>(a, G, w, sg.len);
-        continue;
-      }
-      const int m = sg.tiles;
-      const bool two = kGroups == 2 && w.it.rows > 128;
-      const int U = two ? 2 * m : m;
-      const int row = (two ? grp * 128 : 0) + r;  // row of the item
-      const bool valid = row < w.it.rows;
-      const bool busy = (row & ~31) < w.it.rows;  // some row of the warp exists
-      const int R = w.it.r0 + row, tok = valid ? R / G : 0, g = valid ? R - tok * G : 0;
-      const int pos = w.it.s.kv - w.it.s.n + tok;
-      const int hi = pos + 1, lo = window_lo(hi, a.window);
-      float ref = -INFINITY, sum = 0.0f;  // reference (raw score units) and sum of the row
-      bool acc = false;                   // the accumulator holds something
-
-      for (int u = kGroups == 2 ? grp : 0; u < U; u += kGroups) {
-        const int buf = u & 1;
-        warp_wait(wait, s_full(buf), s_phase >> buf & 1);
-        s_phase ^= 1u << buf;
-        fence_after();
-        if (busy) {
-          const uint32_t s_addr = lanes + C::kColS + buf * kN;
-          uint32_t s[kN];
-#pragma unroll
-          for (int x = 0; x < kN / 32; ++x) tmem_ld32(s_addr + 32 * x, s + 32 * x);
-          wait_ld();
-          const int k0 = (w.it.t0 + sg.first + (two ? u >> 1 : u)) * kN;
-          if (__any_sync(kAll, valid && (hi < k0 + kN || lo > k0))) {
-            const int j1 = hi - k0, j0 = lo - k0;
-#pragma unroll
-            for (int j = 0; j < kN; ++j)
-              if (j >= j1 || j < j0) s[j] = 0xff800000u;
-          }
-          float mx[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = fmaxf(__uint_as_float(s[2 * j]), __uint_as_float(s[2 * j + 1]));
-#pragma unroll
-          for (int j = 8; j < kN; j += 2)
-            mx[j / 2 & 3] = max3(mx[j / 2 & 3], __uint_as_float(s[j]), __uint_as_float(s[j + 1]));
-          const float top = max3(mx[0], mx[1], fmaxf(mx[2], mx[3]));
-          float f = 1.0f;
-          const bool grow = ref == -INFINITY ? top > -INFINITY : (top - ref) * c2 > kGrow;
-          if (grow) {
-            f = ref == -INFINITY ? 0.0f : ex2((ref - top) * c2);
-            ref = top;
-            sum *= f;
-          }
-          if (acc && __any_sync(kAll, grow && valid)) {
-            // The accumulator's last product has to be done.  Two groups: it was issued before this tile's scores,
-            // so it is.  One group: it may still run.
-            if (kGroups == 1) {
-              warp_wait(wait, o_full(buf ^ 1), o_phase >> (buf ^ 1) & 1 ^ 1);
-              fence_after();
-            }
-#pragma unroll 1
-            for (int x = 0; x < D / 32; ++x) {
-              uint32_t o[32];
-              tmem_ld32(o_addr + 32 * x, o);
-              wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tmem_st32(o_addr + 32 * x, o);
-            }
-          }
-          const float shift = ref == -INFINITY ? 0.0f : -ref * c2;
-          const uint64_t cc = f2(c2, c2), sh = f2(shift, shift);
-          uint64_t acc2[2] = {0, 0};
-#pragma unroll
-          for (int j = 0; j < kN; j += 2) {
-            const uint64_t t = f2_fma((uint64_t)s[j] | (uint64_t)s[j + 1] << 32, cc, sh);
-            const float p0 = ex2(f2_lo(t)), p1 = ex2(f2_hi(t));
-            acc2[(j >> 1) & 1] = f2_add(acc2[(j >> 1) & 1], f2(p0, p1));
-            s[j >> 1] = pack16<BF16>(p0, p1);
-          }
-          const uint64_t both = f2_add(acc2[0], acc2[1]);
-          sum += f2_lo(both) + f2_hi(both);
-#pragma unroll
-          for (int x = 0; x < kN / 64; ++x) tmem_st32(s_addr + 32 * x, s + 32 * x);
-          wait_st();
-        }
-        fence_before();
-        __syncwarp();
-        if (lane == 0) bar_arrive(p_full(buf));
-        acc = true;
-        if (kGroups == 1) o_phase ^= 1u << buf;
-      }
-
-      // ---- the segment's result
-      const bool whole = sg.first == 0 && sg.last == w.it.payload();
-      const bool join = kGroups == 2 && !two && U > 1;  // two groups hold sums of the same rows
-      if (acc) {
-        const int lb = kGroups == 2 ? grp : (U - 1) & 1;
-        if (kGroups == 2) o_phase ^= 1u << lb;  // two groups: told once per segment
-        warp_wait(wait, o_full(lb), o_phase >> lb & 1 ^ 1);
-        fence_after();
-      }
-      float m2 = ref == -INFINITY ? -INFINITY : ref * c2;  // log2 units from here on
-      // partial sums: slot 0 if the CTA's first unit is in this item, else 1
-      const int g_item = g_seg - w.off;
-      const int slot = g_seg == st.first ? 0 : 1;
-      float* part = part0 + ((size_t)blockIdx.x * 2 + slot) * kPartFloats;
-      bool writes = two || grp == 0;  // this group puts out columns
-      int col0 = 0, col1 = D;
-      float f_own = 1.0f, f_other = 0.0f;
-      if (join) {  // both groups' accumulators are in reach of either: each puts out half of the columns
-        xch[grp * 128 + r] = make_float2(m2, sum);
-        fence_before();
-        named_sync(1, 256);
-        fence_after();
-        const float2 other = xch[(grp ^ 1) * 128 + r];
-        const float M = fmaxf(m2, other.x);
-        f_own = m2 == -INFINITY ? 0.0f : ex2(m2 - M);
-        f_other = other.x == -INFINITY ? 0.0f : ex2(other.x - M);
-        // the same sum in both groups, to the bit
-        const float a0 = grp ? other.y : sum, b0 = grp ? f_other : f_own, a1 = grp ? sum : other.y, b1 = grp ? f_own : f_other;
-        sum = a0 * b0 + a1 * b1;
-        m2 = M;
-        writes = true;
-        col0 = grp * (D / 2);
-        col1 = col0 + D / 2;
-      }
-      const float inv = inverse_of(sum);
-      // the item's parts are the consecutive CTAs c0 .. c1; they join it when their own work is done
-      const int c0 = whole ? 0 : st.parts ? st.c0 : owner(st, g_item + kItemUnits);
-      const int parts = whole ? 1 : st.parts ? st.parts : owner(st, g_item + w.it.cost() - 1) - c0 + 1;
-      const bool by_row = part_by_row(w.it.rows, parts);
-      const int part_cs = by_row ? 1 : w.it.rows, part_rs = by_row ? D / 4 : 1;
-      const uint32_t other_addr = lanes + C::kColO + (grp ^ 1) * D;
-      if (writes) {
-        constexpr int kW = kGroups == 1 ? 64 : 32;  // columns at a time
-#pragma unroll 1
-        for (int x0 = col0; x0 < col1; x0 += kW) {
-          uint32_t o[kW];
-          if (busy && acc) {
-#pragma unroll
-            for (int y = 0; y < kW; y += 32) tmem_ld32(o_addr + x0 + y, o + y);
-            if (join) {
-              uint32_t e[kW];
-#pragma unroll
-              for (int y = 0; y < kW; y += 32) tmem_ld32(other_addr + x0 + y, e + y);
-              wait_ld();
-#pragma unroll
-              for (int j = 0; j < kW; ++j)
-                o[j] = __float_as_uint(__uint_as_float(o[j]) * f_own + __uint_as_float(e[j]) * f_other);
-            } else {
-              wait_ld();
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < kW; ++j) o[j] = 0u;
-          }
-          if (valid) {
-            if (whole) {
-              uint16_t* out = static_cast<uint16_t*>(a.out) + (int64_t)(w.it.s.q0 + tok) * a.o_stride +
-                              (int64_t)(w.it.h * G + g) * a.o_head_stride + x0;
-#pragma unroll
-              for (int j = 0; j < kW / 2; ++j)
-                o[j] = pack16<BF16>(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
-              if (wide_out) {
-#pragma unroll
-                for (int j = 0; j < kW / 2; j += 8) store32(out + 2 * j, o + j);
-              } else {
-#pragma unroll
-                for (int j = 0; j < kW / 2; j += 4)
-                  *reinterpret_cast<uint4*>(out + 2 * j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-              }
-            } else {
-              float4* dst = reinterpret_cast<float4*>(part + 2 * kRows) + x0 / 4 * part_cs + row * part_rs;
-#pragma unroll
-              for (int j = 0; j < kW; j += 4)
-                dst[j / 4 * part_cs] = make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
-                                                 __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
-            }
-          }
-          __syncwarp();
-        }
-      }
-      fence_before();
-      writes = two || grp == 0;  // the row's statistics are written once
-      if (writes && whole && valid && a.lse)
-        a.lse[(int64_t)(w.it.s.q0 + tok) * a.Hq + w.it.h * G + g] =
-            lse_of(m2, sum);
-      if (!whole) {
-        if (writes && valid) {
-          reinterpret_cast<float2*>(part)[row] = make_float2(m2, sum);
-        }
-        if (tid == 0) {
-          Cut& cut = st.cut[st.n_cut++];
-          cut.c0 = c0;
-          cut.parts = parts;
-          cut.slot0 = st.parts || share(st, c0) >= g_item ? 0 : 1;
-          cut.rows = w.it.rows;
-          cut.r0 = w.it.r0;
-          cut.q0 = w.it.s.q0;
-          cut.h = w.it.h;
-        }
-      }
-      // every group's columns are read before the next item's products, and written before the part is announced
-      if (kGroups == 2 && (join || !whole)) named_sync(1, 256);
-      else if (!whole) named_sync(2, 128);
-      if (!whole && tid == 0) count_up(counters + c0, parts * 2 - 1);
-      g_seg += sg.len;
-      walk_next<kN, kRows>(a, G, w, sg.len);
+    softmax(std::false_type{});
+    if (another(false)) {
+      softmax(std::true_type{});
+      another(true);
     }
-    named_sync(4, kJoin);
-    for (int x = 0; x < st.n_cut; ++x) join_parts<D, BF16>(a, G, st, st.cut[x], part0, counters, smem + C::kSmemRing);
+    unsigned* const counters = reinterpret_cast<unsigned*>(a.ws + 16);
+    if (tid == 0)
+      for (int x = 0; x < st.n_cut; ++x) count_up(counters + st.cut[x].c0, st.cut[x].parts * 2 - 1);
+    for (int x = 0; x < st.n_cut; ++x)
+      join_parts<D, BF16>(a, G, st, st.cut[x], reinterpret_cast<float*>(a.ws + kWsHead), counters, smem + C::kSmemRing);
   }
   fence_before();
   __syncthreads();

@@ -567,11 +567,11 @@ size_t moe_paged_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D);
  * [T, Hq, D] have token and head strides in elements, multiples of 8; all
  * pointers are 16-byte aligned.  Scores and sums are fp32; the weights are
  * rounded to the cache's type before the product with the values.  A key that
- * gives a row a score of NaN makes its out and lse NaN.  The
- * values of keys that a token does not see, but another token of its tile
- * does, have to be finite: they are multiplied by a zero weight.  The cache
- * beyond kv_len is never used.  Head sizes 64, 128 and 256 with a page size
- * that is a power of two >= 16 run on the tensor cores; other sizes run on a
+ * gives a row a score of NaN makes its out and lse NaN; a value that is not
+ * finite leaves no finite number in its column of the rows that see its key.
+ * Keys and values that a row does not see have no effect on it, whatever they
+ * hold, and the cache beyond kv_len is never used.  Head sizes 64, 128 and 256
+ * with a page size that is a power of two >= 16 run on the tensor cores; other sizes run on a
  * general kernel.  The tensor-core form is one cooperative launch of a CTA per
  * SM; calls that could hold 2^31 (row tile, key tile) pairs by T, n_seqs and
  * max_pages alone are refused (MOE_ERR_UNSUPPORTED): cut them.  Sequences with cu_q out of order or out of range, or

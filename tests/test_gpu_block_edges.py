@@ -244,3 +244,33 @@ def test_attention_of_keys_and_values_that_are_not_finite(q_lens, kv_lens, D, dt
     check_special(c, 6, D, 0, dtype, [(0, 3, 0, 5, INF), (0, 20, 1, 7, -INF), (0, 2, 1, D - 1, NAN)])
     c = Cache(q_lens, kv_lens, 2, D, 32, dtype, 82)
     check_special(c, 6, D, 0, dtype, [], [(0, 7, 1)])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256, 80])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,window", [
+    ([4, 5], [40, 33], 4, 0), ([4], [4000], 16, 0), ([150, 3], [200, 60], 6, 0), ([300], [300], 2, 0),
+    ([4, 9], [70, 300], 8, 20), ([150], [600], 4, 33), ([150], [500], 4, 1), ([40], [3000], 32, 1000), ([1], [500], 8, 37)])
+def test_attention_hidden_values_do_not_matter(q_lens, kv_lens, hq, window, D):
+    """Values that are not finite, at keys that a row does not see: of later tokens, and before the window, next to what
+    it sees.  The rows that do see them have them."""
+    page = 32
+    c = Cache(q_lens, kv_lens, 2, D, page, F16, 84)
+    bad, keys = [], []
+    for b, (n, kv) in enumerate(zip(q_lens, kv_lens)):
+        new = range(kv - n, kv)
+        for i, j in enumerate(new):                        # most of the later tokens; the first stays clean
+            if i and (n < 20 or i % 7 == 1):
+                bad.append((b, j, i % 2, (11 * i) % D, [INF, -INF, NAN][i % 3]))
+        if n > 1:
+            bad += [(b, kv - 1, 1, 2, -INF), (b, kv - 1, 0, 2, INF)]
+            keys.append((b, kv - 1, 0))
+        if window:
+            low = kv - n + 1 - window                      # the first key that the first token sees
+            for j in range(max(0, low - page), max(0, low)):
+                bad.append((b, j, j % 2, (5 * j) % D, NAN))
+            for i in range(1, n, 5):                       # seen by the first tokens, not by the later ones
+                if 0 <= low + i - 1 < kv - n:
+                    bad.append((b, low + i - 1, i % 2, (3 * i + 1) % D, INF))
+    check_special(c, hq, D, window, F16, bad)
+    c = Cache(q_lens, kv_lens, 2, D, page, F16, 85)
+    check_special(c, hq, D, window, F16, bad[:3], keys)
