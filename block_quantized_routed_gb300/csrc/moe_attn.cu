@@ -40,8 +40,8 @@
 // is the A operand of P V; V is read as it lies in the cache (MN-major).
 //
 // The output accumulator is rescaled only when a row's maximum has grown by
-// more than 2^8 over the reference: weights stay below 2^8, exactly
-// representable in range for fp16 and bf16, and most tiles skip the pass over
+// more than 2^8 over the reference: weights stay below 2^8 times the
+// reference's, in range for fp16 and bf16, and most tiles skip the pass over
 // the accumulator.
 //
 // Every wait is bounded: after about a second a role records
@@ -73,6 +73,10 @@ static_assert(kWsHead >= 16 + 4 * kMaxCtas, "counters");
 // over 777 keys 12 us, 14 and 19.)
 constexpr int kItemUnits = 3;
 constexpr float kGrow = 8.0f;                    // log2 of the growth that forces a rescale
+// log2 of the reference's weight in 16-bit weights: up to 2^15 in fp16, whose normal numbers then reach down to 2^-21 of
+// the reference (2^-14 without).  Below them a weight is off by up to 2^-32 of the reference.
+template <bool BF16>
+constexpr float kLiftOf = BF16 ? 0.0f : 7.0f;
 
 template <int D_>
 struct Cfg {
@@ -970,6 +974,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 lanes
     const uint32_t o_addr = lanes + C::kColO + grp * D;
     uint32_t s_phase = 0, o_phase = 0;  // bit b: parity of buffer b's next scores / of its last product
+    constexpr float kLift = kLiftOf<BF16>;
     float* const part0 = reinterpret_cast<float*>(a.ws + kWsHead);
     constexpr size_t kPartFloats = C::kPartFloats;
     float2* const xch = reinterpret_cast<float2*>(smem + C::kSmemXch);
@@ -1045,7 +1050,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
               tmem_st32(o_addr + 32 * x, o);
             }
           }
-          const float shift = ref == -INFINITY ? 0.0f : -ref * c2;
+          const float shift = ref == -INFINITY ? 0.0f : kLift - ref * c2;
           const uint64_t cc = f2(c2, c2), sh = f2(shift, shift);
           uint64_t acc2[2] = {0, 0};
 #pragma unroll
@@ -1088,7 +1093,7 @@ attn_kernel(const AttnArgs a, const __grid_constant__ CUtensorMap kmap, const __
         warp_wait(wait, o_full(lb), o_phase >> lb & 1 ^ 1);
         fence_after();
       }
-      float m2 = ref == -INFINITY ? -INFINITY : ref * c2;  // log2 units from here on
+      float m2 = ref == -INFINITY ? -INFINITY : ref * c2 - kLift;  // log2 units from here on
       // partial sums: slot 0 if the CTA's first unit is in this item, else 1
       const int g_item = g_seg - w.off;
       const int slot = g_seg == st.first ? 0 : 1;

@@ -274,3 +274,26 @@ def test_attention_hidden_values_do_not_matter(q_lens, kv_lens, hq, window, D):
     check_special(c, hq, D, window, F16, bad)
     c = Cache(q_lens, kv_lens, 2, D, page, F16, 85)
     check_special(c, hq, D, window, F16, bad[:3], keys)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_many_small_weights_in_fp16(D):
+    """One key far above many others in the same run of tiles: each of those has a weight near 2^-20 of the largest, all
+    of them together a good part of the sum.  Half a step's relative error asks for weights that are normal numbers.
+    (Three hundred sequences share the keys, so that every one is whole.)"""
+    kv, page, n = 16384, 64, 300
+    k, v = torch.zeros(kv // page, page, 1, D, dtype=F16), torch.ones(kv // page, page, 1, D, dtype=F16)
+    k[0, 0], v[0, 0] = 1.0, 0.0
+    table = torch.arange(kv // page, dtype=torch.int32).view(1, -1)
+    cu = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    lens = torch.full((n,), kv, dtype=torch.int32, device="cuda")
+    q = torch.ones(n, 1, D, dtype=F16)
+    out = torch.empty(n, 1, D, dtype=F16, device="cuda")
+    lse = torch.empty(n, 1, device="cuda")
+    ws = torch.zeros(moe.moe_paged_attention_workspace_size(1, 1, D), dtype=torch.uint8, device="cuda")
+    scale = float(np.log(2.0 ** 24 / 10.45)) / D          # weights of 10.45 * 2^-24
+    moe.moe_paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda().repeat(n, 1), cu, lens, scale, out, ws, lse=lse)
+    assert status(ws) == 0
+    want, wl, tol, ltol = block_ref.attention(q[:1], k, v, table, [1], [kv], scale, 0, F16)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+    assert ((lse.cpu().double() - wl).abs() <= ltol).all()
