@@ -433,8 +433,16 @@ __global__ void __launch_bounds__(NV == 1 ? 1024 : 512, NV == 2 ? 2 : 1) add_rms
   } else {
     block_reduce<true, false>(sq, peak, buf);
   }
-  const float r = rsqrtf(fmaf(sq, 1.0f / (float)a.H, a.eps));
+  const float mean = fmaf(sq, 1.0f / (float)a.H, a.eps);
+  const float r = mean == 0.0f ? 0.0f : rsqrtf(mean);  // (eps = 0 and a row of zeros, or squares below fp32's range: z = 0)
   const bool fp8 = fmt == MOE_NORM_Q_E4M3_G128 || fmt == MOE_NORM_Q_E4M3_ROW;
+  if (fp8 && r == 0.0f) {  // fp8 codes are taken before r: z = 0 has codes 0 too
+    peak = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = 0.0f;
+  }
   if (kEarly && !fp8) peak = fmaxf(peak * r, 0.0f);  // (no number: 0, as the maximum of the |z| would be)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {

@@ -484,7 +484,8 @@ typedef enum {
  * sum_out may be x or residual themselves where type and stride agree; no
  * other overlap.  An all-zero group has d = 0 and codes 0; a row holding NaN
  * or an infinity has unspecified y and codes, other rows are not affected.
- * s^2 is summed in fp32: |s| beyond 1e18 overflows it.  Pointers must be
+ * s^2 is summed in fp32: |s| beyond 1e18 overflows it.  Where the mean and eps
+ * together are 0 in fp32 (eps = 0 and a row of zeros), z = 0.  Pointers must be
  * aligned to their element; rows on 16-byte boundaries take the wide loads. */
 int moe_add_rmsnorm(const void* x, int32_t x_dtype, int64_t x_stride, const void* residual, int32_t r_dtype,
                     int64_t r_stride, const void* weight, int32_t w_dtype, float weight_offset, float eps, int64_t T,

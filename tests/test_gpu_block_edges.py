@@ -6,7 +6,7 @@ import torch
 
 import block_quantized_routed_gb300 as moe
 from tests import block_ref
-from tests.test_gpu_block import BF16, F16, F32, Cache, attend, check_route, rnd, status
+from tests.test_gpu_block import BF16, F16, F32, Cache, attend, check_norm, check_route, rnd, status
 
 pytestmark = pytest.mark.gpu
 INF, NAN = float("inf"), float("nan")
@@ -121,6 +121,33 @@ def test_route_gates_of_scores_below_fp32():
     l[1, 40] = 1.0
     for sigmoid in (True, False):
         check_route(l, None, 8, sigmoid, renorm=False)
+
+
+# ------------------------------------------------------------------ norm
+
+@pytest.mark.parametrize("H", [256, 2304, 10240])
+@pytest.mark.parametrize("T", [4, 700])
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("fmt,g,top", [("Q8K", 256, 127.0), ("E4M3_G128", 128, 448.0), ("E4M3_ROW", 0, 448.0),
+                                       ("INT8_ROW", 0, 127.0)])
+def test_norm_zero_rows_without_eps(H, T, off, fmt, g, top):
+    """eps = 0: rows of zeros, and rows whose squares are below fp32's range, have codes, scales and y of 0."""
+    x, w = rnd((T, H), 3), 1 + 0.2 * rnd((H,), 4)
+    x[1] = 0.0
+    x[2] *= 1e-30
+    xb = torch.zeros(T, H + off, device="cuda")
+    xb[:, off:] = x.cuda()
+    q = torch.full((T, H), 5.0, device="cuda").to(torch.float8_e4m3fn if top == 448.0 else torch.int8)
+    d = torch.full((T, -(-H // (g or H))), 9.0, device="cuda")
+    bs = torch.full((T, H // 16), 9, dtype=torch.int16, device="cuda") if fmt == "Q8K" else None
+    y = torch.full((T, H), 9.0, device="cuda")
+    moe.moe_add_rmsnorm(xb[:, off:], w.cuda(), 0.0, y=y, q_fmt=getattr(moe, "NORM_Q_" + fmt), q=q, d=d, bsum16=bs)
+    for t in (1, 2):
+        assert (y[t] == 0).all() and (q[t].float() == 0).all() and (d[t] == 0).all()
+        assert bs is None or (bs[t] == 0).all()
+    key = {"Q8K": "q8k", "E4M3_G128": "g128", "E4M3_ROW": "e4m3", "INT8_ROW": "int8"}[fmt]
+    keep = [i for i in range(T) if i not in (1, 2)]
+    check_norm(x[keep], None, w, 0.0, 0.0, None, y[keep], q[keep], d[keep], None if bs is None else bs[keep], key)
 
 
 # ------------------------------------------------------------------ attention
