@@ -99,9 +99,11 @@ class MoeDecoderBlock:
         return out
 
     def status(self):
-        """Synchronises and returns the first device-recorded error since the last call (0: none)."""
-        for ws in (self.attn_ws, self.bucket_ws, self.ffn_ws):
-            st = moe.moe_get_status(ws)
-            if st != moe.MOE_OK:
-                return st
-        return moe.MOE_OK
+        """Synchronises and returns the first device-recorded error since the last call (0: none).  The block can be used
+        again after any of them: a wait that ran out leaves counters behind, which are cleared here."""
+        import torch
+        found = [moe.moe_get_status(ws) for ws in (self.attn_ws, self.bucket_ws, self.ffn_ws)]
+        if found[0] == moe.MOE_ERR_DEVICE_TIMEOUT:
+            self.attn_ws.zero_()
+            torch.cuda.current_stream().synchronize()
+        return next((st for st in found if st != moe.MOE_OK), moe.MOE_OK)

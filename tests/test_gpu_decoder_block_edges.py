@@ -1,0 +1,50 @@
+"""MoeDecoderBlock beyond its ordinary step: errors and what follows them, strided tensors, the caller's settings, the
+rotary function and the window."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_routed_gb300 as moe
+from tests import block_ref
+from tests.test_gpu_decoder_block import D, E, H, HKV, HQ, PAGE, lay, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    moe.load()
+
+
+def step(blk, rnd, q_lens, kv_lens, x=None, out=None, seed=5):
+    """One call over a cache of random keys: (out, x, cache, table, cu, kv)."""
+    pages, table, cu, kv = lay(q_lens, kv_lens)
+    g = torch.Generator().manual_seed(seed)
+    kc, vc = (torch.randn(pages, PAGE, HKV, D, generator=g).bfloat16().cuda() for _ in range(2))
+    if x is None:
+        x = (2.0 * torch.randn(int(cu[-1]), H, generator=g)).cuda()
+    return blk.forward(x, kc, vc, table.cuda(), cu.cuda(), kv.cuda(), out=out), x, (kc, vc), table, cu, kv
+
+
+def test_status_reads_every_workspace():
+    """An error in two workspaces is told once, not again by the next call."""
+    blk, rnd = make(moe.ROUTE_SIGMOID)
+    step(blk, rnd, [1, 3], [40, 20])
+    assert blk.status() == 0
+    for ws, code in ((blk.attn_ws, moe.MOE_ERR_DEVICE_BOUNDS), (blk.ffn_ws, moe.MOE_ERR_DEVICE_TIMEOUT)):
+        ws[:4].view(torch.int32).fill_(code)
+    assert blk.status() == moe.MOE_ERR_DEVICE_BOUNDS
+    assert blk.status() == 0
+
+
+def test_block_after_a_wait_that_ran_out():
+    """Attention gives up waiting for the parts of a long sequence; the next step is right."""
+    blk, rnd = make(moe.ROUTE_SIGMOID)
+    want = step(blk, rnd, [1], [6000])[0].clone()
+    assert blk.status() == 0
+    counters = blk.attn_ws[16:16 + 4 * 160].view(torch.int32)
+    counters.fill_(2 ** 30)                                  # an increment takes these to 0: the parts never add up
+    step(blk, rnd, [1], [6000])
+    assert blk.status() == moe.MOE_ERR_DEVICE_TIMEOUT
+    assert (counters == 0).all()
+    assert torch.equal(step(blk, rnd, [1], [6000])[0], want) and blk.status() == 0
