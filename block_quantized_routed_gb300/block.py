@@ -64,13 +64,15 @@ class MoeDecoderBlock:
 
     def forward(self, x, k_cache, v_cache, page_table, cu_q, kv_len, out=None):
         """x fp32 [T, H]: the residual stream of the call's new tokens, in the order of cu_q.  kv_len counts the new
-        tokens.  Returns out fp32 [T, H] (may be x)."""
+        tokens.  Returns out fp32 [T, H] (may be x; rows may have a stride)."""
         import torch
         T, d = x.shape[0], self.desc
         if T > d.T_max:
             raise moe.MoeError(moe.MOE_ERR_INVALID_ARG, "MoeDecoderBlock.forward: more tokens than T_max")
         if out is None:
-            out = torch.empty_like(x)
+            out = torch.empty(x.shape, dtype=torch.float32, device=x.device)
+        elif out.shape != x.shape or out.dtype != torch.float32 or out.device != x.device:
+            raise moe.MoeError(moe.MOE_ERR_INVALID_ARG, "MoeDecoderBlock.forward: out must be fp32 like x")
         if T == 0:
             return out
         hq, hkv, D = self.heads, self.kv_heads, self.head_dim
@@ -95,7 +97,11 @@ class MoeDecoderBlock:
         moe.moe_bucket(ids, d.E, d.n_shared, self.counts, self.offsets, self.perm, None, self.bucket_ws)
         moe.moe_expert_ffn(d, self.table, q8, sc, bs, self.counts, self.offsets, self.perm, T, self.y_slots[:P],
                            self.ffn_ws)
-        moe.moe_combine(self.y_slots[:P], gates, T, d.H, d.top_k, d.n_shared, resid, out)
+        # moe_combine takes rows without gaps on 16-byte boundaries
+        rows = out if out.is_contiguous() and out.data_ptr() % 16 == 0 else torch.empty_like(resid)
+        moe.moe_combine(self.y_slots[:P], gates, T, d.H, d.top_k, d.n_shared, resid, rows)
+        if rows is not out:
+            out.copy_(rows)
         return out
 
     def status(self):

@@ -48,3 +48,32 @@ def test_block_after_a_wait_that_ran_out():
     assert blk.status() == moe.MOE_ERR_DEVICE_TIMEOUT
     assert (counters == 0).all()
     assert torch.equal(step(blk, rnd, [1], [6000])[0], want) and blk.status() == 0
+
+
+def test_out_with_a_stride():
+    """x and out as columns of wider tensors, and out in place: rows go where they belong and nowhere else."""
+    blk, rnd = make(moe.ROUTE_SIGMOID)
+    want, x = step(blk, rnd, [1, 6], [40, 30])[:2]
+    want = want.clone()
+    T = x.shape[0]
+    wide = torch.full((T, H + 13), 7.0, device="cuda")
+    out = wide[:, 5:5 + H]
+    assert step(blk, rnd, [1, 6], [40, 30], x=x, out=out)[0] is out
+    assert torch.equal(out, want) and (wide[:, :5] == 7).all() and (wide[:, 5 + H:] == 7).all()
+    wide = torch.full((T, H + 8), 7.0, device="cuda")
+    xs = wide[:, 4:4 + H]
+    xs.copy_(x)
+    step(blk, rnd, [1, 6], [40, 30], x=xs, out=xs)
+    assert torch.equal(xs, want) and (wide[:, :4] == 7).all() and (wide[:, 4 + H:] == 7).all()
+    flat = torch.full((T * H + 1,), 7.0, device="cuda")      # rows without gaps, off the 16-byte boundary
+    step(blk, rnd, [1, 6], [40, 30], x=x, out=flat[1:].view(T, H))
+    assert torch.equal(flat[1:].view(T, H), want) and flat[0] == 7
+    assert blk.status() == 0
+
+
+def test_out_of_another_shape_or_type_is_refused():
+    blk, rnd = make(moe.ROUTE_SIGMOID)
+    for out in (torch.empty(7, H + 1, device="cuda"), torch.empty(6, H, device="cuda"),
+                torch.empty(7, H, device="cuda", dtype=torch.bfloat16), torch.empty(7, H)):
+        with pytest.raises(moe.MoeError):
+            step(blk, rnd, [1, 6], [40, 30], out=out)
