@@ -77,3 +77,49 @@ def test_out_of_another_shape_or_type_is_refused():
                 torch.empty(7, H, device="cuda", dtype=torch.bfloat16), torch.empty(7, H)):
         with pytest.raises(moe.MoeError):
             step(blk, rnd, [1, 6], [40, 30], out=out)
+
+
+SWITCHES = {"allow_tf32": lambda: setattr(torch.backends.cuda.matmul, "allow_tf32", True),
+            "precision": lambda: torch.set_float32_matmul_precision("high"),
+            "fp32_precision": lambda: setattr(torch.backends.cuda.matmul, "fp32_precision", "tf32"),
+            "off": lambda: None}
+
+
+@pytest.mark.parametrize("switch", list(SWITCHES))
+@pytest.mark.parametrize("q_lens,kv_lens", [([1], [30]), ([1, 50], [40, 50]), ([150], [200])])
+def test_routing_does_not_follow_the_callers_tf32_switch(q_lens, kv_lens, switch):
+    """Router logits are fp32 products of the normalised rows: choices depend on them."""
+    if switch == "fp32_precision" and not hasattr(torch.backends.cuda.matmul, "fp32_precision"):
+        pytest.skip("no such switch")
+    blk, rnd = make(moe.ROUTE_SIGMOID, T_max=256)
+    T = sum(q_lens)
+    try:
+        SWITCHES[switch]()
+        step(blk, rnd, q_lens, kv_lens)
+    finally:
+        if hasattr(torch.backends.cuda.matmul, "fp32_precision"):
+            torch.backends.cuda.matmul.fp32_precision = "ieee"
+        torch.set_float32_matmul_precision("highest")
+    z, logits = blk.z[:T].contiguous(), blk.logits[:T]
+    want = torch.empty_like(logits)
+    if switch == "off":
+        torch.matmul(z, blk.w_router.t(), out=want)
+    else:
+        moe.moe_route_topk(z, blk.w_router, None, 4, moe.ROUTE_SIGMOID, want,
+                           torch.empty(T, 4, dtype=torch.int32, device="cuda"), torch.empty(T, 4, device="cuda"))
+    assert torch.equal(logits, want)
+    # H products and sums in fp32 in any order; the split of long chunks' operands keeps 2^-22 of each
+    bound = (z.double().abs() @ blk.w_router.double().abs().t()) * (H * 2.0 ** -24 + 2.0 ** -20)
+    assert ((logits.double() - z.double() @ blk.w_router.double().t()).abs() <= bound).all()
+    assert blk.status() == 0
+
+
+def test_router_weights_of_another_layout_or_type():
+    blk, rnd = make(moe.ROUTE_SIGMOID)
+    want = step(blk, rnd, [3], [20])[0].clone()
+    args = (blk.desc, blk.table, blk.attn_norm, blk.w_qkv, blk.w_o, blk.ffn_norm)
+    other = moe.MoeDecoderBlock(*args, blk.w_router.t().contiguous().t(), HQ, HKV, D)
+    assert torch.equal(step(other, rnd, [3], [20])[0], want)
+    for w in (blk.w_router.bfloat16(), blk.w_router[:-1]):
+        with pytest.raises(moe.MoeError):
+            moe.MoeDecoderBlock(*args, w, HQ, HKV, D)
