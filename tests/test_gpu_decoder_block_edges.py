@@ -123,3 +123,34 @@ def test_router_weights_of_another_layout_or_type():
     for w in (blk.w_router.bfloat16(), blk.w_router[:-1]):
         with pytest.raises(moe.MoeError):
             moe.MoeDecoderBlock(*args, w, HQ, HKV, D)
+
+
+@pytest.mark.parametrize("window", [0, 7, 40])
+def test_rotary_and_window(window):
+    """The caller's rotation of new queries and keys by their positions comes before the cache and the attention; the
+    window limits what the attention sees."""
+    def rotary(q, k, cu, kv):
+        n, t = cu[1:] - cu[:-1], torch.arange(q.shape[0], device="cuda", dtype=torch.int32)
+        seq = torch.searchsorted(cu[1:].contiguous(), t, right=True)
+        pos = (kv - n)[seq] + t - cu[seq]
+        freq = 0.3 ** torch.arange(D // 2, device="cuda")
+        ang = pos[:, None, None] * freq
+        for v in (q, k):
+            a, b = v[..., :D // 2].float(), v[..., D // 2:].float()
+            v.copy_(torch.cat([a * ang.cos() - b * ang.sin(), a * ang.sin() + b * ang.cos()], -1))
+        rotary.seen = (q.clone(), k.clone())
+
+    blk, rnd = make(moe.ROUTE_SIGMOID, rotary=rotary, window=window)
+    q_lens, kv_lens = [1, 4, 20], [40, 4, 150]
+    out, x, (kc, vc), table, cu, kv = step(blk, rnd, q_lens, kv_lens)
+    assert blk.status() == 0
+    T = int(cu[-1])
+    q, k = (t.cpu() for t in rotary.seen)
+    want, _, tol, _ = block_ref.attention(q, kc.cpu(), vc.cpu(), table, q_lens, kv_lens, D ** -0.5, window, torch.bfloat16)
+    assert ((blk.attn[:T].view(T, HQ, D).cpu().double() - want).abs() <= tol).all()
+    for b, (n, kvn) in enumerate(zip(q_lens, kv_lens)):
+        for i in range(n):
+            j, t = kvn - n + i, int(cu[b]) + i
+            assert torch.equal(kc[int(table[b, j // PAGE]), j % PAGE].cpu(), k[t])
+    plain = moe.MoeDecoderBlock(blk.desc, blk.table, blk.attn_norm, blk.w_qkv, blk.w_o, blk.ffn_norm, blk.w_router, HQ, HKV, D)
+    assert not torch.equal(step(plain, rnd, q_lens, kv_lens)[0], out)
