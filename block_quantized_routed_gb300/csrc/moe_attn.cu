@@ -56,6 +56,7 @@
 #include <cuda_fp16.h>
 
 #include "moe_kv.cuh"
+#include "moe_per_device.h"
 
 namespace moe {
 namespace {
@@ -1513,12 +1514,13 @@ template <int D, bool BF16>
 cudaError_t launch_t(const AttnArgs& a, cudaStream_t s) {
   using C = Cfg<D>;
   auto kern = attn_kernel<D, BF16>;
-  static bool opted = false;
-  if (!opted) {
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (err != cudaSuccess) return err;
-    opted = true;
-  }
+  static PerDevice opted;
+  cudaError_t err = cudaSuccess;
+  opted([&](int) {
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return err == cudaSuccess ? 1 : 0;
+  });
+  if (err != cudaSuccess) return err;
   CUtensorMap km, vm;
   const int rows = std::min(a.kv.page_size, (int)C::kN);
   if (!make_cache_map(&km, a.kv, a.k_cache, a.kv.k_row_stride, a.kv.k_head_stride, a.kv.k_page_stride, rows) ||

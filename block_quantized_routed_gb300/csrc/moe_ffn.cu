@@ -24,6 +24,7 @@
 
 #include "moe_device.cuh"
 #include "moe_internal.h"
+#include "moe_per_device.h"
 
 namespace moe {
 namespace {
@@ -366,14 +367,12 @@ cudaError_t launch_debug_dots(int fmt, const void* w, int N, int K, const int8_t
 }
 
 int num_sms() {
-  static int sms = 0;
-  if (sms == 0) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (sms <= 0) sms = 1;
-  }
-  return sms;
+  static PerDevice sms;
+  const int n = sms([](int dev) {
+    int v = 0;
+    return cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? v : 0;
+  });
+  return n > 0 ? n : 1;
 }
 
 }  // namespace moe

@@ -1,4 +1,8 @@
 """The binding and the build of the decoder-block operators on the CPU: what is refused before any launch."""
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 
@@ -54,3 +58,51 @@ def test_a_flag_without_a_truth_value_is_an_error():
     x = torch.zeros(2, 256)
     with pytest.raises(RuntimeError, match="ambiguous|Boolean"):
         moe.moe_route_grouped(x, 4, torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, 4), renorm=torch.ones(2))
+
+
+PER_DEVICE = r"""
+#include <cassert>
+#include <thread>
+#include <vector>
+#include "moe_per_device.h"
+static thread_local int current = 0;
+extern "C" cudaError_t cudaGetDevice(int* dev) { *dev = current; return cudaSuccess; }
+int main() {
+  moe::PerDevice kept;
+  int asked = 0;
+  const auto get = [&](int dev) { ++asked; return 100 + dev; };
+  assert(kept(get) == 100 && kept(get) == 100 && asked == 1);
+  current = 1;                                              // another device has a number of its own
+  assert(kept(get) == 101 && kept(get) == 101 && asked == 2);
+  current = 0;
+  assert(kept(get) == 100 && asked == 2);
+  current = 2;                                              // a failure is not kept
+  assert(kept([](int) { return 0; }) == 0 && kept(get) == 102 && asked == 3);
+  current = 1000;                                           // beyond the table: asked each time
+  assert(kept(get) == 1100 && kept(get) == 1100 && asked == 5);
+  moe::PerDevice shared;
+  std::vector<std::thread> ts;
+  for (int t = 0; t < 16; ++t)
+    ts.emplace_back([&, t] {
+      current = t % 4;
+      for (int i = 0; i < 10000; ++i) assert(shared([](int dev) { return dev + 1; }) == t % 4 + 1);
+    });
+  for (auto& t : ts) t.join();
+}
+"""
+
+
+def test_what_is_kept_per_device(tmp_path):
+    """Settings of a kernel hold for one device: the host keeps them apart, also for threads that call together."""
+    src, exe = tmp_path / "t.cpp", tmp_path / "t"
+    src.write_text(PER_DEVICE)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(_build.nvcc())), "include")
+    subprocess.run([shutil.which("g++"), "-std=c++17", "-O1", "-pthread", "-I" + _build.CSRC, "-I" + cuda, str(src), "-o", str(exe)],
+                   check=True)
+    subprocess.run([str(exe)], check=True)
+
+
+def test_the_attention_opts_in_per_device():
+    """No process-wide flag guards the shared-memory limit, which is set for one device at a time."""
+    src = open(os.path.join(_build.CSRC, "moe_attn.cu")).read()
+    assert "static bool" not in src and "static PerDevice" in src
