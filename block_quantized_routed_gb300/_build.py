@@ -1,7 +1,8 @@
 """In-tree build of the CUDA library (sm_103a) with nvcc: every .cu file in
 csrc/ is compiled in parallel, then linked into _build/libmoe_q8k.so; beside
 it the host compiler builds the tensor binding (csrc/binding.cpp) against
-torch's headers into _build/moe_binding.so."""
+torch's headers into _build/moe_binding.so.  The library is C and needs no
+torch: without it the binding alone is left out."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -37,10 +38,19 @@ def _deps():
     return files
 
 
+def _has_torch() -> bool:
+    import importlib.util
+    import sys
+    if "torch" in sys.modules:
+        return sys.modules["torch"] is not None
+    return importlib.util.find_spec("torch") is not None
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    made = [LIB, BINDING] if _has_torch() else [LIB]
+    if not all(os.path.exists(f) for f in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(f) for f in made)
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
@@ -87,19 +97,27 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     btmp = BINDING + f".tmp{os.getpid()}"
-    bind_compile, bind_link = _binding_commands(btmp)
+
+    def compile_binding():
+        if not _has_torch():
+            return None
+        bind_compile, bind_link = _binding_commands(btmp)
+        _run(bind_compile, "the compilation of csrc/binding.cpp")
+        return bind_link
+
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        bound = ex.submit(_run, bind_compile, "the compilation of csrc/binding.cpp")
+        bound = ex.submit(compile_binding)
         list(ex.map(compile_one, zip(srcs, objs)))
-        bound.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    _run(bind_link, "the link of the binding")
-    os.replace(btmp, BINDING)
+    bind_link = bound.result()  # (the library is there whatever becomes of the binding)
+    if bind_link:
+        _run(bind_link, "the link of the binding")
+        os.replace(btmp, BINDING)
     return LIB
 
 

@@ -106,3 +106,39 @@ def test_the_attention_opts_in_per_device():
     """No process-wide flag guards the shared-memory limit, which is set for one device at a time."""
     src = open(os.path.join(_build.CSRC, "moe_attn.cu")).read()
     assert "static bool" not in src and "static PerDevice" in src
+
+
+@pytest.fixture
+def toy(tmp_path, monkeypatch):
+    """The build with its tools replaced by ones that make empty files."""
+    tool = tmp_path / "tool"
+    tool.write_text('#!/bin/sh\nwhile [ $# -gt 0 ]; do [ "$1" = -o ] && : > "$2"; shift; done\n')
+    tool.chmod(0o755)
+    out = tmp_path / "out"
+    monkeypatch.setattr(_build, "BUILD", str(out))
+    monkeypatch.setattr(_build, "LIB", str(out / "lib.so"))
+    monkeypatch.setattr(_build, "BINDING", str(out / "binding.so"))
+    monkeypatch.setattr(_build, "nvcc", lambda: str(tool))
+    monkeypatch.setenv("CXX", str(tool))
+    return out
+
+
+def test_the_library_builds_without_torch(toy, monkeypatch):
+    """The C library needs the CUDA toolkit alone; the binding is left out."""
+    monkeypatch.setitem(__import__("sys").modules, "torch", None)          # importing it fails
+    assert not _build.up_to_date()
+    assert _build.build() == str(toy / "lib.so")
+    assert (toy / "lib.so").exists() and not (toy / "binding.so").exists()
+    assert _build.up_to_date()
+
+
+def test_the_library_is_built_where_the_binding_fails(toy, monkeypatch):
+    monkeypatch.setenv("CXX", "/bin/false")
+    with pytest.raises(RuntimeError, match="binding"):
+        _build.build()
+    assert (toy / "lib.so").exists() and not _build.up_to_date()
+
+
+def test_both_are_built_with_torch(toy):
+    _build.build()
+    assert (toy / "lib.so").exists() and (toy / "binding.so").exists() and _build.up_to_date()
