@@ -21,10 +21,10 @@
 // depend on timing.
 //
 // What it measured: 2 prompts of up to 4096 new tokens over up to 16384 keys
-// (32 heads over 4 of 128) 690 us, 1520 TFLOP/s, bound by the chain of the
-// softmax and the products that feed it; 48 tokens over up to 8192 keys 74 us,
-// 5.5 TB/s (6.6 to 6.9 where the lengths are equal); one token over 777 keys
-// 10.7 us, latency.
+// (32 heads over 4 of 128) 642 us, 1640 TFLOP/s, bound by the chain of the
+// softmax and the products that feed it; 48 tokens over up to 8192 keys 76 us,
+// 5.4 TB/s (6.6 to 6.9 where the lengths are equal); one token over 777 keys
+// 11.3 us, latency.
 //
 // Inside a CTA (warp roles): one warp feeds a ring of key and value tiles by
 // TMA through the page table, one issues the MMAs, two gather the query rows,
@@ -67,7 +67,8 @@ constexpr int kMaxCtas = 160;                    // the workspace holds the part
 constexpr size_t kWsHead = 1024;                 // status (16 bytes), a counter per CTA
 static_assert(kWsHead >= 16 + 4 * kMaxCtas, "counters");
 // Units of work: a key tile counts 1, an item kItemUnits more (loading its
-// queries, filling the pipeline, writing its rows).  With 0, 2 and 4 units an
+// queries, filling the pipeline, writing its rows).  3 lies between what was
+// measured on an earlier form of this kernel: with 0, 2 and 4 units an
 // 8192-token prompt (32 heads over 4, 128 wide) took 549, 422 and 402 us, 48
 // decoded tokens over up to 8192 keys 82, 77 and 78 us.  (Fewer CTAs of 2 or 4
 // units at least, where the work does not fill the SMs, were slower: one token

@@ -18,11 +18,13 @@
 // compared exactly.  A gap of exactly equal inputs (same logit, same bias) is a
 // tie in any precision and goes to the lower index.
 //
-// What bounds it: instruction issue, about 900 warp instructions a token at
-// 256 experts and k = 8 (8192 tokens: 14 us in 8 groups with a bias, their 8 MB
-// take 1.3 us); for few tokens the latency of the rounds, and more so of code
-// that is fetched for the first time.  So a lane holds no more keys than it has
-// to (528 experts in lanes of 20 and not 32, one warp per CTA: 12 to 6 us).
+// What bounds it: the chain of dependent warp-wide steps of the rounds (largest
+// head, its owner, the shift of the owner's keys), about 900 warp instructions
+// a token at 256 experts and k = 8, with 9 of an SM's 13.5 CTAs resident (8192
+// tokens: 14.9 us in 8 groups with a bias, of which issue takes 6; their 8 MB
+// take 1.3); for few tokens the latency of the rounds, and more so of code that
+// is fetched for the first time.  So a lane holds no more keys than it has to
+// (528 experts in lanes of 20 and not 32, one warp per CTA: 12 to 7.5 us).
 //
 // Error bound of a key p + b, in units of 2^-24.  exp32 is within 4 (2 ulp) and
 // 1.5 |x| (its argument is scaled and rounded).  Sigmoid: the error of e^-l

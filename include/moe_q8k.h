@@ -572,15 +572,16 @@ size_t moe_paged_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D);
  * finite leaves no finite number in its column of the rows that see its key.
  * Keys and values that a row does not see have no effect on it, whatever they
  * hold, and the cache beyond kv_len is never used.  Head sizes 64, 128 and 256
- * with a page size that is a power of two >= 16 run on the tensor cores; other sizes run on a
- * general kernel.  The tensor-core form is one cooperative launch of a CTA per
- * SM; calls that could hold 2^31 (row tile, key tile) pairs by T, n_seqs and
- * max_pages alone are refused (MOE_ERR_UNSUPPORTED): cut them.  Sequences with cu_q out of order or out of range, or
- * kv_len outside 0..max_pages*page_size, are skipped and recorded as
- * MOE_ERR_DEVICE_BOUNDS in the status word of ws, as are page numbers outside
- * 0..num_pages (their keys read as zeros).  Where a cu_q out of order makes
- * the sequences that are left share rows (more than T in all), nothing is
- * computed by the tensor-core form. */
+ * with a page size that is a power of two >= 16 run on the tensor cores; other
+ * sizes run on a general kernel.  The tensor-core form is one cooperative
+ * launch of a CTA per SM; calls that could hold 2^31 (row tile, key tile) pairs
+ * by T, n_seqs and max_pages alone are refused (MOE_ERR_UNSUPPORTED): cut them.
+ * Sequences with cu_q out of order or out of range, or kv_len outside
+ * 0..max_pages*page_size, are skipped and recorded as MOE_ERR_DEVICE_BOUNDS in
+ * the status word of ws, as are page numbers outside 0..num_pages (their keys
+ * read as zeros).  Where a cu_q out of order makes the sequences that are left
+ * share rows (more than T in all), nothing is computed by the tensor-core
+ * form. */
 int moe_paged_attention(const moe_kv_desc* kv, const void* q, int64_t q_stride, int64_t q_head_stride, int32_t Hq,
                         int32_t T, const void* k_cache, const void* v_cache, const int32_t* page_table,
                         const int32_t* cu_q, const int32_t* kv_len, float scale, int32_t window, void* out,
