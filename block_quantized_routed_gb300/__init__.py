@@ -31,6 +31,8 @@ __all__ = [
     "NORM_Q_NONE", "NORM_Q_Q8K", "NORM_Q_E4M3_G128", "NORM_Q_E4M3_ROW", "NORM_Q_INT8_ROW", "GROUP_MAX", "GROUP_TOP2",
     "KvDesc", "moe_add_rmsnorm", "moe_route_grouped", "moe_kv_append", "moe_paged_attention",
     "moe_paged_attention_workspace_size", "MoeDecoderBlock",
+    "KvScales", "moe_kv_append_q8", "moe_kv_read_q8", "moe_paged_attention_q8",
+    "moe_paged_attention_q8_workspace_size",
 ]
 
 FMT_Q4K = 0
@@ -55,6 +57,8 @@ GROUP_TOP2 = 1
 DT_F32 = 0
 DT_BF16 = 1
 DT_F16 = 2
+DT_E4M3 = 3
+DT_INT8 = 4
 
 PATH_DECODE_FUSED = 0
 PATH_GEMV = 1
@@ -105,6 +109,13 @@ class KvDesc(ctypes.Structure):
                                               "v_page_stride", "v_row_stride", "v_head_stride")]
 
 
+class KvScales(ctypes.Structure):
+    """moe_kv_scales: pointers and strides of an 8-bit cache's scales."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + \
+               [(n, ctypes.c_int64) for n in ("k_page_stride", "k_row_stride", "k_head_stride", "v_page_stride",
+                                              "v_row_stride", "v_head_stride")]
+
+
 _lib = None
 
 
@@ -121,6 +132,7 @@ def load():
     F32 = ctypes.c_float
     D = ctypes.POINTER(LayerDesc)
     KV = ctypes.POINTER(KvDesc)
+    SC = ctypes.POINTER(KvScales)
     sig = {
         "moe_layer_workspace_size": (SZ, [D]),
         "moe_workspace_layout": (ctypes.c_int, [D, ctypes.POINTER(WsLayout)]),
@@ -156,6 +168,11 @@ def load():
         "moe_paged_attention_workspace_size": (SZ, [I32, I32, I32]),
         "moe_paged_attention": (ctypes.c_int, [KV, P, I64, I64, I32, I32, P, P, P, P, P, F32, I32, P, I64, I64, P, P,
                                                SZ, P]),
+        "moe_kv_append_q8": (ctypes.c_int, [KV, SC, I32, P, I64, I64, P, I64, I64, P, P, P, P, P, I32, P, SZ, P]),
+        "moe_kv_read_q8": (ctypes.c_int, [KV, SC, P, P, P, P, P, I32, I32, P, I64, I64, P, I64, I64, P, SZ, P]),
+        "moe_paged_attention_q8_workspace_size": (SZ, [I32, I32, I32]),
+        "moe_paged_attention_q8": (ctypes.c_int, [KV, SC, I32, P, I64, I64, I32, I32, P, P, P, P, P, F32, I32, P, I64,
+                                                  I64, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -449,6 +466,32 @@ def moe_paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_len, scale, ou
     moe_paged_attention_workspace_size bytes.  See include/moe_q8k.h."""
     (_ext or _binding()).paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_len, scale, out, ws, lse, window,
                                          stream)
+
+
+def moe_kv_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, ws, stream=None):
+    """moe_kv_append into an 8-bit cache: codes [pages, page_size, Hkv, D] (float8_e4m3fn or int8) and fp32 scales
+    [pages, page_size, Hkv] (any strides; a head's scales of a page lying together suit the kernels best:
+    torch.empty(pages, Hkv, page_size).transpose(1, 2)).  k and v bf16 or fp16.  See include/moe_q8k.h."""
+    (_ext or _binding()).kv_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, ws, stream)
+
+
+def moe_kv_read_q8(k_cache, v_cache, k_scale, v_scale, page_table, kv_len, first, k_out, v_out, ws, stream=None):
+    """Reads sequences of an 8-bit cache back: key j of sequence b to row first[b] + j of k_out [rows, Hkv, D] (fp32,
+    bf16 or fp16), its value to v_out; other rows stay as they were.  See include/moe_q8k.h."""
+    (_ext or _binding()).kv_read_q8(k_cache, v_cache, k_scale, v_scale, page_table, kv_len, first, k_out, v_out, ws,
+                                    stream)
+
+
+def moe_paged_attention_q8_workspace_size(Hq, Hkv, D) -> int:
+    return int(load().moe_paged_attention_q8_workspace_size(Hq, Hkv, D))
+
+
+def moe_paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, scale, out, ws, lse=None,
+                           window=0, stream=None):
+    """moe_paged_attention over an 8-bit cache (moe_kv_append_q8), for single tokens and verify windows; q and out
+    bf16 or fp16.  ws: zeroed uint8 tensor of moe_paged_attention_q8_workspace_size bytes.  See include/moe_q8k.h."""
+    (_ext or _binding()).paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, scale, out,
+                                            ws, lse, window, stream)
 
 
 # ----------------------------------------------------------------- convenience

@@ -182,9 +182,14 @@ PyObject* route_grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// the cache of k_cache, v_cache, page_table, cu_q, kv_len
-moe_kv_desc cache(const at::Tensor& k, const at::Tensor& v, const at::Tensor& table, const at::Tensor& cu,
-                  const at::Tensor& len) {
+// the cache of k_cache, v_cache, page_table, kv_len and cu_q (null: not given); of 16-bit elements or 8-bit codes
+int code_dtype(const at::Tensor& t) {
+  if (t.scalar_type() == at::kFloat8_e4m3fn) return MOE_DT_E4M3;
+  if (t.scalar_type() == at::kChar) return MOE_DT_INT8;
+  refuse(MOE_ERR_UNSUPPORTED, "an 8-bit cache must be float8_e4m3fn or int8");
+}
+moe_kv_desc cache(const at::Tensor& k, const at::Tensor& v, const at::Tensor& table, const at::Tensor* cu,
+                  const at::Tensor& len, bool eight = false) {
   need(k.dim() == 4 && k.sizes() == v.sizes() && k.scalar_type() == v.scalar_type(),
        "caches must be [pages, page_size, Hkv, D] of one type");
   need(k.stride(3) == 1 && v.stride(3) == 1, "a head's elements must be contiguous");
@@ -193,15 +198,16 @@ moe_kv_desc cache(const at::Tensor& k, const at::Tensor& v, const at::Tensor& ta
        "page_table must be int32 [n_seqs, max_pages]");
   const int64_t n = table.size(0);
   need(n < INT32_MAX && table.size(1) <= INT32_MAX, "page_table is too large");
-  need(cu.dim() == 1 && cu.size(0) == n + 1 && cu.scalar_type() == at::kInt && cu.is_contiguous(),
-       "cu_q must be int32 [n_seqs + 1]");
+  if (cu)
+    need(cu->dim() == 1 && cu->size(0) == n + 1 && cu->scalar_type() == at::kInt && cu->is_contiguous(),
+         "cu_q must be int32 [n_seqs + 1]");
   need(len.dim() == 1 && len.size(0) == n && len.scalar_type() == at::kInt && len.is_contiguous(),
        "kv_len must be int32 [n_seqs]");
   moe_kv_desc d{};
   d.n_seqs = (int32_t)n;
   d.Hkv = (int32_t)k.size(2);
   d.D = (int32_t)k.size(3);
-  d.dtype = dtype(k);
+  d.dtype = eight ? code_dtype(k) : dtype(k);
   d.page_size = (int32_t)k.size(1);
   d.num_pages = (int32_t)k.size(0);
   d.max_pages = (int32_t)table.size(1);
@@ -227,7 +233,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kc = tensor(a[2], "k_cache");
     const at::Tensor &vc = tensor(a[3], "v_cache"), &table = tensor(a[4], "page_table"), &cu = tensor(a[5], "cu_q");
     const at::Tensor &len = tensor(a[6], "kv_len"), &ws = tensor(a[7], "ws");
-    const moe_kv_desc d = cache(kc, vc, table, cu, len);
+    const moe_kv_desc d = cache(kc, vc, table, &cu, len);
     need(k.dim() == 3 && k.size(0) <= INT32_MAX, "k must be [T, Hkv, D] of the cache's type");
     heads(k, k.size(0), d.Hkv, kc, "k must be [T, Hkv, D] of the cache's type");
     heads(v, k.size(0), d.Hkv, kc, "v must be like k");
@@ -247,7 +253,7 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor &table = tensor(a[3], "page_table"), &cu = tensor(a[4], "cu_q"), &len = tensor(a[5], "kv_len");
     const at::Tensor &out = tensor(a[7], "out"), &ws = tensor(a[8], "ws");
     const at::Tensor* lse = maybe(a[9], "lse");
-    const moe_kv_desc d = cache(kc, vc, table, cu, len);
+    const moe_kv_desc d = cache(kc, vc, table, &cu, len);
     need(q.dim() == 3 && q.size(0) <= INT32_MAX && q.size(1) <= INT32_MAX, "q must be [T, Hq, D] of the cache's type");
     const int64_t T = q.size(0), Hq = q.size(1);
     heads(q, T, Hq, kc, "q must be [T, Hq, D] of the cache's type");
@@ -266,6 +272,92 @@ PyObject* paged_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// the scales of an 8-bit cache
+moe_kv_scales scales(const at::Tensor& k, const at::Tensor& v, const at::Tensor& cache) {
+  for (const at::Tensor* t : {&k, &v})
+    need(t->dim() == 3 && t->size(0) == cache.size(0) && t->size(1) == cache.size(1) && t->size(2) == cache.size(2) &&
+             t->scalar_type() == at::kFloat,
+         "scales must be fp32 [pages, page_size, Hkv]");
+  return moe_kv_scales{static_cast<float*>(k.data_ptr()), static_cast<float*>(v.data_ptr()),
+                       k.stride(0), k.stride(1), k.stride(2), v.stride(0), v.stride(1), v.stride(2)};
+}
+
+// k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, ws, stream
+PyObject* kv_append_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 11)) return nullptr;
+  return guarded("moe_kv_append_q8", [&] {
+    const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kc = tensor(a[2], "k_cache");
+    const at::Tensor &vc = tensor(a[3], "v_cache"), &ks = tensor(a[4], "k_scale"), &vs = tensor(a[5], "v_scale");
+    const at::Tensor &table = tensor(a[6], "page_table"), &cu = tensor(a[7], "cu_q"), &len = tensor(a[8], "kv_len");
+    const at::Tensor& ws = tensor(a[9], "ws");
+    const moe_kv_desc d = cache(kc, vc, table, &cu, len, true);
+    const moe_kv_scales sc = scales(ks, vs, kc);
+    need(k.dim() == 3 && k.size(0) <= INT32_MAX && k.size(1) == d.Hkv && k.size(2) == d.D && k.stride(2) == 1,
+         "k must be [T, Hkv, D]");
+    need(v.sizes() == k.sizes() && v.stride(2) == 1 && v.scalar_type() == k.scalar_type(), "v must be like k");
+    need(ws.is_contiguous(), "ws must be contiguous");
+    on_device({&k, &v, &kc, &vc, &ks, &vs, &table, &cu, &len, &ws});
+    return moe_kv_append_q8(&d, &sc, dtype(k), k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                            v.stride(1), kc.data_ptr(), vc.data_ptr(), table.data_ptr<int32_t>(),
+                            cu.data_ptr<int32_t>(), len.data_ptr<int32_t>(), (int32_t)k.size(0), ws.data_ptr(),
+                            bytes_of(ws), stream_of(a[10]));
+  });
+}
+
+// k_cache, v_cache, k_scale, v_scale, page_table, kv_len, first, k_out, v_out, ws, stream
+PyObject* kv_read_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 11)) return nullptr;
+  return guarded("moe_kv_read_q8", [&] {
+    const at::Tensor &kc = tensor(a[0], "k_cache"), &vc = tensor(a[1], "v_cache"), &ks = tensor(a[2], "k_scale");
+    const at::Tensor &vs = tensor(a[3], "v_scale"), &table = tensor(a[4], "page_table"), &len = tensor(a[5], "kv_len");
+    const at::Tensor &first = tensor(a[6], "first"), &ko = tensor(a[7], "k_out"), &vo = tensor(a[8], "v_out");
+    const at::Tensor& ws = tensor(a[9], "ws");
+    const moe_kv_desc d = cache(kc, vc, table, nullptr, len, true);
+    const moe_kv_scales sc = scales(ks, vs, kc);
+    need(first.dim() == 1 && first.size(0) == d.n_seqs && first.scalar_type() == at::kInt && first.is_contiguous(),
+         "first must be int32 [n_seqs]");
+    need(ko.dim() == 3 && ko.size(0) <= INT32_MAX && ko.size(1) == d.Hkv && ko.size(2) == d.D && ko.stride(2) == 1,
+         "k_out must be [rows, Hkv, D]");
+    need(vo.sizes() == ko.sizes() && vo.stride(2) == 1 && vo.scalar_type() == ko.scalar_type(),
+         "v_out must be like k_out");
+    need(ws.is_contiguous(), "ws must be contiguous");
+    on_device({&kc, &vc, &ks, &vs, &table, &len, &first, &ko, &vo, &ws});
+    return moe_kv_read_q8(&d, &sc, kc.data_ptr(), vc.data_ptr(), table.data_ptr<int32_t>(), len.data_ptr<int32_t>(),
+                          first.data_ptr<int32_t>(), (int32_t)ko.size(0), dtype(ko), ko.data_ptr(), ko.stride(0),
+                          ko.stride(1), vo.data_ptr(), vo.stride(0), vo.stride(1), ws.data_ptr(), bytes_of(ws),
+                          stream_of(a[10]));
+  });
+}
+
+// q, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, scale, out, ws, lse, window, stream
+PyObject* paged_attention_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 14)) return nullptr;
+  return guarded("moe_paged_attention_q8", [&] {
+    const at::Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &vc = tensor(a[2], "v_cache");
+    const at::Tensor &ks = tensor(a[3], "k_scale"), &vs = tensor(a[4], "v_scale"), &table = tensor(a[5], "page_table");
+    const at::Tensor &cu = tensor(a[6], "cu_q"), &len = tensor(a[7], "kv_len"), &out = tensor(a[9], "out");
+    const at::Tensor& ws = tensor(a[10], "ws");
+    const at::Tensor* lse = maybe(a[11], "lse");
+    const moe_kv_desc d = cache(kc, vc, table, &cu, len, true);
+    const moe_kv_scales sc = scales(ks, vs, kc);
+    need(q.dim() == 3 && q.size(0) <= INT32_MAX && q.size(1) <= INT32_MAX && q.size(2) == d.D && q.stride(2) == 1,
+         "q must be [T, Hq, D]");
+    need(out.sizes() == q.sizes() && out.stride(2) == 1 && out.scalar_type() == q.scalar_type(), "out must be like q");
+    const int64_t T = q.size(0), Hq = q.size(1);
+    if (lse)
+      need(lse->dim() == 2 && lse->size(0) == T && lse->size(1) == Hq && lse->is_contiguous() &&
+               lse->scalar_type() == at::kFloat,
+           "lse must be fp32 [T, Hq]");
+    need(ws.is_contiguous(), "ws must be contiguous");
+    on_device({&q, &kc, &vc, &ks, &vs, &table, &cu, &len, &out, &ws, lse});
+    return moe_paged_attention_q8(&d, &sc, dtype(q), q.data_ptr(), q.stride(0), q.stride(1), (int32_t)Hq, (int32_t)T,
+                                  kc.data_ptr(), vc.data_ptr(), table.data_ptr<int32_t>(), cu.data_ptr<int32_t>(),
+                                  len.data_ptr<int32_t>(), (float)number(a[8]), int32(a[12], "window"), out.data_ptr(),
+                                  out.stride(0), out.stride(1), static_cast<float*>(ptr(lse)), ws.data_ptr(),
+                                  bytes_of(ws), stream_of(a[13]));
+  });
+}
+
 PyObject* on_error(PyObject*, PyObject* f) {
   Py_INCREF(f);
   Py_XDECREF(g_raise);
@@ -278,6 +370,10 @@ PyMethodDef kMethods[] = {
     {"route_grouped", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(route_grouped)), METH_FASTCALL, nullptr},
     {"kv_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append)), METH_FASTCALL, nullptr},
     {"paged_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention)), METH_FASTCALL,
+     nullptr},
+    {"kv_append_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_append_q8)), METH_FASTCALL, nullptr},
+    {"kv_read_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_read_q8)), METH_FASTCALL, nullptr},
+    {"paged_attention_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention_q8)), METH_FASTCALL,
      nullptr},
     {"on_error", on_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -18,10 +18,11 @@ bool rows16(const void* p, int64_t stride, int dt, int64_t T) {
   return !p || (aligned_to(p, 16) && (T <= 1 || stride * dtype_size(dt) % 16 == 0));
 }
 
-// sizes of a cache; MOE_OK or why not
-int kv_desc_check(const moe_kv_desc* kv) {
+// sizes of a cache (eight: of 8-bit codes); MOE_OK or why not
+int kv_desc_check(const moe_kv_desc* kv, bool eight = false) {
   if (!kv) return MOE_ERR_INVALID_ARG;
-  if (kv->dtype != MOE_DT_BF16 && kv->dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
+  if (eight ? kv->dtype != MOE_DT_E4M3 && kv->dtype != MOE_DT_INT8 : kv->dtype != MOE_DT_BF16 && kv->dtype != MOE_DT_F16)
+    return MOE_ERR_UNSUPPORTED;
   if (kv->D < 8 || kv->D > 256 || kv->D % 8 || kv->Hkv < 1 || kv->Hkv > 1024) return MOE_ERR_UNSUPPORTED;
   if (kv->n_seqs < 1 || kv->n_seqs > MOE_MAX_SEQS) return MOE_ERR_UNSUPPORTED;
   if (kv->page_size < 1 || kv->num_pages < 1 || kv->max_pages < 1 || kv->reserved != 0) return MOE_ERR_INVALID_ARG;
@@ -39,6 +40,20 @@ moe_kv_desc tidy(moe_kv_desc kv) {
   if (kv.page_size == 1) kv.k_row_stride = kv.v_row_stride = 0;
   if (kv.Hkv == 1) kv.k_head_stride = kv.v_head_stride = 0;
   return kv;
+}
+// the scales of an 8-bit cache
+int scales_check(const moe_kv_scales* sc) {
+  if (!sc || !sc->k || !sc->v || !aligned_to(sc->k, 4) || !aligned_to(sc->v, 4)) return MOE_ERR_INVALID_ARG;
+  const int64_t st[6] = {sc->k_page_stride, sc->k_row_stride, sc->k_head_stride,
+                         sc->v_page_stride, sc->v_row_stride, sc->v_head_stride};
+  for (int64_t v : st)
+    if (v < 0) return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+// all strides of a cache's codes are multiples of n bytes
+bool code_strides(const moe_kv_desc& kv, int n) {
+  return kv.k_page_stride % n == 0 && kv.k_row_stride % n == 0 && kv.k_head_stride % n == 0 &&
+         kv.v_page_stride % n == 0 && kv.v_row_stride % n == 0 && kv.v_head_stride % n == 0;
 }
 bool kv_strides16(const moe_kv_desc& kv) {
   return kv.k_page_stride % 8 == 0 && kv.k_row_stride % 8 == 0 && kv.k_head_stride % 8 == 0 &&
@@ -168,6 +183,95 @@ int moe_kv_append(const moe_kv_desc* kv, const void* k, int64_t k_stride, int64_
   return done(launch_kv_append(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+int moe_kv_append_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, int32_t x_dtype, const void* k,
+                     int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
+                     void* k_cache, void* v_cache, const int32_t* page_table, const int32_t* cu_q,
+                     const int32_t* kv_len, int32_t T, void* ws, size_t ws_bytes, void* stream) {
+  const int why = kv_desc_check(kv, true);
+  if (why != MOE_OK) return why;
+  if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
+  if (T < 0 || k_stride < 0 || k_head_stride < 0 || v_stride < 0 || v_head_stride < 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!k || !v || !k_cache || !v_cache || !page_table || !cu_q || !kv_len || !ws) return MOE_ERR_INVALID_ARG;
+  if (scales_check(scales) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < 16) return MOE_ERR_WORKSPACE;
+  if (!aligned_to(k, 2) || !aligned_to(v, 2) || !aligned_to(page_table, 4) || !aligned_to(cu_q, 4) ||
+      !aligned_to(kv_len, 4) || !aligned_to(ws, 16))
+    return MOE_ERR_INVALID_ARG;
+  KvAppendQ8Args g{};
+  KvAppendArgs& a = g.a;
+  a.kv = tidy(*kv);
+  if (T == 1) k_stride = v_stride = 0;
+  if (kv->Hkv == 1) k_head_stride = v_head_stride = 0;
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.k_head_stride = k_head_stride;
+  a.v_stride = v_stride;
+  a.v_head_stride = v_head_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.table = page_table;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.T = T;
+  a.status = static_cast<int*>(ws);
+  a.wide = code_strides(a.kv, 8) && k_stride % 8 == 0 && k_head_stride % 8 == 0 && v_stride % 8 == 0 &&
+           v_head_stride % 8 == 0 && aligned_to(k, 16) && aligned_to(v, 16) && aligned_to(k_cache, 8) &&
+           aligned_to(v_cache, 8);
+  g.sc = *scales;
+  g.x_dtype = x_dtype;
+  return done(launch_kv_append_q8(g, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_kv_read_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, const void* k_cache, const void* v_cache,
+                   const int32_t* page_table, const int32_t* kv_len, const int32_t* first, int32_t n_rows,
+                   int32_t out_dtype, void* k_out, int64_t k_stride, int64_t k_head_stride, void* v_out,
+                   int64_t v_stride, int64_t v_head_stride, void* ws, size_t ws_bytes, void* stream) {
+  const int why = kv_desc_check(kv, true);
+  if (why != MOE_OK) return why;
+  if (!dtype_ok(out_dtype)) return MOE_ERR_UNSUPPORTED;
+  if (n_rows < 0 || k_stride < 0 || k_head_stride < 0 || v_stride < 0 || v_head_stride < 0) return MOE_ERR_INVALID_ARG;
+  if (n_rows == 0) return MOE_OK;
+  if (!k_cache || !v_cache || !page_table || !kv_len || !first || !k_out || !v_out || !ws) return MOE_ERR_INVALID_ARG;
+  if (scales_check(scales) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < 16) return MOE_ERR_WORKSPACE;
+  const int es = dtype_size(out_dtype);
+  if (!aligned_to(page_table, 4) || !aligned_to(kv_len, 4) || !aligned_to(first, 4) || !aligned_to(ws, 16) ||
+      !aligned_to(k_out, es) || !aligned_to(v_out, es))
+    return MOE_ERR_INVALID_ARG;
+  if (kv->Hkv == 1) k_head_stride = v_head_stride = 0;
+  if (n_rows == 1) k_stride = v_stride = 0;
+  // rows that overlap would be written in no order
+  const auto apart = [&](int64_t row, int64_t head) {
+    const double heads = (kv->Hkv - 1.0) * head + kv->D, all = (n_rows - 1.0) * row + kv->D;
+    return (kv->Hkv == 1 || head >= kv->D) && (n_rows == 1 || (row >= kv->D && (row >= heads || head >= all)));
+  };
+  if (!apart(k_stride, k_head_stride) || !apart(v_stride, v_head_stride)) return MOE_ERR_INVALID_ARG;
+  KvReadQ8Args a{};
+  a.kv = tidy(*kv);
+  a.sc = *scales;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.table = page_table;
+  a.kv_len = kv_len;
+  a.first = first;
+  a.rows = n_rows;
+  a.out_dtype = out_dtype;
+  a.k_out = k_out;
+  a.v_out = v_out;
+  a.k_stride = k_stride;
+  a.k_head_stride = k_head_stride;
+  a.v_stride = v_stride;
+  a.v_head_stride = v_head_stride;
+  a.status = static_cast<int*>(ws);
+  const int per = 16 / es;
+  a.wide = kv->D % 16 == 0 && code_strides(a.kv, 16) && aligned_to(k_cache, 16) && aligned_to(v_cache, 16) &&
+           k_stride % per == 0 && k_head_stride % per == 0 && v_stride % per == 0 && v_head_stride % per == 0 &&
+           aligned_to(k_out, 16) && aligned_to(v_out, 16);
+  return done(launch_kv_read_q8(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 size_t moe_paged_attention_workspace_size(int32_t Hq, int32_t Hkv, int32_t D) {
   if (Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq > 1024 || Hq % Hkv || D < 8 || D > 256 || D % 8) return 0;
   return attn_workspace(Hq, Hkv, D);
@@ -216,6 +320,61 @@ int moe_paged_attention(const moe_kv_desc* kv, const void* q, int64_t q_stride, 
   a.status = static_cast<int*>(ws);
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return done(attn_tensor_core(a.kv) ? launch_attn(a, s) : launch_attn_general(a, s));
+}
+
+size_t moe_paged_attention_q8_workspace_size(int32_t Hq, int32_t Hkv, int32_t D) {
+  if (Hkv < 1 || Hkv > 1024 || Hq < 1 || Hq > 1024 || Hq % Hkv || D < 8 || D > 256 || D % 8) return 0;
+  return attn_q8_workspace(Hq, Hkv, D);
+}
+
+int moe_paged_attention_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, int32_t x_dtype, const void* q,
+                           int64_t q_stride, int64_t q_head_stride, int32_t Hq, int32_t T, const void* k_cache,
+                           const void* v_cache, const int32_t* page_table, const int32_t* cu_q, const int32_t* kv_len,
+                           float scale, int32_t window, void* out, int64_t o_stride, int64_t o_head_stride, float* lse,
+                           void* ws, size_t ws_bytes, void* stream) {
+  const int why = kv_desc_check(kv, true);
+  if (why != MOE_OK) return why;
+  if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
+  if (T < 0 || Hq < 1 || window < 0 || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+  if (Hq > 1024 || Hq % kv->Hkv || (int64_t)T * Hq > INT32_MAX - 1024) return MOE_ERR_UNSUPPORTED;
+  if (q_stride < 0 || q_head_stride < 0 || o_stride < 0 || o_head_stride < 0) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!q || !k_cache || !v_cache || !page_table || !cu_q || !kv_len || !out || !ws) return MOE_ERR_INVALID_ARG;
+  if (scales_check(scales) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(q, 16) || !aligned_to(k_cache, 8) || !aligned_to(v_cache, 8) || !aligned_to(out, 16) ||
+      !aligned_to(page_table, 4) || !aligned_to(cu_q, 4) || !aligned_to(kv_len, 4) || !aligned_to(lse, 4) ||
+      !aligned_to(ws, 256))
+    return MOE_ERR_INVALID_ARG;
+  if (T == 1) q_stride = o_stride = 0;
+  if (Hq == 1) q_head_stride = o_head_stride = 0;
+  const moe_kv_desc d = tidy(*kv);
+  if (!code_strides(d, 8) || q_stride % 8 || q_head_stride % 8 || o_stride % 8 || o_head_stride % 8)
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < attn_q8_workspace(Hq, kv->Hkv, kv->D)) return MOE_ERR_WORKSPACE;
+  AttnQ8Args g{};
+  AttnArgs& a = g.a;
+  a.kv = d;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.q_head_stride = q_head_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.table = page_table;
+  a.cu_q = cu_q;
+  a.kv_len = kv_len;
+  a.Hq = Hq;
+  a.T = T;
+  a.window = window;
+  a.scale = scale;
+  a.out = out;
+  a.o_stride = o_stride;
+  a.o_head_stride = o_head_stride;
+  a.lse = lse;
+  a.ws = static_cast<char*>(ws);
+  a.status = static_cast<int*>(ws);
+  g.sc = *scales;
+  g.x_dtype = x_dtype;
+  return done(launch_attn_q8_general(g, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -309,6 +309,31 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t s);
 
+// the 8-bit cache (moe_kv_q8.cu)
+struct KvAppendQ8Args {
+  KvAppendArgs a;     // wide: 16-byte loads, 8-byte stores
+  moe_kv_scales sc;
+  int x_dtype;
+};
+cudaError_t launch_kv_append_q8(const KvAppendQ8Args& a, cudaStream_t s);
+
+struct KvReadQ8Args {
+  moe_kv_desc kv;
+  moe_kv_scales sc;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* table;
+  const int32_t* kv_len;
+  const int32_t* first;
+  int rows, out_dtype;
+  void* k_out;
+  void* v_out;
+  int64_t k_stride, k_head_stride, v_stride, v_head_stride;
+  int* status;
+  bool wide;          // D a multiple of 16, 16-byte vectors throughout
+};
+cudaError_t launch_kv_read_q8(const KvReadQ8Args& a, cudaStream_t s);
+
 struct AttnArgs {
   moe_kv_desc kv;
   const void* q;
@@ -331,6 +356,15 @@ bool attn_tensor_core(const moe_kv_desc& kv);  // the sizes that launch_attn tak
 bool attn_units_fit(const moe_kv_desc& kv, int Hq, int T);  // the largest possible work of a call stays below 2^31 tiles
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_general(const AttnArgs& a, cudaStream_t s);
+
+// attention over the 8-bit cache (moe_attn_q8.cu, moe_attn_q8_general.cu)
+struct AttnQ8Args {
+  AttnArgs a;
+  moe_kv_scales sc;
+  int x_dtype;        // of q and out
+};
+size_t attn_q8_workspace(int Hq, int Hkv, int D);
+cudaError_t launch_attn_q8_general(const AttnQ8Args& a, cudaStream_t s);
 
 // One sequence's rows and keys, checked: rows q0 .. q0 + n and kv keys.  A
 // sequence whose numbers are out of range has n = 0 (ok = false).

@@ -12,21 +12,6 @@
 namespace moe {
 namespace {
 
-// the last b with cu_q[b] <= t (cu_q ascending); the whole warp takes part
-__device__ __forceinline__ int find_seq(const int32_t* cu_q, int n_seqs, int t, int lane) {
-  int lo = 0, n = n_seqs;  // the answer is in [lo, lo + n)
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int at = lane * step;
-    const bool le = at < n && (at == 0 || __ldg(cu_q + lo + at) <= t);
-    const unsigned mask = __ballot_sync(0xffffffffu, le);
-    const int last = 31 - __clz((int)mask);
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  return lo;
-}
-
 template <typename V>
 __global__ void __launch_bounds__(128) kv_append_kernel(const KvAppendArgs a) {
   const int lane = threadIdx.x & 31;

@@ -20,4 +20,19 @@ __device__ __forceinline__ SeqInfo seq_info(const moe_kv_desc& kv, const int32_t
 // is not taken off a negative number.
 __device__ __forceinline__ int window_lo(int hi, int window) { return window > 0 ? max(max(hi, 0) - window, 0) : 0; }
 
+// the last b with cu_q[b] <= t (cu_q ascending); the whole warp takes part
+__device__ __forceinline__ int find_seq(const int32_t* cu_q, int n_seqs, int t, int lane) {
+  int lo = 0, n = n_seqs;  // the answer is in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lane * step;
+    const bool le = at < n && (at == 0 || __ldg(cu_q + lo + at) <= t);
+    const unsigned mask = __ballot_sync(0xffffffffu, le);
+    const int last = 31 - __clz((int)mask);
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
 }  // namespace moe

@@ -460,7 +460,13 @@ int moe_debug_prefill_sums(int32_t fmt, const void* w, int32_t N, int32_t K, con
  * (The Pulsar / Strata pages run them around every MoE layer but do not    *
  * specify them; formulas and layouts are this library's own.)              *
  * ======================================================================== */
-typedef enum { MOE_DT_F32 = 0, MOE_DT_BF16 = 1, MOE_DT_F16 = 2 } moe_dtype;
+typedef enum {
+  MOE_DT_F32 = 0,
+  MOE_DT_BF16 = 1,
+  MOE_DT_F16 = 2,
+  MOE_DT_E4M3 = 3, /* 8-bit cache codes only: moe_kv_append_q8 and what reads them */
+  MOE_DT_INT8 = 4
+} moe_dtype;
 
 /* 8-bit outputs of moe_add_rmsnorm.  z is the normalised fp32 row. */
 typedef enum {
@@ -586,6 +592,81 @@ int moe_paged_attention(const moe_kv_desc* kv, const void* q, int64_t q_stride, 
                         int32_t T, const void* k_cache, const void* v_cache, const int32_t* page_table,
                         const int32_t* cu_q, const int32_t* kv_len, float scale, int32_t window, void* out,
                         int64_t o_stride, int64_t o_head_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ *
+ * The same cache in 8 bits: codes with one fp32 scale per token and head.   *
+ * A key or value is code * scale.  moe_kv_desc has dtype MOE_DT_E4M3 or     *
+ * MOE_DT_INT8 and strides in codes (bytes).  All 256 e4m3 codes stand for   *
+ * numbers here: 0x7f and 0xff, which moe_kv_append_q8 never writes, for     *
+ * +-480.  The scale of key j of sequence b and head h is                    *
+ *   k[page * k_page_stride + (j % page_size) * k_row_stride                 *
+ *     + h * k_head_stride]                                                  *
+ * with the page of the codes (strides in floats); one head's scales of a    *
+ * page lying together ([pages, Hkv, page_size]) suits the kernels best.     *
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  float* k;
+  float* v;
+  int64_t k_page_stride, k_row_stride, k_head_stride;
+  int64_t v_page_stride, v_row_stride, v_head_stride;
+} moe_kv_scales;
+
+/* moe_kv_append into an 8-bit cache: each new vector x of D elements (x_dtype
+ * MOE_DT_BF16 or MOE_DT_F16) is quantised as it is written,
+ *   d = max|x| / top          (IEEE fp32 division; top = 448 for e4m3, 127 for
+ *                              int8; at least 2^-126)
+ *   code = x / d              (IEEE fp32 division) rounded to nearest: e4m3 with
+ *                              ties to even, int8 with ties away from zero
+ * A vector of zeros has d = 0 and codes 0, one that holds a NaN or an infinity
+ * d = NaN and codes 0.  Sequences, positions, pages, the status word and ws are
+ * as in moe_kv_append. */
+int moe_kv_append_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, int32_t x_dtype, const void* k,
+                     int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
+                     void* k_cache, void* v_cache, const int32_t* page_table, const int32_t* cu_q,
+                     const int32_t* kv_len, int32_t T, void* ws, size_t ws_bytes, void* stream);
+
+/* Reads sequences of an 8-bit cache back: key j of sequence b, code * scale
+ * rounded once to out_dtype (F32, BF16 or F16), goes to row first[b] + j of
+ * k_out [n_rows, Hkv, D] (row and head strides in elements), its value to v_out.
+ * Rows that belong to no key stay as they were.  first int32 [n_seqs] ascends:
+ * first[b] + kv_len[b] <= first[b + 1], and n_rows after the last.  Keys whose
+ * rows are taken by a later sequence or lie outside 0..n_rows are not written
+ * and recorded as MOE_ERR_DEVICE_BOUNDS in the status word of ws (as in
+ * moe_kv_append), as are a kv_len outside 0..max_pages*page_size (its sequence
+ * is skipped) and page numbers outside 0..num_pages (their keys are skipped). */
+int moe_kv_read_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, const void* k_cache, const void* v_cache,
+                   const int32_t* page_table, const int32_t* kv_len, const int32_t* first, int32_t n_rows,
+                   int32_t out_dtype, void* k_out, int64_t k_stride, int64_t k_head_stride, void* v_out,
+                   int64_t v_stride, int64_t v_head_stride, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of moe_paged_attention_q8 (0 for unsupported sizes): a status
+ * word and counters, zero before the first call, and partial results of
+ * sequences that several CTAs share.  Calls leave the counters at zero. */
+size_t moe_paged_attention_q8_workspace_size(int32_t Hq, int32_t Hkv, int32_t D);
+
+/* moe_paged_attention over an 8-bit cache, made for few new tokens per sequence
+ * (single tokens, verify windows): with K_j, V_j the codes and d_j, e_j the
+ * scales of key j,
+ *   a_j = scale * d_j * (q . K_j),  out = sum_j exp(a_j) e_j V_j / sum_j exp(a_j)
+ *   lse = log(sum_j exp(a_j))
+ * Sequences, positions, windows, empty rows, q, out, lse and what is recorded in
+ * the status word are as there; q and out are x_dtype (BF16 or F16).  Codes lie
+ * on 8-byte boundaries (pointers and strides).  Scores, sums and accumulators are
+ * fp32.  Head sizes 64, 128 and 256 with pages of a multiple of 16 keys and codes
+ * on 16-byte boundaries run on the tensor cores, with q and the weights
+ * exp(a_j) e_j rounded to fp16 relative to their largest (2^-11; below 2^-14 of
+ * it 2^-25 of it); other sizes run on a general kernel.  A scale that is not a
+ * number makes out (and lse, for a key's) of the rows that see its key NaN.
+ * Codes and scales of keys that a row does not see have no effect on it.  Every
+ * length of new tokens is taken, but a prompt chunk reads the cache once for
+ * every 32 rows: moe_kv_read_q8 and moe_paged_attention are faster there.  Calls
+ * that could hold 2^31 (row tile, key tile) pairs by T, n_seqs and max_pages
+ * alone are refused (MOE_ERR_UNSUPPORTED). */
+int moe_paged_attention_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, int32_t x_dtype, const void* q,
+                           int64_t q_stride, int64_t q_head_stride, int32_t Hq, int32_t T, const void* k_cache,
+                           const void* v_cache, const int32_t* page_table, const int32_t* cu_q, const int32_t* kv_len,
+                           float scale, int32_t window, void* out, int64_t o_stride, int64_t o_head_stride, float* lse,
+                           void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
