@@ -104,8 +104,6 @@ __global__ void __launch_bounds__(32 * kWarps) attn_q8_general_kernel(const Attn
 
 }  // namespace
 
-size_t attn_q8_workspace(int, int, int) { return 256; }
-
 cudaError_t launch_attn_q8_general(const AttnQ8Args& g, cudaStream_t s) {
   if (g.a.T == 0) return cudaSuccess;
   const dim3 grid((unsigned)(g.a.T < 65536 ? g.a.T : 65536), (unsigned)g.a.Hq);

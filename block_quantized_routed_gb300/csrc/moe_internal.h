@@ -364,6 +364,8 @@ struct AttnQ8Args {
   int x_dtype;        // of q and out
 };
 size_t attn_q8_workspace(int Hq, int Hkv, int D);
+bool attn_q8_tensor_core(const AttnQ8Args& a);  // what launch_attn_q8 takes
+cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t s);
 cudaError_t launch_attn_q8_general(const AttnQ8Args& a, cudaStream_t s);
 
 // One sequence's rows and keys, checked: rows q0 .. q0 + n and kv keys.  A
