@@ -12,13 +12,14 @@
 //
 // Layout.  Keys are the 16 rows of S^T = K q^T and the 16 terms of out^T = V^T P^T,
 // rows of the query (token, head of the key/value head) the 8 columns of a tile,
-// NT tiles to an item.  The order of a contraction's terms is free, so a lane
-// reads its codes in 16-byte pieces as they lie: it takes 16 consecutive bytes of
-// two keys per 64 columns for S, and for the values the same bytes of four
-// keys, whose pairs become the halves of an operand register.  Each lane copies
-// exactly what it will read itself into a ring of its own (cp.async), so loads
-// run several steps ahead without registers or barriers.  P^T is the
-// transpose of S^T: one movmatrix per 8 x 8 block.
+// NT tiles to an item.  A warp takes 16 keys at a time: TMA boxes of their codes,
+// found through the page table, land in a ring of its own some steps ahead, and
+// no barrier of the CTA is met until the item ends.  The order of a contraction's
+// terms is free, so a lane reads codes in 16-byte pieces as they lie: pieces of
+// two keys for S, and for the values the same piece of four keys, whose pairs
+// become the halves of an operand register; the boxes' swizzle keeps both reads
+// free of bank conflicts.  P^T is the transpose of S^T: one movmatrix per 8 x 8
+// block.
 //
 // References.  The weight's factor e_j belongs to the contraction, so it is
 // folded into the exponent, P'_j = 2^(c a_j + log2 e_j - m'), with a reference m'
@@ -32,6 +33,9 @@
 // workspace, and the CTA that arrives last joins them in the order of the keys,
 // so results do not depend on timing and no CTA waits for another.
 #include <algorithm>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,25 +51,31 @@ constexpr unsigned kAll = 0xffffffffu;
 constexpr int kMaxCtas = 320;                     // the workspace holds the partial sums of this many
 constexpr size_t kWsHead = 2048;                  // status (16 bytes), a counter per CTA
 static_assert(kWsHead >= 16 + 4 * kMaxCtas, "counters");
-constexpr int kOver = 2;                          // units of an item besides its key tiles: queries, join of the warps
+constexpr int kOver = 4;                          // units of an item besides its key tiles: queries, join of the warps
 constexpr int kLeast = 4;                         // units of a CTA at least
 constexpr float kLow = -3.0e38f;                  // a reference before any key
 constexpr float kGrow = 8.0f;                     // log2 of the growth that raises a reference
 constexpr float kLift = 7.0f;                     // log2 of the reference's weight in fp16: at most 2^15 with kGrow
+constexpr long long kWaitCycles = 2000000000ll;  // ~1 s at 2 GHz
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr int kPartMax = 4096;                    // elements of an item's accumulator
 
 template <int D_, int NT_>
 struct Cfg {
   static constexpr int D = D_, NT = NT_, kRows = 8 * NT;
-  static constexpr int W = NT * D <= 256 && D < 256 ? 8 : 4;    // warps
+  static constexpr int W = NT * D <= 128 ? 8 : 4;               // warps: 128 or 256 registers a thread, two CTAs per SM
   static constexpr int kTile = 16 * W;                          // keys of a unit
-  static constexpr int kStage = 32 * D + 128;                   // 16 keys and values, their scales
+  static constexpr int kLine = D < 128 ? D : 128, kHalves = D / kLine;  // a copied box: 16 lines of up to 128 bytes
+  static constexpr int kBox = 16 * kLine;
+  static constexpr int kStage = 2 * kHalves * kBox;             // keys, then values
+  static constexpr int kScales = 128;                           // of a stage: scales of 16 keys, then of their values
   static constexpr int kMisc = kRows * D * 2 + kRows * 16 + W * kRows * 12;
-  static constexpr int kStages = std::min(6, (113 * 1024 - 1024 - kMisc) / (W * kStage));  // two CTAs per SM
+  static constexpr int kStages = std::min(6, (113 * 1024 - 2048 - kMisc) / (W * (kStage + kScales + 8)));  // two CTAs per SM
   static constexpr int kRing = W * kStages * kStage;
+  static constexpr int kSmemScales = kRing, kSmemBars = kSmemScales + W * kStages * kScales;
+  static constexpr int kSmemMisc = kSmemBars + W * kStages * 8;
+  static constexpr int kSmem = kSmemMisc + kMisc + 1024;        // (the ring starts on a 1024-byte boundary)
   static constexpr int kPitch = D + 4;                          // floats of a row in the join of the warps
-  static constexpr int kSmem = kRing + kMisc;
   static constexpr size_t kPartFloats = kPartMax + 3 * 32;      // accumulator; m, m' and sum of each row
   static_assert(kRows * D <= kPartMax && kStages >= 3, "sizes");
   static_assert(W * kRows * kPitch * 4 <= kRing, "the warps' accumulators lie in the ring");
@@ -73,11 +83,32 @@ struct Cfg {
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {  // N bytes, zeros if not there
-  const int n = there ? N : 0;
-  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(n), "n"(N) : "memory");
+__device__ __forceinline__ void bar_init(uint32_t bar) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page,
+                                       uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void fence_proxy() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src, bool there) {  // zeros if not there
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(there ? 4 : 0) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -138,9 +169,16 @@ __device__ __forceinline__ Work work_of(const AttnArgs& a, int G, int b) {
 template <class C>
 struct Shared {
   long long scan[C::W], rows[C::W];
-  long long total, before;
-  int seq, last, over;
+  long long before;
+  int seq, last;
+  volatile int abort;
 };
+
+// a / b of numbers that are not negative, quick where they are short
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 
 // writes 4 columns of a row of out
 __device__ __forceinline__ void put(const AttnQ8Args& g, int64_t at, float4 v) {
@@ -161,25 +199,25 @@ __device__ __forceinline__ void fma4(float4& acc, float f, float4 v) {
   acc.w = fmaf(f, v.w, acc.w);
 }
 // what a row's accumulator is multiplied by, and its lse
-template <int FMT>
 __device__ __forceinline__ float out_factor(float m, float mv, float sum) {
-  return sum == 0.0f ? 0.0f : ex2(mv - m - kLift) / sum * kCodeScale<FMT>;
+  return sum == 0.0f ? 0.0f : ex2(mv - m - kLift) / sum;
 }
 __device__ __forceinline__ float lse_of(float m, float sum) {
   return sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
 }
 
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const AttnQ8Args ga) {
+__global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const AttnQ8Args ga, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
   using C = Cfg<D, NT>;
   constexpr int W = C::W, kRows = C::kRows, kThreads = 32 * W, kStages = C::kStages;
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   __shared__ Shared<C> sh;
   const AttnArgs& a = ga.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
-  const int G = a.Hq / a.kv.Hkv;
-  uint2* const s_q = reinterpret_cast<uint2*>(smem + C::kRing);                   // [NT][D / 16][lane] operand registers
+  const int G = ga.G;
+  uint2* const s_q = reinterpret_cast<uint2*>(smem + C::kSmemMisc);                   // [NT][D / 16][lane] operand registers
   float* const s_f = reinterpret_cast<float*>(s_q + kRows * D / 4);               // [row] factor of the scores
   int* const s_lo = reinterpret_cast<int*>(s_f + kRows);                          // [row] keys that it sees
   int* const s_hi = s_lo + kRows;
@@ -188,7 +226,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
   float* const s_mv = s_m + W * kRows;
   float* const s_l = s_mv + W * kRows;
 
+  const uint32_t bars = smem_u32(smem) + C::kSmemBars + warp * kStages * 8;  // of this warp, one per stage
+  if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tid ? &vm : &km)) : "memory");
+  if (lane < kStages) bar_init(bars + lane * 8);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  if (tid == 0) sh.abort = 0;
+
   // ---- the CTA's share of the units
+  long long total = 0, ctas, u, u1;  // units of the call; CTAs that have some; this CTA's from u to u1
   {
     const int per = (a.kv.n_seqs + kThreads - 1) / kThreads, b0 = tid * per, b1 = min(a.kv.n_seqs, b0 + per);
     long long mine = 0, rows = 0;
@@ -204,12 +249,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       const long long x = __shfl_up_sync(kAll, incl, o);
       if (lane >= o) incl += x;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) rows += __shfl_xor_sync(kAll, rows, o);
-    if (lane == 31) sh.scan[warp] = incl;
-    if (lane == 0) sh.rows[warp] = rows;
+    rows = min(rows, (long long)a.T + 1);
+    rows = ((long long)__reduce_add_sync(kAll, (unsigned)(rows >> 16)) << 16) + __reduce_add_sync(kAll, (unsigned)(rows & 0xffff));
+    if (lane == 31) {
+      sh.scan[warp] = incl;
+      sh.rows[warp] = rows;
+    }
     __syncthreads();
-    long long total = 0, base = 0, all_rows = 0;
+    long long base = 0, all_rows = 0;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       if (w < warp) base += sh.scan[w];
@@ -221,31 +268,35 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       if (tid == 0 && all_rows > a.T) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
       return;
     }
-    const long long ctas = min((long long)gridDim.x, max(1ll, total / kLeast));
+    ctas = min((long long)gridDim.x, max(1ll, total / kLeast));
     if (blockIdx.x >= ctas) return;
-    const long long u0 = blockIdx.x * total / ctas;
+    u = quotient(blockIdx.x * total, ctas);
+    u1 = quotient((blockIdx.x + 1) * total, ctas);
     long long before = base + incl - mine;
-    if (u0 >= before && u0 < before + mine) {
+    if (u >= before && u < before + mine) {
       int b = b0;
       for (;; ++b) {
-        const long long u = work_of<C>(a, G, b).units;
-        if (u0 < before + u) break;
-        before += u;
+        const long long x = work_of<C>(a, G, b).units;
+        if (u < before + x) break;
+        before += x;
       }
       sh.seq = b;
       sh.before = before;
-      sh.total = total;
     }
     __syncthreads();
   }
-  const long long total = sh.total, ctas = min((long long)gridDim.x, max(1ll, total / kLeast));
-  const long long u1 = (blockIdx.x + 1) * total / ctas;
-  const auto owner = [&](long long u) { return (int)(((u + 1) * ctas - 1) / total); };
+  // a row's token, quick where it is one of few
+  const auto by_heads = [&](int r) { return r < 1 << 20 ? (int)__fdividef((float)r + 0.5f, (float)G) : r / G; };
+  const auto owner = [&](long long u) { return (int)quotient((u + 1) * ctas - 1, total); };
   int b = sh.seq;
-  long long u = blockIdx.x * total / ctas, base = sh.before;  // the current unit; units before the sequence
+  long long base = sh.before;  // units before the sequence
   Work w = work_of<C>(a, G, b);
   const uint32_t ring = smem_u32(smem) + warp * (kStages * C::kStage);
   const uint8_t* const ring_p = smem + warp * (kStages * C::kStage);
+  const uint32_t scales = smem_u32(smem) + C::kSmemScales + warp * (kStages * C::kScales);
+  const float* const scales_p = reinterpret_cast<const float*>(smem + C::kSmemScales + warp * (kStages * C::kScales));
+  int fill = 0, got = 0;    // stages that are filled and read next
+  uint32_t parity = 0;      // of the barrier of stage `got`
 
   while (u < u1) {
     while (u >= base + w.units) {  // the next sequence with tokens
@@ -253,55 +304,70 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       w = work_of<C>(a, G, ++b);
     }
     const int cost = w.tiles + kOver;
-    const int item = (int)((u - base) / cost);
+    const int item = (int)quotient(u - base, cost);
     const long long item0 = base + (long long)item * cost, pay0 = item0 + kOver;  // first unit, first key tile
     const int p0 = (int)(max(u, pay0) - pay0), p1 = (int)(min(u1, pay0 + w.tiles) - pay0);
     u = min(u1, item0 + cost);
     if (p0 >= p1) continue;
-    const int h = item / w.row_tiles, r0 = (item - h * w.row_tiles) * kRows, nr = min(kRows, w.s.n * G - r0);
-    const int off = w.s.kv - w.s.n, tok0 = r0 / G, tok1 = (r0 + nr - 1) / G;
+    const int h = w.row_tiles == 1 ? item : item / w.row_tiles, r0 = (item - h * w.row_tiles) * kRows, nr = min(kRows, w.s.n * G - r0);
+    const int off = w.s.kv - w.s.n, tok0 = by_heads(r0), tok1 = by_heads(r0 + nr - 1);
     // keys that some row sees, and those that every row sees (rows behind the last are zeros, and go nowhere)
     const int hi = max(0, off + tok1 + 1), lo = min(hi, window_lo(off + tok0 + 1, a.window));
     const int all_lo = window_lo(off + tok1 + 1, a.window), all_hi = off + tok0 + 1;
     const int from = max(lo, (w.t0 + p0) * C::kTile), to = min(hi, (w.t0 + p1) * C::kTile);
     const int first = from / 16, steps = to > from ? (to + 15) / 16 - first : 0;  // of 16 keys
-    const int mine = steps > warp ? (steps - warp + W - 1) / W : 0;               // this warp's: first + warp + W * i
+    int mine = steps > warp ? (steps - warp + W - 1) / W : 0;  // this warp's: first + warp + W * i
+    if (sh.abort) mine = 0;
 
+    // ---- pages of the first 32 steps, a step to a lane, and the query rows: all asked for at once
+    const int32_t* const table = a.table + (int64_t)b * a.kv.table_stride;
+    int page, slot;  // of step `lane` of the current 32
+    const auto look_up = [&](int i) {
+      const uint32_t key = (uint32_t)(first + warp + W * (i + lane)) * 16, entry = key / (uint32_t)a.kv.page_size;
+      slot = (int)(key - entry * a.kv.page_size);
+      page = i + lane < mine ? __ldg(table + entry) : 0;
+    };
+    look_up(0);
+    constexpr int kMyRows = kRows / W, kWords = (D + 127) / 128;
+    uint2 qw[kMyRows][kWords];
+#pragma unroll
+    for (int y = 0; y < kMyRows; ++y) {
+      const int r = y * W + warp, R = r0 + r, tok = by_heads(R);
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.s.q0 + tok) * a.q_stride +
+                            (int64_t)(h * G + R - tok * G) * a.q_head_stride;
+#pragma unroll
+      for (int x = 0; x < kWords; ++x) {
+        const int word = x * 32 + lane;
+        qw[y][x] = make_uint2(0, 0);
+        if (r < nr && word < D / 4) qw[y][x] = *reinterpret_cast<const uint2*>(src + word * 4);
+      }
+    }
+    fence_proxy();
     __syncthreads();  // the last item's join has been read
     // ---- loads of the first steps
-    const int32_t* table = a.table + (int64_t)b * a.kv.table_stride;
-    const auto page_of = [&](int i) { return i < mine ? __ldg(table + (first + warp + W * i) * 16 / a.kv.page_size) : 0; };
-    int next_page = page_of(0);
+    const bool of_keys = lane < 16;
+    const float* const sc0 = of_keys ? ga.sc.k + h * ga.sc.k_head_stride + lane * ga.sc.k_row_stride
+                                     : ga.sc.v + h * ga.sc.v_head_stride + (lane - 16) * ga.sc.v_row_stride;
+    const int64_t sc_page = of_keys ? ga.sc.k_page_stride : ga.sc.v_page_stride;
+    const int64_t sc_row = of_keys ? ga.sc.k_row_stride : ga.sc.v_row_stride;
     const auto issue = [&](int i) {
       if (i < mine) {
-        const int key = (first + warp + W * i) * 16, page = next_page;
-        const bool there = page >= 0 && page < a.kv.num_pages;
-        if (!there && lane == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-        const int slot = key % a.kv.page_size;
-        const int64_t pg = there ? page : 0;
-        const uint8_t* k = static_cast<const uint8_t*>(a.k_cache) + pg * a.kv.k_page_stride + h * a.kv.k_head_stride +
-                           (int64_t)(slot + g) * a.kv.k_row_stride + c * 16;
-        const uint32_t dst = ring + (uint32_t)(i % kStages) * C::kStage;
-#pragma unroll
-        for (int x = 0; x < D / 64; ++x) {
-          copy_async<16>(dst + (2 * x) * 512 + lane * 16, k + x * 64, there);
-          copy_async<16>(dst + (2 * x + 1) * 512 + lane * 16, k + 8 * a.kv.k_row_stride + x * 64, there);
+        const int pg = __shfl_sync(kAll, page, i & 31), at = __shfl_sync(kAll, slot, i & 31);
+        if ((i & 31) == 31) look_up(i + 1);
+        const bool there = pg >= 0 && pg < a.kv.num_pages;
+        const uint32_t bar = bars + fill * 8;
+        if (lane == 0) {
+          if (!there) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+          bar_expect(bar, C::kStage);
         }
-        constexpr int kV = D == 64 ? 8 : 16;  // bytes of a piece of the values
-        const uint8_t* v = static_cast<const uint8_t*>(a.v_cache) + pg * a.kv.v_page_stride + h * a.kv.v_head_stride +
-                           (int64_t)(slot + 2 * c) * a.kv.v_row_stride + g * kV;
-#pragma unroll
-        for (int x = 0; x < (D + 127) / 128; ++x)
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            copy_async<kV>(dst + 16 * D + ((4 * x + y) * 32 + lane) * kV,
-                           v + ((y & 1) + (y >> 1) * 8) * a.kv.v_row_stride + x * 128, there);
-        const float* sc = lane < 16 ? ga.sc.k + pg * ga.sc.k_page_stride + h * ga.sc.k_head_stride +
-                                          (int64_t)(slot + lane) * ga.sc.k_row_stride
-                                    : ga.sc.v + pg * ga.sc.v_page_stride + h * ga.sc.v_head_stride +
-                                          (int64_t)(slot + lane - 16) * ga.sc.v_row_stride;
-        copy_async<4>(dst + 32 * D + lane * 4, sc, there);
-        next_page = page_of(i + 1);
+        __syncwarp();
+        if (lane < 2 * C::kHalves) {  // a page that is not there: coordinates outside the cache, so zeros
+          const bool values = lane >= C::kHalves;
+          tma_4d(ring + fill * C::kStage + lane * C::kBox, values ? &vm : &km, (values ? lane - C::kHalves : lane) * 128, at,
+                 h, there ? pg : a.kv.num_pages, bar);
+        }
+        copy_async4(scales + fill * C::kScales + lane * 4, sc0 + (there ? pg : 0) * sc_page + at * sc_row, there);
+        if (++fill == kStages) fill = 0;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -309,17 +375,14 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
     // ---- queries: fp16 relative to the power of two at the row's largest element, in operand order
-    for (int r = warp; r < kRows; r += W) {
-      float e[D / 128 > 0 ? D / 128 : 1][4];
-      float peak = 0.0f;
-      const int R = r0 + r, tok = R / G;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.s.q0 + tok) * a.q_stride +
-                            (int64_t)(h * G + R - tok * G) * a.q_head_stride;
 #pragma unroll
-      for (int x = 0; x < (D + 127) / 128; ++x) {
-        const int word = x * 32 + lane;
-        uint2 v = make_uint2(0, 0);
-        if (r < nr && word < D / 4) v = *reinterpret_cast<const uint2*>(src + word * 4);
+    for (int y = 0; y < kMyRows; ++y) {
+      const int r = y * W + warp, tok = by_heads(r0 + r);
+      float e[kWords][4];
+      float peak = 0.0f;
+#pragma unroll
+      for (int x = 0; x < kWords; ++x) {
+        const uint2 v = qw[y][x];
         if (ga.x_dtype == MOE_DT_BF16) {
           e[x][0] = __uint_as_float(v.x << 16), e[x][1] = __uint_as_float(v.x & 0xffff0000u);
           e[x][2] = __uint_as_float(v.y << 16), e[x][3] = __uint_as_float(v.y & 0xffff0000u);
@@ -333,22 +396,25 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(kAll, peak, o));
-      int ex = 0;
-      if (peak > 0.0f && peak < INFINITY) ex = ilogbf(peak);
-      const float up = ldexpf(1.0f, min(14 - ex, 126)), more = ldexpf(1.0f, max(14 - ex - 126, 0));
+      // its exponent, where 2^-126 times it is a number; the largest element becomes 2^14 .. 2^15
+      const uint32_t ex = min(max(__float_as_uint(peak) >> 23, 15u), 254u);
+      const float up = __uint_as_float((268 - ex) << 23);
 #pragma unroll
-      for (int x = 0; x < (D + 127) / 128; ++x) {
+      for (int x = 0; x < kWords; ++x) {
         const int word = x * 32 + lane;
         if (word < D / 4) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[x][i] = e[x][i] * up * more;
-          // word: 64 columns, lane's 16, 4 of them
-          const int at = ((r >> 3) * (D / 16) + (word >> 4) * 4 + (word & 3)) * 32 + (r & 7) * 4 + (word >> 2 & 3);
-          s_q[at] = make_uint2(half2_of(e[x][0], e[x][2]), half2_of(e[x][1], e[x][3]));
+          for (int i = 0; i < 4; ++i) e[x][i] *= up;
+          // a line's pieces of 16 columns go to the lanes c in order (two each, where a line has 8), 4 columns at a time
+          const int piece = word >> 2 & (C::kLine / 16 - 1), of = D == 64 ? piece : piece >> 1;
+          const int step = (D == 64 ? 0 : (word >> 5) * 8 + (piece & 1) * 4) + (word & 3);
+          s_q[((r >> 3) * (D / 16) + step) * 32 + (r & 7) * 4 + of] =
+              FMT == MOE_DT_E4M3 ? make_uint2(half2_of(e[x][0], e[x][1]), half2_of(e[x][2], e[x][3]))
+                                 : make_uint2(half2_of(e[x][0], e[x][2]), half2_of(e[x][1], e[x][3]));
         }
       }
       if (lane == 0) {
-        s_f[r] = ldexpf(a.scale * kLog2e * kCodeScale<FMT>, ex - 14);
+        s_f[r] = a.scale * kLog2e * __uint_as_float((ex - 14) << 23);
         s_hi[r] = r < nr ? off + tok + 1 : 0;
         s_lo[r] = r < nr ? window_lo(off + tok + 1, a.window) : 0;
       }
@@ -368,22 +434,40 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     }
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
+      __syncwarp();  // every lane has read the stage that is filled next
       issue(i + kStages - 1);
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+      if (!bar_try(bars + got * 8, parity)) {
+        const long long t0 = clock64();
+        while (!sh.abort && !bar_try(bars + got * 8, parity))
+          if (clock64() - t0 > kWaitCycles) {
+            sh.abort = 1;
+            set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
+          }
+        if (sh.abort) mine = 0;  // given up: what this call computes is void
+      }
+      if (__any_sync(kAll, mine == 0)) break;
       __syncwarp();
-      const uint8_t* st = ring_p + (i % kStages) * C::kStage;
-      const float* sc = reinterpret_cast<const float*>(st + 32 * D);
+      const uint8_t* const st = ring_p + got * C::kStage;
+      const float* const sc = scales_p + got * (C::kScales / 4);
+      if (++got == kStages) got = 0, parity ^= 1;
       const float ks[2] = {sc[g], sc[g + 8]};
       const float lv[2] = {lg2(sc[16 + g]), lg2(sc[24 + g])};
-      float s[NT][4];
+      constexpr int kChains = NT == 1 ? 2 : 1;  // sums that do not wait for one another
+      float s[NT][4], s2[4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int x = 0; x < 4; ++x) {
+        s2[x] = 0.0f;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[n][x] = 0.0f;
+        for (int n = 0; n < NT; ++n) s[n][x] = 0.0f;
+      }
 #pragma unroll
       for (int x = 0; x < D / 64; ++x) {
-        const uint4 k0 = *reinterpret_cast<const uint4*>(st + (2 * x) * 512 + lane * 16);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(st + (2 * x + 1) * 512 + lane * 16);
+        // lines g and g + 8, the same place in both: the swizzle repeats after 8 lines
+        const uint8_t* src = st + (x >> 1) * C::kBox + g * C::kLine +
+                             ((D == 64 ? c ^ (g >> 1 & 3) : (2 * c + (x & 1)) ^ g) << 4);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(src);
+        const uint4 k1 = *reinterpret_cast<const uint4*>(src + 8 * C::kLine);
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
@@ -393,13 +477,33 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             const uint2 q = s_q[(n * (D / 16) + x * 4 + y) * 32 + lane];
-            mma(s[n], af, q.x, q.y);
+            mma(kChains == 2 && (y & 1) ? s2 : s[n], af, q.x, q.y);
           }
         }
       }
+      if constexpr (kChains == 2) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) s[0][x] += s2[x];
+      }
+      // a lane's piece of the values of its four keys
+      constexpr int kV = D == 64 ? 8 : 16;
+      uint32_t v[C::kHalves][4][kV / 4];
+#pragma unroll
+      for (int x = 0; x < C::kHalves; ++x)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int line = 2 * c + (y & 1);  // and its swizzle; line + 8 has the same
+          const uint8_t* src = st + (C::kHalves + x) * C::kBox + (line + (y >> 1) * 8) * C::kLine;
+          if constexpr (kV == 16) {
+            const uint4 r = *reinterpret_cast<const uint4*>(src + ((g ^ line) << 4));
+            v[x][y][0] = r.x, v[x][y][1] = r.y, v[x][y][2] = r.z, v[x][y][3] = r.w;
+          } else {
+            const uint2 r = *reinterpret_cast<const uint2*>(src + (((g >> 1) ^ (line >> 1)) << 4) + (g & 1) * 8);
+            v[x][y][0] = r.x, v[x][y][1] = r.y;
+          }
+        }
       // scores in powers of two: s of the sum, sv with the value's scale
       float sv[NT][4];
-      bool grow = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -408,15 +512,29 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
           sv[n][x] = s[n][x] + lv[x >> 1];
         }
       const int key = (first + warp + W * i) * 16;
-      if (key < all_lo || key + 16 > all_hi) {  // some row does not see some key
+      const bool partly = key < all_lo || key + 16 > all_hi;  // some row does not see some key
+      if (partly) {
+        uint32_t nan_keys = 0;  // of the 16: a value's code is e4m3's NaN, which only the rows that see it may meet
+        if constexpr (FMT == MOE_DT_E4M3) {
+#pragma unroll
+          for (int x = 0; x < C::kHalves; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+              for (int z = 0; z < kV / 4; ++z)
+                if (__vcmpeq4(v[x][y][z] & 0x7f7f7f7fu, 0x7f7f7f7fu)) nan_keys |= 1u << (2 * c + (y & 1) + (y >> 1) * 8);
+          nan_keys = __reduce_or_sync(kAll, nan_keys);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int r = n * 8 + 2 * c + (x & 1), j = key + g + (x >> 1) * 8;
             if (j < s_lo[r] || j >= s_hi[r]) s[n][x] = sv[n][x] = -INFINITY;
+            else if (nan_keys >> (j - key) & 1) sv[n][x] = NAN;
           }
       }
+      bool grow = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -447,36 +565,32 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
         p[n][0] = transposed(half2_of(sv[n][0], sv[n][1]));
         p[n][1] = transposed(half2_of(sv[n][2], sv[n][3]));
       }
-      // ---- values: columns 2 u and 2 u + 1 of the lane's bytes are the rows g and g + 8 of an operand
-      constexpr int kV = D == 64 ? 8 : 16;
+      // columns 2 z and 2 z + 1 of the lane's piece are the rows g and g + 8 of an operand
+      const auto values = [&](auto finite) {
 #pragma unroll
-      for (int x = 0; x < (D + 127) / 128; ++x) {
-        uint32_t v[4][kV / 4];
+        for (int x = 0; x < C::kHalves; ++x)
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const uint8_t* src = st + 16 * D + ((4 * x + y) * 32 + lane) * kV;
-          if constexpr (kV == 16) {
-            const uint4 r = *reinterpret_cast<const uint4*>(src);
-            v[y][0] = r.x, v[y][1] = r.y, v[y][2] = r.z, v[y][3] = r.w;
-          } else {
-            const uint2 r = *reinterpret_cast<const uint2*>(src);
-            v[y][0] = r.x, v[y][1] = r.y;
+          for (int y = 0; y < kV / 4; ++y) {
+            uint32_t af[2][4];
+            if constexpr (decltype(finite)::value) {
+              two_keys_finite<FMT, 0>(v[x][0][y], v[x][1][y], af[0][0], af[0][1]);
+              two_keys_finite<FMT, 0>(v[x][2][y], v[x][3][y], af[0][2], af[0][3]);
+              two_keys_finite<FMT, 2>(v[x][0][y], v[x][1][y], af[1][0], af[1][1]);
+              two_keys_finite<FMT, 2>(v[x][2][y], v[x][3][y], af[1][2], af[1][3]);
+            } else {
+              two_keys<FMT, 0>(v[x][0][y], v[x][1][y], af[0][0], af[0][1]);
+              two_keys<FMT, 0>(v[x][2][y], v[x][3][y], af[0][2], af[0][3]);
+              two_keys<FMT, 2>(v[x][0][y], v[x][1][y], af[1][0], af[1][1]);
+              two_keys<FMT, 2>(v[x][2][y], v[x][3][y], af[1][2], af[1][3]);
+            }
+#pragma unroll
+            for (int z = 0; z < 2; ++z)
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma(o[n][x * 8 + y * 2 + z], af[z], p[n][0], p[n][1]);
           }
-        }
-#pragma unroll
-        for (int y = 0; y < kV / 4; ++y)
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {  // bytes 0, 1 and 2, 3 of a word
-            constexpr uint32_t kSel[2][2] = {{0x4404, 0x5515}, {0x6626, 0x7737}};
-            uint32_t af[4];
-            af[0] = upper_codes<FMT>(__byte_perm(v[0][y], v[1][y], kSel[z][0]));
-            af[1] = upper_codes<FMT>(__byte_perm(v[0][y], v[1][y], kSel[z][1]));
-            af[2] = upper_codes<FMT>(__byte_perm(v[2][y], v[3][y], kSel[z][0]));
-            af[3] = upper_codes<FMT>(__byte_perm(v[2][y], v[3][y], kSel[z][1]));
-#pragma unroll
-            for (int n = 0; n < NT; ++n) mma(o[n][x * 8 + y * 2 + z], af, p[n][0], p[n][1]);
-          }
-      }
+      };
+      if (FMT == MOE_DT_E4M3 && partly) values(std::true_type{});
+      else values(std::false_type{});
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
@@ -512,12 +626,12 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
                         ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * C::kPartFloats;
     const auto put_lse = [&](int r, float mm, float sum) {
       if (a.lse) {
-        const int R = r0 + r, tok = R / G;
+        const int R = r0 + r, tok = by_heads(R);
         a.lse[(int64_t)(w.s.q0 + tok) * a.Hq + h * G + R - tok * G] = lse_of(mm, sum);
       }
     };
     const auto row_at = [&](int r) {
-      const int R = r0 + r, tok = R / G;
+      const int R = r0 + r, tok = by_heads(R);
       return (int64_t)(w.s.q0 + tok) * a.o_stride + (int64_t)(h * G + R - tok * G) * a.o_head_stride;
     };
     if (tid < nr) {  // weights of the warps, in place of their references
@@ -530,7 +644,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
         s_mv[x * kRows + tid] = ex2(s_mv[x * kRows + tid] - mmv);
       }
       if (parts == 1) {
-        s_rf[tid] = out_factor<FMT>(mm, mmv, sum);
+        s_rf[tid] = out_factor(mm, mmv, sum);
         put_lse(tid, mm, sum);
       } else {
         __stcg(part + kPartMax + tid, mm);
@@ -585,7 +699,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
 #pragma unroll
       for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kAll, sum, x);
       if (lane == 0) {
-        s_rf[r] = out_factor<FMT>(mm, mmv, sum);
+        s_rf[r] = out_factor(mm, mmv, sum);
         put_lse(r, mm, sum);
       }
     }
@@ -595,13 +709,18 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     while (teams * 2 * n <= kThreads && teams * 2 <= parts) teams *= 2;
     const int width = kThreads / teams, team = tid / width;
     float4* const red = reinterpret_cast<float4*>(smem + C::kRing - kThreads * 16);
-    for (int e0 = 0; e0 < n; e0 += width) {  // (once where there are teams)
-      const int e = e0 + tid - team * width;
+    const auto finish = [&](int e, float4 v) {
+      const int r = e / (D / 4), col = e - r * (D / 4);
+      const float rf = s_rf[r];
+      put(ga, row_at(r) + col * 4, make_float4(v.x * rf, v.y * rf, v.z * rf, v.w * rf));
+    };
+    const auto load = [&](int p, int e) { return __ldcg(reinterpret_cast<const float4*>(part_of(p)) + e); };
+    if (n <= width) {
+      const int e = tid - team * width, r = e / (D / 4);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (e < n) {
-        const int r = e / (D / 4);
 #pragma unroll 8
-        for (int p = team; p < parts; p += teams) fma4(v, wgt[p * nr + r], __ldcg(reinterpret_cast<const float4*>(part_of(p)) + e));
+        for (int p = team; p < parts; p += teams) fma4(v, wgt[p * nr + r], load(p, e));
       }
       if (teams > 1) {
         red[tid] = v;
@@ -609,13 +728,56 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
         if (team == 0)
           for (int x = 1; x < teams; ++x) fma4(v, 1.0f, red[tid + x * width]);
       }
-      if (team == 0 && e < n) {
-        const int r = e / (D / 4), col = e - r * (D / 4);
-        const float rf = s_rf[r];
-        put(ga, row_at(r) + col * 4, make_float4(v.x * rf, v.y * rf, v.z * rf, v.w * rf));
+      if (team == 0 && e < n) finish(e, v);
+    } else {
+      constexpr int kB = 4;
+      for (int e0 = tid; e0 < n; e0 += kB * kThreads) {
+        float4 v[kB];
+        int row[kB];
+#pragma unroll
+        for (int x = 0; x < kB; ++x) v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), row[x] = min(e0 + x * kThreads, n - 1) / (D / 4);
+#pragma unroll 2
+        for (int p = 0; p < parts; ++p)
+#pragma unroll
+          for (int x = 0; x < kB; ++x) fma4(v[x], wgt[p * nr + row[x]], load(p, min(e0 + x * kThreads, n - 1)));
+#pragma unroll
+        for (int x = 0; x < kB; ++x)
+          if (e0 + x * kThreads < n) finish(e0 + x * kThreads, v[x]);
       }
     }
   }
+  if (sh.abort) {  // copies may be in flight still
+    const long long t0 = clock64();
+    while (clock64() - t0 < kWaitCycles / 8) {
+    }
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// a cache's codes as [page][head][row][D]: boxes of 16 rows of one head of one page, up to 128 columns
+bool make_map(CUtensorMap* map, const moe_kv_desc& kv, const void* cache, int64_t row, int64_t head, int64_t page) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const auto bytes = [&](int64_t stride) { return (cuuint64_t)(stride ? stride : kv.D); };  // 0: one entry
+  const cuuint64_t dims[4] = {(cuuint64_t)kv.D, (cuuint64_t)kv.page_size, (cuuint64_t)kv.Hkv, (cuuint64_t)kv.num_pages};
+  const cuuint64_t strides[3] = {bytes(row), bytes(head), bytes(page)};
+  const cuuint32_t box[4] = {(cuuint32_t)std::min(kv.D, 128), 16, 1, 1};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, kv.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D, int NT, int FMT>
@@ -629,8 +791,13 @@ cudaError_t launch_t(const AttnQ8Args& a, cudaStream_t s) {
     return err == cudaSuccess ? 1 : 0;
   });
   if (err != cudaSuccess) return err;
+  const moe_kv_desc& kv = a.a.kv;
+  CUtensorMap km, vm;
+  if (!make_map(&km, kv, a.a.k_cache, kv.k_row_stride, kv.k_head_stride, kv.k_page_stride) ||
+      !make_map(&vm, kv, a.a.v_cache, kv.v_row_stride, kv.v_head_stride, kv.v_page_stride))
+    return cudaErrorInvalidValue;
   note_launch();
-  kern<<<std::min(2 * num_sms(), kMaxCtas), 32 * C::W, C::kSmem, s>>>(a);
+  kern<<<std::min(2 * num_sms(), kMaxCtas), 32 * C::W, C::kSmem, s>>>(a, km, vm);
   return cudaGetLastError();
 }
 template <int D, int FMT>
@@ -655,8 +822,12 @@ bool attn_q8_tensor_core(const AttnQ8Args& g) {
   const int64_t strides[] = {kv.k_page_stride, kv.k_row_stride, kv.k_head_stride,
                              kv.v_page_stride, kv.v_row_stride, kv.v_head_stride};
   for (int64_t v : strides)
-    if (v % 16) return false;
-  return (kv.D == 64 || kv.D == 128 || kv.D == 256) && kv.page_size % 16 == 0 &&
+    if (v % 16 || v >= (int64_t)1 << 40) return false;  // (what a tensor map takes)
+  // a stride of 0 over several entries (one key for all heads, say) is not one either
+  const bool repeats = (kv.page_size > 1 && !(kv.k_row_stride && kv.v_row_stride)) ||
+                       (kv.Hkv > 1 && !(kv.k_head_stride && kv.v_head_stride)) ||
+                       (kv.num_pages > 1 && !(kv.k_page_stride && kv.v_page_stride));
+  return !repeats && (kv.D == 64 || kv.D == 128 || kv.D == 256) && kv.page_size % 16 == 0 &&
          reinterpret_cast<uintptr_t>(g.a.k_cache) % 16 == 0 && reinterpret_cast<uintptr_t>(g.a.v_cache) % 16 == 0;
 }
 

@@ -362,6 +362,7 @@ struct AttnQ8Args {
   AttnArgs a;
   moe_kv_scales sc;
   int x_dtype;        // of q and out
+  int G;              // query heads of a key/value head
 };
 size_t attn_q8_workspace(int Hq, int Hkv, int D);
 bool attn_q8_tensor_core(const AttnQ8Args& a);  // what launch_attn_q8 takes

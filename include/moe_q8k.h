@@ -596,9 +596,9 @@ int moe_paged_attention(const moe_kv_desc* kv, const void* q, int64_t q_stride, 
 /* ------------------------------------------------------------------------ *
  * The same cache in 8 bits: codes with one fp32 scale per token and head.   *
  * A key or value is code * scale.  moe_kv_desc has dtype MOE_DT_E4M3 or     *
- * MOE_DT_INT8 and strides in codes (bytes).  All 256 e4m3 codes stand for   *
- * numbers here: 0x7f and 0xff, which moe_kv_append_q8 never writes, for     *
- * +-480.  The scale of key j of sequence b and head h is                    *
+ * MOE_DT_INT8 and strides in codes (bytes).  The e4m3 codes 0x7f and 0xff   *
+ * are NaN; moe_kv_append_q8 never writes them.  The scale of key j of       *
+ * sequence b and head h is                                                  *
  *   k[page * k_page_stride + (j % page_size) * k_row_stride                 *
  *     + h * k_head_stride]                                                  *
  * with the page of the codes (strides in floats); one head's scales of a    *
@@ -656,7 +656,8 @@ size_t moe_paged_attention_q8_workspace_size(int32_t Hq, int32_t Hkv, int32_t D)
  * on 16-byte boundaries run on the tensor cores, with q and the weights
  * exp(a_j) e_j rounded to fp16 relative to their largest (2^-11; below 2^-14 of
  * it 2^-25 of it); other sizes run on a general kernel.  A scale that is not a
- * number makes out (and lse, for a key's) of the rows that see its key NaN.
+ * number makes out (and lse, for a key's) of the rows that see its key NaN; so
+ * does a code that is NaN, a value's in its column at least.
  * Codes and scales of keys that a row does not see have no effect on it.  Every
  * length of new tokens is taken, but a prompt chunk reads the cache once for
  * every 32 rows: moe_kv_read_q8 and moe_paged_attention are faster there.

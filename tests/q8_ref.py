@@ -27,12 +27,13 @@ def quantise(x, fmt):
 
 
 def code_values(codes):
-    """The numbers that codes stand for, in fp64: every e4m3 code is a number, 0x7f and 0xff are +-480."""
+    """The numbers that codes stand for, in fp64."""
     if codes.dtype == INT8:
         return codes.double()
     b = codes.view(torch.uint8).int()
     e, m = (b >> 3) & 15, (b & 7).double()
     mag = torch.where(e > 0, (1 + m / 8) * torch.pow(2.0, e.double() - 7), m / 8 * 2.0 ** -6)
+    mag = torch.where((b & 127) == 127, torch.full_like(mag, float("nan")), mag)
     return torch.where(b >= 128, -mag, mag)
 
 

@@ -186,6 +186,25 @@ def test_numbers_that_are_not_finite(D):
     assert torch.equal(torch.isnan(lse)[0], torch.tensor([False, False, True, False])) and not torch.isnan(got[0, :2]).any()
 
 
+@pytest.mark.parametrize("D,Hkv", [(128, 2), (64, 1), (256, 1), (80, 2)])
+@pytest.mark.parametrize("pos", [10, 37, 39])
+def test_codes_that_are_nan(D, Hkv, pos):
+    """e4m3's NaN in a key or a value: the rows that see it, and no others, whether all rows of a tile do or some."""
+    for name in ("kc", "vc"):
+        c = Q8Cache([40, 30], Hkv, D, 16, E4M3)
+        q = rnd(5, 4, D)
+        want, want_lse = attend(c, q, [4, 1])
+        getattr(c, "g" + name).view(torch.uint8)[int(c.table[0, pos // 16]), pos % 16, Hkv - 1, 11] = 0xff
+        got, lse = attend(c, q, [4, 1])
+        hit = torch.zeros(5, 4, dtype=torch.bool)
+        hit[max(0, pos - 36):4, 4 - 4 // Hkv:] = True
+        if name == "kc":
+            assert torch.isnan(got[hit]).all() and torch.isnan(lse[hit]).all()
+        else:
+            assert torch.isnan(got[hit][:, 11]).all() and torch.equal(lse, want_lse)
+        assert torch.equal(got[~hit], want[~hit]) and torch.equal(lse[~hit], want_lse[~hit])
+
+
 @pytest.mark.parametrize("D,page", [(128, 16), (80, 16)])
 def test_bad_numbers_are_skipped_and_told(D, page):
     c = Q8Cache([40, 40, 40], 2, D, page, E4M3)

@@ -168,7 +168,6 @@ def test_read_every_code(fmt):
             scales[page, t, 0] = d
             gcodes.copy_(codes) if fmt == INT8 else raw(gcodes).copy_(raw(codes))
             gscales.copy_(scales)
-    assert code_values(c.kc[page, 0, 0]).abs().max() == (480.0 if fmt == E4M3 else 128.0)
     check_read(c, [0], 16, F32)
     check_read(c, [0], 16, BF16)
 

@@ -155,9 +155,6 @@ def test_plain_quantiser_by_hand():
         assert quantise(torch.tensor([[2.0 ** -133]]), fmt)[1].item() == 2.0 ** -126
 
 
-def test_every_e4m3_code_is_a_number():
-    codes = torch.arange(256).to(torch.uint8)
-    v = code_values(codes.view(E4M3)).numpy()
-    ref = codes.view(E4M3).float().double().numpy()
-    own = np.isfinite(ref)
-    assert (v[own] == ref[own]).all() and v[0x7f] == 480 and v[0xff] == -480 and own.sum() == 254
+def test_values_of_the_e4m3_codes():
+    codes = torch.arange(256).to(torch.uint8).view(E4M3)
+    assert np.array_equal(code_values(codes).numpy(), codes.float().double().numpy(), equal_nan=True)
