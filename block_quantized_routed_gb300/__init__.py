@@ -32,7 +32,8 @@ __all__ = [
     "KvDesc", "moe_add_rmsnorm", "moe_route_grouped", "moe_kv_append", "moe_paged_attention",
     "moe_paged_attention_workspace_size", "MoeDecoderBlock",
     "KvScales", "moe_kv_append_q8", "moe_kv_read_q8", "moe_paged_attention_q8",
-    "moe_paged_attention_q8_workspace_size",
+    "moe_paged_attention_q8_workspace_size", "moe_linear", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU",
+    "ACT_GELU_TANH",
 ]
 
 FMT_Q4K = 0
@@ -59,6 +60,13 @@ DT_BF16 = 1
 DT_F16 = 2
 DT_E4M3 = 3
 DT_INT8 = 4
+
+# activations of moe_linear
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_SILU = 2
+ACT_GELU = 3
+ACT_GELU_TANH = 4
 
 PATH_DECODE_FUSED = 0
 PATH_GEMV = 1
@@ -173,6 +181,7 @@ def load():
         "moe_paged_attention_q8_workspace_size": (SZ, [I32, I32, I32]),
         "moe_paged_attention_q8": (ctypes.c_int, [KV, SC, I32, P, I64, I64, I32, I32, P, P, P, P, P, F32, I32, P, I64,
                                                   I64, P, P, SZ, P]),
+        "moe_linear": (ctypes.c_int, [P, I32, I64, P, I64, P, I32, P, I32, I64, P, I32, I64, I32, I32, I32, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -492,6 +501,12 @@ def moe_paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu
     bf16 or fp16.  ws: zeroed uint8 tensor of moe_paged_attention_q8_workspace_size bytes.  See include/moe_q8k.h."""
     (_ext or _binding()).paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, scale, out,
                                             ws, lse, window, stream)
+
+
+def moe_linear(x, w, out, bias=None, act=ACT_NONE, residual=None, ws=None, stream=None):
+    """out = act(x w^T + bias) + residual: x [T, K] and w [N, K] bf16 or fp16, bias fp32 [N], residual and out [T, N]
+    of x's type or fp32 (may be one tensor).  ws: zeroed tensor for a status word, optional.  See include/moe_q8k.h."""
+    (_ext or _binding()).linear(x, w, out, bias, act, residual, ws, stream)
 
 
 # ----------------------------------------------------------------- convenience

@@ -358,6 +358,32 @@ PyObject* paged_attention_q8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// x, w, out, bias, act, residual, ws, stream
+PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 8)) return nullptr;
+  return guarded("moe_linear", [&] {
+    const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w"), &out = tensor(a[2], "out");
+    const at::Tensor *bias = maybe(a[3], "bias"), *res = maybe(a[5], "residual"), *ws = maybe(a[6], "ws");
+    need(x.dim() == 2 && w.dim() == 2, "x must be [T, K] and w [N, K]");
+    const int64_t T = x.size(0), K = x.size(1), N = w.size(0);
+    need(T <= INT32_MAX && K <= INT32_MAX && N <= INT32_MAX, "a size is out of range");
+    const int64_t xs = rows(x, T, K, "x must be [T, K] with contiguous rows");
+    const int64_t wst = rows(w, N, K, "w must be [N, K] with contiguous rows");
+    need(w.scalar_type() == x.scalar_type(), "w must have x's type");
+    const int64_t os = rows(out, T, N, "out must be [T, N] with contiguous rows");
+    if (bias)
+      need(bias->dim() == 1 && bias->size(0) == N && bias->is_contiguous() && bias->scalar_type() == at::kFloat,
+           "bias must be fp32 [N]");
+    int64_t rs = 0;
+    if (res) rs = rows(*res, T, N, "residual must be [T, N] with contiguous rows");
+    if (ws) need(ws->is_contiguous() && bytes_of(*ws) >= 4, "ws must be contiguous and hold a status word");
+    on_device({&x, &w, &out, bias, res, ws});
+    return moe_linear(x.data_ptr(), dtype(x), xs, w.data_ptr(), wst, static_cast<const float*>(ptr(bias)),
+                      int32(a[4], "act"), ptr(res), res ? dtype(*res) : dtype(x), rs, out.data_ptr(), dtype(out), os,
+                      (int32_t)T, (int32_t)N, (int32_t)K, static_cast<int32_t*>(ptr(ws)), stream_of(a[7]));
+  });
+}
+
 PyObject* on_error(PyObject*, PyObject* f) {
   Py_INCREF(f);
   Py_XDECREF(g_raise);
@@ -375,6 +401,7 @@ PyMethodDef kMethods[] = {
     {"kv_read_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv_read_q8)), METH_FASTCALL, nullptr},
     {"paged_attention_q8", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention_q8)), METH_FASTCALL,
      nullptr},
+    {"linear", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(linear)), METH_FASTCALL, nullptr},
     {"on_error", on_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "moe_binding", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};

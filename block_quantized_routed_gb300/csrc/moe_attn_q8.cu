@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
   using C = Cfg<D, NT>;
   constexpr int W = C::W, kRows = C::kRows, kThreads = 32 * W, kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023);  // the swizzled boxes start on 1024-byte boundaries
   __shared__ Shared<C> sh;
   const AttnArgs& a = ga.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

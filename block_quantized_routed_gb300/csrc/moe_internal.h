@@ -369,6 +369,20 @@ bool attn_q8_tensor_core(const AttnQ8Args& a);  // what launch_attn_q8 takes
 cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t s);
 cudaError_t launch_attn_q8_general(const AttnQ8Args& a, cudaStream_t s);
 
+// a dense product with bias, activation and residual (moe_linear.cu)
+struct LinearArgs {
+  const void* x;
+  const void* w;
+  const float* bias;     // nullable
+  const void* residual;  // nullable
+  void* out;
+  int64_t x_stride, w_stride, r_stride, o_stride;
+  int x_dtype, r_dtype, o_dtype, act, T, N, K;
+  int split;             // CTAs that share a tile's terms (set by the launcher)
+  int* status;           // nullable
+};
+cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+
 // One sequence's rows and keys, checked: rows q0 .. q0 + n and kv keys.  A
 // sequence whose numbers are out of range has n = 0 (ok = false).
 struct SeqInfo {

@@ -670,6 +670,31 @@ int moe_paged_attention_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, i
                            float scale, int32_t window, void* out, int64_t o_stride, int64_t o_head_stride, float* lse,
                            void* ws, size_t ws_bytes, void* stream);
 
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,     /* v / (1 + exp(-v)) */
+  MOE_ACT_GELU = 3,     /* v (1 + erf(v / sqrt(2))) / 2 */
+  MOE_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+} moe_act;
+
+/* A dense product with its epilogue, the block's projections:
+ *   out = act(x W^T + bias) + residual
+ * x [T, K] and w [N, K] of x_dtype (BF16 or F16; products are exact, sums and
+ * everything after them fp32), bias float [N] or NULL, residual [T, N] of
+ * r_dtype (x's type or F32) or NULL, out [T, N] of o_dtype (x's type or F32),
+ * rounded once.  Row strides are in elements; residual and out may be the same
+ * array (with the same type and stride).  x and w lie on 16-byte boundaries
+ * (pointers, strides, and K a multiple of 8); residual and out on their
+ * elements'.  T >= 0, N and K at least 1, (N / 128) * (T / 16) below 2^30.
+ * status: NULL, or an int in device memory, zero before the first call, that
+ * records MOE_ERR_DEVICE_TIMEOUT where a bounded wait ran out (out is void
+ * then).  Numbers that are not finite in a row of x or of w reach that row or
+ * column of out alone. */
+int moe_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, int64_t w_stride, const float* bias,
+               int32_t act, const void* residual, int32_t r_dtype, int64_t r_stride, void* out, int32_t o_dtype,
+               int64_t o_stride, int32_t T, int32_t N, int32_t K, int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
