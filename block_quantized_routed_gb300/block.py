@@ -1,9 +1,9 @@
 """A decoder block around the MoE layer: the operators of this package run together, as a serving step uses them.
 
     y      = norm(x)                                   moe_add_rmsnorm
-    q,k,v  = y Wqkv  [, rotary embedding]              torch matmul, the caller's function
-    cache += k, v                                      moe_kv_append
-    o      = attention(q, cache) Wo                    moe_paged_attention, torch matmul
+    q,k,v  = y Wqkv  [, rotary embedding]              torch matmul or moe_linear, the caller's function
+    cache += k, v                                      moe_kv_append or moe_kv_append_q8
+    o      = attention(q, cache) Wo                    moe_paged_attention or _q8, torch matmul or moe_linear
     r      = x + o,  z = norm(r),  codes = q8_K(z)     moe_add_rmsnorm
     logits = z Wr;  ids, gates = route(logits)         torch matmul in fp32, moe_route_grouped
     out    = r + sum of the experts' outputs           moe_bucket, moe_expert_ffn, moe_combine
@@ -11,10 +11,19 @@
 A call takes any mixture of sequences (single tokens, drafts to verify, prompt chunks) over one paged cache.  The
 residual stream is fp32, attention runs in the cache's type, the experts on q8_K codes.  Everything is launched on the
 current stream into buffers of the block, so a step can be captured into a CUDA graph.
+
+With `fused` (or with biases) the projections run on moe_linear, which adds the attention's output to the fp32 residual
+stream unrounded.  A cache of 8-bit codes (`q8_cache`, with scales) is quantised as it is written and read as it lies;
+prompt chunks read it back into `read_rows` rows of the block first, where the 16-bit attention is several times faster
+on many rows.
 """
 from __future__ import annotations
 
 import block_quantized_routed_gb300 as moe
+
+
+READ_PAGE = 64   # keys of a page of the rows that an 8-bit cache is read back into
+READ_FROM = 16   # new tokens per sequence, on average, from which on it is read back
 
 
 def _tf32(torch):
@@ -34,12 +43,15 @@ class MoeDecoderBlock:
     w_qkv [(Hq + 2 Hkv) D, H] and w_o [H, Hq D] in the cache's type; norms fp32 [H]; w_router fp32 [E, H];
     router_bias fp32 [E] or None takes part in the selection only.  n_group, topk_group, group_score, renorm and
     scale are moe_route_grouped's; rotary(q, k, cu_q, kv_len) rotates the views q [T, Hq, D] and k [T, Hkv, D] in
-    place; window > 0 limits attention to the last keys.
+    place; window > 0 limits attention to the last keys.  fused: the projections by moe_linear; b_qkv fp32 and b_o fp32,
+    their biases, ask for it too.  q8_cache: forward() may be given 8-bit caches; read_rows: rows of 16 bits for reading
+    them back (a call's sequences take whole runs of 64 rows each), 0 to attend to the codes always.
     """
 
     def __init__(self, desc, table, attn_norm, w_qkv, w_o, ffn_norm, w_router, n_heads, n_kv_heads, head_dim,
                  router_bias=None, n_group=1, topk_group=1, group_score=moe.GROUP_TOP2, renorm=True, scale=1.0,
-                 eps=1e-6, window=0, rotary=None, device="cuda"):
+                 eps=1e-6, window=0, rotary=None, device="cuda", b_qkv=None, b_o=None, fused=False, q8_cache=False,
+                 read_rows=0):
         import torch
         self.desc = d = moe._desc(desc)
         if w_router.shape != (d.E, d.H) or w_router.dtype != torch.float32:
@@ -73,10 +85,37 @@ class MoeDecoderBlock:
         zeros = lambda n: torch.zeros(n, dtype=torch.uint8, device=device)
         self.attn_ws, self.ffn_ws = zeros(attn_ws), zeros(ffn_ws)
         self.bucket_ws = zeros(moe.moe_bucket_workspace_size(T, k, E, S))
+        self.b_qkv, self.b_o, self.fused = b_qkv, b_o, fused or b_qkv is not None or b_o is not None
+        self.q8_ws = self.k_read = self.v_read = None
+        if q8_cache:
+            self.q8_ws = zeros(moe.moe_paged_attention_q8_workspace_size(n_heads, n_kv_heads, head_dim))
+            if read_rows:
+                pages = -(-read_rows // READ_PAGE)
+                self.k_read, self.v_read = (new(pages * READ_PAGE, n_kv_heads, head_dim, dtype=act) for _ in range(2))
 
-    def forward(self, x, k_cache, v_cache, page_table, cu_q, kv_len, out=None):
+    def _attend_q8(self, q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, attn):
+        """Appends to an 8-bit cache and attends to it."""
+        import torch
+        T, n_seqs, D = q.shape[0], kv_len.shape[0], self.head_dim
+        moe.moe_kv_append_q8(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, self.q8_ws)
+        if self.k_read is None or T <= READ_FROM * n_seqs:
+            moe.moe_paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, D ** -0.5, attn,
+                                       self.q8_ws, window=self.window)
+            return
+        # the sequences one after another in whole pages; lengths are known on the device only
+        runs = (kv_len.clamp(min=0) + (READ_PAGE - 1)) // READ_PAGE
+        first = (torch.cumsum(runs, 0) - runs).to(torch.int32)
+        most = -(-page_table.shape[1] * k_cache.shape[1] // READ_PAGE)
+        table = (first.unsqueeze(1) + torch.arange(most, dtype=torch.int32, device=q.device)).to(torch.int32)
+        moe.moe_kv_read_q8(k_cache, v_cache, k_scale, v_scale, page_table, kv_len, first * READ_PAGE, self.k_read,
+                           self.v_read, self.q8_ws)
+        pages = lambda t: t.view(-1, READ_PAGE, self.kv_heads, D)
+        moe.moe_paged_attention(q, pages(self.k_read), pages(self.v_read), table, cu_q, kv_len, D ** -0.5, attn,
+                                self.attn_ws, window=self.window)
+
+    def forward(self, x, k_cache, v_cache, page_table, cu_q, kv_len, out=None, k_scale=None, v_scale=None):
         """x fp32 [T, H]: the residual stream of the call's new tokens, in the order of cu_q.  kv_len counts the new
-        tokens.  Returns out fp32 [T, H] (may be x; rows may have a stride)."""
+        tokens.  k_scale and v_scale: of an 8-bit cache.  Returns out fp32 [T, H] (may be x; rows may have a stride)."""
         import torch
         T, d = x.shape[0], self.desc
         if T > d.T_max:
@@ -85,23 +124,35 @@ class MoeDecoderBlock:
             out = torch.empty(x.shape, dtype=torch.float32, device=x.device)
         elif out.shape != x.shape or out.dtype != torch.float32 or out.device != x.device:
             raise moe.MoeError(moe.MOE_ERR_INVALID_ARG, "MoeDecoderBlock.forward: out must be fp32 like x")
+        if k_scale is not None and self.q8_ws is None:
+            raise moe.MoeError(moe.MOE_ERR_INVALID_ARG, "MoeDecoderBlock.forward: an 8-bit cache needs q8_cache")
         if T == 0:
             return out
         hq, hkv, D = self.heads, self.kv_heads, self.head_dim
         y, qkv, attn, o, resid, z = (t[:T] for t in (self.y, self.qkv, self.attn, self.o, self.resid, self.z))
         moe.moe_add_rmsnorm(x, self.attn_norm, self.eps, y=y)
-        torch.matmul(y, self.w_qkv.t(), out=qkv)
+        if self.fused:
+            moe.moe_linear(y, self.w_qkv, qkv, bias=self.b_qkv, ws=self.attn_ws)
+        else:
+            torch.matmul(y, self.w_qkv.t(), out=qkv)
         h = qkv.view(T, hq + 2 * hkv, D)
         q, k, v = h[:, :hq], h[:, hq:hq + hkv], h[:, hq + hkv:]
         if self.rotary is not None:
             self.rotary(q, k, cu_q, kv_len)
-        moe.moe_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, self.attn_ws)
-        moe.moe_paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_len, D ** -0.5, attn.view(T, hq, D),
-                                self.attn_ws, window=self.window)
-        torch.matmul(attn, self.w_o.t(), out=o)
+        if k_scale is not None:
+            self._attend_q8(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_q, kv_len, attn.view(T, hq, D))
+        else:
+            moe.moe_kv_append(k, v, k_cache, v_cache, page_table, cu_q, kv_len, self.attn_ws)
+            moe.moe_paged_attention(q, k_cache, v_cache, page_table, cu_q, kv_len, D ** -0.5, attn.view(T, hq, D),
+                                    self.attn_ws, window=self.window)
         q8, sc, bs = self.q[:T], self.d[:T], self.bsum16[:T]
-        moe.moe_add_rmsnorm(o, self.ffn_norm, self.eps, residual=x, sum_out=resid, y=z, q_fmt=moe.NORM_Q_Q8K, q=q8,
-                            d=sc, bsum16=bs)
+        if self.fused:
+            moe.moe_linear(attn, self.w_o, resid, bias=self.b_o, residual=x, ws=self.attn_ws)
+            moe.moe_add_rmsnorm(resid, self.ffn_norm, self.eps, y=z, q_fmt=moe.NORM_Q_Q8K, q=q8, d=sc, bsum16=bs)
+        else:
+            torch.matmul(attn, self.w_o.t(), out=o)
+            moe.moe_add_rmsnorm(o, self.ffn_norm, self.eps, residual=x, sum_out=resid, y=z, q_fmt=moe.NORM_Q_Q8K, q=q8,
+                                d=sc, bsum16=bs)
         logits, ids, gates = self.logits[:T], self.ids[:T], self.gates[:T]
         if _tf32(torch):  # (as fast for long chunks alone: 64 tokens of 256 experts 227 us instead of 21)
             moe.moe_route_topk(z, self.w_router, None, d.top_k, d.route, logits, ids, gates)  # (its choices are not used)
@@ -123,8 +174,10 @@ class MoeDecoderBlock:
         """Synchronises and returns the first device-recorded error since the last call (0: none).  The block can be used
         again after any of them: a wait that ran out leaves counters behind, which are cleared here."""
         import torch
-        found = [moe.moe_get_status(ws) for ws in (self.attn_ws, self.bucket_ws, self.ffn_ws)]
-        if found[0] == moe.MOE_ERR_DEVICE_TIMEOUT:
-            self.attn_ws.zero_()
-            torch.cuda.current_stream().synchronize()
+        spaces = [ws for ws in (self.attn_ws, self.bucket_ws, self.ffn_ws, self.q8_ws) if ws is not None]
+        found = [moe.moe_get_status(ws) for ws in spaces]
+        for ws, st in zip(spaces, found):
+            if st == moe.MOE_ERR_DEVICE_TIMEOUT and (ws is self.attn_ws or ws is self.q8_ws):
+                ws.zero_()
+                torch.cuda.current_stream().synchronize()
         return next((st for st in found if st != moe.MOE_OK), moe.MOE_OK)
