@@ -8,14 +8,15 @@
 //
 // Inside a CTA (warp roles): one warp feeds a ring of (W, x) tiles of 64 terms
 // by TMA, one thread issues the products (tcgen05, fp32 accumulators in tensor
-// memory), four warps run the epilogue, a feature to a thread: its bias is one
-// register, and a warp's stores and residual loads of a token are 32 features
-// in a row.  Two accumulators, so the epilogue of a tile runs beside the next
-// tile's products.
+// memory), eight warps run the epilogue, a feature of half the tokens to a
+// thread: its bias is one register, and a warp's stores and residual loads of a
+// token are 32 features in a row.  Residuals are asked for a chunk of tokens
+// ahead, the first before the products are done.  Two accumulators, so the
+// epilogue of a tile runs beside the next tile's products.
 //
 // Few tiles: a cluster of CTAs takes one tile, each a share of its terms, and
 // the accumulators are joined through distributed shared memory: each CTA sums
-// a slice of the tokens, in the order of the ranks, and runs their epilogue.
+// a slice of the features, in the order of the ranks, and runs their epilogue.
 //
 // Every wait is bounded: after about a second a role records
 // MOE_ERR_DEVICE_TIMEOUT (where a status word is given), and all roles run to
@@ -37,7 +38,7 @@ namespace moe {
 namespace {
 
 constexpr long long kWaitCycles = 2000000000ll;  // ~1 s at 2 GHz
-constexpr int kThreads = 256;                    // warps: 0 copies, 1 products, 4 .. 7 epilogue
+constexpr int kThreads = 384;                    // warps: 0 copies, 1 products, 4 .. 11 epilogue
 constexpr int kM = 128, kK = 64;                 // features of a tile, terms of a stage
 constexpr int kW = kM * kK * 2;                  // bytes of a W tile
 
@@ -46,11 +47,13 @@ struct Cfg {
   static constexpr int BT = BT_;
   static constexpr bool kSplit = SPLIT_;
   static constexpr int kX = BT * kK * 2, kStage = kW + kX;
-  static constexpr int kJoin = SPLIT_ ? (BT + 8) * kM * 4 : 0;  // every rank's accumulators of a slice: up to (BT + 7) / ranks tokens each
+  static constexpr int kPitch = BT + 4;                         // floats of a feature in the join: 16-byte reads without conflicts
+  static constexpr int kJoin = SPLIT_ ? (kM + 7) * kPitch * 4 : 0;  // every rank's part of a slice of up to 135 / ranks features
   static constexpr int kPerSm = BT <= 32 ? 2 : 1;               // CTAs
   static constexpr int kBudget = (kPerSm == 2 ? 112 : 225) * 1024 - 2048 - kJoin;
   static constexpr int kStages = std::min(12, kBudget / kStage);
   static constexpr int kBufs = SPLIT_ ? 1 : 2;                  // accumulators
+  static constexpr int kChunk = BT == 16 ? 8 : 16;              // tokens that a thread works on at a time
   static constexpr int kCols = std::max(32, kBufs * BT);
   static constexpr int kSmemJoin = kStages * kStage, kSmemBars = kSmemJoin + kJoin;
   static constexpr int kSmem = 1024 + kSmemBars + 512;
@@ -99,15 +102,27 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-// 16 columns of the warp's 32 lanes, one lane (feature) per thread
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(addr)
-      : "memory");
+// N columns of the warp's 32 lanes, one lane (feature) per thread
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float* v) {
+  uint32_t r[N];
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -116,11 +131,18 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void store_remote(uint32_t local, uint32_t rank, float v) {  // the same place in another CTA
-  asm volatile("{\n .reg .b32 a;\n mapa.shared::cluster.u32 a, %0, %1;\n st.shared::cluster.f32 [a], %2;\n}\n" ::"r"(local),
-               "r"(rank), "f"(v)
+__device__ __forceinline__ uint32_t remote(uint32_t local, uint32_t rank) {  // the same place in another CTA
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void store_remote4(uint32_t to, const float* v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
                : "memory");
 }
+// a / b for numbers that are not negative, quick where a < 2^20: the quotient of a + 1/2 lies at least 1 / (2 b) from a
+// whole number, more than its error
+__device__ __forceinline__ int quotient(int a, int b) { return a < 1 << 20 ? (int)__fdividef((float)a + 0.5f, (float)b) : a / b; }
 // K-major tiles of 128-byte lines, 128-byte swizzle: 8-row groups 1024 bytes apart, a step of 16 terms is 32 bytes
 constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3FFFF) >> 4) | 1u << 16; }
@@ -157,38 +179,40 @@ __device__ __forceinline__ float activate(float v) {
     return 0.5f * v * (1.0f + tanhf(0.797884560802865356f * fmaf(0.044715f * v * v, v, v)));
   else return v;
 }
-__device__ __forceinline__ float to_f(float v) { return v; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
-template <typename R, int N>
-__device__ __forceinline__ void add_residual(const LinearArgs& a, int feature, int t, float* v) {
-  const R* p = static_cast<const R*>(a.residual) + t * a.r_stride + feature;
-  R r[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (t + i < a.T) r[i] = p[i * a.r_stride];
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (t + i < a.T) v[i] += to_f(r[i]);
-}
 template <typename O, int N>
-__device__ __forceinline__ void store(const LinearArgs& a, int feature, int t, const float* v) {
+__device__ __forceinline__ void store(const LinearArgs& a, int feature, int t, int n, const float* v) {
   O* p = static_cast<O*>(a.out) + t * a.o_stride + feature;
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    if (t + i < a.T) put(p + i * a.o_stride, v[i]);
+    if (i < n) put(p + i * a.o_stride, v[i]);
 }
-// N tokens from t on of one feature: `v` their products
 template <int ACT, int N>
 __device__ __forceinline__ void activate_all(float bias, float* v) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = activate<ACT>(v[i] + bias);
 }
+// The residual's n <= N tokens from t on of one feature, as they are stored.
 template <int N>
-__device__ __forceinline__ void finish(const LinearArgs& a, float bias, int feature, int t, float* v) {
+__device__ __forceinline__ void ask_residual(const LinearArgs& a, int feature, int t, int n, uint32_t* raw) {
+  if (!a.residual || feature >= a.N) return;
+  if (a.r_dtype == MOE_DT_F32) {
+    const uint32_t* p = static_cast<const uint32_t*>(a.residual) + t * a.r_stride + feature;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) raw[i] = p[i * a.r_stride];
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(a.residual) + t * a.r_stride + feature;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) raw[i] = p[i * a.r_stride];
+  }
+}
+// n <= N tokens from t on of one feature: `v` their products, `raw` their residuals
+template <int N>
+__device__ __forceinline__ void finish(const LinearArgs& a, float bias, int feature, int t, int n, float* v, const uint32_t* raw) {
   if (feature >= a.N) return;
   switch (a.act) {
     case MOE_ACT_RELU: activate_all<MOE_ACT_RELU, N>(bias, v); break;
@@ -198,13 +222,20 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float bias, int feat
     default: activate_all<MOE_ACT_NONE, N>(bias, v);
   }
   if (a.residual) {
-    if (a.r_dtype == MOE_DT_F32) add_residual<float, N>(a, feature, t, v);
-    else if (a.r_dtype == MOE_DT_BF16) add_residual<__nv_bfloat16, N>(a, feature, t, v);
-    else add_residual<__half, N>(a, feature, t, v);
+    if (a.r_dtype == MOE_DT_F32) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __uint_as_float(raw[i]);
+    } else if (a.r_dtype == MOE_DT_BF16) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __uint_as_float(raw[i] << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __half2float(__ushort_as_half((unsigned short)raw[i]));
+    }
   }
-  if (a.o_dtype == MOE_DT_F32) store<float, N>(a, feature, t, v);
-  else if (a.o_dtype == MOE_DT_BF16) store<__nv_bfloat16, N>(a, feature, t, v);
-  else store<__half, N>(a, feature, t, v);
+  if (a.o_dtype == MOE_DT_F32) store<float, N>(a, feature, t, n, v);
+  else if (a.o_dtype == MOE_DT_BF16) store<__nv_bfloat16, N>(a, feature, t, n, v);
+  else store<__half, N>(a, feature, t, n, v);
 }
 
 template <class C>
@@ -223,19 +254,40 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
   const auto acc_empty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };
   const int ranks = C::kSplit ? a.split : 1, rank = C::kSplit ? (int)cluster_rank() : 0;
   const int blocks = (a.K + kK - 1) / kK;
-  const int k0 = rank * blocks / ranks, k1 = (rank + 1) * blocks / ranks;
+  const int k0 = quotient(rank * blocks, ranks), k1 = quotient((rank + 1) * blocks, ranks);
   const int f_tiles = (a.N + kM - 1) / kM, t_tiles = (a.T + BT - 1) / BT;
-  const int tiles = f_tiles * t_tiles, first = blockIdx.x / ranks, step = gridDim.x / ranks;
+  const int tiles = f_tiles * t_tiles, first = quotient(blockIdx.x, ranks);
+  const int step = C::kSplit ? tiles : gridDim.x;
 
+  // a tile's first feature and token: the tokens of a group of feature tiles before the next group, so that what
+  // runs at one time shares both sides' tiles in L2
+  const auto tile_at = [&](int i, int& f, int& t) {
+    constexpr int kGroup = 16;
+    const int g = quotient(i, kGroup * t_tiles), in = i - g * kGroup * t_tiles, n = min(kGroup, f_tiles - g * kGroup);
+    t = quotient(in, n);
+    f = g * kGroup + in - t * n;
+  };
+  const auto copy = [&](int s, int k, int f, int t) {
+    bar_expect(full(s), C::kStage);
+    tma_2d(base + s * C::kStage, &wm, k * kK, f * kM, full(s));
+    tma_2d(base + s * C::kStage + kW, &xm, k * kK, t * BT, full(s));
+  };
+
+  const int ahead = min(kStages, k1 - k0);  // stages of the first tile that are asked for before anything else
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
-    for (int b = 0; b < 2; ++b) bar_init(acc_full(b), 1), bar_init(acc_empty(b), 4);
+    for (int s = 0; s < kStages; ++s) bar_init(full(s), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    int f, t;
+    tile_at(first, f, t);
+    for (int s = 0; s < ahead; ++s) copy(s, k0 + s, f, t);
+  }
+  if (tid == 32) {
+    for (int s = 0; s < kStages; ++s) bar_init(empty(s), 1);
+    for (int b = 0; b < 2; ++b) bar_init(acc_full(b), 1), bar_init(acc_empty(b), 8);
     s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&wm)) : "memory");
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&xm)) : "memory");
   }
-  if (warp == 1) {
+  if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "n"(C::kCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -246,27 +298,16 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
   if (C::kSplit) cluster_arrive();  // this CTA runs: others may write to it once they have waited
   const uint32_t tmem = s_tmem;
   const Wait wait{&s_abort, a.status};
-  // a tile's first feature and token: the tokens of a group of feature tiles before the next group, so that what
-  // runs at one time shares both sides' tiles in L2
-  const auto tile_at = [&](int i, int& f, int& t) {
-    constexpr int kGroup = 16;
-    const int g = i / (kGroup * t_tiles), in = i - g * kGroup * t_tiles, n = min(kGroup, f_tiles - g * kGroup);
-    t = in / n;
-    f = g * kGroup + in - t * n;
-  };
-
   if (warp == 0) {
     if (elect_one()) {
-      int s = 0;
-      uint32_t parity = 1;  // of the ring's empty barriers: the first round does not wait
+      int s = ahead == kStages ? 0 : ahead;
+      uint32_t parity = ahead == kStages ? 0 : 1;  // of the ring's empty barriers: the first round does not wait
       for (int i = first; i < tiles; i += step) {
         int f, t;
         tile_at(i, f, t);
-        for (int k = k0; k < k1; ++k) {
+        for (int k = i == first ? k0 + ahead : k0; k < k1; ++k) {
           if (!wait(empty(s), parity)) break;
-          bar_expect(full(s), C::kStage);
-          tma_2d(base + s * C::kStage, &wm, k * kK, f * kM, full(s));
-          tma_2d(base + s * C::kStage + kW, &xm, k * kK, t * BT, full(s));
+          copy(s, k, f, t);
           if (++s == kStages) s = 0, parity ^= 1;
         }
         if (s_abort) break;
@@ -299,51 +340,76 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
   } else if (warp >= 4) {
     int buf = 0;
     uint32_t acc_parity = 0;
-    const int row = tid - 128;  // of the tile: a feature
+    constexpr int CH = C::kChunk;
+    const int row = tid & 127, part = (tid >> 7) - 1;  // of the tile: a feature, and one of two parts of the tokens
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     for (int i = first; i < tiles; i += step) {
       int f, t;
       tile_at(i, f, t);
-      const int feature = f * kM + row;
-      const float bias = a.bias && feature < a.N ? __ldg(a.bias + feature) : 0.0f;
-      wait(acc_full(buf), acc_parity);
-      __syncwarp();
-      fence_after();
+      const auto bias_of = [&](int x) { return a.bias && x < a.N ? __ldg(a.bias + x) : 0.0f; };
+      const int feature = f * kM + row, live = min(BT, a.T - t * BT);  // tokens of the tile
+      uint32_t raw[2][CH];
       const uint32_t acc = tmem + lanes + buf * BT;
       if constexpr (C::kSplit) {
-        // slice r of the tokens goes to rank r: [from rank][token of the slice][feature]
+        // slice r of the features goes to rank r: [from rank][feature of the slice][token]
+        const int lo = rank * kM / ranks, nf = (rank + 1) * kM / ranks - lo;       // this rank's
+        const int to = ((row + 1) * ranks - 1) / kM, to_lo = to * kM / ranks, to_nf = (to + 1) * kM / ranks - to_lo;
+        const uint32_t dst = remote(base + C::kSmemJoin + (rank * to_nf + row - to_lo) * (C::kPitch * 4), to);
+        // Of the join a thread takes 4 tokens of one feature at a time, lanes next to each other features.  This code runs
+        // once, so it is kept short rather than unrolled (16 tokens at a time: 1 us more, for instructions that are fetched
+        // for the first time), and the residuals are brought to the first cache meanwhile instead of to registers.
+        const int groups = quotient(256, nf), q0 = quotient(tid - 128, nf), fi = tid - 128 - q0 * nf;
+        const int quads = q0 < groups ? (live + 3) / 4 : 0, mine = f * kM + lo + fi;
+        const float bias = bias_of(mine);
+        if (a.residual && mine < a.N) {
+          const int size = a.r_dtype == MOE_DT_F32 ? 4 : 2;
+          const char* p = static_cast<const char*>(a.residual) + ((int64_t)t * BT * a.r_stride + mine) * size;
+#pragma unroll 1
+          for (int q = q0; q < quads; q += groups)
+            for (int x = 4 * q; x < min(4 * q + 4, live); ++x)
+              asm volatile("prefetch.global.L1 [%0];" ::"l"(p + x * a.r_stride * size));
+        }
+        wait(acc_full(buf), acc_parity);
+        __syncwarp();
+        fence_after();
         cluster_wait();
-        for (int c0 = 0; c0 < BT && t * BT + c0 < a.T; c0 += 16) {
-          uint32_t v[16];
+        for (int c = part * CH; c < live; c += 2 * CH) {
+          float v[CH];
           __syncwarp();
-          tmem_ld16(acc + c0, v);
+          tmem_ld<CH>(acc + c, v);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            if (t * BT + c0 + c >= a.T) break;
-            const int live = min(BT, a.T - t * BT);
-            const int to = ((c0 + c + 1) * ranks - 1) / live;  // the rank whose slice holds the token
-            const int lo = to * live / ranks, n = (to + 1) * live / ranks - lo;
-            store_remote(base + C::kSmemJoin + ((rank * n + c0 + c - lo) * kM + row) * 4, to, __uint_as_float(v[c]));
-          }
+          for (int x = 0; x < CH; x += 4)
+            if (c + x < live) store_remote4(dst + (c + x) * 4, v + x);
         }
         cluster_arrive();
         cluster_wait();
-        const int live = min(BT, a.T - t * BT), lo = rank * live / ranks, n = (rank + 1) * live / ranks - lo;
-        const float* const join = reinterpret_cast<const float*>(smem + C::kSmemJoin) + row;
-        for (int c = 0; c < n; ++c) {
-          float v = join[c * kM];
-          for (int r = 1; r < ranks; ++r) v += join[(r * n + c) * kM];
-          finish<1>(a, bias, feature, t * BT + lo + c, &v);
+        const float* const join = reinterpret_cast<const float*>(smem + C::kSmemJoin);
+#pragma unroll 1
+        for (int q = q0; q < quads; q += groups) {
+          ask_residual<4>(a, mine, t * BT + 4 * q, live - 4 * q, raw[0]);
+          float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int r = 0; r < ranks; ++r) {
+            const float4 w = *reinterpret_cast<const float4*>(join + (r * nf + fi) * C::kPitch + 4 * q);
+            v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
+          }
+          finish<4>(a, bias, mine, t * BT + 4 * q, live - 4 * q, v, raw[0]);
         }
       } else {
-        for (int c0 = 0; c0 < BT && t * BT + c0 < a.T; c0 += 16) {
-          uint32_t v[16];
+        const int c0 = part * (BT / 2), c1 = min(live, c0 + BT / 2);
+        const float bias = bias_of(feature);
+        if (c0 < c1) ask_residual<CH>(a, feature, t * BT + c0, c1 - c0, raw[0]);
+        wait(acc_full(buf), acc_parity);
+        __syncwarp();
+        fence_after();
+#pragma unroll 1
+        for (int c = c0; c < c1; c += CH) {
+          if (c + CH < c1) ask_residual<CH>(a, feature, t * BT + c + CH, c1 - c - CH, raw[1]);
+          float v[CH];
           __syncwarp();
-          tmem_ld16(acc + c0, v);
-          float p[16];
+          tmem_ld<CH>(acc + c, v);
+          finish<CH>(a, bias, feature, t * BT + c, c1 - c, v, raw[0]);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) p[c] = __uint_as_float(v[c]);
-          finish<16>(a, bias, feature, t * BT + c0, p);
+          for (int x = 0; x < CH; ++x) raw[0][x] = raw[1][x];
         }
       }
       fence_before();
@@ -394,66 +460,113 @@ bool make_map(CUtensorMap* map, int dtype, const void* p, int64_t rows, int K, i
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Sets a kernel up once per device.
 template <class C>
-cudaError_t launch_t(LinearArgs a, int split, cudaStream_t s) {
-  auto kern = linear_kernel<C>;
+cudaError_t opt_in() {
   static PerDevice opted;
   cudaError_t err = cudaSuccess;
   opted([&](int) {
-    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    err = cudaFuncSetAttribute(linear_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     return err == cudaSuccess ? 1 : 0;
   });
+  return err;
+}
+template <class C>
+cudaLaunchConfig_t config(cudaLaunchAttribute* attr, int split, int64_t grid, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)split;
+  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = split > 1 ? 1 : 0;
+  return cfg;
+}
+// Tiles of `split` CTAs each that the device holds at one time: clusters stay within a group of SMs, so they leave some idle.
+template <int BT>
+int room(int split) {
+  if (split == 1) return Cfg<BT, false>::kPerSm * num_sms();
+  if constexpr (BT <= 128) {
+    using C = Cfg<BT, true>;
+    static PerDevice kept[9];
+    return kept[split]([&](int) {
+      cudaLaunchAttribute attr;
+      const cudaLaunchConfig_t cfg = config<C>(&attr, split, split, nullptr);
+      int n = 0;
+      if (opt_in<C>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, linear_kernel<C>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+      }
+      return n;
+    });
+  }
+  return 0;
+}
+
+template <class C>
+cudaError_t launch_t(LinearArgs a, int split, cudaStream_t s) {
+  const cudaError_t err = opt_in<C>();
   if (err != cudaSuccess) return err;
   CUtensorMap wm, xm;
   if (!make_map(&wm, a.x_dtype, a.w, a.N, a.K, a.w_stride, kM) || !make_map(&xm, a.x_dtype, a.x, a.T, a.K, a.x_stride, C::BT))
     return cudaErrorInvalidValue;
   a.split = split;
   const int64_t tiles = (int64_t)((a.N + kM - 1) / kM) * ((a.T + C::BT - 1) / C::BT);
-  const int64_t grid = C::kSplit ? tiles * split : std::min<int64_t>(tiles, (int64_t)C::kPerSm * num_sms());
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg =
+      config<C>(&attr, split, C::kSplit ? tiles * split : std::min<int64_t>(tiles, (int64_t)C::kPerSm * num_sms()), s);
   note_launch();
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)split;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = C::kSplit ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, a, wm, xm);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<C>, a, wm, xm);
 }
 template <int BT>
 cudaError_t launch_tokens(const LinearArgs& a, int split, cudaStream_t s) {
-  return split > 1 ? launch_t<Cfg<BT, true>>(a, split, s) : launch_t<Cfg<BT, false>>(a, 1, s);
+  if constexpr (BT <= 128) {
+    if (split > 1) return launch_t<Cfg<BT, true>>(a, split, s);
+  }
+  return launch_t<Cfg<BT, false>>(a, 1, s);
+}
+
+// The least of all tiles and divisions by what they cost.
+struct Choice {
+  int bt, split;
+  double cost;
+};
+template <int BT>
+void consider(const LinearArgs& a, Choice& best) {
+  const int blocks = (a.K + kK - 1) / kK, sms = num_sms();
+  const int64_t tiles = (int64_t)((a.N + kM - 1) / kM) * ((a.T + BT - 1) / BT);
+  for (int split = 1; split <= (BT <= 128 ? 8 : 1) && split <= std::max(1, blocks / 2); ++split) {
+    const int hold = room<BT>(split);
+    if (split > 1 && tiles > hold) continue;
+    const double bytes = kW + BT * 128.0;
+    const int64_t ctas = std::min<int64_t>(tiles, hold) * split;
+    const int on_sm = (int)std::min<int64_t>(Cfg<BT, false>::kPerSm, (ctas + sms - 1) / sms);
+    const double rounds = std::ceil((double)tiles / hold), per = (double)((blocks + split - 1) / split);
+    const double stage = std::max({2.0 * BT * on_sm, bytes * on_sm / 60.0, bytes * ctas / 8000.0});
+    const double cost = rounds * per * stage + (split > 1 ? 2000.0 : 0.0) + (split > 1 ? 80.0 : 30.0) * std::min(BT, a.T);
+    if (cost < best.cost) best = Choice{BT, split, cost};
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
-  if (a.T == 0 || a.N == 0) return cudaSuccess;
-  const int sms = num_sms(), blocks = (a.K + kK - 1) / kK;
-  int best_bt = 256, best_split = 1;
-  double best = 1e30;
-  for (int bt = 16; bt <= 256; bt *= 2) {
-    const int64_t tiles = (int64_t)((a.N + kM - 1) / kM) * ((a.T + bt - 1) / bt);
-    const int room = (bt <= 32 ? 2 : 1) * sms;
-    for (int split = 1; split <= (bt <= 128 ? 8 : 1) && split <= std::max(1, blocks / 2); ++split) {
-      if (split > 1 && tiles * split > room) break;
-      const double waves = std::ceil((double)tiles * split / room);
-      // cycles: a stage's copies or its products; an accumulator's way out
-      const double stage = std::max(2.0 * bt, (kW + bt * 128.0) / (bt <= 32 ? 24.0 : 48.0));
-      const double cost = waves * stage * ((blocks + split - 1) / split) + 2500 + 12.0 * std::min(bt, a.T) + (split > 1 ? 1500 : 0);
-      if (cost < best) best = cost, best_bt = bt, best_split = split;
-    }
-  }
-  switch (best_bt) {
-    case 16: return launch_tokens<16>(a, best_split, s);
-    case 32: return launch_tokens<32>(a, best_split, s);
-    case 64: return launch_tokens<64>(a, best_split, s);
-    case 128: return launch_tokens<128>(a, best_split, s);
-    default: return launch_t<Cfg<256, false>>(a, 1, s);
+  if (a.T == 0) return cudaSuccess;
+  Choice c{256, 1, 1e300};
+  consider<16>(a, c);
+  consider<32>(a, c);
+  consider<64>(a, c);
+  consider<128>(a, c);
+  consider<256>(a, c);
+  switch (c.bt) {
+    case 16: return launch_tokens<16>(a, c.split, s);
+    case 32: return launch_tokens<32>(a, c.split, s);
+    case 64: return launch_tokens<64>(a, c.split, s);
+    case 128: return launch_tokens<128>(a, c.split, s);
+    default: return launch_tokens<256>(a, 1, s);
   }
 }
 
