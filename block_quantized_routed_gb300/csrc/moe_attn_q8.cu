@@ -12,14 +12,14 @@
 //
 // Layout.  Keys are the 16 rows of S^T = K q^T and the 16 terms of out^T = V^T P^T,
 // rows of the query (token, head of the key/value head) the 8 columns of a tile,
-// NT tiles to an item.  A warp takes 16 keys at a time: TMA boxes of their codes,
-// found through the page table, land in a ring of its own some steps ahead, and
-// no barrier of the CTA is met until the item ends.  The order of a contraction's
-// terms is free, so a lane reads codes in 16-byte pieces as they lie: pieces of
-// two keys for S, and for the values the same piece of four keys, whose pairs
-// become the halves of an operand register; the boxes' swizzle keeps both reads
-// free of bank conflicts.  P^T is the transpose of S^T: one movmatrix per 8 x 8
-// block.
+// NT tiles to an item.  A CTA takes a tile of keys at a time, 16 to each warp: TMA
+// boxes of their codes, found through the page table, land in a ring of tiles,
+// and the warp that is the last to finish a tile asks for the one that takes its
+// place, so nobody waits but for data.  The order of a contraction's terms is
+// free, so a lane reads codes in 16-byte pieces as they lie: pieces of two keys
+// for S, and for the values the same piece of four keys, whose pairs become the
+// halves of an operand register; the boxes' swizzle keeps both reads free of bank
+// conflicts.  P^T is the transpose of S^T: one movmatrix per 8 x 8 block.
 //
 // References.  The weight's factor e_j belongs to the contraction, so it is
 // folded into the exponent, P'_j = 2^(c a_j + log2 e_j - m'), with a reference m'
@@ -29,9 +29,11 @@
 // more than 2^8, tested with one vote per 16 keys.
 //
 // Work split.  Each CTA finds its share of the items' key tiles from cu_q and
-// kv_len in a short prologue; an item that is cut leaves partial sums in the
-// workspace, and the CTA that arrives last joins them in the order of the keys,
-// so results do not depend on timing and no CTA waits for another.
+// kv_len in a short prologue: items in equal parts, a part to a CTA, or, where
+// that leaves the CTAs uneven or items are many, even shares of all tiles laid
+// end to end.  An item of several CTAs leaves partial sums in the workspace, and
+// the CTA that arrives last joins them in the order of the keys, so results do
+// not depend on timing and no CTA waits for another.
 #include <algorithm>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -52,7 +54,8 @@ constexpr int kMaxCtas = 320;                     // the workspace holds the par
 constexpr size_t kWsHead = 2048;                  // status (16 bytes), a counter per CTA
 static_assert(kWsHead >= 16 + 4 * kMaxCtas, "counters");
 constexpr int kOver = 4;                          // units of an item besides its key tiles: queries, join of the warps
-constexpr int kLeast = 4;                         // units of a CTA at least
+constexpr int kLeast = 1;                         // key tiles of a CTA at least
+constexpr int kCut = 4;                           // what even shares cost besides: two cut items a CTA
 constexpr float kLow = -3.0e38f;                  // a reference before any key
 constexpr float kGrow = 8.0f;                     // log2 of the growth that raises a reference
 constexpr float kLift = 7.0f;                     // log2 of the reference's weight in fp16: at most 2^15 with kGrow
@@ -65,15 +68,15 @@ struct Cfg {
   static constexpr int D = D_, NT = NT_, kRows = 8 * NT;
   static constexpr int W = NT * D <= 128 ? 8 : 4;               // warps: 128 or 256 registers a thread, two CTAs per SM
   static constexpr int kTile = 16 * W;                          // keys of a unit
-  static constexpr int kLine = D < 128 ? D : 128, kHalves = D / kLine;  // a copied box: 16 lines of up to 128 bytes
-  static constexpr int kBox = 16 * kLine;
-  static constexpr int kStage = 2 * kHalves * kBox;             // keys, then values
-  static constexpr int kScales = 128;                           // of a stage: scales of 16 keys, then of their values
+  static constexpr int kLine = D < 128 ? D : 128, kHalves = D / kLine;  // copied boxes have lines of up to 128 bytes
+  static constexpr int kPlane = kTile * kLine;                  // a tile's lines of one half of the keys or values
+  static constexpr int kStage = 2 * kHalves * kPlane;           // keys, then values
+  static constexpr int kScales = 128;                           // of a warp and stage: scales of 16 keys, then of their values
   static constexpr int kMisc = kRows * D * 2 + kRows * 16 + W * kRows * 12;
-  static constexpr int kStages = std::min(6, (113 * 1024 - 2048 - kMisc) / (W * (kStage + kScales + 8)));  // two CTAs per SM
-  static constexpr int kRing = W * kStages * kStage;
+  static constexpr int kStages = std::min(6, (113 * 1024 - 2048 - kMisc) / (kStage + W * kScales + 16));  // two CTAs per SM
+  static constexpr int kRing = kStages * kStage;
   static constexpr int kSmemScales = kRing, kSmemBars = kSmemScales + W * kStages * kScales;
-  static constexpr int kSmemMisc = kSmemBars + W * kStages * 8;
+  static constexpr int kSmemMisc = kSmemBars + kStages * 16;    // a barrier and a count of warps per stage
   static constexpr int kSmem = kSmemMisc + kMisc + 1024;        // (the ring starts on a 1024-byte boundary)
   static constexpr int kPitch = D + 4;                          // floats of a row in the join of the warps
   static constexpr size_t kPartFloats = kPartMax + 3 * 32;      // accumulator; m, m' and sum of each row
@@ -151,33 +154,34 @@ __device__ __forceinline__ float sum_rows(float x) {
 // A sequence's items: (key/value head, row tile), each over the key tiles of the whole sequence.
 struct Work {
   SeqInfo s;
-  int row_tiles, t0, tiles;
-  long long units;
+  int row_tiles, items, t0, tiles;
+  __device__ __forceinline__ int units() const { return items * (tiles + kOver); }  // of a call fewer than 2^31: attn_q8_fits
 };
 template <class C>
 __device__ __forceinline__ Work work_of(const AttnArgs& a, int G, int b) {
   Work w;
   w.s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, b);
-  w.row_tiles = (int)(((long long)w.s.n * G + C::kRows - 1) / C::kRows);
+  w.row_tiles = (w.s.n * G + C::kRows - 1) / C::kRows;
+  w.items = a.kv.Hkv * w.row_tiles;
   const int lo = window_lo(w.s.kv - w.s.n + 1, a.window);
   w.t0 = lo / C::kTile;
   w.tiles = max(1, (w.s.kv + C::kTile - 1) / C::kTile - w.t0);
-  w.units = (long long)a.kv.Hkv * w.row_tiles * (w.tiles + kOver);
   return w;
 }
 
+constexpr int kTries = 8;  // sizes of a part that are tried
 template <class C>
 struct Shared {
-  long long scan[C::W], rows[C::W];
-  long long before;
-  int seq, last;
+  int scan[C::W], units[C::W], items[C::W], ctas[C::W][kTries];
+  long long rows[C::W];
+  int seq, before, last;
   volatile int abort;
 };
 
 // a / b of numbers that are not negative, quick where they are short
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
+__device__ __forceinline__ int quotient(int a, int b) { return a < 1 << 20 ? (int)__fdividef((float)a + 0.5f, (float)b) : a / b; }
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // writes 4 columns of a row of out
@@ -226,57 +230,116 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
   float* const s_mv = s_m + W * kRows;
   float* const s_l = s_mv + W * kRows;
 
-  const uint32_t bars = smem_u32(smem) + C::kSmemBars + warp * kStages * 8;  // of this warp, one per stage
+  const uint32_t ring = smem_u32(smem), bars = ring + C::kSmemBars;
+  int* const s_done = reinterpret_cast<int*>(smem + C::kSmemBars + kStages * 8);  // [stage] warps that have finished with it
   if (tid < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tid ? &vm : &km)) : "memory");
-  if (lane < kStages) bar_init(bars + lane * 8);
+  if (tid < kStages) {
+    bar_init(bars + tid * 8);
+    s_done[tid] = 0;
+  }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   if (tid == 0) sh.abort = 0;
 
-  // ---- the CTA's share of the units
-  long long total = 0, ctas, u, u1;  // units of the call; CTAs that have some; this CTA's from u to u1
+  // ---- the CTA's share of the work: parts of `size` key tiles, or (size 0) the units from u to u1 of `total` on `ctas` CTAs
+  int size = 0, total = 0, ctas = gridDim.x, u = 0, u1 = 1;
   {
     const int per = (a.kv.n_seqs + kThreads - 1) / kThreads, b0 = tid * per, b1 = min(a.kv.n_seqs, b0 + per);
-    long long mine = 0, rows = 0;
-    for (int b = b0; b < b1; ++b) {
-      const Work w = work_of<C>(a, G, b);
-      if (!w.s.ok) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-      mine += w.units;
-      rows += w.s.n;
-    }
-    long long incl = mine;
+    const auto over = [&](auto f) {  // the sum of f over the thread's sequences
+      int sum = 0;
+      for (int b = b0; b < b1; ++b) sum += f(work_of<C>(a, G, b));
+      return sum;
+    };
+    // sums over the threads before, in the order of the sequences; scan[] has the warps'
+    const auto scan = [&](int mine) {
+      int incl = mine;
 #pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const long long x = __shfl_up_sync(kAll, incl, o);
-      if (lane >= o) incl += x;
-    }
+      for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += x;
+      }
+      if (lane == 31) sh.scan[warp] = incl;
+      return incl - mine;
+    };
+    long long rows = 0;
+    int items = 0;
+    const int units = over([&](const Work& w) {
+      if (!w.s.ok) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      rows += w.s.n;
+      items += w.items;
+      return w.units();
+    });
     rows = min(rows, (long long)a.T + 1);
     rows = ((long long)__reduce_add_sync(kAll, (unsigned)(rows >> 16)) << 16) + __reduce_add_sync(kAll, (unsigned)(rows & 0xffff));
-    if (lane == 31) {
-      sh.scan[warp] = incl;
+    items = __reduce_add_sync(kAll, items);
+    int before = scan(units);
+    if (lane == 0) {
+      sh.items[warp] = items;
       sh.rows[warp] = rows;
     }
     __syncthreads();
-    long long base = 0, all_rows = 0;
+    long long all_rows = 0;
+    items = 0;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) base += sh.scan[w];
-      total += sh.scan[w];
-      all_rows += sh.rows[w];
+    for (int x = 0; x < W; ++x) {
+      if (x < warp) before += sh.scan[x];
+      total += sh.scan[x];
+      items += sh.items[x];
+      all_rows += sh.rows[x];
     }
     // sequences that share rows (a cu_q out of order): nothing is computed
     if (total == 0 || all_rows > a.T) {
       if (tid == 0 && all_rows > a.T) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
       return;
     }
-    ctas = min((long long)gridDim.x, max(1ll, total / kLeast));
-    if (blockIdx.x >= ctas) return;
-    u = quotient(blockIdx.x * total, ctas);
-    u1 = quotient((blockIdx.x + 1) * total, ctas);
-    long long before = base + incl - mine;
-    if (u >= before && u < before + mine) {
+    // Equal parts: the smallest of a few sizes for which there are CTAs enough, if it is not much larger than an even share.
+    if (items <= ctas) {
+      const int shared = min(ctas, max(1, total / (kLeast + kOver)));  // CTAs of even shares
+      const int least = max(kLeast, (total - kOver * items + ctas - 1) / ctas);
+      const auto tried = [&](int k) { return least + (least * k + kTries - 1) / kTries; };
+      int need[kTries] = {};
+      for (int b = b0; b < b1; ++b) {
+        const Work w = work_of<C>(a, G, b);
+#pragma unroll
+        for (int k = 0; k < kTries; ++k) need[k] += w.items * quotient(w.tiles + tried(k) - 1, tried(k));
+      }
+#pragma unroll
+      for (int k = 0; k < kTries; ++k) {
+        const int sum = __reduce_add_sync(kAll, need[k]);
+        if (lane == 0) sh.ctas[warp][k] = sum;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = kTries - 1; k >= 0; --k) {
+        int sum = 0;
+#pragma unroll
+        for (int x = 0; x < W; ++x) sum += sh.ctas[x][k];
+        if (sum <= ctas && tried(k) + kOver <= quotient(total, shared) + kCut) size = tried(k);
+      }
+    }
+    int mine = units;
+    if (size) {
+      mine = over([&](const Work& w) { return w.items * quotient(w.tiles + size - 1, size); });
+      before = scan(mine);
+      __syncthreads();
+      total = 0;
+#pragma unroll
+      for (int x = 0; x < W; ++x) {
+        if (x < warp) before += sh.scan[x];
+        total += sh.scan[x];
+      }
+      u = blockIdx.x;
+      if (u >= total) return;
+    } else {
+      ctas = min(ctas, max(1, total / (kLeast + kOver)));
+      if ((int)blockIdx.x >= ctas) return;
+      u = (int)quotient((long long)blockIdx.x * total, ctas);
+      u1 = (int)quotient((long long)(blockIdx.x + 1) * total, ctas);
+    }
+    if (u >= before && u < before + mine) {  // this thread has the sequence of the CTA's first unit (of its part)
       int b = b0;
       for (;; ++b) {
-        const long long x = work_of<C>(a, G, b).units;
+        const Work w = work_of<C>(a, G, b);
+        const int x = size ? w.items * quotient(w.tiles + size - 1, size) : w.units();
         if (u < before + x) break;
         before += x;
       }
@@ -285,54 +348,74 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     }
     __syncthreads();
   }
-  // a row's token, quick where it is one of few
-  const auto by_heads = [&](int r) { return r < 1 << 20 ? (int)__fdividef((float)r + 0.5f, (float)G) : r / G; };
-  const auto owner = [&](long long u) { return (int)quotient((u + 1) * ctas - 1, total); };
-  int b = sh.seq;
-  long long base = sh.before;  // units before the sequence
+  const auto owner = [&](int x) { return (int)quotient(((long long)x + 1) * ctas - 1, total); };
+  int b = sh.seq, base = sh.before;  // units before the sequence
   Work w = work_of<C>(a, G, b);
-  const uint32_t ring = smem_u32(smem) + warp * (kStages * C::kStage);
-  const uint8_t* const ring_p = smem + warp * (kStages * C::kStage);
-  const uint32_t scales = smem_u32(smem) + C::kSmemScales + warp * (kStages * C::kScales);
   const float* const scales_p = reinterpret_cast<const float*>(smem + C::kSmemScales + warp * (kStages * C::kScales));
-  int fill = 0, got = 0;    // stages that are filled and read next
-  uint32_t parity = 0;      // of the barrier of stage `got`
+  const uint32_t scales = smem_u32(scales_p);
+  // keys of a box: a power of two that divides a page and a tile
+  const int box = min(C::kTile, a.kv.page_size & -a.kv.page_size), boxes = C::kTile / box, batch = 32 / boxes;
+  int got = 0;              // the stage that is read next
+  uint32_t parity = 0;      // of its barrier
 
-  while (u < u1) {
-    while (u >= base + w.units) {  // the next sequence with tokens
-      base += w.units;
-      w = work_of<C>(a, G, ++b);
+  for (bool more = true; more;) {
+    int item, p0, p1, c0, parts;  // the item and its tiles of this CTA; the first of its CTAs, and how many
+    if (size) {
+      parts = quotient(w.tiles + size - 1, size);
+      item = quotient(u - base, parts);
+      c0 = base + item * parts;
+      const int each = quotient(w.tiles + parts - 1, parts);
+      p0 = (u - c0) * each;
+      p1 = min(w.tiles, p0 + each);
+      more = false;
+    } else {
+      while (u - base >= w.units()) {  // the next sequence with tokens
+        base += w.units();
+        w = work_of<C>(a, G, ++b);
+      }
+      const int cost = w.tiles + kOver;
+      item = quotient(u - base, cost);
+      const int pay0 = base + item * cost + kOver;  // the unit of the first key tile
+      p0 = max(u, pay0) - pay0;
+      p1 = min(u1, pay0 + w.tiles) - pay0;
+      u = min(u1, pay0 + w.tiles);
+      more = u < u1;
+      if (p0 >= p1) continue;
+      c0 = owner(pay0);
+      parts = owner(pay0 + w.tiles - 1) - c0 + 1;
     }
-    const int cost = w.tiles + kOver;
-    const int item = (int)quotient(u - base, cost);
-    const long long item0 = base + (long long)item * cost, pay0 = item0 + kOver;  // first unit, first key tile
-    const int p0 = (int)(max(u, pay0) - pay0), p1 = (int)(min(u1, pay0 + w.tiles) - pay0);
-    u = min(u1, item0 + cost);
-    if (p0 >= p1) continue;
-    const int h = w.row_tiles == 1 ? item : item / w.row_tiles, r0 = (item - h * w.row_tiles) * kRows, nr = min(kRows, w.s.n * G - r0);
-    const int off = w.s.kv - w.s.n, tok0 = by_heads(r0), tok1 = by_heads(r0 + nr - 1);
+    const int h = w.row_tiles == 1 ? item : quotient(item, w.row_tiles), r0 = (item - h * w.row_tiles) * kRows;
+    const int nr = min(kRows, w.s.n * G - r0);
+    const int off = w.s.kv - w.s.n, tok0 = quotient(r0, G), tok1 = quotient(r0 + nr - 1, G);
     // keys that some row sees, and those that every row sees (rows behind the last are zeros, and go nowhere)
     const int hi = max(0, off + tok1 + 1), lo = min(hi, window_lo(off + tok0 + 1, a.window));
     const int all_lo = window_lo(off + tok1 + 1, a.window), all_hi = off + tok0 + 1;
     const int from = max(lo, (w.t0 + p0) * C::kTile), to = min(hi, (w.t0 + p1) * C::kTile);
-    const int first = from / 16, steps = to > from ? (to + 15) / 16 - first : 0;  // of 16 keys
-    int mine = steps > warp ? (steps - warp + W - 1) / W : 0;  // this warp's: first + warp + W * i
-    if (sh.abort) mine = 0;
+    const int first = from / C::kTile;                                                   // key tile
+    const int tiles = to > from && !sh.abort ? (to + C::kTile - 1) / C::kTile - first : 0;
 
-    // ---- pages of the first 32 steps, a step to a lane, and the query rows: all asked for at once
+    // ---- pages of the first tiles, a box to a lane, and the query rows: all asked for at once
     const int32_t* const table = a.table + (int64_t)b * a.kv.table_stride;
-    int page, slot;  // of step `lane` of the current 32
+    int page, slot;  // of box `lane` of the current batch of tiles; page -1: reads as zeros
     const auto look_up = [&](int i) {
-      const uint32_t key = (uint32_t)(first + warp + W * (i + lane)) * 16, entry = key / (uint32_t)a.kv.page_size;
+      const int tile = i + lane / boxes;
+      const uint32_t key = (uint32_t)(first + tile) * C::kTile + (lane % boxes) * box, entry = key / (uint32_t)a.kv.page_size;
       slot = (int)(key - entry * a.kv.page_size);
-      page = i + lane < mine ? __ldg(table + entry) : 0;
+      page = -1;
+      if (tile < tiles && key < (uint32_t)to && key + box > (uint32_t)from) {  // (some of its keys are seen)
+        page = __ldg(table + entry);
+        if (page < 0 || page >= a.kv.num_pages) {
+          if (warp == 0) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+          page = -1;
+        }
+      }
     };
     look_up(0);
     constexpr int kMyRows = kRows / W, kWords = (D + 127) / 128;
     uint2 qw[kMyRows][kWords];
 #pragma unroll
     for (int y = 0; y < kMyRows; ++y) {
-      const int r = y * W + warp, R = r0 + r, tok = by_heads(R);
+      const int r = y * W + warp, R = r0 + r, tok = quotient(R, G);
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.s.q0 + tok) * a.q_stride +
                             (int64_t)(h * G + R - tok * G) * a.q_head_stride;
 #pragma unroll
@@ -344,73 +427,86 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     }
     fence_proxy();
     __syncthreads();  // the last item's join has been read
-    // ---- loads of the first steps
+    // ---- loads of the first tiles
     const bool of_keys = lane < 16;
-    const float* const sc0 = of_keys ? ga.sc.k + h * ga.sc.k_head_stride + lane * ga.sc.k_row_stride
-                                     : ga.sc.v + h * ga.sc.v_head_stride + (lane - 16) * ga.sc.v_row_stride;
+    const float* const sc0 = of_keys ? ga.sc.k + h * ga.sc.k_head_stride : ga.sc.v + h * ga.sc.v_head_stride;
     const int64_t sc_page = of_keys ? ga.sc.k_page_stride : ga.sc.v_page_stride;
     const int64_t sc_row = of_keys ? ga.sc.k_row_stride : ga.sc.v_row_stride;
-    const auto issue = [&](int i) {
-      if (i < mine) {
-        const int pg = __shfl_sync(kAll, page, i & 31), at = __shfl_sync(kAll, slot, i & 31);
-        if ((i & 31) == 31) look_up(i + 1);
-        const bool there = pg >= 0 && pg < a.kv.num_pages;
-        const uint32_t bar = bars + fill * 8;
-        if (lane == 0) {
-          if (!there) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-          bar_expect(bar, C::kStage);
-        }
-        __syncwarp();
-        if (lane < 2 * C::kHalves) {  // a page that is not there: coordinates outside the cache, so zeros
-          const bool values = lane >= C::kHalves;
-          tma_4d(ring + fill * C::kStage + lane * C::kBox, values ? &vm : &km, (values ? lane - C::kHalves : lane) * 128, at,
-                 h, there ? pg : a.kv.num_pages, bar);
-        }
-        copy_async4(scales + fill * C::kScales + lane * 4, sc0 + (there ? pg : 0) * sc_page + at * sc_row, there);
-        if (++fill == kStages) fill = 0;
+    const int my_box = warp * 16 / box, my_line = warp * 16 % box + (lane & 15);
+    // the warp's scales of tile i into stage st
+    const auto ask_scales = [&](int i, int st) {
+      const int from_lane = i % batch * boxes + my_box;
+      const int pg = __shfl_sync(kAll, page, from_lane), at = __shfl_sync(kAll, slot, from_lane) + my_line;
+      copy_async4(scales + st * C::kScales + lane * 4, sc0 + max(pg, 0) * sc_page + at * sc_row, pg >= 0);
+    };
+    // the codes of tile i into stage st: a box to a lane
+    const auto ask_codes = [&](int i, int st) {
+      const int which = lane % boxes, plane = lane / boxes;
+      const int from_lane = i % batch * boxes + which;
+      const int pg = __shfl_sync(kAll, page, from_lane), at = __shfl_sync(kAll, slot, from_lane);
+      const uint32_t bar = bars + st * 8;
+      if (lane == 0) bar_expect(bar, C::kStage);
+      __syncwarp();
+      if (plane < 2 * C::kHalves) {
+        const bool values = plane >= C::kHalves;
+        tma_4d(ring + st * C::kStage + plane * C::kPlane + which * box * C::kLine, values ? &vm : &km,
+               (values ? plane - C::kHalves : plane) * 128, at, h, pg >= 0 ? pg : a.kv.num_pages, bar);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll 1
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
+    for (int i = 0; i < kStages; ++i) {
+      if (i < tiles) {
+        const int st = got + i < kStages ? got + i : got + i - kStages;
+        if (i && i % batch == 0) look_up(i);
+        if (warp == 0) ask_codes(i, st);
+        ask_scales(i, st);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
 
     // ---- queries: fp16 relative to the power of two at the row's largest element, in operand order
+    float e[kMyRows][kWords][4], peak[kMyRows];
 #pragma unroll
     for (int y = 0; y < kMyRows; ++y) {
-      const int r = y * W + warp, tok = by_heads(r0 + r);
-      float e[kWords][4];
-      float peak = 0.0f;
+      peak[y] = 0.0f;
 #pragma unroll
       for (int x = 0; x < kWords; ++x) {
         const uint2 v = qw[y][x];
         if (ga.x_dtype == MOE_DT_BF16) {
-          e[x][0] = __uint_as_float(v.x << 16), e[x][1] = __uint_as_float(v.x & 0xffff0000u);
-          e[x][2] = __uint_as_float(v.y << 16), e[x][3] = __uint_as_float(v.y & 0xffff0000u);
+          e[y][x][0] = __uint_as_float(v.x << 16), e[y][x][1] = __uint_as_float(v.x & 0xffff0000u);
+          e[y][x][2] = __uint_as_float(v.y << 16), e[y][x][3] = __uint_as_float(v.y & 0xffff0000u);
         } else {
           const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
           const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
-          e[x][0] = p.x, e[x][1] = p.y, e[x][2] = q.x, e[x][3] = q.y;
+          e[y][x][0] = p.x, e[y][x][1] = p.y, e[y][x][2] = q.x, e[y][x][3] = q.y;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) peak = fmaxf(peak, fabsf(e[x][i]));
+        for (int i = 0; i < 4; ++i) peak[y] = fmaxf(peak[y], fabsf(e[y][x][i]));
       }
+    }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) peak = fmaxf(peak, __shfl_xor_sync(kAll, peak, o));
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int y = 0; y < kMyRows; ++y) peak[y] = fmaxf(peak[y], __shfl_xor_sync(kAll, peak[y], o));
+#pragma unroll
+    for (int y = 0; y < kMyRows; ++y) {
+      const int r = y * W + warp, tok = quotient(r0 + r, G);
       // its exponent, where 2^-126 times it is a number; the largest element becomes 2^14 .. 2^15
-      const uint32_t ex = min(max(__float_as_uint(peak) >> 23, 15u), 254u);
+      const uint32_t ex = min(max(__float_as_uint(peak[y]) >> 23, 15u), 254u);
       const float up = __uint_as_float((268 - ex) << 23);
 #pragma unroll
       for (int x = 0; x < kWords; ++x) {
         const int word = x * 32 + lane;
         if (word < D / 4) {
+          float* v = e[y][x];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) e[x][i] *= up;
+          for (int i = 0; i < 4; ++i) v[i] *= up;
           // a line's pieces of 16 columns go to the lanes c in order (two each, where a line has 8), 4 columns at a time
           const int piece = word >> 2 & (C::kLine / 16 - 1), of = D == 64 ? piece : piece >> 1;
           const int step = (D == 64 ? 0 : (word >> 5) * 8 + (piece & 1) * 4) + (word & 3);
           s_q[((r >> 3) * (D / 16) + step) * 32 + (r & 7) * 4 + of] =
-              FMT == MOE_DT_E4M3 ? make_uint2(half2_of(e[x][0], e[x][1]), half2_of(e[x][2], e[x][3]))
-                                 : make_uint2(half2_of(e[x][0], e[x][2]), half2_of(e[x][1], e[x][3]));
+              FMT == MOE_DT_E4M3 ? make_uint2(half2_of(v[0], v[1]), half2_of(v[2], v[3]))
+                                 : make_uint2(half2_of(v[0], v[2]), half2_of(v[1], v[3]));
         }
       }
       if (lane == 0) {
@@ -433,9 +529,8 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       for (int i = 0; i < 2; ++i) m[n][i] = mv[n][i] = kLow, l[n][i] = 0.0f, f[n][i] = s_f[n * 8 + 2 * c + i];
     }
 #pragma unroll 1
-    for (int i = 0; i < mine; ++i) {
-      __syncwarp();  // every lane has read the stage that is filled next
-      issue(i + kStages - 1);
+    for (int i = 0; i < tiles; ++i) {
+      const int st_no = got;
       asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
       if (!bar_try(bars + got * 8, parity)) {
         const long long t0 = clock64();
@@ -444,153 +539,168 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
             sh.abort = 1;
             set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
           }
-        if (sh.abort) mine = 0;  // given up: what this call computes is void
       }
-      if (__any_sync(kAll, mine == 0)) break;
-      __syncwarp();
-      const uint8_t* const st = ring_p + got * C::kStage;
-      const float* const sc = scales_p + got * (C::kScales / 4);
+      if (__any_sync(kAll, sh.abort)) break;  // given up: what this call computes is void
       if (++got == kStages) got = 0, parity ^= 1;
-      const float ks[2] = {sc[g], sc[g + 8]};
-      const float lv[2] = {lg2(sc[16 + g]), lg2(sc[24 + g])};
-      constexpr int kChains = NT == 1 ? 2 : 1;  // sums that do not wait for one another
-      float s[NT][4], s2[4];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        s2[x] = 0.0f;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) s[n][x] = 0.0f;
-      }
-#pragma unroll
-      for (int x = 0; x < D / 64; ++x) {
-        // lines g and g + 8, the same place in both: the swizzle repeats after 8 lines
-        const uint8_t* src = st + (x >> 1) * C::kBox + g * C::kLine +
-                             ((D == 64 ? c ^ (g >> 1 & 3) : (2 * c + (x & 1)) ^ g) << 4);
-        const uint4 k0 = *reinterpret_cast<const uint4*>(src);
-        const uint4 k1 = *reinterpret_cast<const uint4*>(src + 8 * C::kLine);
-        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t af[4];
-          four_codes<FMT>(w0[y], af[0], af[2]);
-          four_codes<FMT>(w1[y], af[1], af[3]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint2 q = s_q[(n * (D / 16) + x * 4 + y) * 32 + lane];
-            mma(kChains == 2 && (y & 1) ? s2 : s[n], af, q.x, q.y);
-          }
-        }
-      }
-      if constexpr (kChains == 2) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s[0][x] += s2[x];
-      }
-      // a lane's piece of the values of its four keys
-      constexpr int kV = D == 64 ? 8 : 16;
-      uint32_t v[C::kHalves][4][kV / 4];
-#pragma unroll
-      for (int x = 0; x < C::kHalves; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int line = 2 * c + (y & 1);  // and its swizzle; line + 8 has the same
-          const uint8_t* src = st + (C::kHalves + x) * C::kBox + (line + (y >> 1) * 8) * C::kLine;
-          if constexpr (kV == 16) {
-            const uint4 r = *reinterpret_cast<const uint4*>(src + ((g ^ line) << 4));
-            v[x][y][0] = r.x, v[x][y][1] = r.y, v[x][y][2] = r.z, v[x][y][3] = r.w;
-          } else {
-            const uint2 r = *reinterpret_cast<const uint2*>(src + (((g >> 1) ^ (line >> 1)) << 4) + (g & 1) * 8);
-            v[x][y][0] = r.x, v[x][y][1] = r.y;
-          }
-        }
-      // scores in powers of two: s of the sum, sv with the value's scale
-      float sv[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
+      const int key = (first + i) * C::kTile + warp * 16;
+      if (key < to && key + 16 > from) {
+        const uint8_t* const st = smem + st_no * C::kStage + warp * 16 * C::kLine;
+        const float* const sc = scales_p + st_no * (C::kScales / 4);
+        const float ks[2] = {sc[g], sc[g + 8]};
+        const float lv[2] = {lg2(sc[16 + g]), lg2(sc[24 + g])};
+        constexpr int kChains = NT == 1 ? 2 : 1;  // sums that do not wait for one another
+        float s[NT][4], s2[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          s[n][x] *= f[n][x & 1] * ks[x >> 1];
-          sv[n][x] = s[n][x] + lv[x >> 1];
+          s2[x] = 0.0f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) s[n][x] = 0.0f;
         }
-      const int key = (first + warp + W * i) * 16;
-      const bool partly = key < all_lo || key + 16 > all_hi;  // some row does not see some key
-      if (partly) {
-        uint32_t nan_keys = 0;  // of the 16: a value's code is e4m3's NaN, which only the rows that see it may meet
-        if constexpr (FMT == MOE_DT_E4M3) {
 #pragma unroll
-          for (int x = 0; x < C::kHalves; ++x)
+        for (int x = 0; x < D / 64; ++x) {
+          // lines g and g + 8, the same place in both: the swizzle repeats after 8 lines
+          const uint8_t* src = st + (x >> 1) * C::kPlane + g * C::kLine +
+                               ((D == 64 ? c ^ (g >> 1 & 3) : (2 * c + (x & 1)) ^ g) << 4);
+          const uint4 k0 = *reinterpret_cast<const uint4*>(src);
+          const uint4 k1 = *reinterpret_cast<const uint4*>(src + 8 * C::kLine);
+          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-            for (int y = 0; y < 4; ++y)
+          for (int y = 0; y < 4; ++y) {
+            uint32_t af[4];
+            four_codes<FMT>(w0[y], af[0], af[2]);
+            four_codes<FMT>(w1[y], af[1], af[3]);
 #pragma unroll
-              for (int z = 0; z < kV / 4; ++z)
-                if (__vcmpeq4(v[x][y][z] & 0x7f7f7f7fu, 0x7f7f7f7fu)) nan_keys |= 1u << (2 * c + (y & 1) + (y >> 1) * 8);
-          nan_keys = __reduce_or_sync(kAll, nan_keys);
+            for (int n = 0; n < NT; ++n) {
+              const uint2 q = s_q[(n * (D / 16) + x * 4 + y) * 32 + lane];
+              mma(kChains == 2 && (y & 1) ? s2 : s[n], af, q.x, q.y);
+            }
+          }
         }
+        if constexpr (kChains == 2) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) s[0][x] += s2[x];
+        }
+        // a lane's piece of the values of its four keys
+        constexpr int kV = D == 64 ? 8 : 16;
+        uint32_t v[C::kHalves][4][kV / 4];
+#pragma unroll
+        for (int x = 0; x < C::kHalves; ++x)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int line = 2 * c + (y & 1);  // and its swizzle; line + 8 has the same
+            const uint8_t* src = st + (C::kHalves + x) * C::kPlane + (line + (y >> 1) * 8) * C::kLine;
+            if constexpr (kV == 16) {
+              const uint4 r = *reinterpret_cast<const uint4*>(src + ((g ^ line) << 4));
+              v[x][y][0] = r.x, v[x][y][1] = r.y, v[x][y][2] = r.z, v[x][y][3] = r.w;
+            } else {
+              const uint2 r = *reinterpret_cast<const uint2*>(src + (((g >> 1) ^ (line >> 1)) << 4) + (g & 1) * 8);
+              v[x][y][0] = r.x, v[x][y][1] = r.y;
+            }
+          }
+        // scores in powers of two: s of the sum, sv with the value's scale
+        float sv[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int r = n * 8 + 2 * c + (x & 1), j = key + g + (x >> 1) * 8;
-            if (j < s_lo[r] || j >= s_hi[r]) s[n][x] = sv[n][x] = -INFINITY;
-            else if (nan_keys >> (j - key) & 1) sv[n][x] = NAN;
+            s[n][x] *= f[n][x & 1] * ks[x >> 1];
+            sv[n][x] = s[n][x] + lv[x >> 1];
           }
-      }
-      bool grow = false;
+        const bool partly = key < all_lo || key + 16 > all_hi;  // some row does not see some key
+        if (partly) {
+          uint32_t nan_keys = 0;  // of the 16: a value's code is e4m3's NaN, which only the rows that see it may meet
+          if constexpr (FMT == MOE_DT_E4M3) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+            for (int x = 0; x < C::kHalves; ++x)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) grow |= s[n][x] > m[n][x & 1] + kGrow || sv[n][x] > mv[n][x & 1] + kGrow;
-      if (__any_sync(kAll, grow)) {
+              for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int z = 0; z < kV / 4; ++z)
+                  if (__vcmpeq4(v[x][y][z] & 0x7f7f7f7fu, 0x7f7f7f7fu)) nan_keys |= 1u << (2 * c + (y & 1) + (y >> 1) * 8);
+            nan_keys = __reduce_or_sync(kAll, nan_keys);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int r = n * 8 + 2 * c + (x & 1), j = key + g + (x >> 1) * 8;
+              if (j < s_lo[r] || j >= s_hi[r]) s[n][x] = sv[n][x] = -INFINITY;
+              else if (nan_keys >> (j - key) & 1) sv[n][x] = NAN;
+            }
+        }
+        bool grow = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float m1 = fmaxf(m[n][x], max_rows(fmaxf(s[n][x], s[n][x + 2])));
-            const float v1 = fmaxf(mv[n][x], max_rows(fmaxf(sv[n][x], sv[n][x + 2])));
-            l[n][x] *= ex2(m[n][x] - m1);
-            const float fo = ex2(mv[n][x] - v1);
+          for (int x = 0; x < 4; ++x) grow |= s[n][x] > m[n][x & 1] + kGrow || sv[n][x] > mv[n][x & 1] + kGrow;
+        if (__any_sync(kAll, grow)) {
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) o[n][t][x] *= fo, o[n][t][x + 2] *= fo;
-            m[n][x] = m1;
-            mv[n][x] = v1;
-          }
-      }
-      uint32_t p[NT][2];
+          for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+            for (int x = 0; x < 2; ++x) {
+              const float m1 = fmaxf(m[n][x], max_rows(fmaxf(s[n][x], s[n][x + 2])));
+              const float v1 = fmaxf(mv[n][x], max_rows(fmaxf(sv[n][x], sv[n][x + 2])));
+              l[n][x] *= ex2(m[n][x] - m1);
+              const float fo = ex2(mv[n][x] - v1);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          l[n][x & 1] += ex2(s[n][x] - m[n][x & 1]);
-          sv[n][x] = ex2(sv[n][x] - mv[n][x & 1] + kLift);
-        }
-        p[n][0] = transposed(half2_of(sv[n][0], sv[n][1]));
-        p[n][1] = transposed(half2_of(sv[n][2], sv[n][3]));
-      }
-      // columns 2 z and 2 z + 1 of the lane's piece are the rows g and g + 8 of an operand
-      const auto values = [&](auto finite) {
-#pragma unroll
-        for (int x = 0; x < C::kHalves; ++x)
-#pragma unroll
-          for (int y = 0; y < kV / 4; ++y) {
-            uint32_t af[2][4];
-            if constexpr (decltype(finite)::value) {
-              two_keys_finite<FMT, 0>(v[x][0][y], v[x][1][y], af[0][0], af[0][1]);
-              two_keys_finite<FMT, 0>(v[x][2][y], v[x][3][y], af[0][2], af[0][3]);
-              two_keys_finite<FMT, 2>(v[x][0][y], v[x][1][y], af[1][0], af[1][1]);
-              two_keys_finite<FMT, 2>(v[x][2][y], v[x][3][y], af[1][2], af[1][3]);
-            } else {
-              two_keys<FMT, 0>(v[x][0][y], v[x][1][y], af[0][0], af[0][1]);
-              two_keys<FMT, 0>(v[x][2][y], v[x][3][y], af[0][2], af[0][3]);
-              two_keys<FMT, 2>(v[x][0][y], v[x][1][y], af[1][0], af[1][1]);
-              two_keys<FMT, 2>(v[x][2][y], v[x][3][y], af[1][2], af[1][3]);
+              for (int t = 0; t < D / 16; ++t) o[n][t][x] *= fo, o[n][t][x + 2] *= fo;
+              m[n][x] = m1;
+              mv[n][x] = v1;
             }
+        }
+        uint32_t p[NT][2];
 #pragma unroll
-            for (int z = 0; z < 2; ++z)
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma(o[n][x * 8 + y * 2 + z], af[z], p[n][0], p[n][1]);
+          for (int x = 0; x < 4; ++x) {
+            l[n][x & 1] += ex2(s[n][x] - m[n][x & 1]);
+            sv[n][x] = ex2(sv[n][x] - mv[n][x & 1] + kLift);
           }
-      };
-      if (FMT == MOE_DT_E4M3 && partly) values(std::true_type{});
-      else values(std::false_type{});
+          p[n][0] = transposed(half2_of(sv[n][0], sv[n][1]));
+          p[n][1] = transposed(half2_of(sv[n][2], sv[n][3]));
+        }
+        // columns 2 z and 2 z + 1 of the lane's piece are the rows g and g + 8 of an operand
+        const auto values = [&](auto finite) {
+#pragma unroll
+          for (int x = 0; x < C::kHalves; ++x)
+#pragma unroll
+            for (int y = 0; y < kV / 4; ++y) {
+              uint32_t af[2][4];
+              if constexpr (decltype(finite)::value) {
+                two_keys_finite<FMT, 0>(v[x][0][y], v[x][1][y], af[0][0], af[0][1]);
+                two_keys_finite<FMT, 0>(v[x][2][y], v[x][3][y], af[0][2], af[0][3]);
+                two_keys_finite<FMT, 2>(v[x][0][y], v[x][1][y], af[1][0], af[1][1]);
+                two_keys_finite<FMT, 2>(v[x][2][y], v[x][3][y], af[1][2], af[1][3]);
+              } else {
+                two_keys<FMT, 0>(v[x][0][y], v[x][1][y], af[0][0], af[0][1]);
+                two_keys<FMT, 0>(v[x][2][y], v[x][3][y], af[0][2], af[0][3]);
+                two_keys<FMT, 2>(v[x][0][y], v[x][1][y], af[1][0], af[1][1]);
+                two_keys<FMT, 2>(v[x][2][y], v[x][3][y], af[1][2], af[1][3]);
+              }
+#pragma unroll
+              for (int z = 0; z < 2; ++z)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma(o[n][x * 8 + y * 2 + z], af[z], p[n][0], p[n][1]);
+            }
+        };
+        if (FMT == MOE_DT_E4M3 && partly) values(std::true_type{});
+        else values(std::false_type{});
+      }
+      // ---- the tile that takes this one's place: its scales by each warp, its codes by the last that is done
+      const int next = i + kStages;
+      if (next < tiles) {
+        if (next % batch == 0) look_up(next);
+        __syncwarp();
+        ask_scales(next, st_no);
+        int before = 0;
+        if (lane == 0)
+          asm volatile("atom.acq_rel.cta.shared::cta.add.s32 %0, [%1], 1;" : "=r"(before) : "r"(smem_u32(s_done + st_no)) : "memory");
+        if (__shfl_sync(kAll, before, 0) == W - 1) {
+          if (lane == 0) s_done[st_no] = 0;
+          ask_codes(next, st_no);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 
@@ -621,17 +731,16 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
                 make_float4(o[n][t][x], o[n][t][x + 2], o[n][t + 1][x], o[n][t + 1][x + 2]);
         }
       }
-    const int c0 = owner(pay0), parts = owner(pay0 + w.tiles - 1) - c0 + 1;
     float* const part = reinterpret_cast<float*>(a.ws + kWsHead) +
                         ((size_t)blockIdx.x * 2 + ((int)blockIdx.x == c0 ? 1 : 0)) * C::kPartFloats;
     const auto put_lse = [&](int r, float mm, float sum) {
       if (a.lse) {
-        const int R = r0 + r, tok = by_heads(R);
+        const int R = r0 + r, tok = quotient(R, G);
         a.lse[(int64_t)(w.s.q0 + tok) * a.Hq + h * G + R - tok * G] = lse_of(mm, sum);
       }
     };
     const auto row_at = [&](int r) {
-      const int R = r0 + r, tok = by_heads(R);
+      const int R = r0 + r, tok = quotient(R, G);
       return (int64_t)(w.s.q0 + tok) * a.o_stride + (int64_t)(h * G + R - tok * G) * a.o_head_stride;
     };
     if (tid < nr) {  // weights of the warps, in place of their references
@@ -669,10 +778,10 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     if (parts == 1) continue;
 
     // ---- an item of several CTAs: the last to arrive joins its parts
-    __threadfence();
     __syncthreads();
-    if (tid == 0) {
+    if (tid == 0) {  // (what the other threads wrote is ordered by the barrier)
       unsigned* counter = reinterpret_cast<unsigned*>(a.ws + 16) + c0;
+      __threadfence();
       sh.last = atomicInc(counter, (unsigned)parts - 1) == (unsigned)parts - 1;  // wraps to 0 behind the last
       __threadfence();
     }
@@ -766,14 +875,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// a cache's codes as [page][head][row][D]: boxes of 16 rows of one head of one page, up to 128 columns
-bool make_map(CUtensorMap* map, const moe_kv_desc& kv, const void* cache, int64_t row, int64_t head, int64_t page) {
+// a cache's codes as [page][head][row][D]: boxes of `rows` rows of one head of one page, up to 128 columns
+bool make_map(CUtensorMap* map, const moe_kv_desc& kv, const void* cache, int64_t row, int64_t head, int64_t page, int rows) {
   auto fn = encode_fn();
   if (!fn) return false;
   const auto bytes = [&](int64_t stride) { return (cuuint64_t)(stride ? stride : kv.D); };  // 0: one entry
   const cuuint64_t dims[4] = {(cuuint64_t)kv.D, (cuuint64_t)kv.page_size, (cuuint64_t)kv.Hkv, (cuuint64_t)kv.num_pages};
   const cuuint64_t strides[3] = {bytes(row), bytes(head), bytes(page)};
-  const cuuint32_t box[4] = {(cuuint32_t)std::min(kv.D, 128), 16, 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)std::min(kv.D, 128), (cuuint32_t)rows, 1, 1};
   const cuuint32_t one[4] = {1, 1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, one,
             CU_TENSOR_MAP_INTERLEAVE_NONE, kv.D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
@@ -793,8 +902,9 @@ cudaError_t launch_t(const AttnQ8Args& a, cudaStream_t s) {
   if (err != cudaSuccess) return err;
   const moe_kv_desc& kv = a.a.kv;
   CUtensorMap km, vm;
-  if (!make_map(&km, kv, a.a.k_cache, kv.k_row_stride, kv.k_head_stride, kv.k_page_stride) ||
-      !make_map(&vm, kv, a.a.v_cache, kv.v_row_stride, kv.v_head_stride, kv.v_page_stride))
+  const int rows = std::min(C::kTile, kv.page_size & -kv.page_size);
+  if (!make_map(&km, kv, a.a.k_cache, kv.k_row_stride, kv.k_head_stride, kv.k_page_stride, rows) ||
+      !make_map(&vm, kv, a.a.v_cache, kv.v_row_stride, kv.v_head_stride, kv.v_page_stride, rows))
     return cudaErrorInvalidValue;
   note_launch();
   kern<<<std::min(2 * num_sms(), kMaxCtas), 32 * C::W, C::kSmem, s>>>(a, km, vm);
@@ -829,6 +939,12 @@ bool attn_q8_tensor_core(const AttnQ8Args& g) {
                        (kv.num_pages > 1 && !(kv.k_page_stride && kv.v_page_stride));
   return !repeats && (kv.D == 64 || kv.D == 128 || kv.D == 256) && kv.page_size % 16 == 0 &&
          reinterpret_cast<uintptr_t>(g.a.k_cache) % 16 == 0 && reinterpret_cast<uintptr_t>(g.a.v_cache) % 16 == 0;
+}
+
+bool attn_q8_fits(const AttnQ8Args& g) {  // units are 32-bit numbers
+  const moe_kv_desc& kv = g.a.kv;
+  const int64_t items = ((int64_t)g.a.T * g.G / 8 + kv.n_seqs) * kv.Hkv;
+  return items * ((int64_t)kv.max_pages * kv.page_size / 64 + 2 + kOver) < (int64_t)1 << 31;
 }
 
 size_t attn_q8_workspace(int, int, int D) {

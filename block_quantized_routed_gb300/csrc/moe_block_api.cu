@@ -376,6 +376,7 @@ int moe_paged_attention_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, i
   g.x_dtype = x_dtype;
   g.G = Hq / kv->Hkv;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (attn_q8_tensor_core(g) && !attn_q8_fits(g)) return MOE_ERR_UNSUPPORTED;
   return done(attn_q8_tensor_core(g) ? launch_attn_q8(g, s) : launch_attn_q8_general(g, s));
 }
 

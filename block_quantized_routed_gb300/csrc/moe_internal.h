@@ -366,6 +366,7 @@ struct AttnQ8Args {
 };
 size_t attn_q8_workspace(int Hq, int Hkv, int D);
 bool attn_q8_tensor_core(const AttnQ8Args& a);  // what launch_attn_q8 takes
+bool attn_q8_fits(const AttnQ8Args& a);         // the largest possible work of a call stays below 2^31 units
 cudaError_t launch_attn_q8(const AttnQ8Args& a, cudaStream_t s);
 cudaError_t launch_attn_q8_general(const AttnQ8Args& a, cudaStream_t s);
 

@@ -4,10 +4,13 @@
 //   d = max|x| / top,  code = x / d;      x' = code * d
 //
 // What bounds both: memory, and for a decode step latency.  Every element is
-// read once and written once.  Appending takes one warp per token: a head's D
-// elements are 8 to a lane, so its maximum is a few shuffles among a group of
-// lanes, and several heads' keys and values are in flight before the token's
-// page is looked up.  Reading back takes one warp per row, 16 codes to a lane.
+// read once and written once.  Appending takes a warp per token and few heads: a
+// head's D elements are 8 to a lane, so its maximum is a few shuffles among a
+// group of lanes (keys and values together, a half of a register each), and all
+// of a warp's loads are under way before the token's page is looked up.  Reading
+// back takes 16 codes to a lane, as many lanes to a row as it has of them, up to
+// a warp.  (A warp for all 8 heads of 128 of a token: 12.3 us for 5257 tokens;
+// four rows of a warp read back together: 83 against 72 us for 99328 rows of the same.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -26,46 +29,55 @@ __device__ __forceinline__ float2 pair_f(uint32_t w, bool bf16) {
 // 8 elements of 16 bits, in pairs
 template <bool WIDE>
 __device__ __forceinline__ uint4 load8(const uint16_t* p) {
-  if constexpr (WIDE) return *reinterpret_cast<const uint4*>(p);
-  uint32_t w[4];
+  if constexpr (WIDE) {
+    return *reinterpret_cast<const uint4*>(p);
+  } else {
+    uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
-  return make_uint4(w[0], w[1], w[2], w[3]);
+    for (int i = 0; i < 4; ++i) w[i] = (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
-// Codes and scale of a vector whose elements are spread over `width` lanes (a power of two), 8 each.
+// A vector's scale from its largest magnitude (the bits of a 16-bit number), and its reciprocal.
 template <bool BF16, int FMT>
-__device__ __forceinline__ uint2 quantise(uint4 x, int width, float& d) {
+__device__ __forceinline__ float scale_of(uint32_t peak) {
+  if (peak >= (BF16 ? 0x7f80u : 0x7c00u)) return __uint_as_float(0x7fc00000u);
+  if (peak == 0) return 0.0f;
+  return fmaxf(pair_f(peak, BF16).x / (FMT == MOE_DT_E4M3 ? 448.0f : 127.0f), 1.17549435e-38f);
+}
+// Codes of 8 elements x / d.  The quotient is rounded as IEEE division rounds it, by Markstein's theorem (IBM J. Res.
+// Dev. 34, 1990): with the correctly rounded reciprocal r and the exact remainder of q = x r, q + r (x - q d) in fused
+// operations.  The remainder is exact while it is a normal number or 0; tiny scales take the division itself.
+template <bool BF16, int FMT>
+__device__ __forceinline__ uint2 codes_of(uint4 x, float d) {
+  if (!(d > 0.0f)) return make_uint2(0, 0);  // zeros, or not finite
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  // magnitudes of 16-bit numbers order as integers, infinities and NaN last
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-  m = max(m & 0xffffu, m >> 16);
-  for (int o = width >> 1; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (m >= (BF16 ? 0x7f80u : 0x7c00u)) {
-    d = __uint_as_float(0x7fc00000u);
-    return make_uint2(0, 0);
-  }
-  if (m == 0) {
-    d = 0.0f;
-    return make_uint2(0, 0);
-  }
-  d = fmaxf(pair_f(m, BF16).x / (FMT == MOE_DT_E4M3 ? 448.0f : 127.0f), 1.17549435e-38f);
+  const float r = __frcp_rn(d);
+  const bool tiny = d < 1e-28f;
   uint32_t code[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     float2 z = pair_f(w[i], BF16);
-    z.x /= d;
-    z.y /= d;
+    if (tiny) {
+      z.x /= d;
+      z.y /= d;
+    } else {
+      const float q0 = z.x * r, q1 = z.y * r;
+      z.x = fmaf(fmaf(-q0, d, z.x), r, q0);
+      z.y = fmaf(fmaf(-q1, d, z.y), r, q1);
+    }
     if constexpr (FMT == MOE_DT_E4M3) {
       code[i] = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
     } else {
-      const int a = (int)fminf(127.0f, fmaxf(-127.0f, roundf(z.x))), b = (int)fminf(127.0f, fmaxf(-127.0f, roundf(z.y)));
+      const int a = (int)roundf(z.x), b = (int)roundf(z.y);  // |z| < 127.5: the scale is off by half a step at most
       code[i] = (uint32_t)(a & 0xff) | (uint32_t)(b & 0xff) << 8;
     }
   }
   return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+}
+__device__ __forceinline__ uint32_t peak_of(uint4 x) {  // in two halves; magnitudes of 16-bit numbers order as integers
+  return __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
 }
 
 template <bool WIDE>
@@ -78,33 +90,31 @@ __device__ __forceinline__ void store_codes(uint8_t* p, uint2 c) {
   }
 }
 
-template <bool BF16, int FMT, bool WIDE>
+// kBatch: loads of a lane that are under way at one time, of keys and of values each.
+template <bool BF16, int FMT, bool WIDE, int kBatch>
 __global__ void __launch_bounds__(128) append_kernel(const KvAppendQ8Args g) {
   const KvAppendArgs& a = g.a;
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.T) return;
-  constexpr int kBatch = 4;
   const int vecs = a.kv.D / 8;  // 1 .. 32 of a head
   int width = 1;
   while (width < vecs) width *= 2;
-  const int per = 32 / width, h0 = lane / width, c = (lane - h0 * width) * 8;
+  const int per = 32 / width, group = lane / width, c = (lane - group * width) * 8;
+  const int h0 = blockIdx.y * kBatch * per + group;  // the warp's first heads, and per more for each of its loads
   const bool in_row = c < a.kv.D;
   const uint16_t* k = static_cast<const uint16_t*>(a.k) + (int64_t)t * a.k_stride;
   const uint16_t* v = static_cast<const uint16_t*>(a.v) + (int64_t)t * a.v_stride;
   uint4 kb[kBatch], vb[kBatch];
-  const auto load = [&](int first) {
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int h = first + u * per + h0;
-      kb[u] = vb[u] = make_uint4(0, 0, 0, 0);
-      if (h < a.kv.Hkv && in_row) {
-        kb[u] = load8<WIDE>(k + h * a.k_head_stride + c);
-        vb[u] = load8<WIDE>(v + h * a.v_head_stride + c);
-      }
+  for (int u = 0; u < kBatch; ++u) {
+    const int h = h0 + u * per;
+    kb[u] = vb[u] = make_uint4(0, 0, 0, 0);
+    if (h < a.kv.Hkv && in_row) {
+      kb[u] = load8<WIDE>(k + h * a.k_head_stride + c);
+      vb[u] = load8<WIDE>(v + h * a.v_head_stride + c);
     }
-  };
-  load(0);
+  }
   const int b = find_seq(a.cu_q, a.kv.n_seqs, t, lane);
   const SeqInfo s = seq_info(a.kv, a.cu_q, a.kv_len, a.T, b);
   if (!s.ok) {
@@ -123,21 +133,21 @@ __global__ void __launch_bounds__(128) append_kernel(const KvAppendQ8Args g) {
   uint8_t* vc = static_cast<uint8_t*>(a.v_cache) + (int64_t)page * a.kv.v_page_stride + slot * a.kv.v_row_stride;
   float* ks = g.sc.k + (int64_t)page * g.sc.k_page_stride + slot * g.sc.k_row_stride;
   float* vs = g.sc.v + (int64_t)page * g.sc.v_page_stride + slot * g.sc.v_row_stride;
-  for (int first = 0; first < a.kv.Hkv; first += kBatch * per) {
-    if (first) load(first);
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      if (first + u * per >= a.kv.Hkv) break;  // the same for the whole warp
-      const int h = first + u * per + h0;
-      float kd, vd;
-      const uint2 kq = quantise<BF16, FMT>(kb[u], width, kd), vq = quantise<BF16, FMT>(vb[u], width, vd);
-      if (h < a.kv.Hkv && in_row) {
-        store_codes<WIDE>(kc + h * a.kv.k_head_stride + c, kq);
-        store_codes<WIDE>(vc + h * a.kv.v_head_stride + c, vq);
-        if (c == 0) {
-          ks[h * g.sc.k_head_stride] = kd;
-          vs[h * g.sc.v_head_stride] = vd;
-        }
+  for (int u = 0; u < kBatch; ++u) {
+    const int h = h0 + u * per;
+    // the largest of the key and of the value, a half each, over the lanes that hold them
+    const uint32_t kp = peak_of(kb[u]), vp = peak_of(vb[u]);
+    uint32_t m = max(kp & 0xffffu, kp >> 16) | max(vp & 0xffffu, vp >> 16) << 16;
+    for (int o = width >> 1; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float kd = scale_of<BF16, FMT>(m & 0xffffu), vd = scale_of<BF16, FMT>(m >> 16);
+    const uint2 kq = codes_of<BF16, FMT>(kb[u], kd), vq = codes_of<BF16, FMT>(vb[u], vd);
+    if (h < a.kv.Hkv && in_row) {
+      store_codes<WIDE>(kc + h * a.kv.k_head_stride + c, kq);
+      store_codes<WIDE>(vc + h * a.kv.v_head_stride + c, vq);
+      if (c == 0) {
+        ks[h * g.sc.k_head_stride] = kd;
+        vs[h * g.sc.v_head_stride] = vd;
       }
     }
   }
@@ -193,10 +203,10 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* w) {
   }
 }
 
+// A row is the work of 2^shift lanes of a warp: 32, or as many as it has pieces of N codes.
 template <int FMT, int OUT, bool WIDE>
-__global__ void __launch_bounds__(128) read_kernel(const KvReadQ8Args a) {
+__global__ void __launch_bounds__(128) read_kernel(const KvReadQ8Args a, int shift) {
   constexpr int N = WIDE ? 16 : 8;
-  const int lane = threadIdx.x & 31;
   if (blockIdx.x == 0) {  // every sequence's rows: in range, and before the next one's
     for (int b = threadIdx.x; b < a.kv.n_seqs; b += blockDim.x) {
       const int64_t len = __ldg(a.kv_len + b), at = __ldg(a.first + b);
@@ -205,11 +215,17 @@ __global__ void __launch_bounds__(128) read_kernel(const KvReadQ8Args a) {
         set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
     }
   }
-  const int r = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int width = 1 << shift, lane = threadIdx.x & (width - 1);
+  const int64_t r = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> shift;
   if (r >= a.rows) return;
-  const int b = find_seq(a.first, a.kv.n_seqs, r, lane);
+  int b = 0;  // the last sequence that starts at or before the row
+  for (int n = a.kv.n_seqs; n > 1;) {
+    const int half = n / 2;
+    if (__ldg(a.first + b + half) <= r) b += half, n -= half;
+    else n = half;
+  }
   const int len = __ldg(a.kv_len + b);
-  const int64_t j64 = (int64_t)r - __ldg(a.first + b);
+  const int64_t j64 = r - __ldg(a.first + b);
   if (len > (int64_t)a.kv.max_pages * a.kv.page_size || j64 < 0 || j64 >= len) return;
   const int j = (int)j64, slot = j % a.kv.page_size;
   const int page = __ldg(a.table + (int64_t)b * a.kv.table_stride + j / a.kv.page_size);
@@ -222,43 +238,41 @@ __global__ void __launch_bounds__(128) read_kernel(const KvReadQ8Args a) {
   const float* ks = a.sc.k + (int64_t)page * a.sc.k_page_stride + slot * a.sc.k_row_stride;
   const float* vs = a.sc.v + (int64_t)page * a.sc.v_page_stride + slot * a.sc.v_row_stride;
   const int vecs = a.kv.D / N, total = a.kv.Hkv * vecs;
-  constexpr int kBatch = 2;
-  for (int i0 = lane; i0 < total; i0 += 32 * kBatch) {
-    uint32_t kw[kBatch][N / 4], vw[kBatch][N / 4];
-    float kd[kBatch], vd[kBatch];
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + 32 * u;
-      if (i < total) {
-        const int h = i / vecs, c = (i - h * vecs) * N;
-        load_codes<N, WIDE>(kc + h * a.kv.k_head_stride + c, kw[u]);
-        load_codes<N, WIDE>(vc + h * a.kv.v_head_stride + c, vw[u]);
-        kd[u] = ks[h * a.sc.k_head_stride];
-        vd[u] = vs[h * a.sc.v_head_stride];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int i = i0 + 32 * u;
-      if (i < total) {
-        const int h = i / vecs, c = (i - h * vecs) * N;
-        put_values<FMT, OUT, N, WIDE>(kw[u], kd[u], a.k_out, r * a.k_stride + h * a.k_head_stride + c);
-        put_values<FMT, OUT, N, WIDE>(vw[u], vd[u], a.v_out, r * a.v_stride + h * a.v_head_stride + c);
-      }
-    }
+  for (int i = lane; i < total; i += width) {
+    const int h = i / vecs, c = (i - h * vecs) * N;
+    uint32_t kw[N / 4], vw[N / 4];
+    load_codes<N, WIDE>(kc + h * a.kv.k_head_stride + c, kw);
+    load_codes<N, WIDE>(vc + h * a.kv.v_head_stride + c, vw);
+    const float kd = ks[h * a.sc.k_head_stride], vd = vs[h * a.sc.v_head_stride];
+    put_values<FMT, OUT, N, WIDE>(kw, kd, a.k_out, r * a.k_stride + h * a.k_head_stride + c);
+    put_values<FMT, OUT, N, WIDE>(vw, vd, a.v_out, r * a.v_stride + h * a.v_head_stride + c);
   }
 }
 
+template <bool BF16, int FMT, int kBatch>
+void append_as(const KvAppendQ8Args& a, int warps, cudaStream_t s) {
+  int width = 1;  // lanes of a head
+  while (width < a.a.kv.D / 8) width *= 2;
+  const int heads = kBatch * (32 / width);  // of a warp
+  const dim3 grid((unsigned)((a.a.T + warps - 1) / warps), (unsigned)((a.a.kv.Hkv + heads - 1) / heads));
+  if (a.a.wide) append_kernel<BF16, FMT, true, kBatch><<<grid, 32 * warps, 0, s>>>(a);
+  else append_kernel<BF16, FMT, false, kBatch><<<grid, 32 * warps, 0, s>>>(a);
+}
 template <bool BF16, int FMT>
-void append(const KvAppendQ8Args& a, unsigned grid, int threads, cudaStream_t s) {
-  if (a.a.wide) append_kernel<BF16, FMT, true><<<grid, threads, 0, s>>>(a);
-  else append_kernel<BF16, FMT, false><<<grid, threads, 0, s>>>(a);
+void append(const KvAppendQ8Args& a, cudaStream_t s) {
+  // Few tokens are latency: a warp to each token and as few heads as it holds (64 tokens of 4 heads of 128: 2.8 us, with
+  // two loads of a lane 3.4).  Many share the way to their page among two (5257 tokens of 8 heads: 10.8 us, with one 11.8).
+  if (a.a.T <= 4 * num_sms()) append_as<BF16, FMT, 1>(a, 1, s);
+  else append_as<BF16, FMT, 2>(a, 4, s);
 }
 template <int FMT, int OUT>
 void read(const KvReadQ8Args& a, cudaStream_t s) {
-  const unsigned grid = (unsigned)((a.rows + 3) / 4);
-  if (a.wide) read_kernel<FMT, OUT, true><<<grid, 128, 0, s>>>(a);
-  else read_kernel<FMT, OUT, false><<<grid, 128, 0, s>>>(a);
+  const int pieces = a.kv.Hkv * a.kv.D / (a.wide ? 16 : 8);
+  int shift = 0;
+  while (shift < 5 && 1 << shift < pieces) ++shift;
+  const unsigned grid = (unsigned)((((int64_t)a.rows << shift) + 127) / 128);
+  if (a.wide) read_kernel<FMT, OUT, true><<<grid, 128, 0, s>>>(a, shift);
+  else read_kernel<FMT, OUT, false><<<grid, 128, 0, s>>>(a, shift);
 }
 template <int FMT>
 void read_as(const KvReadQ8Args& a, cudaStream_t s) {
@@ -271,12 +285,10 @@ void read_as(const KvReadQ8Args& a, cudaStream_t s) {
 
 cudaError_t launch_kv_append_q8(const KvAppendQ8Args& a, cudaStream_t s) {
   if (a.a.T == 0) return cudaSuccess;
-  const int warps = a.a.T <= 4 * num_sms() ? 1 : 4;
-  const unsigned grid = (unsigned)((a.a.T + warps - 1) / warps);
   const bool bf16 = a.x_dtype == MOE_DT_BF16, e4m3 = a.a.kv.dtype == MOE_DT_E4M3;
   note_launch();
-  if (bf16) e4m3 ? append<true, MOE_DT_E4M3>(a, grid, 32 * warps, s) : append<true, MOE_DT_INT8>(a, grid, 32 * warps, s);
-  else e4m3 ? append<false, MOE_DT_E4M3>(a, grid, 32 * warps, s) : append<false, MOE_DT_INT8>(a, grid, 32 * warps, s);
+  if (bf16) e4m3 ? append<true, MOE_DT_E4M3>(a, s) : append<true, MOE_DT_INT8>(a, s);
+  else e4m3 ? append<false, MOE_DT_E4M3>(a, s) : append<false, MOE_DT_INT8>(a, s);
   return cudaGetLastError();
 }
 
