@@ -54,7 +54,7 @@ constexpr int kMaxCtas = 320;                     // the workspace holds the par
 constexpr size_t kWsHead = 2048;                  // status (16 bytes), a counter per CTA
 static_assert(kWsHead >= 16 + 4 * kMaxCtas, "counters");
 constexpr int kOver = 4;                          // units of an item besides its key tiles: queries, join of the warps
-constexpr int kLeast = 1;                         // key tiles of a CTA at least
+constexpr int kLeast = 2;                         // key tiles of a CTA at least
 constexpr int kCut = 4;                           // what even shares cost besides: two cut items a CTA
 constexpr float kLow = -3.0e38f;                  // a reference before any key
 constexpr float kGrow = 8.0f;                     // log2 of the growth that raises a reference
@@ -169,19 +169,21 @@ __device__ __forceinline__ Work work_of(const AttnArgs& a, int G, int b) {
   return w;
 }
 
-constexpr int kTries = 8;  // sizes of a part that are tried
+constexpr int kTries = 4;  // sizes of a part that are tried, in steps of an eighth
 template <class C>
 struct Shared {
   int scan[C::W], units[C::W], items[C::W], ctas[C::W][kTries];
   long long rows[C::W];
   int seq, before, last;
+  Work work;
   volatile int abort;
 };
 
-// a / b of numbers that are not negative, quick where they are short
+// a / b of numbers that are not negative, quick where a < 2^20: the quotient of a + 1/2 lies at least 1 / (2 b) from a
+// whole number, more than its error.
 __device__ __forceinline__ int quotient(int a, int b) { return a < 1 << 20 ? (int)__fdividef((float)a + 0.5f, (float)b) : a / b; }
-__device__ __forceinline__ long long quotient(long long a, int b) {
-  return (a >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+__device__ __forceinline__ int quotient(long long a, int b) {
+  return a < 1 << 20 ? quotient((int)a, b) : (int)(a / b);
 }
 
 // writes 4 columns of a row of out
@@ -244,113 +246,95 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
   int size = 0, total = 0, ctas = gridDim.x, u = 0, u1 = 1;
   {
     const int per = (a.kv.n_seqs + kThreads - 1) / kThreads, b0 = tid * per, b1 = min(a.kv.n_seqs, b0 + per);
-    const auto over = [&](auto f) {  // the sum of f over the thread's sequences
-      int sum = 0;
-      for (int b = b0; b < b1; ++b) sum += f(work_of<C>(a, G, b));
-      return sum;
-    };
-    // sums over the threads before, in the order of the sequences; scan[] has the warps'
-    const auto scan = [&](int mine) {
-      int incl = mine;
+    Work mine{};  // of the thread's (last) sequence
+    long long rows = 0;
+    int items = 0, units = 0;
+    for (int b = b0; b < b1; ++b) {
+      mine = work_of<C>(a, G, b);
+      if (!mine.s.ok) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
+      rows += mine.s.n;
+      items += mine.items;
+      units += mine.units();
+    }
+    // sums over the threads before, in the order of the sequences, and over all
+    const auto scan = [&](int x, int& all) {
+      int incl = x;
 #pragma unroll
       for (int o = 1; o < 32; o *= 2) {
-        const int x = __shfl_up_sync(kAll, incl, o);
-        if (lane >= o) incl += x;
+        const int y = __shfl_up_sync(kAll, incl, o);
+        if (lane >= o) incl += y;
       }
       if (lane == 31) sh.scan[warp] = incl;
-      return incl - mine;
+      __syncthreads();
+      const int y = lane < W ? sh.scan[lane] : 0;
+      all = __reduce_add_sync(kAll, y);
+      const int before = incl - x + __reduce_add_sync(kAll, lane < warp ? y : 0);
+      return before;
     };
-    long long rows = 0;
-    int items = 0;
-    const int units = over([&](const Work& w) {
-      if (!w.s.ok) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
-      rows += w.s.n;
-      items += w.items;
-      return w.units();
-    });
     rows = min(rows, (long long)a.T + 1);
     rows = ((long long)__reduce_add_sync(kAll, (unsigned)(rows >> 16)) << 16) + __reduce_add_sync(kAll, (unsigned)(rows & 0xffff));
-    items = __reduce_add_sync(kAll, items);
-    int before = scan(units);
+    const int warp_items = __reduce_add_sync(kAll, items);
     if (lane == 0) {
-      sh.items[warp] = items;
+      sh.items[warp] = warp_items;
       sh.rows[warp] = rows;
     }
-    __syncthreads();
+    int before = scan(units, total);
+    const int all_items = __reduce_add_sync(kAll, lane < W ? sh.items[lane] : 0);
     long long all_rows = 0;
-    items = 0;
-#pragma unroll
-    for (int x = 0; x < W; ++x) {
-      if (x < warp) before += sh.scan[x];
-      total += sh.scan[x];
-      items += sh.items[x];
-      all_rows += sh.rows[x];
-    }
+#pragma unroll 1
+    for (int x = 0; x < W; ++x) all_rows += sh.rows[x];
     // sequences that share rows (a cu_q out of order): nothing is computed
     if (total == 0 || all_rows > a.T) {
       if (tid == 0 && all_rows > a.T) set_status(a.status, MOE_ERR_DEVICE_BOUNDS);
       return;
     }
     // Equal parts: the smallest of a few sizes for which there are CTAs enough, if it is not much larger than an even share.
-    if (items <= ctas) {
+    if (all_items <= ctas && per == 1) {
       const int shared = min(ctas, max(1, total / (kLeast + kOver)));  // CTAs of even shares
-      const int least = max(kLeast, (total - kOver * items + ctas - 1) / ctas);
-      const auto tried = [&](int k) { return least + (least * k + kTries - 1) / kTries; };
-      int need[kTries] = {};
-      for (int b = b0; b < b1; ++b) {
-        const Work w = work_of<C>(a, G, b);
-#pragma unroll
-        for (int k = 0; k < kTries; ++k) need[k] += w.items * quotient(w.tiles + tried(k) - 1, tried(k));
-      }
+      const int least = max(kLeast, (total - kOver * all_items + ctas - 1) / ctas);
+      const auto tried = [&](int k) { return least + (least * k + 7) / 8; };
 #pragma unroll
       for (int k = 0; k < kTries; ++k) {
-        const int sum = __reduce_add_sync(kAll, need[k]);
+        const int sum = __reduce_add_sync(kAll, items * quotient(mine.tiles + tried(k) - 1, tried(k)));
         if (lane == 0) sh.ctas[warp][k] = sum;
       }
       __syncthreads();
+      const int even = quotient(total, shared) + kCut - kOver;
 #pragma unroll
       for (int k = kTries - 1; k >= 0; --k) {
-        int sum = 0;
-#pragma unroll
-        for (int x = 0; x < W; ++x) sum += sh.ctas[x][k];
-        if (sum <= ctas && tried(k) + kOver <= quotient(total, shared) + kCut) size = tried(k);
+        const int sum = __reduce_add_sync(kAll, lane < W ? sh.ctas[lane][k] : 0);
+        if (sum <= ctas && tried(k) <= even) size = tried(k);
       }
     }
-    int mine = units;
     if (size) {
-      mine = over([&](const Work& w) { return w.items * quotient(w.tiles + size - 1, size); });
-      before = scan(mine);
-      __syncthreads();
-      total = 0;
-#pragma unroll
-      for (int x = 0; x < W; ++x) {
-        if (x < warp) before += sh.scan[x];
-        total += sh.scan[x];
-      }
+      units = items * quotient(mine.tiles + size - 1, size);
+      before = scan(units, total);
       u = blockIdx.x;
       if (u >= total) return;
     } else {
       ctas = min(ctas, max(1, total / (kLeast + kOver)));
       if ((int)blockIdx.x >= ctas) return;
-      u = (int)quotient((long long)blockIdx.x * total, ctas);
-      u1 = (int)quotient((long long)(blockIdx.x + 1) * total, ctas);
+      u = quotient((long long)blockIdx.x * total, ctas);
+      u1 = quotient((long long)(blockIdx.x + 1) * total, ctas);
     }
-    if (u >= before && u < before + mine) {  // this thread has the sequence of the CTA's first unit (of its part)
+    if (u >= before && u < before + units) {  // this thread has the sequence of the CTA's first unit (of its part)
       int b = b0;
-      for (;; ++b) {
-        const Work w = work_of<C>(a, G, b);
-        const int x = size ? w.items * quotient(w.tiles + size - 1, size) : w.units();
-        if (u < before + x) break;
-        before += x;
+      if (per > 1) {
+        for (;; ++b) {
+          mine = work_of<C>(a, G, b);
+          if (u < before + mine.units()) break;
+          before += mine.units();
+        }
       }
       sh.seq = b;
       sh.before = before;
+      sh.work = mine;
     }
     __syncthreads();
   }
-  const auto owner = [&](int x) { return (int)quotient(((long long)x + 1) * ctas - 1, total); };
+  const auto owner = [&](int x) { return quotient(((long long)x + 1) * ctas - 1, total); };
   int b = sh.seq, base = sh.before;  // units before the sequence
-  Work w = work_of<C>(a, G, b);
+  Work w = sh.work;
   const float* const scales_p = reinterpret_cast<const float*>(smem + C::kSmemScales + warp * (kStages * C::kScales));
   const uint32_t scales = smem_u32(scales_p);
   // keys of a box: a power of two that divides a page and a tile
@@ -411,18 +395,21 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       }
     };
     look_up(0);
-    constexpr int kMyRows = kRows / W, kWords = (D + 127) / 128;
-    uint2 qw[kMyRows][kWords];
+    // lane r: where row r of the queries lies; a pass of a warp takes one row, two where a row is half a warp's words
+    constexpr int kWide = D == 64 ? 16 : 32, kRowsOfPass = 32 / kWide, kWords = (D + 127) / 128;
+    constexpr int kPasses = kRows / (W * kRowsOfPass) > 0 ? kRows / (W * kRowsOfPass) : 1;
+    const int my_tok = quotient(r0 + min(lane, nr - 1), G);
+    const int64_t my_row = (int64_t)(w.s.q0 + my_tok) * a.q_stride + (int64_t)(h * G + r0 + min(lane, nr - 1) - my_tok * G) * a.q_head_stride;
+    const auto row_of = [&](int y) { return (y * W + warp) * kRowsOfPass + lane / kWide; };
+    uint2 qw[kPasses][kWords];
 #pragma unroll
-    for (int y = 0; y < kMyRows; ++y) {
-      const int r = y * W + warp, R = r0 + r, tok = quotient(R, G);
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.s.q0 + tok) * a.q_stride +
-                            (int64_t)(h * G + R - tok * G) * a.q_head_stride;
+    for (int y = 0; y < kPasses; ++y) {
+      const int r = row_of(y);
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + __shfl_sync(kAll, my_row, r);
 #pragma unroll
       for (int x = 0; x < kWords; ++x) {
-        const int word = x * 32 + lane;
         qw[y][x] = make_uint2(0, 0);
-        if (r < nr && word < D / 4) qw[y][x] = *reinterpret_cast<const uint2*>(src + word * 4);
+        if (r < nr) qw[y][x] = *reinterpret_cast<const uint2*>(src + (x * 32 + lane % kWide) * 4);
       }
     }
     fence_proxy();
@@ -458,16 +445,16 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       if (i < tiles) {
         const int st = got + i < kStages ? got + i : got + i - kStages;
         if (i && i % batch == 0) look_up(i);
-        if (warp == 0) ask_codes(i, st);
+        if (warp == i % W) ask_codes(i, st);
         ask_scales(i, st);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     }
 
     // ---- queries: fp16 relative to the power of two at the row's largest element, in operand order
-    float e[kMyRows][kWords][4], peak[kMyRows];
+    float e[kPasses][kWords][4], peak[kPasses];
 #pragma unroll
-    for (int y = 0; y < kMyRows; ++y) {
+    for (int y = 0; y < kPasses; ++y) {
       peak[y] = 0.0f;
 #pragma unroll
       for (int x = 0; x < kWords; ++x) {
@@ -485,35 +472,34 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = kWide / 2; o > 0; o >>= 1)
 #pragma unroll
-      for (int y = 0; y < kMyRows; ++y) peak[y] = fmaxf(peak[y], __shfl_xor_sync(kAll, peak[y], o));
+      for (int y = 0; y < kPasses; ++y) peak[y] = fmaxf(peak[y], __shfl_xor_sync(kAll, peak[y], o));
 #pragma unroll
-    for (int y = 0; y < kMyRows; ++y) {
-      const int r = y * W + warp, tok = quotient(r0 + r, G);
+    for (int y = 0; y < kPasses; ++y) {
+      const int r = row_of(y);
+      if (r >= kRows) break;  // (more warps than rows)
       // its exponent, where 2^-126 times it is a number; the largest element becomes 2^14 .. 2^15
       const uint32_t ex = min(max(__float_as_uint(peak[y]) >> 23, 15u), 254u);
       const float up = __uint_as_float((268 - ex) << 23);
 #pragma unroll
       for (int x = 0; x < kWords; ++x) {
-        const int word = x * 32 + lane;
-        if (word < D / 4) {
-          float* v = e[y][x];
+        const int word = x * 32 + lane % kWide;
+        float* v = e[y][x];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] *= up;
-          // a line's pieces of 16 columns go to the lanes c in order (two each, where a line has 8), 4 columns at a time
-          const int piece = word >> 2 & (C::kLine / 16 - 1), of = D == 64 ? piece : piece >> 1;
-          const int step = (D == 64 ? 0 : (word >> 5) * 8 + (piece & 1) * 4) + (word & 3);
-          s_q[((r >> 3) * (D / 16) + step) * 32 + (r & 7) * 4 + of] =
-              FMT == MOE_DT_E4M3 ? make_uint2(half2_of(v[0], v[1]), half2_of(v[2], v[3]))
-                                 : make_uint2(half2_of(v[0], v[2]), half2_of(v[1], v[3]));
-        }
+        for (int i = 0; i < 4; ++i) v[i] *= up;
+        // a line's pieces of 16 columns go to the lanes c in order (two each, where a line has 8), 4 columns at a time
+        const int piece = word >> 2 & (C::kLine / 16 - 1), of = D == 64 ? piece : piece >> 1;
+        const int step = (D == 64 ? 0 : (word >> 5) * 8 + (piece & 1) * 4) + (word & 3);
+        s_q[((r >> 3) * (D / 16) + step) * 32 + (r & 7) * 4 + of] =
+            FMT == MOE_DT_E4M3 ? make_uint2(half2_of(v[0], v[1]), half2_of(v[2], v[3]))
+                               : make_uint2(half2_of(v[0], v[2]), half2_of(v[1], v[3]));
       }
-      if (lane == 0) {
-        s_f[r] = a.scale * kLog2e * __uint_as_float((ex - 14) << 23);
-        s_hi[r] = r < nr ? off + tok + 1 : 0;
-        s_lo[r] = r < nr ? window_lo(off + tok + 1, a.window) : 0;
-      }
+      if (lane % kWide == 0) s_f[r] = a.scale * kLog2e * __uint_as_float((ex - 14) << 23);
+    }
+    if (warp == W - 1 && lane < kRows) {
+      s_hi[lane] = lane < nr ? off + my_tok + 1 : 0;
+      s_lo[lane] = lane < nr ? window_lo(off + my_tok + 1, a.window) : 0;
     }
     __syncthreads();
 
@@ -790,41 +776,69 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     const float* const part0 = reinterpret_cast<const float*>(a.ws + kWsHead);
     const auto part_of = [&](int p) { return part0 + ((size_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * C::kPartFloats; };
     float* const wgt = reinterpret_cast<float*>(smem);  // [part][nr]
-    for (int r = warp; r < nr; r += W) {                // a warp per row, a lane per part
-      float mm = kLow, mmv = kLow, sum = 0.0f;
-      for (int p = lane; p < parts; p += 32) {
-        mm = fmaxf(mm, __ldcg(part_of(p) + kPartMax + r));
-        mmv = fmaxf(mmv, __ldcg(part_of(p) + kPartMax + 32 + r));
-      }
+    constexpr int kHeld = kRows / W;  // a warp takes every W-th row, a lane a part
+    float pm[kHeld], pv[kHeld], pl[kHeld], mm[kHeld], mmv[kHeld], sum[kHeld];
+    const auto ask_rows = [&](int p) {
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) {
-        mm = fmaxf(mm, __shfl_xor_sync(kAll, mm, x));
-        mmv = fmaxf(mmv, __shfl_xor_sync(kAll, mmv, x));
+      for (int y = 0; y < kHeld; ++y) {
+        pm[y] = pv[y] = kLow, pl[y] = 0.0f;
+        const int r = y * W + warp;
+        if (p < parts && r < nr) {
+          const float* q = part_of(p) + kPartMax + r;
+          pm[y] = __ldcg(q), pv[y] = __ldcg(q + 32), pl[y] = __ldcg(q + 64);
+        }
       }
-      for (int p = lane; p < parts; p += 32) {
-        sum += __ldcg(part_of(p) + kPartMax + 64 + r) * ex2(__ldcg(part_of(p) + kPartMax + r) - mm);
-        wgt[p * nr + r] = ex2(__ldcg(part_of(p) + kPartMax + 32 + r) - mmv);
-      }
+    };
 #pragma unroll
-      for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(kAll, sum, x);
-      if (lane == 0) {
-        s_rf[r] = out_factor(mm, mmv, sum);
-        put_lse(r, mm, sum);
+    for (int y = 0; y < kHeld; ++y) mm[y] = mmv[y] = kLow, sum[y] = 0.0f;
+#pragma unroll 1
+    for (int p = lane; p < parts + lane; p += 32) {  // (every lane as often)
+      ask_rows(p);
+#pragma unroll
+      for (int y = 0; y < kHeld; ++y) mm[y] = fmaxf(mm[y], pm[y]), mmv[y] = fmaxf(mmv[y], pv[y]);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+#pragma unroll
+      for (int y = 0; y < kHeld; ++y) {
+        mm[y] = fmaxf(mm[y], __shfl_xor_sync(kAll, mm[y], x));
+        mmv[y] = fmaxf(mmv[y], __shfl_xor_sync(kAll, mmv[y], x));
+      }
+#pragma unroll 1
+    for (int p = lane; p < parts + lane; p += 32) {
+      if (parts > 32) ask_rows(p);
+#pragma unroll
+      for (int y = 0; y < kHeld; ++y) {
+        sum[y] += pl[y] * ex2(pm[y] - mm[y]);
+        if (p < parts && y * W + warp < nr) wgt[p * nr + y * W + warp] = ex2(pv[y] - mmv[y]);
       }
     }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+#pragma unroll
+      for (int y = 0; y < kHeld; ++y) sum[y] += __shfl_xor_sync(kAll, sum[y], x);
+    if (lane == 0) {
+#pragma unroll
+      for (int y = 0; y < kHeld; ++y)
+        if (y * W + warp < nr) {
+          s_rf[y * W + warp] = out_factor(mm[y], mmv[y], sum[y]);
+          put_lse(y * W + warp, mm[y], sum[y]);
+        }
+    }
     __syncthreads();
-    const int n = nr * (D / 4);
-    int teams = 1;  // teams of threads share the parts where there are few vectors
+    const int n = nr * (D / 4);  // vectors of 4 columns
+    int teams = 1;               // teams of threads share the parts where there are few
     while (teams * 2 * n <= kThreads && teams * 2 <= parts) teams *= 2;
     const int width = kThreads / teams, team = tid / width;
-    float4* const red = reinterpret_cast<float4*>(smem + C::kRing - kThreads * 16);
+    const auto load = [&](int p, int e) { return __ldcg(reinterpret_cast<const float4*>(part_of(p)) + e); };
     const auto finish = [&](int e, float4 v) {
       const int r = e / (D / 4), col = e - r * (D / 4);
       const float rf = s_rf[r];
       put(ga, row_at(r) + col * 4, make_float4(v.x * rf, v.y * rf, v.z * rf, v.w * rf));
     };
-    const auto load = [&](int p, int e) { return __ldcg(reinterpret_cast<const float4*>(part_of(p)) + e); };
+    constexpr int kAhead = 8;  // parts that are asked for together
     if (n <= width) {
+      float4* const red = reinterpret_cast<float4*>(smem + C::kRing - kThreads * 16);
       const int e = tid - team * width, r = e / (D / 4);
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (e < n) {
@@ -839,16 +853,25 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       }
       if (team == 0 && e < n) finish(e, v);
     } else {
-      constexpr int kB = 4;
+      constexpr int kB = 2;  // vectors of a thread
       for (int e0 = tid; e0 < n; e0 += kB * kThreads) {
         float4 v[kB];
         int row[kB];
 #pragma unroll
         for (int x = 0; x < kB; ++x) v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f), row[x] = min(e0 + x * kThreads, n - 1) / (D / 4);
-#pragma unroll 2
-        for (int p = 0; p < parts; ++p)
+#pragma unroll 1
+        for (int p0 = 0; p0 < parts; p0 += kAhead) {
+          float4 in[kAhead][kB];
 #pragma unroll
-          for (int x = 0; x < kB; ++x) fma4(v[x], wgt[p * nr + row[x]], load(p, min(e0 + x * kThreads, n - 1)));
+          for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+            for (int x = 0; x < kB; ++x) in[y][x] = load(min(p0 + y, parts - 1), min(e0 + x * kThreads, n - 1));
+#pragma unroll
+          for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+            for (int x = 0; x < kB; ++x)
+              if (p0 + y < parts) fma4(v[x], wgt[(p0 + y) * nr + row[x]], in[y][x]);
+        }
 #pragma unroll
         for (int x = 0; x < kB; ++x)
           if (e0 + x * kThreads < n) finish(e0 + x * kThreads, v[x]);
