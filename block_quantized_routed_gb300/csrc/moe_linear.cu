@@ -95,6 +95,30 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo,
       " tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
       "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((int)acc));
 }
+// The same for a pair of CTAs: a copy that is counted by a barrier of either, products over both CTAs' tiles, a commit to
+// the same barrier of both, an arrival at a barrier of the other.
+__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+      "[%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss_pair(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n setp.ne.b32 p, %5, 0;\n mov.b64 a, {%1, %3};\n mov.b64 b, {%2, %3};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %4, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"((int)acc));
+}
+__device__ __forceinline__ void bar_arrive_remote(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -146,9 +170,9 @@ __device__ __forceinline__ int quotient(int a, int b) { return a < 1 << 20 ? (in
 // K-major tiles of 128-byte lines, 128-byte swizzle: 8-row groups 1024 bytes apart, a step of 16 terms is 32 bytes
 constexpr uint32_t kDescHi = (uint32_t)(1024 >> 4) | 1u << 14 | 2u << 29;
 __device__ __forceinline__ uint32_t desc_k(uint32_t addr) { return ((addr & 0x3FFFF) >> 4) | 1u << 16; }
-// kind::f16, fp32 accumulation, M = 128
-__device__ __forceinline__ uint32_t idesc(bool bf16, int N) {
-  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(kM >> 4) << 24;
+// kind::f16, fp32 accumulation
+__device__ __forceinline__ uint32_t idesc(bool bf16, int M, int N) {
+  return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (uint32_t)(N >> 3) << 17 | (uint32_t)(M >> 4) << 24;
 }
 
 struct Wait {
@@ -173,7 +197,11 @@ struct Wait {
 template <int ACT>
 __device__ __forceinline__ float activate(float v) {
   if constexpr (ACT == MOE_ACT_RELU) return v < 0.0f ? 0.0f : v;  // (NaN stays)
-  else if constexpr (ACT == MOE_ACT_SILU) return v / (1.0f + expf(-v));
+  else if constexpr (ACT == MOE_ACT_SILU) {  // 2^x within 2 ulp of its rounded argument, a quotient within 2 ulp
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.44269504088896341f));
+    return __fdividef(v, 1.0f + e);
+  }
   else if constexpr (ACT == MOE_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.707106781186547524f));
   else if constexpr (ACT == MOE_ACT_GELU_TANH)
     return 0.5f * v * (1.0f + tanhf(0.797884560802865356f * fmaf(0.044715f * v * v, v, v)));
@@ -185,30 +213,37 @@ __device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v
 template <typename O, int N>
 __device__ __forceinline__ void store(const LinearArgs& a, int feature, int t, int n, const float* v) {
   O* p = static_cast<O*>(a.out) + t * a.o_stride + feature;
+  if (n >= N) {  // (a test at each store, though never false, made an epilogue of stores alone 2.5 times as long)
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i < n) put(p + i * a.o_stride, v[i]);
+    for (int i = 0; i < N; ++i) put(p + i * a.o_stride, v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) put(p + i * a.o_stride, v[i]);
+  }
 }
 template <int ACT, int N>
 __device__ __forceinline__ void activate_all(float bias, float* v) {
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = activate<ACT>(v[i] + bias);
 }
+template <typename T, int N>
+__device__ __forceinline__ void ask_rows(const T* p, int64_t stride, int n, uint32_t* raw) {
+  if (n >= N) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) raw[i] = p[i * stride];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i < n) raw[i] = p[i * stride];
+  }
+}
 // The residual's n <= N tokens from t on of one feature, as they are stored.
 template <int N>
 __device__ __forceinline__ void ask_residual(const LinearArgs& a, int feature, int t, int n, uint32_t* raw) {
   if (!a.residual || feature >= a.N) return;
-  if (a.r_dtype == MOE_DT_F32) {
-    const uint32_t* p = static_cast<const uint32_t*>(a.residual) + t * a.r_stride + feature;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < n) raw[i] = p[i * a.r_stride];
-  } else {
-    const uint16_t* p = static_cast<const uint16_t*>(a.residual) + t * a.r_stride + feature;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i < n) raw[i] = p[i * a.r_stride];
-  }
+  if (a.r_dtype == MOE_DT_F32) ask_rows<uint32_t, N>(static_cast<const uint32_t*>(a.residual) + t * a.r_stride + feature, a.r_stride, n, raw);
+  else ask_rows<uint16_t, N>(static_cast<const uint16_t*>(a.residual) + t * a.r_stride + feature, a.r_stride, n, raw);
 }
 // n <= N tokens from t on of one feature: `v` their products, `raw` their residuals
 template <int N>
@@ -238,6 +273,50 @@ __device__ __forceinline__ void finish(const LinearArgs& a, float bias, int feat
   else store<__half, N>(a, feature, t, n, v);
 }
 
+__device__ __forceinline__ float bias_of(const LinearArgs& a, int feature) {
+  return a.bias && feature < a.N ? __ldg(a.bias + feature) : 0.0f;
+}
+// Brings a tile's residuals to L2, 128 bytes to each of the 256 epilogue threads (`thread`) at a time.  Asked for a tile ahead:
+// the way from memory takes as long as the epilogue of half a tile.
+__device__ __forceinline__ void prefetch_residual(const LinearArgs& a, int feature, int t, int live, int thread) {
+  if (!a.residual) return;
+  const int size = a.r_dtype == MOE_DT_F32 ? 4 : 2, lines = kM * size / 128;
+  for (int i = thread; i < live * lines; i += 256) {
+    const int token = i / lines, f = feature + (i - token * lines) * (128 / size);
+    if (f < a.N)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.residual) + ((t + token) * a.r_stride + f) * size));
+  }
+}
+// A thread's part of a tile that is not shared: feature, tokens t .. t + live, of its accumulator's columns the half `part`;
+// `ready` waits for the products.
+template <int BT, int CH, typename F>
+__device__ __forceinline__ void finish_tile(const LinearArgs& a, uint32_t acc, int feature, int t, int live, int part, F ready) {
+  uint32_t raw[2][CH];
+  const int c0 = part * (BT / 2), c1 = min(live, c0 + BT / 2);
+  const float bias = bias_of(a, feature);
+  if (c0 < c1) ask_residual<CH>(a, feature, t + c0, c1 - c0, raw[0]);
+  ready();
+#pragma unroll 1
+  for (int c = c0; c < c1; c += CH) {
+    if (c + CH < c1) ask_residual<CH>(a, feature, t + c + CH, c1 - c - CH, raw[1]);
+    float v[CH];
+    __syncwarp();
+    tmem_ld<CH>(acc + c, v);
+    finish<CH>(a, bias, feature, t + c, c1 - c, v, raw[0]);
+#pragma unroll
+    for (int x = 0; x < CH; ++x) raw[0][x] = raw[1][x];
+  }
+}
+
+// A tile's place among f_tiles x t_tiles: the tokens of a group of kGroup feature tiles before the next group, so that what
+// runs at one time shares both sides' tiles in L2.
+template <int kGroup>
+__device__ __forceinline__ void tile_of(int i, int f_tiles, int t_tiles, int& f, int& t) {
+  const int g = quotient(i, kGroup * t_tiles), in = i - g * kGroup * t_tiles, n = min(kGroup, f_tiles - g * kGroup);
+  t = quotient(in, n);
+  f = g * kGroup + in - t * n;
+}
+
 template <class C>
 __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wm,
                                                                      const __grid_constant__ CUtensorMap xm) {
@@ -259,14 +338,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
   const int tiles = f_tiles * t_tiles, first = quotient(blockIdx.x, ranks);
   const int step = C::kSplit ? tiles : gridDim.x;
 
-  // a tile's first feature and token: the tokens of a group of feature tiles before the next group, so that what
-  // runs at one time shares both sides' tiles in L2
-  const auto tile_at = [&](int i, int& f, int& t) {
-    constexpr int kGroup = 16;
-    const int g = quotient(i, kGroup * t_tiles), in = i - g * kGroup * t_tiles, n = min(kGroup, f_tiles - g * kGroup);
-    t = quotient(in, n);
-    f = g * kGroup + in - t * n;
-  };
+  const auto tile_at = [&](int i, int& f, int& t) { tile_of<16>(i, f_tiles, t_tiles, f, t); };
   const auto copy = [&](int s, int k, int f, int t) {
     bar_expect(full(s), C::kStage);
     tma_2d(base + s * C::kStage, &wm, k * kK, f * kM, full(s));
@@ -318,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
     if (elect_one()) {
       int s = 0, buf = 0;
       uint32_t parity = 0, acc_parity = 1;
-      const uint32_t id = idesc(a.x_dtype == MOE_DT_BF16, BT);
+      const uint32_t id = idesc(a.x_dtype == MOE_DT_BF16, kM, BT);
       for (int i = first; i < tiles; i += step) {
         if (!wait(acc_empty(buf), acc_parity)) break;
         fence_after();
@@ -346,9 +418,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
     for (int i = first; i < tiles; i += step) {
       int f, t;
       tile_at(i, f, t);
-      const auto bias_of = [&](int x) { return a.bias && x < a.N ? __ldg(a.bias + x) : 0.0f; };
       const int feature = f * kM + row, live = min(BT, a.T - t * BT);  // tokens of the tile
-      uint32_t raw[2][CH];
       const uint32_t acc = tmem + lanes + buf * BT;
       if constexpr (C::kSplit) {
         // slice r of the features goes to rank r: [from rank][feature of the slice][token]
@@ -360,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
         // for the first time), and the residuals are brought to the first cache meanwhile instead of to registers.
         const int groups = quotient(256, nf), q0 = quotient(tid - 128, nf), fi = tid - 128 - q0 * nf;
         const int quads = q0 < groups ? (live + 3) / 4 : 0, mine = f * kM + lo + fi;
-        const float bias = bias_of(mine);
+        const float bias = bias_of(a, mine);
         if (a.residual && mine < a.N) {
           const int size = a.r_dtype == MOE_DT_F32 ? 4 : 2;
           const char* p = static_cast<const char*>(a.residual) + ((int64_t)t * BT * a.r_stride + mine) * size;
@@ -386,31 +456,27 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
         const float* const join = reinterpret_cast<const float*>(smem + C::kSmemJoin);
 #pragma unroll 1
         for (int q = q0; q < quads; q += groups) {
-          ask_residual<4>(a, mine, t * BT + 4 * q, live - 4 * q, raw[0]);
+          uint32_t raw[4];
+          ask_residual<4>(a, mine, t * BT + 4 * q, live - 4 * q, raw);
           float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           for (int r = 0; r < ranks; ++r) {
             const float4 w = *reinterpret_cast<const float4*>(join + (r * nf + fi) * C::kPitch + 4 * q);
             v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
           }
-          finish<4>(a, bias, mine, t * BT + 4 * q, live - 4 * q, v, raw[0]);
+          finish<4>(a, bias, mine, t * BT + 4 * q, live - 4 * q, v, raw);
         }
       } else {
-        const int c0 = part * (BT / 2), c1 = min(live, c0 + BT / 2);
-        const float bias = bias_of(feature);
-        if (c0 < c1) ask_residual<CH>(a, feature, t * BT + c0, c1 - c0, raw[0]);
-        wait(acc_full(buf), acc_parity);
-        __syncwarp();
-        fence_after();
-#pragma unroll 1
-        for (int c = c0; c < c1; c += CH) {
-          if (c + CH < c1) ask_residual<CH>(a, feature, t * BT + c + CH, c1 - c - CH, raw[1]);
-          float v[CH];
-          __syncwarp();
-          tmem_ld<CH>(acc + c, v);
-          finish<CH>(a, bias, feature, t * BT + c, c1 - c, v, raw[0]);
-#pragma unroll
-          for (int x = 0; x < CH; ++x) raw[0][x] = raw[1][x];
+        if (i == first) prefetch_residual(a, f * kM, t * BT, live, tid - 128);
+        if (i + step < tiles) {
+          int nf, nt;
+          tile_at(i + step, nf, nt);
+          prefetch_residual(a, nf * kM, nt * BT, min(BT, a.T - nt * BT), tid - 128);
         }
+        finish_tile<BT, CH>(a, acc, feature, t * BT, live, part, [&] {
+          wait(acc_full(buf), acc_parity);
+          __syncwarp();
+          fence_after();
+        });
       }
       fence_before();
       __syncwarp();
@@ -433,6 +499,153 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
   if (warp == 1) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kCols));
+  }
+}
+
+// ---------------------------------------------------------------- pairs of CTAs
+// Many tokens: two CTAs on neighbouring SMs form products over 256 features and BT tokens.  Each holds the W tile of its 128
+// features and the x tile of half the tokens, and the tensor pipes of both read both halves, so an SM takes 64 bytes per
+// clock at BT = 256.  Alone it takes 96 for its products, and gets 75: 8192 tokens of 5120 x 4096 were bound by that.
+template <int BT_>
+struct PairCfg {
+  static constexpr int BT = BT_;
+  static constexpr int kX = BT / 2 * kK * 2, kStage = kW + kX;  // of each CTA
+  static constexpr int kStages = std::min(9, (225 * 1024 - 2048) / kStage);
+  static constexpr int kCols = 2 * BT;
+  static constexpr int kSmemBars = kStages * kStage;
+  static constexpr int kSmem = 1024 + kSmemBars + 512;
+  static_assert(kCols <= 512 && 8 * (2 * kStages + 4) <= 512, "sizes");
+};
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const LinearArgs a, const __grid_constant__ CUtensorMap wm,
+                                                                  const __grid_constant__ CUtensorMap xm) {
+  constexpr int BT = C::BT, kStages = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* const smem = smem_raw + (-smem_u32(smem_raw) & 1023);
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const uint32_t base = smem_u32(smem), bars = base + C::kSmemBars;
+  const auto full = [&](int s) { return bars + s * 8; };               // of the leader (rank 0): both CTAs' copies
+  const auto empty = [&](int s) { return bars + (kStages + s) * 8; };  // of each
+  const auto acc_full = [&](int b) { return bars + (2 * kStages + b) * 8; };
+  const auto acc_empty = [&](int b) { return bars + (2 * kStages + 2 + b) * 8; };  // of the leader: both CTAs' epilogues
+  const int rank = (int)cluster_rank();
+  const int blocks = (a.K + kK - 1) / kK;
+  const int f_tiles = (a.N + 2 * kM - 1) / (2 * kM), t_tiles = (a.T + BT - 1) / BT, tiles = f_tiles * t_tiles;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) bar_init(full(s), 1), bar_init(empty(s), 1);
+    for (int b = 0; b < 2; ++b) bar_init(acc_full(b), 1), bar_init(acc_empty(b), 16);
+    s_abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (tid == 32) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&wm)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&xm)) : "memory");
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "n"(C::kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  __syncwarp();
+  fence_before();
+  cluster_arrive();
+  cluster_wait();  // both CTAs' barriers and tensor memory are there
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  const Wait wait{&s_abort, a.status};
+  const auto tile_at = [&](int i, int& f, int& t) { tile_of<8>(i, f_tiles, t_tiles, f, t); };
+
+  if (warp == 0) {
+    if (elect_one()) {
+      int s = 0;
+      uint32_t parity = 1;  // of the ring's empty barriers: the first round does not wait
+      for (int i = first; i < tiles; i += step) {
+        int f, t;
+        tile_at(i, f, t);
+        for (int k = 0; k < blocks; ++k) {
+          if (!wait(empty(s), parity)) break;
+          const uint32_t bar = remote(full(s), 0), dst = base + s * C::kStage;
+          if (rank == 0) bar_expect(full(s), 2 * C::kStage);
+          tma_2d_pair(dst, &wm, k * kK, (2 * f + rank) * kM, bar);
+          tma_2d_pair(dst + kW, &xm, k * kK, t * BT + rank * (BT / 2), bar);
+          if (++s == kStages) s = 0, parity ^= 1;
+        }
+        if (s_abort) break;
+      }
+      // the last commits reach this CTA before it ends
+      for (int j = 0; j < kStages && !s_abort; ++j) {
+        wait(empty(s), parity);
+        if (++s == kStages) s = 0, parity ^= 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && rank == 0) {
+    if (elect_one()) {
+      int s = 0, buf = 0;
+      uint32_t parity = 0, acc_parity = 1;
+      const uint32_t id = idesc(a.x_dtype == MOE_DT_BF16, 2 * kM, BT);
+      for (int i = first; i < tiles; i += step) {
+        if (!wait(acc_empty(buf), acc_parity)) break;
+        fence_after();
+        for (int k = 0; k < blocks; ++k) {
+          if (!wait(full(s), parity)) break;
+          fence_after();
+          const uint32_t w = desc_k(base + s * C::kStage), x = desc_k(base + s * C::kStage + kW);
+#pragma unroll
+          for (int j = 0; j < kK / 16; ++j) mma_ss_pair(tmem + buf * BT, w + 2 * j, x + 2 * j, kDescHi, id, k > 0 || j > 0);
+          mma_commit_pair(empty(s));
+          if (++s == kStages) s = 0, parity ^= 1;
+        }
+        mma_commit_pair(acc_full(buf));
+        buf ^= 1;
+        if (!buf) acc_parity ^= 1;
+        if (s_abort) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    int buf = 0;
+    uint32_t acc_parity = 0;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    for (int i = first; i < tiles; i += step) {
+      int f, t;
+      tile_at(i, f, t);
+      if (i == first) prefetch_residual(a, (2 * f + rank) * kM, t * BT, min(BT, a.T - t * BT), tid - 128);
+      if (i + step < tiles) {
+        int nf, nt;
+        tile_at(i + step, nf, nt);
+        prefetch_residual(a, (2 * nf + rank) * kM, nt * BT, min(BT, a.T - nt * BT), tid - 128);
+      }
+      finish_tile<BT, 16>(a, tmem + lanes + buf * BT, (2 * f + rank) * kM + (tid & 127), t * BT, min(BT, a.T - t * BT), (tid >> 7) - 1,
+                          [&] {
+                            wait(acc_full(buf), acc_parity);
+                            __syncwarp();
+                            fence_after();
+                          });
+      fence_before();
+      __syncwarp();
+      if ((tid & 31) == 0) bar_arrive_remote(remote(acc_empty(buf), 0));
+      buf ^= 1;
+      if (!buf) acc_parity ^= 1;
+    }
+  }
+  if (s_abort) {  // copies and products may be in flight still
+    const long long t0 = clock64();
+    while (clock64() - t0 < kWaitCycles / 8) {
+    }
+  }
+  __syncwarp();
+  fence_before();
+  cluster_arrive();
+  cluster_wait();  // the other CTA reads no tile of this one any more, and signals no barrier
+  if (warp == 2) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kCols));
   }
 }
 
@@ -529,11 +742,61 @@ cudaError_t launch_tokens(const LinearArgs& a, int split, cudaStream_t s) {
   return launch_t<Cfg<BT, false>>(a, 1, s);
 }
 
-// The least of all tiles and divisions by what they cost.
+template <int BT>
+cudaError_t launch_pair(const LinearArgs& a, cudaStream_t s) {
+  using C = PairCfg<BT>;
+  static PerDevice opted;
+  cudaError_t err = cudaSuccess;
+  opted([&](int) {
+    err = cudaFuncSetAttribute(linear_pair_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return err == cudaSuccess ? 1 : 0;
+  });
+  if (err != cudaSuccess) return err;
+  CUtensorMap wm, xm;
+  if (!make_map(&wm, a.x_dtype, a.w, a.N, a.K, a.w_stride, kM) || !make_map(&xm, a.x_dtype, a.x, a.T, a.K, a.x_stride, BT / 2))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = (int64_t)((a.N + 2 * kM - 1) / (2 * kM)) * ((a.T + BT - 1) / BT);
+  note_launch();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, num_sms() / 2)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<C>, a, wm, xm);
+}
+
+// The least of all tiles and divisions by what they cost (bt, split; split 0: pairs of CTAs), in clocks: rounds of the tiles,
+// each a number of stages that wait for the products or for the copies into an SM, and the last epilogue.  The constants are
+// fits to measured times; with tiles and divisions forced, in us (bf16, bias):
+//                              64     64, 2 CTAs   128    128, 3 CTAs    256   pairs 128   pairs 256
+//    37 x  6144 x 4096       14.9         14.9    19.3           24.6      -           -           -
+//   100 x  5120 x 2048        9.0            -    11.6           12.4   16.4        11.1        15.3
+//  1021 x  7001 x 2048       33.2            -    26.8              -   29.8        24.7        27.2
+//  4096 x  2048 x 1024       23.0            -    19.7              -   19.0        20.1        17.7
+//  8192 x  5120 x 4096        325            -     235              -    228         207         187
 struct Choice {
   int bt, split;
   double cost;
 };
+double epilogue_cost(const LinearArgs& a, int bt) {  // of a tile
+  const double act = a.act == MOE_ACT_SILU ? 12 : a.act == MOE_ACT_GELU ? 35 : a.act == MOE_ACT_GELU_TANH ? 27 : 0;
+  return std::min(bt, a.T) * (20.0 + act + (a.residual ? 30.0 : 0.0));
+}
+template <int BT>
+void consider_pair(const LinearArgs& a, Choice& best) {
+  const int blocks = (a.K + kK - 1) / kK;
+  const int64_t tiles = (int64_t)((a.N + 2 * kM - 1) / (2 * kM)) * ((a.T + BT - 1) / BT);
+  const double rounds = std::ceil((double)tiles / (num_sms() / 2));
+  const double stage = std::max(2.0 * BT, PairCfg<BT>::kStage / 75.0);
+  const double cost = rounds * blocks * stage + epilogue_cost(a, BT) + 4500.0;
+  if (cost < best.cost) best = Choice{BT, 0, cost};
+}
 template <int BT>
 void consider(const LinearArgs& a, Choice& best) {
   const int blocks = (a.K + kK - 1) / kK, sms = num_sms();
@@ -546,7 +809,7 @@ void consider(const LinearArgs& a, Choice& best) {
     const int on_sm = (int)std::min<int64_t>(Cfg<BT, false>::kPerSm, (ctas + sms - 1) / sms);
     const double rounds = std::ceil((double)tiles / hold), per = (double)((blocks + split - 1) / split);
     const double stage = std::max({2.0 * BT * on_sm, bytes * on_sm / 60.0, bytes * ctas / 8000.0});
-    const double cost = rounds * per * stage + (split > 1 ? 2000.0 : 0.0) + (split > 1 ? 80.0 : 30.0) * std::min(BT, a.T);
+    const double cost = rounds * per * stage + epilogue_cost(a, BT) + (split > 1 ? 2000.0 + 60.0 * std::min(BT, a.T) : 0.0);
     if (cost < best.cost) best = Choice{BT, split, cost};
   }
 }
@@ -561,6 +824,9 @@ cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
   consider<64>(a, c);
   consider<128>(a, c);
   consider<256>(a, c);
+  consider_pair<128>(a, c);
+  consider_pair<256>(a, c);
+  if (c.split == 0) return c.bt == 128 ? launch_pair<128>(a, s) : launch_pair<256>(a, s);
   switch (c.bt) {
     case 16: return launch_tokens<16>(a, c.split, s);
     case 32: return launch_tokens<32>(a, c.split, s);
