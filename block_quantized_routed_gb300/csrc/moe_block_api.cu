@@ -388,7 +388,9 @@ int moe_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, 
   if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
   if ((r_dtype != x_dtype && r_dtype != MOE_DT_F32) || (o_dtype != x_dtype && o_dtype != MOE_DT_F32)) return MOE_ERR_UNSUPPORTED;
   if (act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH || K % 8) return MOE_ERR_UNSUPPORTED;
-  if (((int64_t)N / 128 + 1) * ((int64_t)T / 16 + 1) > 1 << 30) return MOE_ERR_UNSUPPORTED;  // (tiles are 32-bit numbers)
+  // tiles and rows are 32-bit numbers
+  if (((int64_t)N / 128 + 1) * ((int64_t)T / 16 + 1) > 1 << 30 || T > INT32_MAX - 1024 || N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
+    return MOE_ERR_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !w || !out) return MOE_ERR_INVALID_ARG;
   if (T > 1 && (x_stride < K || o_stride < N || (residual && r_stride < N))) return MOE_ERR_INVALID_ARG;

@@ -39,38 +39,42 @@ __device__ __forceinline__ uint4 load8(const uint16_t* p) {
   }
 }
 
-// A vector's scale from its largest magnitude (the bits of a 16-bit number), and its reciprocal.
+// A vector's scale from its largest magnitude, the bits of a 16-bit number.
 template <bool BF16, int FMT>
 __device__ __forceinline__ float scale_of(uint32_t peak) {
-  if (peak >= (BF16 ? 0x7f80u : 0x7c00u)) return __uint_as_float(0x7fc00000u);
-  if (peak == 0) return 0.0f;
-  return fmaxf(pair_f(peak, BF16).x / (FMT == MOE_DT_E4M3 ? 448.0f : 127.0f), 1.17549435e-38f);
+  const float d = fmaxf(pair_f(peak, BF16).x / (FMT == MOE_DT_E4M3 ? 448.0f : 127.0f), 1.17549435e-38f);
+  return peak >= (BF16 ? 0x7f80u : 0x7c00u) ? __uint_as_float(0x7fc00000u) : peak == 0 ? 0.0f : d;
 }
 // Codes of 8 elements x / d.  The quotient is rounded as IEEE division rounds it, by Markstein's theorem (IBM J. Res.
 // Dev. 34, 1990): with the correctly rounded reciprocal r and the exact remainder of q = x r, q + r (x - q d) in fused
 // operations.  The remainder is exact while it is a normal number or 0; tiny scales take the division itself.
 template <bool BF16, int FMT>
 __device__ __forceinline__ uint2 codes_of(uint4 x, float d) {
-  if (!(d > 0.0f)) return make_uint2(0, 0);  // zeros, or not finite
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-  const float r = __frcp_rn(d);
-  const bool tiny = d < 1e-28f;
+  float2 z[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = pair_f(w[i], BF16);
+  if (d >= 1e-28f) {
+    const float r = __frcp_rn(d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float q0 = z[i].x * r, q1 = z[i].y * r;
+      z[i].x = fmaf(fmaf(-q0, d, z[i].x), r, q0);
+      z[i].y = fmaf(fmaf(-q1, d, z[i].y), r, q1);
+    }
+  } else if (d > 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i].x /= d, z[i].y /= d;
+  } else {  // zeros, or not finite
+    return make_uint2(0, 0);
+  }
   uint32_t code[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    float2 z = pair_f(w[i], BF16);
-    if (tiny) {
-      z.x /= d;
-      z.y /= d;
-    } else {
-      const float q0 = z.x * r, q1 = z.y * r;
-      z.x = fmaf(fmaf(-q0, d, z.x), r, q0);
-      z.y = fmaf(fmaf(-q1, d, z.y), r, q1);
-    }
     if constexpr (FMT == MOE_DT_E4M3) {
-      code[i] = __nv_cvt_float2_to_fp8x2(z, __NV_SATFINITE, __NV_E4M3);
+      code[i] = __nv_cvt_float2_to_fp8x2(z[i], __NV_SATFINITE, __NV_E4M3);
     } else {
-      const int a = (int)roundf(z.x), b = (int)roundf(z.y);  // |z| < 127.5: the scale is off by half a step at most
+      const int a = (int)roundf(z[i].x), b = (int)roundf(z[i].y);  // |z| < 127.5: the scale is off by half a step at most
       code[i] = (uint32_t)(a & 0xff) | (uint32_t)(b & 0xff) << 8;
     }
   }

@@ -157,3 +157,45 @@ def test_results_repeat_on_streams_and_in_graphs():
 def test_no_tokens():
     out = torch.full((0, 64), 7.0, device="cuda")
     moe.moe_linear(torch.empty(0, 64, dtype=BF16, device="cuda"), torch.zeros(64, 64, dtype=BF16, device="cuda"), out)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows of out, residual and x that start beyond 2^32 bytes."""
+    T, N, K = 66000, 33000, 8
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, w = (torch.randn(n, K, generator=g, device="cuda").to(BF16) for n in (T, N))
+    out = torch.zeros(T, N, dtype=BF16, device="cuda")
+    out[-1] = 1.0
+    moe.moe_linear(x, w, out, residual=out)
+    for t in (0, T // 2, T - 300, T - 1):
+        y, tol = reference(x[t:t + 1], w, None, "none", torch.full((1, N), float(t == T - 1), device="cuda"), BF16)
+        assert ((out[t:t + 1].double() - y).abs() <= tol).all()
+    wide = torch.zeros(3, 1 << 31, dtype=BF16, device="cuda")
+    wide[:, :K] = x[:3]
+    small = torch.empty(3, 64, device="cuda")
+    moe.moe_linear(wide[:, :K], w[:64], small)
+    y, tol = reference(x[:3], w[:64], None, "none", None, F32)
+    assert ((small.double() - y).abs() <= tol).all()
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """What the host asks of the device once does not disturb a capture."""
+    code = """
+import torch
+import block_quantized_routed_gb300 as moe
+x, w = torch.ones(3, 512, device="cuda").bfloat16(), torch.ones(700, 512, device="cuda").bfloat16()
+big = torch.ones(900, 512, device="cuda").bfloat16()
+out, out2 = torch.zeros(3, 700, device="cuda"), torch.zeros(900, 700, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    moe.moe_linear(x, w, out)
+    moe.moe_linear(big, w, out2)
+g.replay()
+torch.cuda.synchronize()
+assert (out == 512).all() and (out2 == 512).all()
+"""
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr

@@ -24,7 +24,8 @@ def lib():
     (dict(act=-1), UNS), (dict(act=5), UNS), (dict(x=None), INV), (dict(w=None), INV), (dict(out=None), INV), (dict(x=OFF8), INV),
     (dict(w=OFF8), INV), (dict(xs=56), INV), (dict(xs=68), INV), (dict(wst=56), INV), (dict(wst=68), INV), (dict(os=31), INV),
     (dict(r=FAKE, rt=1, rs=31), INV), (dict(b=ODD), INV), (dict(out=ODD), INV), (dict(r=ODD, rt=1, rs=32), INV), (dict(st=ODD), INV),
-    (dict(wst=1 << 40), INV), (dict(T=1 << 30, N=1 << 20, os=1 << 20), UNS)])
+    (dict(wst=1 << 40), INV), (dict(T=1 << 30, N=1 << 20, os=1 << 20), UNS), (dict(T=2 ** 31 - 8, N=1, os=8), UNS),
+    (dict(K=2 ** 31 - 8, xs=2 ** 31, wst=2 ** 31), UNS)])
 def test_refusals(lib, kw, want):
     a = dict(x=FAKE, xt=1, xs=64, w=FAKE, wst=64, b=None, act=0, r=None, rt=0, rs=0, out=FAKE, ot=1, os=32, T=2, N=32, K=64, st=None)
     a.update(kw)
