@@ -34,6 +34,13 @@
 // end to end.  An item of several CTAs leaves partial sums in the workspace, and
 // the CTA that arrives last joins them in the order of the keys, so results do
 // not depend on timing and no CTA waits for another.
+//
+// What it measured (e4m3): four tokens over up to 131072 keys each (64 heads over
+// 8 of 128) 103 to 113 us, 5.1 to 5.6 TB/s; 48 over up to 8192 keys (32 over 4 of
+// 128) 49 us, 4.6 TB/s: tile by tile about 7, besides 5 us to the first and 4 from
+// the last; one over 777 keys 12 us, latency: half of 6 us on the device is the
+// way to the first tile, through cu_q, the page table and instructions that are
+// fetched for the first time.
 #include <algorithm>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -213,7 +220,8 @@ __device__ __forceinline__ float lse_of(float m, float sum) {
 }
 
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const AttnQ8Args ga, const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
+__global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const AttnQ8Args ga, const __grid_constant__ CUtensorMap km,
+                                                                        const __grid_constant__ CUtensorMap vm) {
   using C = Cfg<D, NT>;
   constexpr int W = C::W, kRows = C::kRows, kThreads = 32 * W, kStages = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, c = lane & 3;
   const int G = ga.G;
-  uint2* const s_q = reinterpret_cast<uint2*>(smem + C::kSmemMisc);                   // [NT][D / 16][lane] operand registers
+  uint2* const s_q = reinterpret_cast<uint2*>(smem + C::kSmemMisc);               // [NT][D / 16][lane] operand registers
   float* const s_f = reinterpret_cast<float*>(s_q + kRows * D / 4);               // [row] factor of the scores
   int* const s_lo = reinterpret_cast<int*>(s_f + kRows);                          // [row] keys that it sees
   int* const s_hi = s_lo + kRows;
@@ -399,7 +407,8 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     constexpr int kWide = D == 64 ? 16 : 32, kRowsOfPass = 32 / kWide, kWords = (D + 127) / 128;
     constexpr int kPasses = kRows / (W * kRowsOfPass) > 0 ? kRows / (W * kRowsOfPass) : 1;
     const int my_tok = quotient(r0 + min(lane, nr - 1), G);
-    const int64_t my_row = (int64_t)(w.s.q0 + my_tok) * a.q_stride + (int64_t)(h * G + r0 + min(lane, nr - 1) - my_tok * G) * a.q_head_stride;
+    const int64_t my_row = (int64_t)(w.s.q0 + my_tok) * a.q_stride +
+                           (int64_t)(h * G + r0 + min(lane, nr - 1) - my_tok * G) * a.q_head_stride;
     const auto row_of = [&](int y) { return (y * W + warp) * kRowsOfPass + lane / kWide; };
     uint2 qw[kPasses][kWords];
 #pragma unroll
@@ -935,10 +944,10 @@ cudaError_t launch_t(const AttnQ8Args& a, cudaStream_t s) {
 }
 template <int D, int FMT>
 cudaError_t launch_rows(const AttnQ8Args& g, cudaStream_t s) {
-  // Rows of an item: those of a sequence of the mean number of new tokens, and a third more, since the lengths of
-  // verify windows differ and a window that does not fit reads its keys twice.
-  const int64_t mean = (g.a.T + (int64_t)g.a.kv.n_seqs - 1) / g.a.kv.n_seqs, rows = g.a.Hq / g.a.kv.Hkv * mean;
-  const int64_t want = mean > 1 ? rows + rows / 3 : rows;
+  // Rows of an item: those of a sequence of the mean number of new tokens.  A longer one has several items and reads its
+  // keys as often, a shorter one leaves rows empty.  16 windows of up to 4 tokens, 5 heads to a key/value head of 64, whose
+  // mean are 15 rows: 16.1 us with 16 rows, 18.1 with 32; 2 tokens of 8 heads of 128 over 65536 keys: 55 and 73 us.
+  const int64_t mean = (g.a.T + (int64_t)g.a.kv.n_seqs - 1) / g.a.kv.n_seqs, want = g.a.Hq / g.a.kv.Hkv * mean;
   if (want <= 8) return launch_t<D, 1, FMT>(g, s);
   if (D == 256 || want <= 16) return launch_t<D, 2, FMT>(g, s);
   return launch_t<D, D == 256 ? 2 : 4, FMT>(g, s);

@@ -9,8 +9,13 @@
 // group of lanes (keys and values together, a half of a register each), and all
 // of a warp's loads are under way before the token's page is looked up.  Reading
 // back takes 16 codes to a lane, as many lanes to a row as it has of them, up to
-// a warp.  (A warp for all 8 heads of 128 of a token: 12.3 us for 5257 tokens;
-// four rows of a warp read back together: 83 against 72 us for 99328 rows of the same.)
+// a warp.
+//
+// What it measured: 5257 tokens of 8 heads of 128 (bf16 to e4m3) appended in 10.4
+// us, 3.1 TB/s, two rounds of CTAs whose warps wait for their loads and then
+// divide (a warp for all 8 heads of a token: 12.3 us); 64 tokens of 4 heads 2.6.
+// Up to 32768 keys of each of three sequences, 8 heads of 128, e4m3 to bf16, read
+// back in 72 us, 5.8 TB/s (four rows of a warp at a time: 83 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

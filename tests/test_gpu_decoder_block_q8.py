@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import block_quantized_routed_gb300 as moe
+from block_quantized_routed_gb300.block import READ_FROM
 from tests import block_ref
 from tests.q8_ref import E4M3, INT8, Q8Cache, attention, code_values, quantise
 from tests.test_gpu_decoder_block import D, H, HKV, HQ, PAGE, lay, make
@@ -54,7 +55,7 @@ def test_stage_by_stage(fmt, q_lens, kv_lens, read_rows):
             assert torch.equal(c.sequence(b, name)[kv - n:], want)
         at += n
     got = blk.attn[:T].view(T, HQ, D).cpu().double()
-    if read_rows and T > 16 * len(q_lens):     # over the cache read back to bf16: one more rounding of keys and values
+    if read_rows and T > READ_FROM * len(q_lens):     # over the cache read back to bf16: one more rounding of keys and values
         rows = [(c.sequence(b, "k").bfloat16(), c.sequence(b, "v").bfloat16()) for b in range(len(q_lens))]
         pages, table, _, _ = lay(q_lens, kv_lens)
         kc, vc = (torch.zeros(pages, PAGE, HKV, D, dtype=torch.bfloat16) for _ in range(2))
