@@ -83,7 +83,12 @@ __device__ __forceinline__ uint2 codes_of(uint4 x, float d) {
       code[i] = (uint32_t)(a & 0xff) | (uint32_t)(b & 0xff) << 8;
     }
   }
-  return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+  uint2 c = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+  if constexpr (FMT == MOE_DT_E4M3) {  // the sign of a zero, which the corrected quotient has lost
+    c.x |= __byte_perm(w[0], w[1], 0x7531) & 0x80808080u;
+    c.y |= __byte_perm(w[2], w[3], 0x7531) & 0x80808080u;
+  }
+  return c;
 }
 __device__ __forceinline__ uint32_t peak_of(uint4 x) {  // in two halves; magnitudes of 16-bit numbers order as integers
   return __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));

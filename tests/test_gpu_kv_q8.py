@@ -100,6 +100,15 @@ def test_append_values_at_the_limits(fmt, dtype):
         assert torch.isnan(c.gks[page, t, 0]) and not raw(c.gkc)[page, t].any()
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_append_negative_zeros_and_what_rounds_to_them(fmt, dtype):
+    x = torch.randn(16, 2, 64, generator=torch.Generator().manual_seed(6))
+    x[:, :, ::3] = -0.0
+    x[:, :, 1::3] *= -1e-6
+    check_append(Q8Cache([16], 2, 64, 16, fmt), [16], x.to(dtype), x.flip(0).to(dtype))
+
+
 def test_append_bad_pages_lengths_and_rows():
     """Each is skipped and told; the others are written."""
     for what in ("page", "negative page", "length", "order", "none"):
