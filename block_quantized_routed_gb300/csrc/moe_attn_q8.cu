@@ -50,6 +50,7 @@
 #include <cuda_fp16.h>
 
 #include "moe_kv.cuh"
+#include "moe_overlap.cuh"
 #include "moe_per_device.h"
 #include "moe_q8.cuh"
 
@@ -249,6 +250,8 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   if (tid == 0) sh.abort = 0;
+  let_next_start();
+  wait_for_previous();
 
   // ---- the CTA's share of the work: parts of `size` key tiles, or (size 0) the units from u to u1 of `total` on `ctas` CTAs
   int size = 0, total = 0, ctas = gridDim.x, u = 0, u1 = 1;
@@ -939,8 +942,7 @@ cudaError_t launch_t(const AttnQ8Args& a, cudaStream_t s) {
       !make_map(&vm, kv, a.a.v_cache, kv.v_row_stride, kv.v_head_stride, kv.v_page_stride, rows))
     return cudaErrorInvalidValue;
   note_launch();
-  kern<<<std::min(2 * num_sms(), kMaxCtas), 32 * C::W, C::kSmem, s>>>(a, km, vm);
-  return cudaGetLastError();
+  return launch_overlapping(kern, dim3((unsigned)std::min(2 * num_sms(), kMaxCtas)), 32 * C::W, C::kSmem, 1, s, a, km, vm);
 }
 template <int D, int FMT>
 cudaError_t launch_rows(const AttnQ8Args& g, cudaStream_t s) {

@@ -21,6 +21,7 @@
 #include <cuda_fp8.h>
 
 #include "moe_kv.cuh"
+#include "moe_overlap.cuh"
 #include "moe_q8.cuh"
 
 namespace moe {
@@ -108,6 +109,8 @@ __device__ __forceinline__ void store_codes(uint8_t* p, uint2 c) {
 template <bool BF16, int FMT, bool WIDE, int kBatch>
 __global__ void __launch_bounds__(128) append_kernel(const KvAppendQ8Args g) {
   const KvAppendArgs& a = g.a;
+  let_next_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (t >= a.T) return;
@@ -221,6 +224,8 @@ __device__ __forceinline__ void load_codes(const uint8_t* p, uint32_t* w) {
 template <int FMT, int OUT, bool WIDE>
 __global__ void __launch_bounds__(128) read_kernel(const KvReadQ8Args a, int shift) {
   constexpr int N = WIDE ? 16 : 8;
+  let_next_start();
+  wait_for_previous();
   if (blockIdx.x == 0) {  // every sequence's rows: in range, and before the next one's
     for (int b = threadIdx.x; b < a.kv.n_seqs; b += blockDim.x) {
       const int64_t len = __ldg(a.kv_len + b), at = __ldg(a.first + b);
@@ -264,35 +269,32 @@ __global__ void __launch_bounds__(128) read_kernel(const KvReadQ8Args a, int shi
 }
 
 template <bool BF16, int FMT, int kBatch>
-void append_as(const KvAppendQ8Args& a, int warps, cudaStream_t s) {
+cudaError_t append_as(const KvAppendQ8Args& a, int warps, cudaStream_t s) {
   int width = 1;  // lanes of a head
   while (width < a.a.kv.D / 8) width *= 2;
   const int heads = kBatch * (32 / width);  // of a warp
   const dim3 grid((unsigned)((a.a.T + warps - 1) / warps), (unsigned)((a.a.kv.Hkv + heads - 1) / heads));
-  if (a.a.wide) append_kernel<BF16, FMT, true, kBatch><<<grid, 32 * warps, 0, s>>>(a);
-  else append_kernel<BF16, FMT, false, kBatch><<<grid, 32 * warps, 0, s>>>(a);
+  return launch_overlapping(a.a.wide ? append_kernel<BF16, FMT, true, kBatch> : append_kernel<BF16, FMT, false, kBatch>, grid,
+                            32 * warps, 0, 1, s, a);
 }
 template <bool BF16, int FMT>
-void append(const KvAppendQ8Args& a, cudaStream_t s) {
+cudaError_t append(const KvAppendQ8Args& a, cudaStream_t s) {
   // Few tokens are latency: a warp to each token and as few heads as it holds (64 tokens of 4 heads of 128: 2.8 us, with
   // two loads of a lane 3.4).  Many share the way to their page among two (5257 tokens of 8 heads: 10.8 us, with one 11.8).
-  if (a.a.T <= 4 * num_sms()) append_as<BF16, FMT, 1>(a, 1, s);
-  else append_as<BF16, FMT, 2>(a, 4, s);
+  return a.a.T <= 4 * num_sms() ? append_as<BF16, FMT, 1>(a, 1, s) : append_as<BF16, FMT, 2>(a, 4, s);
 }
 template <int FMT, int OUT>
-void read(const KvReadQ8Args& a, cudaStream_t s) {
+cudaError_t read(const KvReadQ8Args& a, cudaStream_t s) {
   const int pieces = a.kv.Hkv * a.kv.D / (a.wide ? 16 : 8);
   int shift = 0;
   while (shift < 5 && 1 << shift < pieces) ++shift;
   const unsigned grid = (unsigned)((((int64_t)a.rows << shift) + 127) / 128);
-  if (a.wide) read_kernel<FMT, OUT, true><<<grid, 128, 0, s>>>(a, shift);
-  else read_kernel<FMT, OUT, false><<<grid, 128, 0, s>>>(a, shift);
+  return launch_overlapping(a.wide ? read_kernel<FMT, OUT, true> : read_kernel<FMT, OUT, false>, dim3(grid), 128, 0, 1, s, a, shift);
 }
 template <int FMT>
-void read_as(const KvReadQ8Args& a, cudaStream_t s) {
-  if (a.out_dtype == MOE_DT_F32) read<FMT, MOE_DT_F32>(a, s);
-  else if (a.out_dtype == MOE_DT_BF16) read<FMT, MOE_DT_BF16>(a, s);
-  else read<FMT, MOE_DT_F16>(a, s);
+cudaError_t read_as(const KvReadQ8Args& a, cudaStream_t s) {
+  if (a.out_dtype == MOE_DT_F32) return read<FMT, MOE_DT_F32>(a, s);
+  return a.out_dtype == MOE_DT_BF16 ? read<FMT, MOE_DT_BF16>(a, s) : read<FMT, MOE_DT_F16>(a, s);
 }
 
 }  // namespace
@@ -301,17 +303,14 @@ cudaError_t launch_kv_append_q8(const KvAppendQ8Args& a, cudaStream_t s) {
   if (a.a.T == 0) return cudaSuccess;
   const bool bf16 = a.x_dtype == MOE_DT_BF16, e4m3 = a.a.kv.dtype == MOE_DT_E4M3;
   note_launch();
-  if (bf16) e4m3 ? append<true, MOE_DT_E4M3>(a, s) : append<true, MOE_DT_INT8>(a, s);
-  else e4m3 ? append<false, MOE_DT_E4M3>(a, s) : append<false, MOE_DT_INT8>(a, s);
-  return cudaGetLastError();
+  if (bf16) return e4m3 ? append<true, MOE_DT_E4M3>(a, s) : append<true, MOE_DT_INT8>(a, s);
+  return e4m3 ? append<false, MOE_DT_E4M3>(a, s) : append<false, MOE_DT_INT8>(a, s);
 }
 
 cudaError_t launch_kv_read_q8(const KvReadQ8Args& a, cudaStream_t s) {
   if (a.rows == 0) return cudaSuccess;
   note_launch();
-  if (a.kv.dtype == MOE_DT_E4M3) read_as<MOE_DT_E4M3>(a, s);
-  else read_as<MOE_DT_INT8>(a, s);
-  return cudaGetLastError();
+  return a.kv.dtype == MOE_DT_E4M3 ? read_as<MOE_DT_E4M3>(a, s) : read_as<MOE_DT_INT8>(a, s);
 }
 
 }  // namespace moe

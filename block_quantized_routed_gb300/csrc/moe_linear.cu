@@ -39,6 +39,7 @@
 
 #include "moe_device.cuh"
 #include "moe_internal.h"
+#include "moe_overlap.cuh"
 #include "moe_per_device.h"
 
 namespace moe {
@@ -359,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     int f, t;
     tile_at(first, f, t);
+    wait_for_previous();
     for (int s = 0; s < ahead; ++s) copy(s, k0 + s, f, t);
   }
   if (tid == 32) {
@@ -372,9 +374,11 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  wait_for_previous();
   fence_before();
   __syncthreads();
   fence_after();
+  let_next_start();  // (this CTA has its tensor memory: one of the next kernel can no longer take it and wait for this one)
   if (C::kSplit) cluster_arrive();  // this CTA runs: others may write to it once they have waited
   const uint32_t tmem = s_tmem;
   const Wait wait{&s_abort, a.status};
@@ -560,10 +564,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const LinearAr
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
   }
   __syncwarp();
+  wait_for_previous();
   fence_before();
   cluster_arrive();
   cluster_wait();  // both CTAs' barriers and tensor memory are there
   fence_after();
+  let_next_start();
   const uint32_t tmem = s_tmem;
   const Wait wait{&s_abort, a.status};
   const auto tile_at = [&](int i, int& f, int& t) { tile_of<8>(i, f_tiles, t_tiles, f, t); };
@@ -692,20 +698,6 @@ cudaError_t opt_in() {
   });
   return err;
 }
-template <class C>
-cudaLaunchConfig_t config(cudaLaunchAttribute* attr, int split, int64_t grid, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  attr->id = cudaLaunchAttributeClusterDimension;
-  attr->val.clusterDim.x = (unsigned)split;
-  attr->val.clusterDim.y = attr->val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = split > 1 ? 1 : 0;
-  return cfg;
-}
 // Tiles of `split` CTAs each that the device holds at one time: clusters stay within a group of SMs, so they leave some idle.
 template <int BT>
 int room(int split) {
@@ -714,8 +706,16 @@ int room(int split) {
     using C = Cfg<BT, true>;
     static PerDevice kept[9];
     return kept[split]([&](int) {
-      cudaLaunchAttribute attr;
-      const cudaLaunchConfig_t cfg = config<C>(&attr, split, split, nullptr);
+      cudaLaunchAttribute attr{};
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = (unsigned)split;
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg{};
+      cfg.gridDim = dim3((unsigned)split);
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = C::kSmem;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
       int n = 0;
       if (opt_in<C>() != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, linear_kernel<C>, &cfg) != cudaSuccess) {
         cudaGetLastError();
@@ -736,11 +736,9 @@ cudaError_t launch_t(LinearArgs a, int split, cudaStream_t s) {
     return cudaErrorInvalidValue;
   a.split = split;
   const int64_t tiles = (int64_t)((a.N + kM - 1) / kM) * ((a.T + C::BT - 1) / C::BT);
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg =
-      config<C>(&attr, split, C::kSplit ? tiles * split : std::min<int64_t>(tiles, (int64_t)C::kPerSm * num_sms()), s);
+  const int64_t grid = C::kSplit ? tiles * split : std::min<int64_t>(tiles, (int64_t)C::kPerSm * num_sms());
   note_launch();
-  return cudaLaunchKernelEx(&cfg, linear_kernel<C>, a, wm, xm);
+  return launch_overlapping(linear_kernel<C>, dim3((unsigned)grid), kThreads, C::kSmem, split, s, a, wm, xm);
 }
 template <int BT>
 cudaError_t launch_tokens(const LinearArgs& a, int split, cudaStream_t s) {
@@ -765,18 +763,8 @@ cudaError_t launch_pair(const LinearArgs& a, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)((a.N + 2 * kM - 1) / (2 * kM)) * ((a.T + BT - 1) / BT);
   note_launch();
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, num_sms() / 2)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 2;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_pair_kernel<C>, a, wm, xm);
+  return launch_overlapping(linear_pair_kernel<C>, dim3((unsigned)(2 * std::min<int64_t>(tiles, num_sms() / 2))), kThreads, C::kSmem, 2,
+                            s, a, wm, xm);
 }
 
 // The least of all tiles and divisions by what they cost (bt, split; split 0: pairs of CTAs), in clocks: rounds of the tiles,
