@@ -37,8 +37,8 @@
 //
 // What it measured (e4m3): four tokens over up to 131072 keys each (64 heads over
 // 8 of 128) 103 to 113 us, 5.1 to 5.6 TB/s; 48 over up to 8192 keys (32 over 4 of
-// 128) 49 us, 4.6 TB/s: tile by tile about 7, besides 5 us to the first and 4 from
-// the last; one over 777 keys 12 us, latency: half of 6 us on the device is the
+// 128) 48 us, 4.7 TB/s: tile by tile about 7, besides 5 us to the first and 4 from
+// the last; one over 777 keys 11.6 us, latency: half of 6 us on the device is the
 // way to the first tile, through cu_q, the page table and instructions that are
 // fetched for the first time.
 #include <algorithm>

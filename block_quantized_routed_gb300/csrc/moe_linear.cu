@@ -18,11 +18,11 @@
 // the accumulators are joined through distributed shared memory: each CTA sums
 // a slice of the features, in the order of the ranks, and runs their epilogue.
 //
-// What it measured (bf16 but for the third): one token of 5120 x 2048 8.1 us, 37 of
-// 6144 x 4096 onto an fp32 residual 15 us: 3 us to the first data, 7 for the
+// What it measured (bf16 but for the third): one token of 5120 x 2048 7.1 us, 37 of
+// 6144 x 4096 onto an fp32 residual 14 us: 3 us to the first data, 7 for the
 // weights, 3 for the join and the way out; 1021 of 7001 x 2048 with gelu (fp16)
-// 28 us, three rounds of tiles; 8192 of 5120 x 4096 with silu and a residual 198
-// us, 1735 TFLOP/s, the tensor pipe 90% active.  One token of 32768 x 4096: 42 us,
+// 27 us, three rounds of tiles; 8192 of 5120 x 4096 with silu and a residual 195
+// us, 1765 TFLOP/s, the tensor pipe 90% active.  One token of 32768 x 4096: 42 us,
 // 6.4 TB/s.
 //
 // Every wait is bounded: after about a second a role records
