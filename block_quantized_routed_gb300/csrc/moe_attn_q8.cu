@@ -212,10 +212,16 @@ __device__ __forceinline__ void fma4(float4& acc, float f, float4 v) {
   acc.z = fmaf(f, v.z, acc.z);
   acc.w = fmaf(f, v.w, acc.w);
 }
-// what a row's accumulator is multiplied by, and its lse
-__device__ __forceinline__ float out_factor(float m, float mv, float sum) {
-  return sum == 0.0f ? 0.0f : ex2(mv - m - kLift) / sum;
+// What a row's accumulator is multiplied by, one after the other: 2^(mv - m - kLift) / sum in two halves, because the
+// power alone is no fp32 number where all scales are small (2^-126 is the least) though the product is one.
+__device__ __forceinline__ void out_factors(float m, float mv, float sum, float& first, float& second) {
+  first = ex2((mv - m - kLift) * 0.5f);
+  second = sum == 0.0f ? 0.0f : first / sum;
 }
+__device__ __forceinline__ float4 times(float4 v, float first, float second) {
+  return make_float4(v.x * first * second, v.y * first * second, v.z * first * second, v.w * first * second);
+}
+// a row's lse
 __device__ __forceinline__ float lse_of(float m, float sum) {
   return sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945309f;
 }
@@ -233,7 +239,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
   const int g = lane >> 2, c = lane & 3;
   const int G = ga.G;
   uint2* const s_q = reinterpret_cast<uint2*>(smem + C::kSmemMisc);               // [NT][D / 16][lane] operand registers
-  float* const s_f = reinterpret_cast<float*>(s_q + kRows * D / 4);               // [row] factor of the scores
+  float* const s_f = reinterpret_cast<float*>(s_q + kRows * D / 4);               // [row] factor of the scores; in a join, s_rf's second
   int* const s_lo = reinterpret_cast<int*>(s_f + kRows);                          // [row] keys that it sees
   int* const s_hi = s_lo + kRows;
   float* const s_rf = reinterpret_cast<float*>(s_hi + kRows);                     // [row] factor of its output
@@ -751,7 +757,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
         s_mv[x * kRows + tid] = ex2(s_mv[x * kRows + tid] - mmv);
       }
       if (parts == 1) {
-        s_rf[tid] = out_factor(mm, mmv, sum);
+        out_factors(mm, mmv, sum, s_rf[tid], s_f[tid]);
         put_lse(tid, mm, sum);
       } else {
         __stcg(part + kPartMax + tid, mm);
@@ -767,8 +773,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
       for (int x = 0; x < W; ++x)
         fma4(v, s_mv[x * kRows + r], *reinterpret_cast<const float4*>(acc + (x * kRows + r) * C::kPitch + col * 4));
       if (parts == 1) {
-        const float rf = s_rf[r];
-        put(ga, row_at(r) + col * 4, make_float4(v.x * rf, v.y * rf, v.z * rf, v.w * rf));
+        put(ga, row_at(r) + col * 4, times(v, s_rf[r], s_f[r]));
       } else {
         __stcg(reinterpret_cast<float4*>(part) + e, v);
       }
@@ -833,7 +838,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
 #pragma unroll
       for (int y = 0; y < kHeld; ++y)
         if (y * W + warp < nr) {
-          s_rf[y * W + warp] = out_factor(mm[y], mmv[y], sum[y]);
+          out_factors(mm[y], mmv[y], sum[y], s_rf[y * W + warp], s_f[y * W + warp]);
           put_lse(y * W + warp, mm[y], sum[y]);
         }
     }
@@ -845,8 +850,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
     const auto load = [&](int p, int e) { return __ldcg(reinterpret_cast<const float4*>(part_of(p)) + e); };
     const auto finish = [&](int e, float4 v) {
       const int r = e / (D / 4), col = e - r * (D / 4);
-      const float rf = s_rf[r];
-      put(ga, row_at(r) + col * 4, make_float4(v.x * rf, v.y * rf, v.z * rf, v.w * rf));
+      put(ga, row_at(r) + col * 4, times(v, s_rf[r], s_f[r]));
     };
     constexpr int kAhead = 8;  // parts that are asked for together
     if (n <= width) {
