@@ -544,6 +544,7 @@ __global__ void __launch_bounds__(32 * Cfg<D, NT>::W, 2) attn_q8_kernel(const At
             set_status(a.status, MOE_ERR_DEVICE_TIMEOUT);
           }
       }
+      __syncwarp();  // the scales that other lanes asked for are there too (a vote orders no memory)
       if (__any_sync(kAll, sh.abort)) break;  // given up: what this call computes is void
       if (++got == kStages) got = 0, parity ^= 1;
       const int key = (first + i) * C::kTile + warp * 16;
