@@ -1,6 +1,7 @@
 // C ABI of the decoder-block operators around the experts: argument
 // validation and dispatch.  As in the layer's entry points, everything is
 // checked on the host before a launch.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -54,6 +55,26 @@ int scales_check(const moe_kv_scales* sc) {
 bool code_strides(const moe_kv_desc& kv, int n) {
   return kv.k_page_stride % n == 0 && kv.k_row_stride % n == 0 && kv.k_head_stride % n == 0 &&
          kv.v_page_stride % n == 0 && kv.v_row_stride % n == 0 && kv.v_head_stride % n == 0;
+}
+// An array of n rows of `bytes` bytes, `stride` bytes apart.
+struct Rows {
+  const void* p;
+  int64_t n, bytes, stride;
+};
+// Whether two arrays share a byte.  Rows that lie among one another are told apart where the strides are the same, or one
+// array has a single row; others whose spans overlap count as shared.
+bool share(const Rows& a, const Rows& b) {
+  using Wide = __int128;
+  if (!a.p || !b.p || a.n < 1 || b.n < 1) return false;
+  const Wide at = (Wide)reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p);  // b's first row from a's
+  if (at >= (Wide)(a.n - 1) * a.stride + a.bytes || -at >= (Wide)(b.n - 1) * b.stride + b.bytes) return false;
+  if (a.n > 1 && b.n > 1 && a.stride != b.stride) return true;
+  const Wide s = a.n > 1 ? a.stride : b.stride;
+  if ((a.n == 1 && b.n == 1) || s == 0) return true;
+  // row j of b from row i of a: at + (j - i) s, between -b.bytes and a.bytes where they meet
+  const auto down = [s](Wide x) { return x >= 0 ? x / s : -((-x + s - 1) / s); };
+  const Wide least = down(-b.bytes - at) + 1, most = down(a.bytes - 1 - at);  // of j - i
+  return std::max<Wide>(least, 1 - a.n) <= std::min<Wide>(most, b.n - 1);
 }
 bool kv_strides16(const moe_kv_desc& kv) {
   return kv.k_page_stride % 8 == 0 && kv.k_row_stride % 8 == 0 && kv.k_head_stride % 8 == 0 &&
@@ -400,6 +421,15 @@ int moe_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, 
   if (x_stride % 8 || w_stride % 8 || x_stride >= (int64_t)1 << 39 || w_stride >= (int64_t)1 << 39) return MOE_ERR_INVALID_ARG;
   if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(bias, 4) || !aligned_to(residual, dtype_size(r_dtype)) ||
       !aligned_to(out, dtype_size(o_dtype)) || !aligned_to(status, 4))
+    return MOE_ERR_INVALID_ARG;
+  // tiles are written while others are read; a residual's element is read by the thread that writes its place
+  const auto rows = [](const void* p, int64_t n, int64_t cols, int64_t stride, int size) {
+    return Rows{p, n, cols * size, stride * size};
+  };
+  const Rows to = rows(out, T, N, o_stride, dtype_size(o_dtype));
+  const bool in_place = residual == out && r_dtype == o_dtype && r_stride == o_stride;
+  if (share(to, rows(x, T, K, x_stride, 2)) || share(to, rows(w, N, K, w_stride, 2)) || share(to, rows(bias, 1, N, 0, 4)) ||
+      (!in_place && share(to, rows(residual, T, N, r_stride, dtype_size(r_dtype)))) || share(to, rows(status, 1, 1, 0, 4)))
     return MOE_ERR_INVALID_ARG;
   LinearArgs a{};
   a.x = x;

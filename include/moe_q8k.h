@@ -686,7 +686,9 @@ typedef enum {
  * everything after them fp32), bias float [N] or NULL, residual [T, N] of
  * r_dtype (x's type or F32) or NULL, out [T, N] of o_dtype (x's type or F32),
  * rounded once.  Row strides are in elements; residual and out may be the same
- * array (with the same type and stride).  x and w lie on 16-byte boundaries
+ * array (with the same type and stride), otherwise out shares no element with
+ * x, w, bias, residual or status (MOE_ERR_INVALID_ARG; columns of one array are
+ * told apart where the rows have one stride).  x and w lie on 16-byte boundaries
  * (pointers, strides, and K a multiple of 8); residual and out on their
  * elements'.  T >= 0, N and K at least 1, (N / 128) * (T / 16) below 2^30.
  * status: NULL, or an int in device memory, zero before the first call, that
