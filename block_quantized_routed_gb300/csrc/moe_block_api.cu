@@ -253,9 +253,11 @@ int moe_kv_read_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, const voi
   if (why != MOE_OK) return why;
   if (!dtype_ok(out_dtype)) return MOE_ERR_UNSUPPORTED;
   if (n_rows < 0 || k_stride < 0 || k_head_stride < 0 || v_stride < 0 || v_head_stride < 0) return MOE_ERR_INVALID_ARG;
-  if (n_rows == 0) return MOE_OK;
-  if (!k_cache || !v_cache || !page_table || !kv_len || !first || !k_out || !v_out || !ws) return MOE_ERR_INVALID_ARG;
-  if (scales_check(scales) != MOE_OK) return MOE_ERR_INVALID_ARG;
+  // without rows the lengths alone are looked at: no key has a place
+  if (n_rows == 0 && (!kv_len || !first || !ws)) return MOE_OK;
+  if (!kv_len || !first || !ws) return MOE_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!k_cache || !v_cache || !page_table || !k_out || !v_out || scales_check(scales) != MOE_OK))
+    return MOE_ERR_INVALID_ARG;
   if (ws_bytes < 16) return MOE_ERR_WORKSPACE;
   const int es = dtype_size(out_dtype);
   if (!aligned_to(page_table, 4) || !aligned_to(kv_len, 4) || !aligned_to(first, 4) || !aligned_to(ws, 16) ||
@@ -268,10 +270,10 @@ int moe_kv_read_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, const voi
     const double heads = (kv->Hkv - 1.0) * head + kv->D, all = (n_rows - 1.0) * row + kv->D;
     return (kv->Hkv == 1 || head >= kv->D) && (n_rows == 1 || (row >= kv->D && (row >= heads || head >= all)));
   };
-  if (!apart(k_stride, k_head_stride) || !apart(v_stride, v_head_stride)) return MOE_ERR_INVALID_ARG;
+  if (n_rows > 0 && (!apart(k_stride, k_head_stride) || !apart(v_stride, v_head_stride))) return MOE_ERR_INVALID_ARG;
   KvReadQ8Args a{};
   a.kv = tidy(*kv);
-  a.sc = *scales;
+  if (scales) a.sc = *scales;
   a.k_cache = k_cache;
   a.v_cache = v_cache;
   a.table = page_table;
