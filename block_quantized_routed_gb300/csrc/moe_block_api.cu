@@ -56,6 +56,27 @@ bool code_strides(const moe_kv_desc& kv, int n) {
   return kv.k_page_stride % n == 0 && kv.k_row_stride % n == 0 && kv.k_head_stride % n == 0 &&
          kv.v_page_stride % n == 0 && kv.v_row_stride % n == 0 && kv.v_head_stride % n == 0;
 }
+struct Dim {
+  int64_t n, stride;
+};
+// Whether pieces of `piece` elements over some dimensions share none: by rising stride, each dimension's entries lie behind
+// all of the dimensions before it.
+template <int N>
+bool apart(Dim (&d)[N], int64_t piece) {
+  std::sort(d, d + N, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  __int128 span = piece;
+  for (const Dim& x : d) {
+    if (x.n <= 1) continue;
+    if (x.stride < span) return false;
+    span += (__int128)(x.n - 1) * x.stride;
+  }
+  return true;
+}
+// the entries of a cache that is written: (page, row, head)
+bool entries_apart(const moe_kv_desc& kv, int64_t page, int64_t row, int64_t head, int64_t piece) {
+  Dim d[3] = {{kv.num_pages, page}, {kv.page_size, row}, {kv.Hkv, head}};
+  return apart(d, piece);
+}
 // An array of n rows of `bytes` bytes, `stride` bytes apart.
 struct Rows {
   const void* p;
@@ -219,6 +240,12 @@ int moe_kv_append_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, int32_t
   if (!aligned_to(k, 2) || !aligned_to(v, 2) || !aligned_to(page_table, 4) || !aligned_to(cu_q, 4) ||
       !aligned_to(kv_len, 4) || !aligned_to(ws, 16))
     return MOE_ERR_INVALID_ARG;
+  // a code beside another entry's scale would be neither's (a cache that is only read may repeat entries)
+  if (!entries_apart(*kv, kv->k_page_stride, kv->k_row_stride, kv->k_head_stride, kv->D) ||
+      !entries_apart(*kv, kv->v_page_stride, kv->v_row_stride, kv->v_head_stride, kv->D) ||
+      !entries_apart(*kv, scales->k_page_stride, scales->k_row_stride, scales->k_head_stride, 1) ||
+      !entries_apart(*kv, scales->v_page_stride, scales->v_row_stride, scales->v_head_stride, 1))
+    return MOE_ERR_INVALID_ARG;
   KvAppendQ8Args g{};
   KvAppendArgs& a = g.a;
   a.kv = tidy(*kv);
@@ -266,11 +293,8 @@ int moe_kv_read_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, const voi
   if (kv->Hkv == 1) k_head_stride = v_head_stride = 0;
   if (n_rows == 1) k_stride = v_stride = 0;
   // rows that overlap would be written in no order
-  const auto apart = [&](int64_t row, int64_t head) {
-    const double heads = (kv->Hkv - 1.0) * head + kv->D, all = (n_rows - 1.0) * row + kv->D;
-    return (kv->Hkv == 1 || head >= kv->D) && (n_rows == 1 || (row >= kv->D && (row >= heads || head >= all)));
-  };
-  if (n_rows > 0 && (!apart(k_stride, k_head_stride) || !apart(v_stride, v_head_stride))) return MOE_ERR_INVALID_ARG;
+  Dim ko[2] = {{n_rows, k_stride}, {kv->Hkv, k_head_stride}}, vo[2] = {{n_rows, v_stride}, {kv->Hkv, v_head_stride}};
+  if (n_rows > 0 && (!apart(ko, kv->D) || !apart(vo, kv->D))) return MOE_ERR_INVALID_ARG;
   KvReadQ8Args a{};
   a.kv = tidy(*kv);
   if (scales) a.sc = *scales;
@@ -373,6 +397,8 @@ int moe_paged_attention_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, i
   const moe_kv_desc d = tidy(*kv);
   if (!code_strides(d, 8) || q_stride % 8 || q_head_stride % 8 || o_stride % 8 || o_head_stride % 8)
     return MOE_ERR_INVALID_ARG;
+  Dim o[2] = {{T, o_stride}, {Hq, o_head_stride}};
+  if (!apart(o, kv->D)) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < attn_q8_workspace(Hq, kv->Hkv, kv->D)) return MOE_ERR_WORKSPACE;
   AttnQ8Args g{};
   AttnArgs& a = g.a;

@@ -618,8 +618,10 @@ typedef struct {
  *   code = x / d              (IEEE fp32 division) rounded to nearest: e4m3 with
  *                              ties to even, int8 with ties away from zero
  * A vector of zeros has d = 0 and codes 0, one that holds a NaN or an infinity
- * d = NaN and codes 0.  Sequences, positions, pages, the status word and ws are
- * as in moe_kv_append. */
+ * d = NaN and codes 0.  Entries of the caches and of the scales that share memory
+ * (a stride of 0, say) are refused (MOE_ERR_INVALID_ARG); a cache that is only
+ * read may have them.  Sequences, positions, pages, the status word and ws are as
+ * in moe_kv_append. */
 int moe_kv_append_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, int32_t x_dtype, const void* k,
                      int64_t k_stride, int64_t k_head_stride, const void* v, int64_t v_stride, int64_t v_head_stride,
                      void* k_cache, void* v_cache, const int32_t* page_table, const int32_t* cu_q,
@@ -650,8 +652,9 @@ size_t moe_paged_attention_q8_workspace_size(int32_t Hq, int32_t Hkv, int32_t D)
  *   a_j = scale * d_j * (q . K_j),  out = sum_j exp(a_j) e_j V_j / sum_j exp(a_j)
  *   lse = log(sum_j exp(a_j))
  * Sequences, positions, windows, empty rows, q, out, lse and what is recorded in
- * the status word are as there; q and out are x_dtype (BF16 or F16).  Codes lie
- * on 8-byte boundaries (pointers and strides).  Scores, sums and accumulators are
+ * the status word are as there; q and out are x_dtype (BF16 or F16), and rows of
+ * out share no memory (MOE_ERR_INVALID_ARG).  Codes lie on 8-byte boundaries
+ * (pointers and strides).  Scores, sums and accumulators are
  * fp32.  Head sizes 64, 128 and 256 with pages of a multiple of 16 keys and codes
  * on 16-byte boundaries run on the tensor cores, with q and the weights
  * exp(a_j) e_j rounded to fp16 relative to their largest (2^-11; below 2^-14 of

@@ -24,3 +24,29 @@ def test_keys_without_rows_are_told():
         ws = new_ws()
         moe.moe_kv_read_q8(c.gkc, c.gvc, c.gks, c.gvs, c.gtable, c.kv_len, first, out, out.clone(), ws)
         assert status(ws) == want, lens
+
+
+def test_layouts_that_are_apart_are_taken():
+    """Keys and values interleaved in one array, rows of every second place, scales of one array: none share memory.  A
+    scale for the whole cache serves what reads it, and is refused where codes are written."""
+    g = torch.Generator().manual_seed(4)
+    both = torch.zeros(6, 2, 16, 4, 64, dtype=torch.uint8, device="cuda").view(E4M3)
+    sc = torch.zeros(6, 4, 32, 2, device="cuda")
+    kc, vc = both[:, 0, :, ::2], both[:, 1, :, 1::2]
+    ks, vs = (sc[:, ::2, ::2, i].transpose(1, 2) for i in (0, 1))
+    table, cu = torch.tensor([[4, 1, 3]], dtype=torch.int32).cuda(), torch.tensor([0, 40], dtype=torch.int32).cuda()
+    kv_len, x = torch.tensor([40], dtype=torch.int32).cuda(), torch.randn(2, 40, 2, 64, generator=g).to(torch.bfloat16).cuda()
+    ws = new_ws()
+    moe.moe_kv_append_q8(x[0], x[1], kc, vc, ks, vs, table, cu, kv_len, ws)
+    rows = torch.zeros(2, 40, 2, 64, device="cuda")
+    moe.moe_kv_read_q8(kc, vc, ks, vs, table, kv_len, cu[:1], rows[0], rows[1], ws)
+    assert status(ws) == 0
+    d = x.float().abs().amax(-1, keepdim=True) / 448.0
+    assert ((rows - x.float()).abs() <= torch.maximum(x.float().abs() * 2.0 ** -4, d * 2.0 ** -10) * (1 + 2.0 ** -10)).all()
+    one = torch.full((1, 1, 1), 0.5, device="cuda").expand(6, 16, 2)
+    with pytest.raises(moe.MoeError):
+        moe.moe_kv_append_q8(x[0], x[1], kc, vc, one, vs, table, cu, kv_len, ws)
+    moe.moe_kv_read_q8(kc, vc, one, one, table, kv_len, cu[:1], rows[0], rows[1], ws)
+    ids = table[0].long()
+    want = kc.view(torch.uint8)[ids].contiguous().view(E4M3).float().view(-1, 2, 64)[:40] * 0.5
+    assert torch.equal(rows[0], want) and status(ws) == 0
