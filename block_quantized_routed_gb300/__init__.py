@@ -32,7 +32,7 @@ __all__ = [
     "KvDesc", "moe_add_rmsnorm", "moe_route_grouped", "moe_kv_append", "moe_paged_attention",
     "moe_paged_attention_workspace_size", "MoeDecoderBlock",
     "KvScales", "moe_kv_append_q8", "moe_kv_read_q8", "moe_paged_attention_q8",
-    "moe_paged_attention_q8_workspace_size", "moe_linear", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU",
+    "moe_paged_attention_q8_workspace_size", "moe_linear", "moe_debug_linear", "ACT_NONE", "ACT_RELU", "ACT_SILU", "ACT_GELU",
     "ACT_GELU_TANH",
 ]
 
@@ -182,6 +182,8 @@ def load():
         "moe_paged_attention_q8": (ctypes.c_int, [KV, SC, I32, P, I64, I64, I32, I32, P, P, P, P, P, F32, I32, P, I64,
                                                   I64, P, P, SZ, P]),
         "moe_linear": (ctypes.c_int, [P, I32, I64, P, I64, P, I32, P, I32, I64, P, I32, I64, I32, I32, I32, P, P]),
+        "moe_debug_linear": (ctypes.c_int, [P, I32, I64, P, I64, P, I32, P, I32, I64, P, I32, I64, I32, I32, I32, I32, I32,
+                                            P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -508,6 +510,16 @@ def moe_linear(x, w, out, bias=None, act=ACT_NONE, residual=None, ws=None, strea
     of x's type or fp32 (may be one tensor; out shares no memory with the others).  ws: zeroed tensor for a status word,
     optional.  See include/moe_q8k.h."""
     (_ext or _binding()).linear(x, w, out, bias, act, residual, ws, stream)
+
+
+def moe_debug_linear(x, w, out, tokens, ctas, bias=None, act=ACT_NONE, residual=None, ws=None, stream=None):
+    """Test hook: moe_linear with a given plan (see include/moe_q8k.h)."""
+    import torch
+    dt = {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}
+    r, (T, K) = out if residual is None else residual, x.shape
+    _check(load().moe_debug_linear(_ptr(x), dt[x.dtype], x.stride(0), _ptr(w), w.stride(0), _ptr(bias), act, _ptr(residual),
+                                   dt[r.dtype], r.stride(0), _ptr(out), dt[out.dtype], out.stride(0), T, w.shape[0], K,
+                                   tokens, ctas, _ptr(ws), _stream(stream)), "moe_debug_linear")
 
 
 # ----------------------------------------------------------------- convenience

@@ -102,6 +102,58 @@ bool kv_strides16(const moe_kv_desc& kv) {
          kv.v_page_stride % 8 == 0 && kv.v_row_stride % 8 == 0 && kv.v_head_stride % 8 == 0;
 }
 
+// moe_linear with its plan (tokens 0: by cost)
+int linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, int64_t w_stride, const float* bias,
+           int32_t act, const void* residual, int32_t r_dtype, int64_t r_stride, void* out, int32_t o_dtype,
+           int64_t o_stride, int32_t T, int32_t N, int32_t K, int32_t* status, void* stream, LinearPlan plan) {
+  if (!residual) r_dtype = x_dtype;
+  if (T < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+  if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
+  if ((r_dtype != x_dtype && r_dtype != MOE_DT_F32) || (o_dtype != x_dtype && o_dtype != MOE_DT_F32)) return MOE_ERR_UNSUPPORTED;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH || K % 8) return MOE_ERR_UNSUPPORTED;
+  // tiles and rows are 32-bit numbers
+  if (((int64_t)N / 128 + 1) * ((int64_t)T / 16 + 1) > 1 << 30 || T > INT32_MAX - 1024 || N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
+    return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (!x || !w || !out) return MOE_ERR_INVALID_ARG;
+  if (T > 1 && (x_stride < K || o_stride < N || (residual && r_stride < N))) return MOE_ERR_INVALID_ARG;
+  if (N > 1 && w_stride < K) return MOE_ERR_INVALID_ARG;
+  if (T == 1) x_stride = r_stride = o_stride = 0;
+  if (N == 1) w_stride = 0;
+  if (x_stride % 8 || w_stride % 8 || x_stride >= (int64_t)1 << 39 || w_stride >= (int64_t)1 << 39) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(bias, 4) || !aligned_to(residual, dtype_size(r_dtype)) ||
+      !aligned_to(out, dtype_size(o_dtype)) || !aligned_to(status, 4))
+    return MOE_ERR_INVALID_ARG;
+  // tiles are written while others are read; a residual's element is read by the thread that writes its place
+  const auto rows = [](const void* p, int64_t n, int64_t cols, int64_t stride, int size) {
+    return Rows{p, n, cols * size, stride * size};
+  };
+  const Rows to = rows(out, T, N, o_stride, dtype_size(o_dtype));
+  const bool in_place = residual == out && r_dtype == o_dtype && r_stride == o_stride;
+  if (share(to, rows(x, T, K, x_stride, 2)) || share(to, rows(w, N, K, w_stride, 2)) || share(to, rows(bias, 1, N, 0, 4)) ||
+      (!in_place && share(to, rows(residual, T, N, r_stride, dtype_size(r_dtype)))) || share(to, rows(status, 1, 1, 0, 4)))
+    return MOE_ERR_INVALID_ARG;
+  LinearArgs a{};
+  a.x = x;
+  a.w = w;
+  a.bias = bias;
+  a.residual = residual;
+  a.out = out;
+  a.x_stride = x_stride;
+  a.w_stride = w_stride;
+  a.r_stride = r_stride;
+  a.o_stride = o_stride;
+  a.x_dtype = x_dtype;
+  a.r_dtype = r_dtype;
+  a.o_dtype = o_dtype;
+  a.act = act;
+  a.T = T;
+  a.N = N;
+  a.K = K;
+  a.status = status;
+  return done(launch_linear(a, plan, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -432,52 +484,17 @@ int moe_paged_attention_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, i
 int moe_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, int64_t w_stride, const float* bias,
                int32_t act, const void* residual, int32_t r_dtype, int64_t r_stride, void* out, int32_t o_dtype,
                int64_t o_stride, int32_t T, int32_t N, int32_t K, int32_t* status, void* stream) {
-  if (!residual) r_dtype = x_dtype;
-  if (T < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
-  if (x_dtype != MOE_DT_BF16 && x_dtype != MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
-  if ((r_dtype != x_dtype && r_dtype != MOE_DT_F32) || (o_dtype != x_dtype && o_dtype != MOE_DT_F32)) return MOE_ERR_UNSUPPORTED;
-  if (act < MOE_ACT_NONE || act > MOE_ACT_GELU_TANH || K % 8) return MOE_ERR_UNSUPPORTED;
-  // tiles and rows are 32-bit numbers
-  if (((int64_t)N / 128 + 1) * ((int64_t)T / 16 + 1) > 1 << 30 || T > INT32_MAX - 1024 || N > INT32_MAX - 1024 || K > INT32_MAX - 1024)
-    return MOE_ERR_UNSUPPORTED;
-  if (T == 0) return MOE_OK;
-  if (!x || !w || !out) return MOE_ERR_INVALID_ARG;
-  if (T > 1 && (x_stride < K || o_stride < N || (residual && r_stride < N))) return MOE_ERR_INVALID_ARG;
-  if (N > 1 && w_stride < K) return MOE_ERR_INVALID_ARG;
-  if (T == 1) x_stride = r_stride = o_stride = 0;
-  if (N == 1) w_stride = 0;
-  if (x_stride % 8 || w_stride % 8 || x_stride >= (int64_t)1 << 39 || w_stride >= (int64_t)1 << 39) return MOE_ERR_INVALID_ARG;
-  if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(bias, 4) || !aligned_to(residual, dtype_size(r_dtype)) ||
-      !aligned_to(out, dtype_size(o_dtype)) || !aligned_to(status, 4))
-    return MOE_ERR_INVALID_ARG;
-  // tiles are written while others are read; a residual's element is read by the thread that writes its place
-  const auto rows = [](const void* p, int64_t n, int64_t cols, int64_t stride, int size) {
-    return Rows{p, n, cols * size, stride * size};
-  };
-  const Rows to = rows(out, T, N, o_stride, dtype_size(o_dtype));
-  const bool in_place = residual == out && r_dtype == o_dtype && r_stride == o_stride;
-  if (share(to, rows(x, T, K, x_stride, 2)) || share(to, rows(w, N, K, w_stride, 2)) || share(to, rows(bias, 1, N, 0, 4)) ||
-      (!in_place && share(to, rows(residual, T, N, r_stride, dtype_size(r_dtype)))) || share(to, rows(status, 1, 1, 0, 4)))
-    return MOE_ERR_INVALID_ARG;
-  LinearArgs a{};
-  a.x = x;
-  a.w = w;
-  a.bias = bias;
-  a.residual = residual;
-  a.out = out;
-  a.x_stride = x_stride;
-  a.w_stride = w_stride;
-  a.r_stride = r_stride;
-  a.o_stride = o_stride;
-  a.x_dtype = x_dtype;
-  a.r_dtype = r_dtype;
-  a.o_dtype = o_dtype;
-  a.act = act;
-  a.T = T;
-  a.N = N;
-  a.K = K;
-  a.status = status;
-  return done(launch_linear(a, reinterpret_cast<cudaStream_t>(stream)));
+  return linear(x, x_dtype, x_stride, w, w_stride, bias, act, residual, r_dtype, r_stride, out, o_dtype, o_stride, T, N, K, status,
+                stream, LinearPlan{0, 0});
+}
+
+int moe_debug_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, int64_t w_stride, const float* bias,
+                     int32_t act, const void* residual, int32_t r_dtype, int64_t r_stride, void* out, int32_t o_dtype,
+                     int64_t o_stride, int32_t T, int32_t N, int32_t K, int32_t tokens, int32_t ctas, int32_t* status,
+                     void* stream) {
+  if (!linear_plan_ok(LinearPlan{tokens, ctas}, T, N, K)) return MOE_ERR_UNSUPPORTED;
+  return linear(x, x_dtype, x_stride, w, w_stride, bias, act, residual, r_dtype, r_stride, out, o_dtype, o_stride, T, N, K, status,
+                stream, LinearPlan{tokens, ctas});
 }
 
 }  // extern "C"

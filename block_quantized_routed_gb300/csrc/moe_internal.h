@@ -382,7 +382,12 @@ struct LinearArgs {
   int split;             // CTAs that share a tile's terms (set by the launcher)
   int* status;           // nullable
 };
-cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s);
+struct LinearPlan {
+  int tokens;            // of a tile: 16, 32, 64, 128 or 256 (0: chosen by cost)
+  int ctas;              // that share a tile's terms; 0: a pair of CTAs with 256 features
+};
+bool linear_plan_ok(LinearPlan p, int T, int N, int K);
+cudaError_t launch_linear(const LinearArgs& a, LinearPlan p, cudaStream_t s);
 
 // One sequence's rows and keys, checked: rows q0 .. q0 + n and kv keys.  A
 // sequence whose numbers are out of range has n = 0 (ok = false).

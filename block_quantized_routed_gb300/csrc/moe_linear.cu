@@ -812,22 +812,32 @@ void consider(const LinearArgs& a, Choice& best) {
 
 }  // namespace
 
-cudaError_t launch_linear(const LinearArgs& a, cudaStream_t s) {
+bool linear_plan_ok(LinearPlan p, int T, int N, int K) {
+  const int t = p.tokens, blocks = (K + kK - 1) / kK;
+  if (t != 16 && t != 32 && t != 64 && t != 128 && t != 256) return false;
+  if (p.ctas < 0 || p.ctas > 8 || (p.ctas == 0 && t < 128) || (p.ctas > 1 && (t > 128 || p.ctas > blocks))) return false;
+  return ((int64_t)N / kM + 1) * ((int64_t)T / t + 1) < 1 << 24;  // (a split's CTAs are the grid)
+}
+
+cudaError_t launch_linear(const LinearArgs& a, LinearPlan p, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  Choice c{256, 1, 1e300};
-  consider<16>(a, c);
-  consider<32>(a, c);
-  consider<64>(a, c);
-  consider<128>(a, c);
-  consider<256>(a, c);
-  consider_pair<128>(a, c);
-  consider_pair<256>(a, c);
-  if (c.split == 0) return c.bt == 128 ? launch_pair<128>(a, s) : launch_pair<256>(a, s);
-  switch (c.bt) {
-    case 16: return launch_tokens<16>(a, c.split, s);
-    case 32: return launch_tokens<32>(a, c.split, s);
-    case 64: return launch_tokens<64>(a, c.split, s);
-    case 128: return launch_tokens<128>(a, c.split, s);
+  if (p.tokens == 0) {
+    Choice c{256, 1, 1e300};
+    consider<16>(a, c);
+    consider<32>(a, c);
+    consider<64>(a, c);
+    consider<128>(a, c);
+    consider<256>(a, c);
+    consider_pair<128>(a, c);
+    consider_pair<256>(a, c);
+    p = LinearPlan{c.bt, c.split};
+  }
+  if (p.ctas == 0) return p.tokens == 128 ? launch_pair<128>(a, s) : launch_pair<256>(a, s);
+  switch (p.tokens) {
+    case 16: return launch_tokens<16>(a, p.ctas, s);
+    case 32: return launch_tokens<32>(a, p.ctas, s);
+    case 64: return launch_tokens<64>(a, p.ctas, s);
+    case 128: return launch_tokens<128>(a, p.ctas, s);
     default: return launch_tokens<256>(a, 1, s);
   }
 }

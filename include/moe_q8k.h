@@ -702,6 +702,16 @@ int moe_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, 
                int32_t act, const void* residual, int32_t r_dtype, int64_t r_stride, void* out, int32_t o_dtype,
                int64_t o_stride, int32_t T, int32_t N, int32_t K, int32_t* status, void* stream);
 
+/* Test hook: moe_linear on tiles of `tokens` tokens (16, 32, 64, 128 or 256) whose
+ * terms `ctas` CTAs share (1 .. 8, at most K / 64 rounded up; 256 tokens take 1;
+ * 0: pairs of CTAs over 256 features, with 128 or 256 tokens), instead of the plan
+ * that moe_linear chooses by cost.  MOE_ERR_UNSUPPORTED for other plans and for
+ * 2^24 tiles or more. */
+int moe_debug_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, int64_t w_stride, const float* bias,
+                     int32_t act, const void* residual, int32_t r_dtype, int64_t r_stride, void* out, int32_t o_dtype,
+                     int64_t o_stride, int32_t T, int32_t N, int32_t K, int32_t tokens, int32_t ctas, int32_t* status,
+                     void* stream);
+
 #ifdef __cplusplus
 }
 #endif
