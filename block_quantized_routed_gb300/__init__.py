@@ -507,8 +507,9 @@ def moe_paged_attention_q8(q, k_cache, v_cache, k_scale, v_scale, page_table, cu
 
 def moe_linear(x, w, out, bias=None, act=ACT_NONE, residual=None, ws=None, stream=None):
     """out = act(x w^T + bias) + residual: x [T, K] and w [N, K] bf16 or fp16, bias fp32 [N], residual and out [T, N]
-    of x's type or fp32 (may be one tensor; out shares no memory with the others).  ws: zeroed tensor for a status word,
-    optional.  See include/moe_q8k.h."""
+    of x's type or fp32 (may be one tensor; out shares no memory with the others).  ws: zeroed tensor for a status word
+    (moe_get_status), which tells why an output would be NaN after a wait that ran out; optional.  See
+    include/moe_q8k.h."""
     (_ext or _binding()).linear(x, w, out, bias, act, residual, ws, stream)
 
 

@@ -27,7 +27,7 @@
 //
 // Every wait is bounded: after about a second a role records
 // MOE_ERR_DEVICE_TIMEOUT (where a status word is given), and all roles run to
-// the end without waiting.
+// the end without waiting; the CTA's tiles from then on are NaN.
 #include <algorithm>
 #include <cmath>
 #include <cuda.h>
@@ -186,6 +186,7 @@ __device__ __forceinline__ uint32_t idesc(bool bf16, int M, int N) {
 struct Wait {
   volatile int* abort;
   int* status;
+  uint32_t other;  // the other CTA's abort word, of a pair (else 0)
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
     if (bar_try(bar, parity)) return true;
     const long long t0 = clock64();
@@ -193,6 +194,7 @@ struct Wait {
       if (*abort) return false;
       if (clock64() - t0 > kWaitCycles) {
         *abort = 1;
+        if (other) asm volatile("st.shared::cluster.u32 [%0], 1;\n fence.acq_rel.cluster;" ::"r"(other) : "memory");
         set_status(status, MOE_ERR_DEVICE_TIMEOUT);
         return false;
       }
@@ -297,14 +299,14 @@ __device__ __forceinline__ void prefetch_residual(const LinearArgs& a, int featu
   }
 }
 // A thread's part of a tile that is not shared: feature, tokens t .. t + live, of its accumulator's columns the half `part`;
-// `ready` waits for the products.
+// `ready` waits for the products and tells whether they are all there: what is written without them is NaN.
 template <int BT, int CH, typename F>
 __device__ __forceinline__ void finish_tile(const LinearArgs& a, uint32_t acc, int feature, int t, int live, int part, F ready) {
   uint32_t raw[2][CH];
   const int c0 = part * (BT / 2), c1 = min(live, c0 + BT / 2);
-  const float bias = bias_of(a, feature);
+  float bias = bias_of(a, feature);
   if (c0 < c1) ask_residual<CH>(a, feature, t + c0, c1 - c0, raw[0]);
-  ready();
+  if (!ready()) bias = NAN;
 #pragma unroll 1
   for (int c = c0; c < c1; c += CH) {
     if (c + CH < c1) ask_residual<CH>(a, feature, t + c + CH, c1 - c - CH, raw[1]);
@@ -381,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
   let_next_start();  // (this CTA has its tensor memory: one of the next kernel can no longer take it and wait for this one)
   if (C::kSplit) cluster_arrive();  // this CTA runs: others may write to it once they have waited
   const uint32_t tmem = s_tmem;
-  const Wait wait{&s_abort, a.status};
+  const Wait wait{&s_abort, a.status, 0};
   if (warp == 0) {
     if (elect_one()) {
       int s = ahead == kStages ? 0 : ahead;
@@ -459,6 +461,10 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
           float v[CH];
           __syncwarp();
           tmem_ld<CH>(acc + c, v);
+          if (s_abort) {
+#pragma unroll
+            for (int x = 0; x < CH; ++x) v[x] = NAN;
+          }
 #pragma unroll
           for (int x = 0; x < CH; x += 4)
             if (c + x < live) store_remote4(dst + (c + x) * 4, v + x);
@@ -488,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, C::kPerSm) linear_kernel(const Linea
           wait(acc_full(buf), acc_parity);
           __syncwarp();
           fence_after();
+          return !s_abort;
         });
       }
       fence_before();
@@ -571,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const LinearAr
   fence_after();
   let_next_start();
   const uint32_t tmem = s_tmem;
-  const Wait wait{&s_abort, a.status};
+  const Wait wait{&s_abort, a.status, remote(smem_u32(const_cast<int*>(&s_abort)), rank ^ 1)};
   const auto tile_at = [&](int i, int& f, int& t) { tile_of<8>(i, f_tiles, t_tiles, f, t); };
 
   if (warp == 0) {
@@ -640,6 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_pair_kernel(const LinearAr
                             wait(acc_full(buf), acc_parity);
                             __syncwarp();
                             fence_after();
+                            return !s_abort;
                           });
       fence_before();
       __syncwarp();

@@ -695,9 +695,9 @@ typedef enum {
  * (pointers, strides, and K a multiple of 8); residual and out on their
  * elements'.  T >= 0, N and K at least 1, (N / 128) * (T / 16) below 2^30.
  * status: NULL, or an int in device memory, zero before the first call, that
- * records MOE_ERR_DEVICE_TIMEOUT where a bounded wait ran out (out is void
- * then).  Numbers that are not finite in a row of x or of w reach that row or
- * column of out alone. */
+ * records MOE_ERR_DEVICE_TIMEOUT where a bounded wait ran out; tiles whose sums
+ * were not complete then are NaN, with a status word or without.  Numbers that
+ * are not finite in a row of x or of w reach that row or column of out alone. */
 int moe_linear(const void* x, int32_t x_dtype, int64_t x_stride, const void* w, int64_t w_stride, const float* bias,
                int32_t act, const void* residual, int32_t r_dtype, int64_t r_stride, void* out, int32_t o_dtype,
                int64_t o_stride, int32_t T, int32_t N, int32_t K, int32_t* status, void* stream);
