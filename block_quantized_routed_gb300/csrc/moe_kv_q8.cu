@@ -187,7 +187,7 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
   return r;
 }
 
-// N codes times their scale to N elements of type OUT
+// N codes times their scale to N elements of type OUT: an fp32 product, rounded again where OUT is narrower
 template <int FMT, int OUT, int N, bool WIDE>
 __device__ __forceinline__ void put_values(const uint32_t* w, float d, void* out, int64_t at) {
   float v[N];

@@ -627,9 +627,11 @@ int moe_kv_append_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, int32_t
                      void* k_cache, void* v_cache, const int32_t* page_table, const int32_t* cu_q,
                      const int32_t* kv_len, int32_t T, void* ws, size_t ws_bytes, void* stream);
 
-/* Reads sequences of an 8-bit cache back: key j of sequence b, code * scale
- * rounded once to out_dtype (F32, BF16 or F16), goes to row first[b] + j of
- * k_out [n_rows, Hkv, D] (row and head strides in elements), its value to v_out.
+/* Reads sequences of an 8-bit cache back: key j of sequence b, code * scale as an
+ * fp32 product, goes to row first[b] + j of k_out [n_rows, Hkv, D] (row and head
+ * strides in elements), its value to v_out.  out_dtype is F32, or BF16 or F16, to
+ * which the fp32 product is rounded a second time (to nearest, off by half a step
+ * and 2^-24 of the value at most).
  * Rows that belong to no key stay as they were.  first int32 [n_seqs] ascends:
  * first[b] + kv_len[b] <= first[b + 1], and n_rows after the last.  Keys whose
  * rows are taken by a later sequence or lie outside 0..n_rows are not written

@@ -50,3 +50,23 @@ def test_layouts_that_are_apart_are_taken():
     ids = table[0].long()
     want = kc.view(torch.uint8)[ids].contiguous().view(E4M3).float().view(-1, 2, 64)[:40] * 0.5
     assert torch.equal(rows[0], want) and status(ws) == 0
+
+
+@pytest.mark.parametrize("D", [64, 72])
+def test_products_are_rounded_to_fp32_and_then_to_16_bits(D):
+    """Scales whose product with the code 2.25 rounds to an fp32 number halfway between two of the output's: the second
+    rounding goes by that number, half a step and 2^-24 off at most."""
+    cases = {torch.bfloat16: [("0x1.a471c80000000p-1", 1.84375), ("0x1.29c71c0000000p-1", 1.3125), ("0x1.daaaaa0000000p-2", 1.046875)],
+             torch.float16: [("0x1.1571c80000000p-1", 1.21875), ("0x1.64c71c0000000p-1", 1.568359375), ("0x1.be8e380000000p-1", 1.962890625)]}
+    for dtype, pairs in cases.items():
+        codes = torch.full((1, 16, 1, D), 0x41, dtype=torch.uint8, device="cuda").view(E4M3)
+        scales = torch.ones(1, 16, 1, device="cuda")
+        scales[0, :3, 0] = torch.tensor([float.fromhex(d) for d, _ in pairs])
+        table, kv_len, first = (torch.tensor(t, dtype=torch.int32).cuda() for t in ([[0]], [3], [0]))
+        out, ws = torch.zeros(2, 3, 1, D, dtype=dtype, device="cuda"), new_ws()
+        moe.moe_kv_read_q8(codes, codes, scales, scales, table, kv_len, first, out[0], out[1], ws)
+        assert status(ws) == 0
+        for j, (d, want) in enumerate(pairs):
+            assert (out[:, j].double() == want).all()
+            exact = 2.25 * float.fromhex(d)
+            assert abs(want - exact) <= torch.finfo(dtype).eps / 2 + 2.0 ** -24 * exact     # (values between 1 and 2)
