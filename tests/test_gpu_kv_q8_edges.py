@@ -1,9 +1,10 @@
-"""The 8-bit paged cache: what is told of a call without rows."""
+"""The 8-bit paged cache: codes and scales over all 16-bit numbers, layouts, roundings, and calls without rows."""
+import numpy as np
 import pytest
 import torch
 
 import block_quantized_routed_gb300 as moe
-from tests.q8_ref import E4M3, Q8Cache, new_ws, status
+from tests.q8_ref import E4M3, INT8, Q8Cache, new_ws, quantise, status
 
 pytestmark = pytest.mark.gpu
 
@@ -11,6 +12,31 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def _lib():
     moe.load()
+
+
+@pytest.mark.parametrize("fmt", [E4M3, INT8])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_every_finite_number_is_a_largest_element(fmt, dtype):
+    """A vector for each finite magnitude, the other elements any bits up to it: scales and codes are those of IEEE
+    division, bit for bit."""
+    top = 0x7f80 if dtype == torch.bfloat16 else 0x7c00
+    g = torch.Generator().manual_seed(8)
+    peak = torch.arange(top).unsqueeze(1)
+    mag = torch.minimum((torch.rand(top, 63, generator=g, dtype=torch.float64) * (peak + 1)).long(), peak)
+    mag[:, 32:] = (peak - torch.randint(0, 1500, (top, 31), generator=g)).clamp_min(0)    # near it: codes other than 0
+    bits = torch.cat([peak, mag], 1) | torch.randint(0, 2, (top, 64), generator=g) << 15
+    x = torch.from_numpy(bits.numpy().astype(np.uint16).view(np.int16)).view(dtype).view(top, 1, 64)
+    c = Q8Cache([top], 1, 64, 64, fmt)
+    ws, cu = new_ws(), torch.tensor([0, top], dtype=torch.int32).cuda()
+    moe.moe_kv_append_q8(x.cuda(), x.flip(0).cuda(), c.gkc, c.gvc, c.gks, c.gvs, c.gtable, cu, c.kv_len, ws)
+    assert status(ws) == 0
+    ids = c.table[0].long()
+    for v, codes, scales in ((x, c.gkc, c.gks), (x.flip(0), c.gvc, c.gvs)):
+        want, d = quantise(v, fmt)
+        got = codes.view(torch.uint8).cpu()[ids].view(-1, 1, 64)[:top]
+        zero = (v == 0).all(-1)                                    # (zeros have code 0 whatever their sign)
+        assert torch.equal(scales.cpu()[ids].view(-1, 1)[:top], d)
+        assert torch.equal(got[~zero], want.view(torch.uint8)[~zero]) and not got[zero].any()
 
 
 def test_keys_without_rows_are_told():
