@@ -659,8 +659,9 @@ size_t moe_paged_attention_q8_workspace_size(int32_t Hq, int32_t Hkv, int32_t D)
  * (pointers and strides).  Scores, sums and accumulators are
  * fp32.  Head sizes 64, 128 and 256 with pages of a multiple of 16 keys and codes
  * on 16-byte boundaries run on the tensor cores, with q and the weights
- * exp(a_j) e_j rounded to fp16 relative to their largest (2^-11; below 2^-14 of
- * it 2^-25 of it); other sizes run on a general kernel.  A scale that is not a
+ * exp(a_j) e_j rounded to fp16 relative to their largest (2^-11; a weight below
+ * 2^-21 of it is off by 2^-32 of it, an element of q below 2^-28 by 2^-39); other
+ * sizes run on a general kernel.  A scale that is not a
  * number makes out (and lse, for a key's) of the rows that see its key NaN; so
  * does a code that is NaN, a value's in its column at least.
  * Codes and scales of keys that a row does not see have no effect on it.  Every
@@ -680,21 +681,22 @@ int moe_paged_attention_q8(const moe_kv_desc* kv, const moe_kv_scales* scales, i
 typedef enum {
   MOE_ACT_NONE = 0,
   MOE_ACT_RELU = 1,
-  MOE_ACT_SILU = 2,     /* v / (1 + exp(-v)) */
+  MOE_ACT_SILU = 2,     /* v / (1 + exp(-v)); off by 2^-20 + |v| 2^-23 of itself at most, 0 below -87 */
   MOE_ACT_GELU = 3,     /* v (1 + erf(v / sqrt(2))) / 2 */
   MOE_ACT_GELU_TANH = 4 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
 } moe_act;
 
 /* A dense product with its epilogue, the block's projections:
  *   out = act(x W^T + bias) + residual
- * x [T, K] and w [N, K] of x_dtype (BF16 or F16; products are exact, sums and
- * everything after them fp32), bias float [N] or NULL, residual [T, N] of
- * r_dtype (x's type or F32) or NULL, out [T, N] of o_dtype (x's type or F32),
- * rounded once.  Row strides are in elements; residual and out may be the same
- * array (with the same type and stride), otherwise out shares no element with
- * x, w, bias, residual or status (MOE_ERR_INVALID_ARG; columns of one array are
- * told apart where the rows have one stride).  x and w lie on 16-byte boundaries
- * (pointers, strides, and K a multiple of 8); residual and out on their
+ * x [T, K] and w [N, K] of x_dtype (BF16 or F16; products are exact, sums are the
+ * tensor pipe's fp32 accumulators, whose additions may cut instead of round, up to
+ * 2^-23 of a partial sum each; everything after them is fp32), bias float [N] or
+ * NULL, residual [T, N] of r_dtype (x's type or F32) or NULL, out [T, N] of o_dtype
+ * (x's type or F32), rounded once.  Row strides are in elements; residual and out
+ * may be the same array (with the same type and stride), otherwise out shares no
+ * element with x, w, bias, residual or status (MOE_ERR_INVALID_ARG; columns of one
+ * array are told apart where the rows have one stride).  x and w lie on 16-byte
+ * boundaries (pointers, strides, and K a multiple of 8); residual and out on their
  * elements'.  T >= 0, N and K at least 1, (N / 128) * (T / 16) below 2^30.
  * status: NULL, or an int in device memory, zero before the first call, that
  * records MOE_ERR_DEVICE_TIMEOUT where a bounded wait ran out; tiles whose sums

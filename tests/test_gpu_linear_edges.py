@@ -1,4 +1,4 @@
-"""The dense product where its arrays lie among one another."""
+"""The dense product where its arrays lie among one another, and its activations over all numbers."""
 import pytest
 import torch
 
@@ -46,3 +46,20 @@ def test_residuals_that_are_not_quite_out_are_refused():
     assert not out.any()
     moe.moe_linear(x, w, out[:8], residual=out[:8])
     assert (out[:8] == 64).all() and not out[8].any()
+
+
+def test_silu_of_every_number_that_it_holds():
+    """2^-20 + |v| 2^-23 of itself: the exponential of a rounded argument within 2 ulp, a quotient within 2 ulp."""
+    bits = torch.arange(1 << 16).int()
+    v = bits.where(bits < 1 << 15, bits - (1 << 16)).short().view(BF16)
+    v = v[torch.isfinite(v) & (v > -87)]
+    x = torch.zeros(len(v), 8, dtype=BF16, device="cuda")
+    x[:, 0] = v.cuda()
+    w = torch.zeros(1, 8, dtype=BF16, device="cuda")
+    w[0, 0] = 1
+    out = torch.empty(len(v), 1, device="cuda")
+    moe.moe_linear(x, w, out, act=moe.ACT_SILU)
+    d = v.double()
+    want = d / (1 + torch.exp(-d))
+    err = (out[:, 0].cpu().double() - want).abs()
+    assert (err <= (2.0 ** -20 + d.abs() * 2.0 ** -23) * want.abs() + 2.0 ** -126).all()
