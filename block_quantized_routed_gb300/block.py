@@ -23,8 +23,10 @@ import block_quantized_routed_gb300 as moe
 
 
 READ_PAGE = 64   # keys of a page of the rows that an 8-bit cache is read back into
-# it is for more new tokens per sequence, on average, than this (32 heads over 4 of 128, 16 sequences of 4096 keys: 16 new
-# tokens each 78 us against 114, 4 of them 76 against 43)
+# It is for more new tokens per sequence, on average, than this.  Over the codes / by way of 16 bits, in us, every sequence
+# with 4 / 8 / 16 new tokens: 16 of 4096 keys (32 heads over 4 of 128) 43/74, 66/75, 115/77; 2 of 8192 35/28, 37/29, 44/31;
+# 1 of 65536 (64 over 8) 84/125, 117/126, 206/128; 8 of 4096 (40 over 8 of 64) 29/46, 44/51, 60/51; 4 of 4096 (16 over 2 of
+# 256) 25/29, 31/30, 39/34.  One rule for the call: a long chunk among single tokens takes their caches with it.
 READ_FROM = 8
 
 

@@ -4,11 +4,15 @@
 //
 // in one pass over the keys with running references (c = log2 e).
 //
-// What bounds it: memory.  With 8 query heads to a key/value head a key is
-// 4 * 8 * D operations for 2 (D + 4) bytes, a sixth of what mma.sync does
-// while the bytes arrive, so the products stay on it: its operands are
+// What bounds it: for single tokens memory.  With 8 query heads to a key/value
+// head a key is 4 * 8 * D operations for 2 (D + 4) bytes, a sixth of what mma.sync
+// does while the bytes arrive, so the products stay on it: its operands are
 // registers, and codes become fp16 numbers there (moe_q8.cuh), which tcgen05,
 // whose keys and values come from shared memory, would need written back first.
+// That reason ends with 8 rows: at 32, four tokens of such heads, a key costs two
+// thirds of mma.sync's rate and four times the exponentials, and more rows read
+// their keys again.  16 sequences of 4096 keys (32 heads over 4 of 128): 1, 4, 8
+// and 16 new tokens each 21, 43, 66 and 115 us.
 //
 // Layout.  Keys are the 16 rows of S^T = K q^T and the 16 terms of out^T = V^T P^T,
 // rows of the query (token, head of the key/value head) the 8 columns of a tile,
@@ -38,9 +42,10 @@
 // What it measured (e4m3): four tokens over up to 131072 keys each (64 heads over
 // 8 of 128) 103 to 113 us, 5.1 to 5.6 TB/s; 48 over up to 8192 keys (32 over 4 of
 // 128) 48 us, 4.7 TB/s: tile by tile about 7, besides 5 us to the first and 4 from
-// the last; one over 777 keys 11.6 us, latency: half of 6 us on the device is the
-// way to the first tile, through cu_q, the page table and instructions that are
-// fetched for the first time.
+// the last; one over 777 keys 11.5 us, latency: of a CTA's clocks a third go by
+// until its first boxes are asked for, through cu_q, the page table and
+// instructions that are fetched for the first time, and half in the joins of its
+// warps and of the parts, through global memory.
 #include <algorithm>
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -180,7 +185,7 @@ __device__ __forceinline__ Work work_of(const AttnArgs& a, int G, int b) {
 constexpr int kTries = 4;  // sizes of a part that are tried, in steps of an eighth
 template <class C>
 struct Shared {
-  int scan[C::W], units[C::W], items[C::W], ctas[C::W][kTries];
+  int scan[C::W], items[C::W], ctas[C::W][kTries];
   long long rows[C::W];
   int seq, before, last;
   Work work;
@@ -952,8 +957,14 @@ cudaError_t launch_t(const AttnQ8Args& a, cudaStream_t s) {
 template <int D, int FMT>
 cudaError_t launch_rows(const AttnQ8Args& g, cudaStream_t s) {
   // Rows of an item: those of a sequence of the mean number of new tokens.  A longer one has several items and reads its
-  // keys as often, a shorter one leaves rows empty.  16 windows of up to 4 tokens, 5 heads to a key/value head of 64, whose
-  // mean are 15 rows: 16.1 us with 16 rows, 18.1 with 32; 2 tokens of 8 heads of 128 over 65536 keys: 55 and 73 us.
+  // keys as often, a shorter one leaves rows empty.  In us with 8 / 16 / 32 rows, 16 sequences of 4096 keys but for the last:
+  //   rows of each       8               16              24              32              48              64
+  //   D = 64, 8 heads    26 / 30 / 42    42 / 30 / 43    57 / 49 / 44    73 / 50 / 44    103 / 68 / 76   133 / 87 / 77
+  //   D = 128, 4 heads   21 / 25 / 36    31 / 28 / 38    42 / 41 / 41    52 / 42 / 42    71 / 56 / 65    92 / 71 / 66
+  //   D = 256, 2 heads   22 / 26         29 / 31         38 / 38         47 / 39         64 / 50         83 / 61
+  //   2 of 65536, 128    39 / 45 / 65    50 / 52 / 73    72 / 69 / 78    88 / 71 / 83    126 / 99 / 117  163 / 125 / 118
+  // Windows of 1 to 4 tokens of 5 heads of 64, whose mean are 15 rows: 42 / 35 / 44.  So 16 rows would be as good or better
+  // than 32 up to 48 rows of 128 columns and from 33 to 48 of 64.
   const int64_t mean = (g.a.T + (int64_t)g.a.kv.n_seqs - 1) / g.a.kv.n_seqs, want = g.a.Hq / g.a.kv.Hkv * mean;
   if (want <= 8) return launch_t<D, 1, FMT>(g, s);
   if (D == 256 || want <= 16) return launch_t<D, 2, FMT>(g, s);

@@ -296,8 +296,12 @@ cudaError_t append_as(const KvAppendQ8Args& a, int warps, cudaStream_t s) {
 }
 template <bool BF16, int FMT>
 cudaError_t append(const KvAppendQ8Args& a, cudaStream_t s) {
-  // Few tokens are latency: a warp to each token and as few heads as it holds (64 tokens of 4 heads of 128: 2.8 us, with
-  // two loads of a lane 3.4).  Many share the way to their page among two (5257 tokens of 8 heads: 10.8 us, with one 11.8).
+  // Few tokens are latency: a warp to each token and as few heads as it holds.  Many share the way to their page among the
+  // heads of two loads.  In us with one / two, bf16 to e4m3, tokens one after the other in a sequence:
+  //                      64           304          456          608          1000         1500         5257
+  //   4 heads of 128     1.9 / 2.3    2.0 / 2.3    2.2 / 2.3    2.5 / 2.3    3.1 / 3.4    3.4 / 4.2    11.1 / 4.9
+  //   8 heads of 128     1.9 / 2.3    2.5 / 2.4    3.0 / 2.5    2.9 / 3.6    4.4 / 4.5    6.4 / 4.7    21.6 / 8.8
+  //   2 heads of 256     2.0 / 2.3    2.0 / 2.4    2.3 / 2.4    2.6 / 2.4    3.2 / 3.4    3.4 / 4.2    11.1 / 5.0
   return a.a.T <= 4 * num_sms() ? append_as<BF16, FMT, 1>(a, 1, s) : append_as<BF16, FMT, 2>(a, 4, s);
 }
 template <int FMT, int OUT>

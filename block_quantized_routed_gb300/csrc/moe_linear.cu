@@ -18,12 +18,15 @@
 // the accumulators are joined through distributed shared memory: each CTA sums
 // a slice of the features, in the order of the ranks, and runs their epilogue.
 //
-// What it measured (bf16 but for the third): one token of 5120 x 2048 7.1 us, 37 of
+// What it measured (bf16 but for the third): one token of 5120 x 2048 7.2 us, 37 of
 // 6144 x 4096 onto an fp32 residual 14 us: 3 us to the first data, 7 for the
 // weights, 3 for the join and the way out; 1021 of 7001 x 2048 with gelu (fp16)
-// 27 us, three rounds of tiles; 8192 of 5120 x 4096 with silu and a residual 195
-// us, 1765 TFLOP/s, the tensor pipe 90% active.  One token of 32768 x 4096: 42 us,
-// 6.4 TB/s.
+// 27 us, three rounds of tiles; 8192 of 5120 x 4096 with silu and a residual 193 to
+// 198 us, 1735 to 1784 TFLOP/s, the tensor pipe 91% active.  One token of 32768 x
+// 4096: 42 us, 6.4 TB/s.  Beside a library product that adds no bias, all in bf16:
+// 1 x 5120 x 2048 7.2 (library 5.6), 16 x 5120 x 2048 7.6 (5.7), 37 x 6144 x 4096
+// 13.5 (11.7), 256 x 5120 x 2048 10.4 (6.8), 8192 x 5120 x 4096 180 (183), and rows
+// of an odd width, 1021 x 7001 x 2048, 23 (232).
 //
 // Every wait is bounded: after about a second a role records
 // MOE_ERR_DEVICE_TIMEOUT (where a status word is given), and all roles run to
