@@ -1,4 +1,5 @@
-"""The dense product's refusals of outputs that lie in its inputs (before any launch; no compute call is made here)."""
+"""The dense product's refusals of outputs that lie in its inputs and of plans that are none (before any launch; no compute
+call is made here)."""
 import ctypes
 
 import pytest
@@ -32,3 +33,12 @@ def test_out_in_an_input_is_refused(lib, kw):
     for name in ("x", "w", "b", "r", "out", "st"):
         a[name] = ctypes.c_void_p(a[name]) if a[name] else None
     assert lib.moe_linear(*a.values(), None) == INV
+
+
+@pytest.mark.parametrize("tokens,ctas,T,N,K", [(0, 1, 4, 32, 64), (48, 1, 4, 32, 64), (512, 1, 4, 32, 64), (16, 0, 4, 32, 64),
+                                               (64, 0, 4, 32, 64), (256, 2, 4, 32, 512), (16, 9, 4, 32, 1024), (16, 3, 4, 32, 128),
+                                               (128, -1, 4, 32, 64), (16, 1, 1 << 20, 1 << 20, 64)])
+def test_plans_that_are_none_are_refused(lib, tokens, ctas, T, N, K):
+    p = [ctypes.c_void_p(x) for x in (X, W, OUT)]
+    assert lib.moe_debug_linear(p[0], 1, K, p[1], K, None, 0, None, 1, 0, p[2], 1, N, T, N, K, tokens, ctas, None,
+                                None) == moe.MOE_ERR_UNSUPPORTED
