@@ -95,3 +95,41 @@ def test_calls_that_overlap_repeat_calls_that_do_not():
         assert status(ws) == 0
         results.append([t.clone() for t in (x, qkv, o, up, rows, c.gkc.view(torch.uint8), c.gks)])
     assert all(torch.equal(a, b) for a, b in zip(*results)) and torch.isfinite(results[0][0].float()).all()
+
+
+def test_operators_beside_one_another_on_streams():
+    """Products of every kind, attention over both caches and the cache's own calls at one time, each stream with its own
+    workspaces: the results of one after the other."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF16)
+    Hq, Hkv, D, n = 16, 2, 128, 4
+    c = Q8Cache([5000, 800, 17, 2000], Hkv, D, 64, E4M3)
+    k16, v16 = (rand(c.pages, 64, Hkv, D) for _ in range(2))
+    q, cu = rand(n, Hq, D), torch.arange(n + 1, dtype=torch.int32).cuda()
+    first = torch.tensor([0, 5000, 5800, 5817], dtype=torch.int32).cuda()
+    xs = {t: (rand(t, 2048), rand(1100, 2048)) for t in (1, 40, 300, 1500)}
+
+    def work():
+        """The calls of a stream, their outputs and status words."""
+        ws8, ws16, wl = (new_ws(b) for b in (moe.moe_paged_attention_q8_workspace_size(Hq, Hkv, D),
+                                             moe.moe_paged_attention_workspace_size(Hq, Hkv, D), 16))
+        o8, o16, rows = torch.zeros_like(q), torch.zeros_like(q), torch.zeros(2, 7817, Hkv, D, dtype=BF16, device="cuda")
+        ys = {t: torch.zeros(t, 1100, dtype=BF16, device="cuda") for t in xs}
+        calls = [lambda t=t: moe.moe_linear(*xs[t], ys[t], ws=wl) for t in xs]
+        calls.insert(1, lambda: moe.moe_paged_attention_q8(q, c.gkc, c.gvc, c.gks, c.gvs, c.gtable, cu, c.kv_len, 0.1, o8, ws8))
+        calls.insert(3, lambda: moe.moe_paged_attention(q, k16, v16, c.gtable, cu, c.kv_len, 0.1, o16, ws16))
+        calls.insert(5, lambda: moe.moe_kv_read_q8(c.gkc, c.gvc, c.gks, c.gvs, c.gtable, c.kv_len, first, rows[0], rows[1], wl))
+        return calls, [o8, o16, rows, *ys.values()], (ws8, ws16, wl)
+    calls, want, _ = work()
+    for f in calls:
+        f()
+        torch.cuda.synchronize()
+    streams, parts = [torch.cuda.Stream() for _ in range(3)], [work() for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(60):
+        for j, (s, (calls, _, _)) in enumerate(zip(streams, parts)):
+            with torch.cuda.stream(s):
+                calls[(i + 2 * j) % len(calls)]()
+    torch.cuda.synchronize()
+    for _, outs, spaces in parts:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)) and [status(ws) for ws in spaces] == [0, 0, 0]
